@@ -16,6 +16,8 @@ from pathlib import Path
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libpararnn.so"
+# the operators of the layer around the solver (include/pararnn_layer.h)
+LAYER_LIB = PKG / "libpararnn_layer.so"
 # measurement kernels for the device ceilings bench.py reports (not the solver)
 CEIL_LIB = PKG / "libceilings.so"
 ARCH = "gfx950"
@@ -50,6 +52,7 @@ def build_one(src: Path, out: Path, verbose: bool = False, extra_flags=(), host_
 
 def build(verbose: bool = False, extra_flags=()) -> Path:
     build_one(CSRC / "ceilings.hip", CEIL_LIB, verbose, extra_flags)
+    build_one(CSRC / "layer.hip", LAYER_LIB, verbose, extra_flags)
     return build_one(CSRC / "pararnn.hip", LIB, verbose, extra_flags)
 
 

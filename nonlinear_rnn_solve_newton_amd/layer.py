@@ -1,0 +1,223 @@
+"""Operators of the recurrent layer around the solver (libpararnn_layer.so).
+
+  norm_residual   root-mean-square norm with the residual's addition, in the
+                  input's type or in 8 bits with scales, and its adjoint
+  matmul_fp8      product of 8-bit matrices with a scale for each block of 128:
+                  the projection that makes the gate inputs u
+  gated_scan      gated linear recurrence over the sequence, its adjoint, and
+                  gated_step, its form for single tokens
+
+Like `binding`, this module checks tensors, allocates outputs and workspace
+with torch and passes raw device pointers plus torch's current HIP stream to
+the C entry points of include/pararnn_layer.h, whose comments define the
+operators. Every tensor must be contiguous and on the same ROCm device; a
+wrong type, shape or placement raises PararnnError. There is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import re
+from typing import Optional
+
+import torch
+
+from .binding import BF16, F32, PKG, PararnnError, alloc_workspace, strerror
+
+LIB_PATH = PKG / "libpararnn_layer.so"
+HEADER = PKG.parent / "include" / "pararnn_layer.h"
+
+_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+class GatedOpts(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("L", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("c", ctypes.c_float),
+        ("lengths", ctypes.c_void_p),
+        ("reset", ctypes.c_void_p),
+    ]
+
+
+def header_functions() -> list[str]:
+    """Names of the functions declared in include/pararnn_layer.h."""
+    return re.findall(r"^\s*[a-z_0-9]+\s+(pararnn_[a-z_0-9]+)\s*\(", HEADER.read_text(), re.M)
+
+
+_lib = None
+
+
+def lib():
+    global _lib
+    if _lib is None:
+        if not LIB_PATH.exists():
+            raise PararnnError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
+        L = ctypes.CDLL(str(LIB_PATH))
+        P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+        G = ctypes.POINTER(GatedOpts)
+        L.pararnn_gated_workspace_bytes.argtypes = [I32, G]
+        L.pararnn_gated_workspace_bytes.restype = SZ
+        L.pararnn_gated_saved_rows.argtypes = [I32]
+        L.pararnn_gated_saved_rows.restype = I32
+        L.pararnn_gated_scan.argtypes = [P, P, P, P, P, P, P, SZ, G, P]
+        L.pararnn_gated_scan.restype = I32
+        L.pararnn_gated_scan_adjoint.argtypes = [P, P, P, P, P, P, P, P, P, SZ, G, P]
+        L.pararnn_gated_scan_adjoint.restype = I32
+        L.pararnn_gated_step.argtypes = [P, P, P, P, P, I32, I32, I32, I32, F, P]
+        L.pararnn_gated_step.restype = I32
+        _lib = L
+    return _lib
+
+
+def _check(status: int, what: str):
+    if status != 0:
+        raise PararnnError(f"{what} failed: {status} ({strerror(status)})")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _dev(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """Checks an argument that may be None; dtype None takes any."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PararnnError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise PararnnError(f"{name} must be on {device}, got {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise PararnnError(f"{name} must be contiguous")
+
+
+def _first(t, name: str, dims: int) -> torch.device:
+    """The device of a call, from its first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PararnnError(f"{name} must be a device tensor")
+    if t.dim() != dims:
+        raise PararnnError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if not t.is_contiguous():
+        raise PararnnError(f"{name} must be contiguous")
+    return t.device
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _workspace(ws, need: int, device):
+    if need == 0:
+        raise PararnnError("invalid sizes or options")
+    if ws is None:
+        return alloc_workspace(need, device)
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
+        raise PararnnError("ws must be a contiguous uint8 tensor on the inputs' device")
+    return ws
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence
+
+def _gated_opts(u, lam, c, lengths, reset):
+    dev = _first(u, "u", 4)
+    B, L, G, D = u.shape
+    if G != 3:
+        raise PararnnError("u must be [B][L][3][D]")
+    if u.dtype not in _DTYPE:
+        raise PararnnError(f"u must be float32 or bfloat16, got {u.dtype}")
+    _dev(lam, "lam", torch.float32, (D,), dev)
+    _dev(lengths, "lengths", torch.int32, (B,), dev)
+    if reset is not None and reset.dtype == torch.bool:
+        reset = reset.view(torch.uint8)
+    _dev(reset, "reset", torch.uint8, (B, L), dev)
+    o = GatedOpts(B, L, D, _DTYPE[u.dtype], c, _ptr(lengths), _ptr(reset))
+    return o, dev, B, L, D
+
+
+def gated_scan(u: torch.Tensor, lam: torch.Tensor, *, c: float = 8.0, h0: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None, reset: Optional[torch.Tensor] = None, save: bool = False,
+               out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> dict:
+    """h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(u_i) x_t, log a_t = -c softplus(lam) s(u_r).
+
+    u [B][L][3][D] (gates r, i, x) bf16 or fp32, lam [D] fp32, h0 [B][D] fp32 or
+    None (zero), lengths [B] int32 (steps of each row), reset [B][L] uint8 or
+    bool (document starts). Returns dict(h [B][L][D] in u's type, hT [B][D]
+    fp32 state after the last step, saved (with save=True, for the adjoint), ws).
+    """
+    o, dev, B, L, D = _gated_opts(u, lam, c, lengths, reset)
+    _dev(h0, "h0", torch.float32, (B, D), dev)
+    if out is None:
+        out = torch.empty(B, L, D, dtype=u.dtype, device=dev)
+    _dev(out, "out", u.dtype, (B, L, D), dev)
+    need = lib().pararnn_gated_workspace_bytes(0, ctypes.byref(o))
+    ws = _workspace(ws, need, dev)
+    hT = torch.empty(B, D, dtype=torch.float32, device=dev)
+    saved = (torch.empty(lib().pararnn_gated_saved_rows(L), B, D, dtype=torch.float32, device=dev)
+             if save else None)
+    with torch.cuda.device(dev):
+        st = lib().pararnn_gated_scan(_ptr(u), _ptr(lam), _ptr(h0), _ptr(out), _ptr(hT), _ptr(saved), _ptr(ws),
+                                      ws.numel(), ctypes.byref(o), _stream(dev))
+    _check(st, "pararnn_gated_scan")
+    return dict(h=out, hT=hT, saved=saved, ws=ws)
+
+
+def gated_scan_adjoint(u: torch.Tensor, lam: torch.Tensor, dh: torch.Tensor, saved: torch.Tensor, *,
+                       c: float = 8.0, dhT: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                       reset: Optional[torch.Tensor] = None, want_dlam: bool = True, want_dh0: bool = False,
+                       du: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> dict:
+    """Adjoint of gated_scan for dh = dL/dh [B][L][D] (u's type) and dhT = dL/dhT
+    [B][D] fp32 or None; `saved` and the options are those of the forward call.
+    Returns dict(du [B][L][3][D] in u's type, dlam [D], dh0 [B][D], ws)."""
+    o, dev, B, L, D = _gated_opts(u, lam, c, lengths, reset)
+    _dev(dh, "dh", u.dtype, (B, L, D), dev)
+    _dev(saved, "saved", torch.float32, (lib().pararnn_gated_saved_rows(L), B, D), dev)
+    if saved is None:
+        raise PararnnError("the adjoint needs the states saved by gated_scan(save=True)")
+    _dev(dhT, "dhT", torch.float32, (B, D), dev)
+    if du is None:
+        du = torch.empty(B, L, 3, D, dtype=u.dtype, device=dev)
+    _dev(du, "du", u.dtype, (B, L, 3, D), dev)
+    need = lib().pararnn_gated_workspace_bytes(1, ctypes.byref(o))
+    ws = _workspace(ws, need, dev)
+    dlam = torch.empty(D, dtype=torch.float32, device=dev) if want_dlam else None
+    dh0 = torch.empty(B, D, dtype=torch.float32, device=dev) if want_dh0 else None
+    with torch.cuda.device(dev):
+        st = lib().pararnn_gated_scan_adjoint(_ptr(u), _ptr(lam), _ptr(saved), _ptr(dh), _ptr(dhT), _ptr(du),
+                                              _ptr(dlam), _ptr(dh0), _ptr(ws), ws.numel(), ctypes.byref(o),
+                                              _stream(dev))
+    _check(st, "pararnn_gated_scan_adjoint")
+    return dict(du=du, dlam=dlam, dh0=dh0, ws=ws)
+
+
+def gated_step(u: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *, c: float = 8.0,
+               slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One step for each of B requests, u [B][3][D]: updates the rows slots[b]
+    (int32 [B]; None: row b) of the pool `state` [S][D] fp32 in place and
+    returns h [B][D] in u's type. A slot outside 0..S-1 (-1, say) is a row
+    without a request: h = 0. The slots must differ from each other."""
+    dev = _first(u, "u", 3)
+    B, G, D = u.shape
+    if G != 3:
+        raise PararnnError("u must be [B][3][D]")
+    if u.dtype not in _DTYPE:
+        raise PararnnError(f"u must be float32 or bfloat16, got {u.dtype}")
+    _dev(lam, "lam", torch.float32, (D,), dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise PararnnError("state must be [S][D]")
+    S = state.shape[0]
+    _dev(state, "state", torch.float32, (S, D), dev)
+    _dev(slots, "slots", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty(B, D, dtype=u.dtype, device=dev)
+    _dev(out, "out", u.dtype, (B, D), dev)
+    with torch.cuda.device(dev):
+        st = lib().pararnn_gated_step(_ptr(u), _ptr(lam), _ptr(slots), _ptr(state), _ptr(out), B, D, S,
+                                      _DTYPE[u.dtype], c, _stream(dev))
+    _check(st, "pararnn_gated_step")
+    return out
