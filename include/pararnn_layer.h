@@ -68,6 +68,67 @@ int32_t pararnn_gated_scan_adjoint(const void* u, const float* lam, const float*
 int32_t pararnn_gated_step(const void* u, const float* lam, const int32_t* slots, float* state, void* h, int32_t B,
                            int32_t D, int32_t S, int32_t dtype, float c, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition, rows of D columns:
+ *   s = x + residual (x if NULL),  y = s / sqrt(mean(s^2) + eps) * w.
+ * x, residual, s, dy, ds, dx [N][D] in `dtype`, w, dw [D] fp32.
+ */
+typedef enum {
+  PARARNN_NORM_SAME = 0,      /* y [N][D] in `dtype`; scale is not used */
+  PARARNN_NORM_FP8 = 1,       /* y [N][D] e4m3, scale [ceil(D/128)][N] fp32 */
+  PARARNN_NORM_FP8_E8M0 = 2   /* y [N][D] e4m3, scale [ceil(D/128)][N] e8m0 (powers of two) */
+} pararnn_norm_out;
+
+typedef struct {
+  int64_t N;      /* rows, >= 1 */
+  int32_t D;      /* columns, 1..16384 */
+  int32_t dtype;  /* pararnn_dtype */
+  int32_t out;    /* pararnn_norm_out; ignored by the adjoint */
+  float eps;      /* >= 0 and finite */
+} pararnn_norm_opts;
+
+/* Forward: y, and optionally s (NULL: not written), from one pass. y is made
+ * from the sum before its rounding to `dtype`. With an 8-bit y every 128
+ * columns of a row share scale = max(max|y|, 2^-100) / 448, or the next power
+ * of two at or above that, and hold y / scale rounded to nearest even; a block
+ * with an infinity or a NaN stands for NaN. */
+int32_t pararnn_norm_residual(const void* x, const void* residual, const float* w, void* s, void* y, void* scale,
+                              const pararnn_norm_opts* o, void* stream);
+
+/* Workspace of the adjoint's dw; 0 for invalid options. Host-only. */
+size_t pararnn_norm_workspace_bytes(const pararnn_norm_opts* o);
+
+/* Adjoint for dy = dL/dy and, optionally, ds = dL/ds of the other uses of s
+ * (NULL = zero): dx (the gradient of x and of the residual), and optionally
+ * dw (NULL: not computed, and no workspace needed). An 8-bit y passes its
+ * gradient straight through. */
+int32_t pararnn_norm_residual_adjoint(const void* s, const float* w, const void* dy, const void* ds, void* dx,
+                                      float* dw, void* ws, size_t ws_bytes, const pararnn_norm_opts* o,
+                                      void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Product of 8-bit (e4m3) matrices with a scale for each block of 128 along K:
+ *   y[m][n] = sum_k a[m][k] sa[k/128][m] w[n][k] sw[n/w_rows][k/128] + bias[n].
+ * a [M][K], sa [ceil(K/128)][M] (as norm_residual writes them), w [N][K],
+ * sw [ceil(N/w_rows)][ceil(K/128)], bias [N] fp32 or NULL, y [M][N].
+ * With N = G*D this makes the gate inputs u [B*L][G][D] of the recurrences.
+ * A bf16 y is computed with the 8-bit matrix instructions, which round the
+ * products they add to about 2^-16 of the largest; an fp32 y from exact
+ * products. K % 16 == 0 with 16-byte aligned a and w selects the widest
+ * accesses.
+ */
+typedef enum { PARARNN_SCALE_F32 = 0, PARARNN_SCALE_E8M0 = 1 } pararnn_scale_type;
+
+typedef struct {
+  int32_t M, N, K;   /* all >= 1; K <= 2^22 */
+  int32_t w_rows;    /* rows of w that share a scale: 128 or 1 */
+  int32_t scale;     /* pararnn_scale_type of sa and sw */
+  int32_t y_dtype;   /* pararnn_dtype of y */
+} pararnn_matmul_opts;
+
+int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void* w, const void* sw, const float* bias, void* y,
+                           const pararnn_matmul_opts* o, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

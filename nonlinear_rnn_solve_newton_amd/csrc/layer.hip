@@ -7,9 +7,12 @@
 #include <string.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "../../include/pararnn_layer.h"
 #include "gated_scan.h"
+#include "matmul_fp8.h"
+#include "norm.h"
 
 namespace pararnn {
 namespace {
@@ -178,6 +181,80 @@ int gated(bool adj, GatedArgs& a, float* dlam, void* ws, size_t ws_bytes, const 
                 static_cast<int>(o->D), a.lam, o->c);
 }
 
+// ---------------------------------------------------------------------------
+// norm
+
+constexpr int kNormMaxD = 16384;
+
+// Threads per row (tpr), 8-column vectors per thread (nv): a wave per row
+// while its vectors fit 4 per lane, then a workgroup per row
+struct NormShape {
+  int tpr, nv;
+};
+NormShape norm_shape(int D) {
+  if (D <= 512) return {64, 1};
+  if (D <= 1024) return {64, 2};
+  if (D <= 2048) return {256, 1};
+  if (D <= 4096) return {256, 2};
+  if (D <= 8192) return {256, 4};
+  return {1024, 2};
+}
+int norm_rows(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
+
+// workgroups of the adjoint: each leaves one partial row of dw
+long long norm_adjoint_grid(const pararnn_norm_opts* o) {
+  const long long rounds = ceil_div(o->N, norm_rows(norm_shape(o->D).tpr));
+  return rounds < 512 ? rounds : 512;
+}
+
+bool norm_ok(const pararnn_norm_opts* o) {
+  return o && o->N >= 1 && o->D >= 1 && o->D <= kNormMaxD && o->eps >= 0.0f && isfinite(o->eps) &&
+         static_cast<double>(o->N) * o->D < 2.0e18;
+}
+
+template <class XT, bool VEC, class F>
+int norm_dispatch(int D, F go) {
+  const NormShape k = norm_shape(D);
+  if (k.tpr == 64) return k.nv == 1 ? go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{})
+                                    : go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (k.tpr == 256) {
+    if (k.nv == 1) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    if (k.nv == 2) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+  }
+  return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+
+template <class XT, int OUT, bool VEC>
+int launch_norm(const NormArgs& a, hipStream_t s) {
+  return norm_dispatch<XT, VEC>(a.D, [&](auto tpr, auto nv) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    long long grid = ceil_div(a.N, TPR < 256 ? 256 / TPR : 1);
+    if (grid > 8192) grid = 8192;
+    return launch(norm_kernel<XT, TPR, NV, OUT, VEC>, grid, TPR < 256 ? 256 : TPR, s, a);
+  });
+}
+template <class XT, bool VEC>
+int launch_norm_out(int out, const NormArgs& a, hipStream_t s) {
+  return out == kNormSame  ? launch_norm<XT, kNormSame, VEC>(a, s)
+         : out == kNormFp8 ? launch_norm<XT, kNormFp8, VEC>(a, s)
+                           : launch_norm<XT, kNormFp8Pow2, VEC>(a, s);
+}
+template <class XT, bool VEC>
+int launch_norm_adjoint(const NormArgs& a, long long grid, hipStream_t s) {
+  return norm_dispatch<XT, VEC>(a.D, [&](auto tpr, auto nv) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    return launch(norm_adjoint_kernel<XT, TPR, NV, VEC>, grid, TPR < 256 ? 256 : TPR, s, a);
+  });
+}
+
+// rows of 8-column vectors that every pointer is 16-byte aligned for
+bool norm_vec(int D, std::initializer_list<const void*> ptrs) {
+  bool ok = D % 8 == 0;
+  for (const void* q : ptrs) ok = ok && (!q || aligned(q, 16));
+  return ok;
+}
+
 }  // namespace
 }  // namespace pararnn
 
@@ -259,4 +336,105 @@ extern "C" int32_t pararnn_gated_step(const void* u, const float* lam, const int
   float* hp = static_cast<float*>(h);
   return C == 4 ? go(gated_step_kernel<float, 4>, up, hp) : C == 2 ? go(gated_step_kernel<float, 2>, up, hp)
                                                                    : go(gated_step_kernel<float, 1>, up, hp);
+}
+
+extern "C" int32_t pararnn_norm_residual(const void* x, const void* residual, const float* w, void* s, void* y,
+                                         void* scale, const pararnn_norm_opts* o, void* stream_) {
+  if (!norm_ok(o) || !x || !w || !y) return PARARNN_EINVAL;
+  if (o->out < PARARNN_NORM_SAME || o->out > PARARNN_NORM_FP8_E8M0) return PARARNN_EINVAL;
+  if (o->out != PARARNN_NORM_SAME && !scale) return PARARNN_EINVAL;
+  if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
+  const size_t es = o->dtype == PARARNN_BF16 ? 2 : 4;
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(s, es) || !aligned(w, 4) ||
+      (o->out == PARARNN_NORM_SAME && !aligned(y, es)) || (o->out == PARARNN_NORM_FP8 && !aligned(scale, 4)))
+    return PARARNN_EUNSUPPORTED;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.residual = residual;
+  a.w = w;
+  a.s = s;
+  a.y = y;
+  a.scale = scale;
+  a.N = o->N;
+  a.D = o->D;
+  a.eps = o->eps;
+  hipStream_t st = static_cast<hipStream_t>(stream_);
+  const bool vec = norm_vec(o->D, {x, residual, w, s, y});
+  if (o->dtype == PARARNN_BF16)
+    return vec ? launch_norm_out<bf16, true>(o->out, a, st) : launch_norm_out<bf16, false>(o->out, a, st);
+  return vec ? launch_norm_out<float, true>(o->out, a, st) : launch_norm_out<float, false>(o->out, a, st);
+}
+
+extern "C" size_t pararnn_norm_workspace_bytes(const pararnn_norm_opts* o) {
+  if (!norm_ok(o) || !dtype_ok(o->dtype)) return 0;
+  return round_up(sizeof(float) * static_cast<size_t>(norm_adjoint_grid(o)) * o->D);
+}
+
+extern "C" int32_t pararnn_norm_residual_adjoint(const void* s, const float* w, const void* dy, const void* ds,
+                                                 void* dx, float* dw, void* ws, size_t ws_bytes,
+                                                 const pararnn_norm_opts* o, void* stream_) {
+  if (!norm_ok(o) || !s || !w || !dy || !dx || (dw && !ws)) return PARARNN_EINVAL;
+  if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
+  const size_t es = o->dtype == PARARNN_BF16 ? 2 : 4;
+  if (!aligned(s, es) || !aligned(dy, es) || !aligned(ds, es) || !aligned(dx, es) || !aligned(w, 4) || !aligned(dw, 4))
+    return PARARNN_EUNSUPPORTED;
+  if (dw && ws_bytes < pararnn_norm_workspace_bytes(o)) return PARARNN_EWORKSPACE;
+  if (dw && !aligned(ws, kAlign)) return PARARNN_EUNSUPPORTED;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = s;
+  a.w = w;
+  a.dy = dy;
+  a.ds = ds;
+  a.dx = dx;
+  a.dw_part = dw ? static_cast<float*>(ws) : nullptr;
+  a.N = o->N;
+  a.D = o->D;
+  a.eps = o->eps;
+  hipStream_t st = static_cast<hipStream_t>(stream_);
+  const bool vec = norm_vec(o->D, {s, w, dy, ds, dx});
+  const long long grid = norm_adjoint_grid(o);
+  int rc;
+  if (o->dtype == PARARNN_BF16)
+    rc = vec ? launch_norm_adjoint<bf16, true>(a, grid, st) : launch_norm_adjoint<bf16, false>(a, grid, st);
+  else
+    rc = vec ? launch_norm_adjoint<float, true>(a, grid, st) : launch_norm_adjoint<float, false>(a, grid, st);
+  if (rc || !dw) return rc;
+  return launch(column_sum_kernel, ceil_div(o->D, kSumCols), kSumCols * kSumGroups, st,
+                static_cast<const float*>(a.dw_part), dw, grid, static_cast<int>(o->D),
+                static_cast<const float*>(nullptr), 0.0f);
+}
+
+extern "C" int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void* w, const void* sw, const float* bias,
+                                      void* y, const pararnn_matmul_opts* o, void* stream_) {
+  if (!o || o->M < 1 || o->N < 1 || o->K < 1 || !a || !sa || !w || !sw || !y) return PARARNN_EINVAL;
+  if (o->w_rows != 1 && o->w_rows != 128) return PARARNN_EINVAL;
+  if (o->scale != PARARNN_SCALE_F32 && o->scale != PARARNN_SCALE_E8M0) return PARARNN_EINVAL;
+  if (!dtype_ok(o->y_dtype)) return PARARNN_EUNSUPPORTED;
+  const bool e8 = o->scale == PARARNN_SCALE_E8M0, f32 = o->y_dtype == PARARNN_F32;
+  if (!aligned(bias, 4) || !aligned(y, f32 ? 4 : 2) || (!e8 && (!aligned(sa, 4) || !aligned(sw, 4))))
+    return PARARNN_EUNSUPPORTED;
+  if (o->M > 2147483647 - 256 || o->N > 2147483647 - 256 || o->K > (1 << 22)) return PARARNN_EINVAL;
+  const double tiles = static_cast<double>(ceil_div(o->M, kTile)) * ceil_div(o->N, kTile);
+  if (tiles > 2.0e9) return PARARNN_EINVAL;
+  MatmulArgs p;
+  p.a = static_cast<const uint8_t*>(a);
+  p.sa = sa;
+  p.w = static_cast<const uint8_t*>(w);
+  p.sw = sw;
+  p.bias = bias;
+  p.y = y;
+  p.M = o->M;
+  p.N = o->N;
+  p.K = o->K;
+  p.KB = static_cast<int>(ceil_div(o->K, 128));
+  const int al = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
+  hipStream_t s = static_cast<hipStream_t>(stream_);
+  const long long grid = ceil_div(o->M, kTile) * ceil_div(o->N, kTile);
+  const int rows = o->w_rows;
+  if (f32) return e8 ? launch(matmul_kernel<true, true, true>, grid, 256, s, p, rows, al)
+                     : launch(matmul_kernel<false, true, true>, grid, 256, s, p, rows, al);
+  return e8 ? launch(matmul_kernel<true, false, false>, grid, 256, s, p, rows, al)
+            : launch(matmul_kernel<false, false, false>, grid, 256, s, p, rows, al);
 }

@@ -41,6 +41,24 @@ class GatedOpts(ctypes.Structure):
     ]
 
 
+class NormOpts(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int64),
+        ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("out", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class MatmulOpts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "w_rows", "scale", "y_dtype")]
+
+
+NORM_SAME, NORM_FP8, NORM_FP8_E8M0 = 0, 1, 2
+BLOCK = 128  # columns that share a scale
+
+
 def header_functions() -> list[str]:
     """Names of the functions declared in include/pararnn_layer.h."""
     return re.findall(r"^\s*[a-z_0-9]+\s+(pararnn_[a-z_0-9]+)\s*\(", HEADER.read_text(), re.M)
@@ -67,6 +85,16 @@ def lib():
         L.pararnn_gated_scan_adjoint.restype = I32
         L.pararnn_gated_step.argtypes = [P, P, P, P, P, I32, I32, I32, I32, F, P]
         L.pararnn_gated_step.restype = I32
+        N = ctypes.POINTER(NormOpts)
+        L.pararnn_norm_residual.argtypes = [P, P, P, P, P, P, N, P]
+        L.pararnn_norm_residual.restype = I32
+        L.pararnn_norm_workspace_bytes.argtypes = [N]
+        L.pararnn_norm_workspace_bytes.restype = SZ
+        L.pararnn_norm_residual_adjoint.argtypes = [P, P, P, P, P, P, P, SZ, N, P]
+        L.pararnn_norm_residual_adjoint.restype = I32
+        M = ctypes.POINTER(MatmulOpts)
+        L.pararnn_matmul_fp8.argtypes = [P, P, P, P, P, P, M, P]
+        L.pararnn_matmul_fp8.restype = I32
         _lib = L
     return _lib
 
@@ -220,4 +248,135 @@ def gated_step(u: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *, c: fl
         st = lib().pararnn_gated_step(_ptr(u), _ptr(lam), _ptr(slots), _ptr(state), _ptr(out), B, D, S,
                                       _DTYPE[u.dtype], c, _stream(dev))
     _check(st, "pararnn_gated_step")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# norm
+
+def norm_residual(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  scale_dtype: Optional[torch.dtype] = None) -> dict:
+    """s = x + residual, y = s / sqrt(mean(s^2) + eps) * w over the last of the
+    two dimensions of x [N][D] (bf16 or fp32); w [D] fp32.
+
+    scale_dtype None: y in x's type. torch.float32 or torch.float8_e8m0fnu: y in
+    float8_e4m3fn with one scale of that type per row and 128 columns, laid out
+    [ceil(D/128)][N] as matmul_fp8 takes them. Returns dict(y, s, scale); s is x
+    itself without a residual.
+    """
+    dev = _first(x, "x", 2)
+    N, D = x.shape
+    if x.dtype not in _DTYPE:
+        raise PararnnError(f"x must be float32 or bfloat16, got {x.dtype}")
+    _dev(residual, "residual", x.dtype, (N, D), dev)
+    _dev(w, "w", torch.float32, (D,), dev)
+    scale = None
+    if scale_dtype is None:
+        out = NORM_SAME
+        y = torch.empty_like(x)
+    else:
+        if scale_dtype not in (torch.float32, torch.float8_e8m0fnu):
+            raise PararnnError(f"scale_dtype must be float32 or float8_e8m0fnu, got {scale_dtype}")
+        out = NORM_FP8 if scale_dtype == torch.float32 else NORM_FP8_E8M0
+        y = torch.empty(N, D, dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(-(-D // BLOCK), N, dtype=scale_dtype, device=dev)
+    s = x if residual is None else torch.empty_like(x)
+    o = NormOpts(N, D, _DTYPE[x.dtype], out, eps)
+    with torch.cuda.device(dev):
+        st = lib().pararnn_norm_residual(_ptr(x), _ptr(residual), _ptr(w), None if s is x else _ptr(s), _ptr(y),
+                                         _ptr(scale), ctypes.byref(o), _stream(dev))
+    _check(st, "pararnn_norm_residual")
+    return dict(y=y, s=s, scale=scale)
+
+
+def norm_residual_adjoint(s: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, *, ds: Optional[torch.Tensor] = None,
+                          eps: float = 1e-6, want_dw: bool = True, ws: Optional[torch.Tensor] = None) -> dict:
+    """Adjoint of norm_residual at its sum s [N][D], for dy = dL/dy and ds, the
+    gradient that reaches s by its other uses (None: zero). Returns dict(dx, the
+    gradient of x and of the residual, in s's type, dw [D] fp32, ws)."""
+    dev = _first(s, "s", 2)
+    N, D = s.shape
+    if s.dtype not in _DTYPE:
+        raise PararnnError(f"s must be float32 or bfloat16, got {s.dtype}")
+    _dev(w, "w", torch.float32, (D,), dev)
+    _dev(dy, "dy", s.dtype, (N, D), dev)
+    _dev(ds, "ds", s.dtype, (N, D), dev)
+    o = NormOpts(N, D, _DTYPE[s.dtype], NORM_SAME, eps)
+    dw = None
+    if want_dw:
+        ws = _workspace(ws, lib().pararnn_norm_workspace_bytes(ctypes.byref(o)), dev)
+        dw = torch.empty(D, dtype=torch.float32, device=dev)
+    dx = torch.empty_like(s)
+    with torch.cuda.device(dev):
+        st = lib().pararnn_norm_residual_adjoint(_ptr(s), _ptr(w), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw), _ptr(ws),
+                                                 0 if ws is None else ws.numel(), ctypes.byref(o), _stream(dev))
+    _check(st, "pararnn_norm_residual_adjoint")
+    return dict(dx=dx, dw=dw, ws=ws)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit product
+
+_SCALE = {torch.float32: 0, torch.float8_e8m0fnu: 1}
+
+
+def quantize_weight(w: torch.Tensor, *, rows: int = 128, scale_dtype: torch.dtype = torch.float32):
+    """Lays out a weight matrix [N][K] for matmul_fp8, once: (w in
+    float8_e4m3fn, sw [ceil(N/rows)][ceil(K/128)]) with scale = max(max|w|,
+    2^-100) / 448 over each rows x 128 block (rows 128 or 1), or the next power
+    of two at or above it for scale_dtype float8_e8m0fnu. Works on any device."""
+    if w.dim() != 2 or not w.is_floating_point():
+        raise PararnnError("w must be a floating-point matrix [N][K]")
+    if rows not in (1, BLOCK):
+        raise PararnnError(f"rows must be 1 or {BLOCK}, got {rows}")
+    if scale_dtype not in _SCALE:
+        raise PararnnError(f"scale_dtype must be float32 or float8_e8m0fnu, got {scale_dtype}")
+    N, K = w.shape
+    nb, kb = -(-N // rows), -(-K // BLOCK)
+    v = torch.nn.functional.pad(w.float(), (0, kb * BLOCK - K, 0, nb * rows - N)).view(nb, rows, kb, BLOCK)
+    scale = v.abs().amax(dim=(1, 3)).clamp_min(2.0 ** -100) / 448.0
+    sw = scale
+    if scale_dtype != torch.float32:
+        m, e = torch.frexp(scale)
+        e = torch.where(m == 0.5, e - 1, e)
+        sw = torch.where(torch.isfinite(scale), e + 127, 255).to(torch.uint8).view(scale_dtype)
+        scale = torch.ldexp(torch.ones_like(scale), e)
+    q = (v / scale[:, None, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    q = q.reshape(nb * rows, kb * BLOCK)[:N, :K].contiguous().view(torch.float8_e4m3fn)
+    return q, sw.contiguous()
+
+
+def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, *,
+               bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """a w^T with the blocks' scales, plus bias: a [M][K] and w [N][K]
+    float8_e4m3fn, sa [ceil(K/128)][M] and sw [ceil(N/128)][ceil(K/128)] or
+    [N][ceil(K/128)], both float32 or both float8_e8m0fnu, bias [N] fp32.
+    Returns [M][N] in out_dtype (bfloat16 or float32)."""
+    dev = _first(a, "a", 2)
+    M, K = a.shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise PararnnError("w must be [N][K]")
+    N = w.shape[0]
+    _dev(a, "a", torch.float8_e4m3fn, (M, K), dev)
+    _dev(w, "w", torch.float8_e4m3fn, (N, K), dev)
+    KB = -(-K // BLOCK)
+    if not isinstance(sa, torch.Tensor) or sa.dtype not in _SCALE:
+        raise PararnnError("sa must be float32 or float8_e8m0fnu")
+    _dev(sa, "sa", None, (KB, M), dev)
+    if not isinstance(sw, torch.Tensor):
+        raise PararnnError("sw must be a device tensor")
+    rows = 1 if N > 1 and sw.shape == (N, KB) else BLOCK
+    _dev(sw, "sw", sa.dtype, (-(-N // rows), KB), dev)
+    _dev(bias, "bias", torch.float32, (N,), dev)
+    if out_dtype not in _DTYPE:
+        raise PararnnError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    _dev(out, "out", out_dtype, (M, N), dev)
+    o = MatmulOpts(M, N, K, rows, _SCALE[sa.dtype], _DTYPE[out_dtype])
+    with torch.cuda.device(dev):
+        st = lib().pararnn_matmul_fp8(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _ptr(bias), _ptr(out), ctypes.byref(o),
+                                      _stream(dev))
+    _check(st, "pararnn_matmul_fp8")
     return out

@@ -91,8 +91,41 @@ def gated(u, lam, c=8.0, h0=None, lengths=None, reset=None, dh=None, dhT=None):
         return out
 
 
-def quantize_rows(y):
-    """Scales (fp32 amax / 448) and unrounded values of [N][D] in blocks of 128 columns."""
+def blocks_max(y):
+    """Largest magnitude of each 128 columns of [N][D], at least 2^-100: [N][blocks]."""
     n = -(-y.shape[1] // 128)
     p = np.pad(np.abs(y), ((0, 0), (0, n * 128 - y.shape[1]))).reshape(y.shape[0], n, 128)
-    return np.maximum(p.max(2), 2.0 ** -100) / 448.0
+    return np.maximum(p.max(2), 2.0 ** -100)
+
+
+def norm(x, w, residual=None, eps=1e-6):
+    """(value, bound) of s and y, float64 arrays; the sum of squares is good to
+    a relative 72 roundings (a lane's 32 terms, 6 + 5 levels across lanes and
+    waves, twice that for their spread), its root to half of them."""
+    s = x if residual is None else x + residual
+    y = s / np.sqrt((s * s).mean(1, keepdims=True) + eps) * w
+    return {"s": (s, U * np.abs(s)), "y": (y, 48 * U * np.abs(y) + TINY)}
+
+
+def norm_adjoint(s, w, dy, ds=None, eps=1e-6):
+    rstd = 1.0 / np.sqrt((s * s).mean(1, keepdims=True) + eps)
+    t, n = dy * w, s * rstd
+    mean, amean = (t * n).mean(1, keepdims=True), np.abs(t * n).mean(1, keepdims=True)
+    o = 0.0 if ds is None else ds
+    dx = rstd * (t - n * mean) + o
+    e = 96 * U * rstd * (np.abs(t) + np.abs(n) * amean) + 4 * U * np.abs(o) + TINY
+    mag = np.abs(dy * n).sum(0)
+    return {"dx": (dx, e), "dw": ((dy * n).sum(0), U * (96 + s.shape[0] / 256) * mag + TINY)}
+
+
+def matmul(a, sa, w, sw, rows, bias=None, fp32=True):
+    """y = (a sa) (w sw)^T + bias and its bound: fp32 sums of exact products, or
+    products that the 8-bit matrix instructions round (2^-12.4 of a block's sum
+    of magnitudes at the worst measured; 2^-11 here)."""
+    K, N = a.shape[1], w.shape[0]
+    A = a * np.repeat(sa, 128, axis=0)[:K].T
+    W = w * np.repeat(np.repeat(sw, rows, axis=0)[:N], 128, axis=1)[:, :K]
+    y, mag = A @ W.T, np.abs(A) @ np.abs(W).T
+    if bias is not None:
+        y, mag = y + bias, mag + np.abs(bias)
+    return y, mag * (U * (16 + 2 * sa.shape[0]) if fp32 else 2.0 ** -11) + TINY
