@@ -255,6 +255,39 @@ bool norm_vec(int D, std::initializer_list<const void*> ptrs) {
   return ok;
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit product
+
+// 256 x 256 of y by 8 waves (64 x 128 each), 128 x 128 by 4 (64 x 64 each),
+// 64 x 64 by 4 (32 x 32 each)
+typedef MatmulShape<4, 2, 4, 8> MatmulLarge;
+typedef MatmulShape<2, 2, 4, 4> MatmulMid;
+typedef MatmulShape<2, 2, 2, 2> MatmulSmall;
+constexpr int kCUs = 256;
+
+template <class S, int MODE, bool E8, int ROWS, bool F32OUT>
+int launch_matmul(const MatmulArgs& p, bool direct, hipStream_t s) {
+  const long long grid = ceil_div(p.M, S::BM) * ceil_div(p.N, S::BN);
+  return direct ? launch(matmul_kernel<S, MODE, E8, ROWS, F32OUT, true>, grid, S::NT, s, p)
+                : launch(matmul_kernel<S, MODE, E8, ROWS, F32OUT, false>, grid, S::NT, s, p);
+}
+template <int MODE, bool E8, int ROWS, bool F32OUT>
+int launch_matmul_shape(const MatmulArgs& p, bool direct, hipStream_t s) {
+  if constexpr (MODE != kMulExact) {
+    if (direct && ceil_div(p.M, 256) * ceil_div(p.N, 256) >= kCUs)
+      return launch(matmul_kernel<MatmulLarge, MODE, E8, ROWS, F32OUT, true>,
+                    ceil_div(p.M, 256) * ceil_div(p.N, 256), MatmulLarge::NT, s, p);
+  }
+  if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= kCUs)
+    return launch_matmul<MatmulMid, MODE, E8, ROWS, F32OUT>(p, direct, s);
+  return launch_matmul<MatmulSmall, MODE, E8, ROWS, F32OUT>(p, direct, s);
+}
+template <int MODE, bool E8, bool F32OUT>
+int launch_matmul_rows(const MatmulArgs& p, int rows, bool direct, hipStream_t s) {
+  return rows == 1 ? launch_matmul_shape<MODE, E8, 1, F32OUT>(p, direct, s)
+                   : launch_matmul_shape<MODE, E8, 128, F32OUT>(p, direct, s);
+}
+
 }  // namespace
 }  // namespace pararnn
 
@@ -416,8 +449,7 @@ extern "C" int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void*
   if (!aligned(bias, 4) || !aligned(y, f32 ? 4 : 2) || (!e8 && (!aligned(sa, 4) || !aligned(sw, 4))))
     return PARARNN_EUNSUPPORTED;
   if (o->M > 2147483647 - 256 || o->N > 2147483647 - 256 || o->K > (1 << 22)) return PARARNN_EINVAL;
-  const double tiles = static_cast<double>(ceil_div(o->M, kTile)) * ceil_div(o->N, kTile);
-  if (tiles > 2.0e9) return PARARNN_EINVAL;
+  if (static_cast<double>(ceil_div(o->M, 64)) * ceil_div(o->N, 64) > 2.0e9) return PARARNN_EINVAL;
   MatmulArgs p;
   p.a = static_cast<const uint8_t*>(a);
   p.sa = sa;
@@ -429,12 +461,12 @@ extern "C" int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void*
   p.N = o->N;
   p.K = o->K;
   p.KB = static_cast<int>(ceil_div(o->K, 128));
-  const int al = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
+  p.vec = o->N % 4 == 0 && aligned(y, f32 ? 16 : 8);
+  const bool direct = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
   hipStream_t s = static_cast<hipStream_t>(stream_);
-  const long long grid = ceil_div(o->M, kTile) * ceil_div(o->N, kTile);
   const int rows = o->w_rows;
-  if (f32) return e8 ? launch(matmul_kernel<true, true, true>, grid, 256, s, p, rows, al)
-                     : launch(matmul_kernel<false, true, true>, grid, 256, s, p, rows, al);
-  return e8 ? launch(matmul_kernel<true, false, false>, grid, 256, s, p, rows, al)
-            : launch(matmul_kernel<false, false, false>, grid, 256, s, p, rows, al);
+  if (f32) return e8 ? launch_matmul_rows<kMulExact, true, true>(p, rows, direct, s)
+                     : launch_matmul_rows<kMulExact, false, true>(p, rows, direct, s);
+  return e8 ? launch_matmul_rows<kMulE8m0, true, false>(p, rows, direct, s)
+            : launch_matmul_rows<kMulScale, false, false>(p, rows, direct, s);
 }

@@ -16,6 +16,8 @@
 // whose sums are good to 1e-8.
 #pragma once
 
+#include <type_traits>
+
 #include "layer_common.h"
 
 namespace pararnn {
@@ -28,7 +30,33 @@ struct MatmulArgs {
   const float* bias;  // [N] or nullptr
   void* y;            // [M][N] bf16 or fp32
   int M, N, K, KB;
+  int vec;            // y and its rows are aligned for 4 columns at a time
 };
+
+// 4 columns of y at element i, `left` of them inside the row
+template <bool F32OUT>
+__device__ __forceinline__ void store_row4(void* y, long long i, int left, int vec, const float (&o)[4]) {
+  if constexpr (F32OUT) {
+    float* q = static_cast<float*>(y) + i;
+    if (vec) {
+      *reinterpret_cast<f32x4*>(q) = f32x4{o[0], o[1], o[2], o[3]};
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (v < left) q[v] = o[v];
+    }
+  } else {
+    bf16* q = static_cast<bf16*>(y) + i;
+    const uint32_t lo = pack_bf16(o[0], o[1]), hi = pack_bf16(o[2], o[3]);
+    if (vec) {
+      *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (v < left) q[v].bits = static_cast<uint16_t>((v < 2 ? lo : hi) >> (16 * (v & 1)));
+    }
+  }
+}
 
 // fp32 value of a scale: fp32 itself, or e8m0 (2^(b - 127), 255: NaN)
 template <bool E8>
@@ -41,114 +69,275 @@ __device__ __forceinline__ float scale_at(const void* p, long long i) {
   }
 }
 
-// one 16 x 16 tile of y^T over a whole 128-block, from zero
-template <bool EXACT>
-__device__ __forceinline__ f32x4 tile_product(const i32x8& w, const i32x8& a) {
-  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (EXACT) {
+// 32 e4m3 values widened to bf16, which holds each of them
+__device__ __forceinline__ void widen(const i32x8& v, bf16x8 (&o)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bf16x8 x, y;
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int ws = w[2 * j + i], as = a[2 * j + i];
-        const f32x2 w0 = __builtin_amdgcn_cvt_pk_f32_fp8(ws, false), w1 = __builtin_amdgcn_cvt_pk_f32_fp8(ws, true);
-        const f32x2 a0 = __builtin_amdgcn_cvt_pk_f32_fp8(as, false), a1 = __builtin_amdgcn_cvt_pk_f32_fp8(as, true);
-        x[4 * i] = static_cast<__bf16>(w0.x); x[4 * i + 1] = static_cast<__bf16>(w0.y);
-        x[4 * i + 2] = static_cast<__bf16>(w1.x); x[4 * i + 3] = static_cast<__bf16>(w1.y);
-        y[4 * i] = static_cast<__bf16>(a0.x); y[4 * i + 1] = static_cast<__bf16>(a0.y);
-        y[4 * i + 2] = static_cast<__bf16>(a1.x); y[4 * i + 3] = static_cast<__bf16>(a1.y);
-      }
-      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, d, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t q = static_cast<uint32_t>(v[2 * j + i]);
+      const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, false);
+      const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, true);
+      o[j][4 * i] = lo.x;
+      o[j][4 * i + 1] = lo.y;
+      o[j][4 * i + 2] = hi.x;
+      o[j][4 * i + 3] = hi.y;
     }
+}
+
+// How a 16 x 16 tile takes its 128-block: the 8-bit instruction and an fp32
+// multiply-add with the scales, the 8-bit instruction with e8m0 scales of its
+// own, or exact products (bf16) and the multiply-add
+enum { kMulScale = 0, kMulE8m0 = 1, kMulExact = 2 };
+
+// fragments of one operand: 32 bytes per lane of row lane % 16
+template <int MODE>
+struct Frag {
+  i32x8 v;
+  __device__ __forceinline__ void set(const i32x4& lo, const i32x4& hi) {
+    v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+template <>
+struct Frag<kMulExact> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(const i32x4& lo, const i32x4& hi) {
+    widen(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), v);
+  }
+};
+template <int MODE>
+__device__ __forceinline__ f32x4 tile_product(const Frag<MODE>& w, const Frag<MODE>& a) {
+  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (MODE == kMulExact) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[j], a.v[j], d, 0, 0, 0);
   } else {
-    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, d, 0, 0, 0, 127, 0, 127);
+    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, d, 0, 0, 0, 0, 0, 0);
   }
   return d;
 }
 
-// 16 bytes of row `row` from column k on, zeros past the last column and row
-__device__ __forceinline__ i32x4 load16(const uint8_t* p, long long row, int rows, int k, int K, bool aligned) {
+// 16 bytes of a row from column k on, zeros past column K, at any alignment
+__device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
   i32x4 v = {0, 0, 0, 0};
-  if (row >= rows || k >= K) return v;
-  const uint8_t* q = p + row * K + k;
-  if (aligned) return *reinterpret_cast<const i32x4*>(q);
-  uint8_t t[16];
+  if (k + 16 <= K) {
+    __builtin_memcpy(&v, row + k, 16);
+  } else if (k < K) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) t[i] = k + i < K ? q[i] : uint8_t{0};
-  __builtin_memcpy(&v, t, 16);
+    for (int i = 0; i < 16; ++i)
+      if (k + i < K) v[i / 4] |= static_cast<int>(static_cast<uint32_t>(row[k + i]) << (8 * (i % 4)));
+  }
   return v;
 }
 
-// 128 x 128 of y per workgroup of 4 waves, 64 x 64 per wave
-constexpr int kTile = 128;
-template <bool E8, bool EXACT, bool F32OUT>
-__global__ void __launch_bounds__(256) matmul_kernel(const MatmulArgs p, int rows, int aligned) {
-  __shared__ i32x4 s_w[kTile * 8], s_a[kTile * 8];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int ntn = (p.N + kTile - 1) / kTile;
-  const int m0 = static_cast<int>(blockIdx.x / ntn) * kTile, n0 = static_cast<int>(blockIdx.x % ntn) * kTile;
-  const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-  f32x4 acc[4][4];  // [n][m]
+// Tiles in the order of their numbers run near each other in time. Workgroup
+// i runs on XCD i % 8, each with an L2 of its own: consecutive numbers go to
+// one XCD, and 8 row tiles by as many column tiles as it takes follow each
+// other, so that an XCD's workgroups share the panels in its L2.
+__device__ __forceinline__ void tile_of(unsigned int id, unsigned int ntm, unsigned int ntn, int* tm, int* tn) {
+  const unsigned int total = ntm * ntn, per = total / 8, rest = total % 8, x = id % 8, l = id / 8;
+  const unsigned int t = x * per + min(x, rest) + l;
+  const unsigned int grp = t / (8 * ntn), m0 = grp * 8, gm = min(ntm - m0, 8u), u = t - grp * 8 * ntn;
+  *tm = static_cast<int>(m0 + u % gm);
+  *tn = static_cast<int>(u / gm);
+}
+
+// The shape of a tile: waves along n and m, 16 x 16 tiles per wave along n and m
+template <int WN_, int WM_, int TN_, int TM_>
+struct MatmulShape {
+  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_;
+  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, NT = 64 * WN * WM;
+};
+
+// BM x BN of y per workgroup. Each step brings 128 columns of both operands
+// into workgroup memory while the matrix cores work on the step before (two
+// buffers); DIRECT: by 16-byte loads that write there without passing through
+// registers, where every row is aligned for them, else through registers.
+// 16-byte chunk c of row q lies at position c ^ (q & 7) of its 128 bytes, so
+// that 8 rows read at one c touch different banks.
+// ROWS: rows of w that share a scale, 128 (uniform per wave: TN * 16 <= 64
+// columns that start at a multiple of that) or 1.
+template <class S, int MODE, bool E8, int ROWS, bool F32OUT, bool DIRECT>
+struct Matmul {
+  static constexpr int BN = S::BN, BM = S::BM, NT = S::NT, TN = S::TN, TM = S::TM;
+  static constexpr int LN = BN * 8 / NT, LM = BM * 8 / NT;  // 16-byte chunks per thread
+  static_assert(TN * 16 <= 64, "one scale block of w per wave");
+  static_assert(NT % 64 == 0, "a thread's rows share their low 3 bits");
+  typedef std::conditional_t<MODE == kMulE8m0, int, float> SV;
+  // e8m0 rows of w scale the first operand's rows, lane % 16; fp32 ones the
+  // result's rows, 4 per lane
+  static constexpr int NSW = ROWS == 128 ? 1 : MODE == kMulE8m0 ? TN : TN * 4;
+  typedef __attribute__((address_space(3))) void lds_void;
+
+  MatmulArgs p;
+  int tid, wave, r, g, m0, n0, wn, wm, mrows, nrows;
+  __amdgpu_buffer_rsrc_t rsa, rsw;
+  uint32_t v0;  // the thread's first chunk
+  int q0, c0;
+  i32x4 ra[DIRECT ? 1 : LM], rw[DIRECT ? 1 : LN];  // in flight
+  SV fsa[TM], fsw[NSW];                            // scales in flight
+  f32x4 acc[TN][TM];
+
+  // thread's chunk i: row (tid + NT i) / 8, position tid % 8, column chunk c0
+  __device__ __forceinline__ void fetch(int kb, i32x4* sw, i32x4* sa) {
+    if constexpr (DIRECT) {
+      const uint32_t v = kb * 128 + c0 * 16 < p.K ? v0 : 0x80000000u;  // extents stay below 2^31 bytes
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < LN; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(sw + wave * 64 + NT * i), 16, v,
+                                                 kb * 128 + i * (NT / 8) * p.K, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = 0; kb < p.KB; ++kb) {
-    __syncthreads();
-    // 16-byte chunk c of row q lies at c ^ (q & 7): rows of 128 bytes read
-    // down a column touch different banks
+      for (int i = 0; i < LM; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sa + wave * 64 + NT * i), 16, v,
+                                                 kb * 128 + i * (NT / 8) * p.K, 0, 0);
+    } else {
+      const uint8_t* abase = p.a + static_cast<long long>(m0) * p.K;
+      const uint8_t* wbase = p.w + static_cast<long long>(n0) * p.K;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid + 256 * i, q = e >> 3, c = e & 7;
-      s_a[q * 8 + (c ^ (q & 7))] = load16(p.a, m0 + q, p.M, kb * 128 + c * 16, p.K, aligned);
-      s_w[q * 8 + (c ^ (q & 7))] = load16(p.w, n0 + q, p.N, kb * 128 + c * 16, p.K, aligned);
-    }
-    __syncthreads();
-    float sa[4];
-    i32x8 fa[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int q = wm + 16 * j + r;
-      sa[j] = scale_at<E8>(p.sa, static_cast<long long>(kb) * p.M + min(m0 + q, p.M - 1));
-      const i32x4 lo = s_a[q * 8 + (g ^ (q & 7))], hi = s_a[q * 8 + ((g + 4) ^ (q & 7))];
-      fa[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = wn + 16 * i + r;
-      const i32x4 lo = s_w[q * 8 + (g ^ (q & 7))], hi = s_w[q * 8 + ((g + 4) ^ (q & 7))];
-      const i32x8 fw = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      float sw[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int n = min(n0 + wn + 16 * i + 4 * g + v, p.N - 1);
-        sw[v] = scale_at<E8>(p.sw, static_cast<long long>(rows == 1 ? n : n / 128) * p.KB + kb);
+      for (int i = 0; i < LN; ++i) {
+        const int q = q0 + i * (NT / 8);
+        rw[i] = load16(wbase + static_cast<long long>(min(q, nrows - 1)) * p.K, kb * 128 + c0 * 16, p.K);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4 d = tile_product<EXACT>(fw, fa[j]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(d[v], sa[j] * sw[v], acc[i][j][v]);
+      for (int i = 0; i < LM; ++i) {
+        const int q = q0 + i * (NT / 8);
+        ra[i] = load16(abase + static_cast<long long>(min(q, mrows - 1)) * p.K, kb * 128 + c0 * 16, p.K);
       }
     }
   }
+  __device__ __forceinline__ void land(i32x4* sw, i32x4* sa) {
+    if constexpr (!DIRECT) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < LN; ++i) sw[tid + NT * i] = rw[i];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long m = m0 + wm + 16 * j + r;
-      const int n = n0 + wn + 16 * i + 4 * g;
-      if (m >= p.M) continue;
+      for (int i = 0; i < LM; ++i) sa[tid + NT * i] = ra[i];
+    }
+  }
+  __device__ __forceinline__ SV scale_of(const void* q, long long i) const {
+    if constexpr (MODE == kMulE8m0) return static_cast<const uint8_t*>(q)[i];
+    else return scale_at<E8>(q, i);
+  }
+  __device__ __forceinline__ void scales(int kb) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (n + v >= p.N) continue;
-        const float o = acc[i][j][v] + (p.bias ? p.bias[n + v] : 0.0f);
-        if constexpr (F32OUT) static_cast<float*>(p.y)[m * p.N + n + v] = o;
-        else static_cast<bf16*>(p.y)[m * p.N + n + v].bits = static_cast<uint16_t>(pack_bf16(o, o));
+    for (int j = 0; j < TM; ++j)
+      fsa[j] = scale_of(p.sa, static_cast<long long>(kb) * p.M + min(m0 + wm + 16 * j + r, p.M - 1));
+    if constexpr (ROWS == 128) {
+      fsw[0] = scale_of(p.sw, static_cast<long long>(min(n0 + wn, p.N - 1) / 128) * p.KB + kb);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NSW; ++i) {
+        const int n = MODE == kMulE8m0 ? 16 * i + r : 16 * (i / 4) + 4 * g + i % 4;
+        fsw[i] = scale_of(p.sw, static_cast<long long>(min(n0 + wn + n, p.N - 1)) * p.KB + kb);
       }
     }
+  }
+  // One step: the next block's loads into nw and na, this block's products
+  // from cw and ca. The pointers' restrict is what lets the compiler read this
+  // block while the next one's loads write workgroup memory.
+  __device__ __forceinline__ void step(int kb, const i32x4* __restrict__ cw, const i32x4* __restrict__ ca,
+                                       i32x4* __restrict__ nw, i32x4* __restrict__ na) {
+    SV csa[TM], csw[NSW];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) csa[j] = fsa[j];
+#pragma unroll
+    for (int i = 0; i < NSW; ++i) csw[i] = fsw[i];
+    if (kb + 1 < p.KB) {
+      fetch(kb + 1, nw, na);
+      scales(kb + 1);
+    }
+    // lane's two chunks of a row of its tile 0; tile i: 128 i further
+    const int bw0 = (wn + r) * 8 + (g ^ (r & 7)), bw1 = (wn + r) * 8 + ((g + 4) ^ (r & 7));
+    const int ba0 = (wm + r) * 8 + (g ^ (r & 7)), ba1 = (wm + r) * 8 + ((g + 4) ^ (r & 7));
+    Frag<MODE> fw[TN];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) fw[i].set(cw[bw0 + 128 * i], cw[bw1 + 128 * i]);
+    i32x4 lo = ca[ba0], hi = ca[ba1];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      Frag<MODE> fa;
+      fa.set(lo, hi);
+      if (j + 1 < TM) {
+        lo = ca[ba0 + 128 * (j + 1)];
+        hi = ca[ba1 + 128 * (j + 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        if constexpr (MODE == kMulE8m0) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[i].v, fa.v, acc[i][j], 0, 0, 0,
+                                                                       csw[ROWS == 128 ? 0 : i], 0, csa[j]);
+        } else {
+          const f32x4 d = tile_product<MODE>(fw[i], fa);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[i][j][v] = fmaf(d[v], csa[j] * csw[ROWS == 128 ? 0 : 4 * i + v], acc[i][j][v]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kb + 1 < p.KB) land(nw, na);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the loads into workgroup memory are done
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ void run(i32x4* lds) {
+    constexpr int HALF = (BN + BM) * 8;
+    tid = threadIdx.x;
+    const int lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    r = lane & 15;
+    g = lane >> 4;
+    int tm, tn;
+    tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &tm, &tn);
+    m0 = tm * BM;
+    n0 = tn * BN;
+    wn = (wave % S::WN) * TN * 16;
+    wm = (wave / S::WN) * TM * 16;
+    mrows = min(p.M - m0, BM);
+    nrows = min(p.N - n0, BN);
+    q0 = tid >> 3;
+    c0 = (tid & 7) ^ (q0 & 7);
+    v0 = static_cast<uint32_t>(q0) * p.K + c0 * 16;
+    rsa = make_rsrc(p.a + static_cast<long long>(m0) * p.K, static_cast<uint32_t>(mrows) * p.K);
+    rsw = make_rsrc(p.w + static_cast<long long>(n0) * p.K, static_cast<uint32_t>(nrows) * p.K);
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    fetch(0, lds, lds + BN * 8);
+    scales(0);
+    land(lds, lds + BN * 8);
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    __syncthreads();
+    for (int kb = 0; kb < p.KB; ++kb) {
+      i32x4* c = lds + (kb & 1) * HALF;
+      i32x4* n = lds + (1 - (kb & 1)) * HALF;
+      step(kb, c, c + BN * 8, n, n + BN * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int n = n0 + wn + 16 * i + 4 * g;
+      float bv[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const long long m = m0 + wm + 16 * j + r;
+        if (m >= p.M || n >= p.N) continue;
+        float o[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
+        store_row4<F32OUT>(p.y, m * p.N + n, p.N - n, p.vec, o);
+      }
+    }
+  }
+};
+
+template <class S, int MODE, bool E8, int ROWS, bool F32OUT, bool DIRECT>
+__global__ void __launch_bounds__(S::NT) matmul_kernel(const MatmulArgs p) {
+  __shared__ i32x4 lds[2 * (S::BN + S::BM) * 8];
+  Matmul<S, MODE, E8, ROWS, F32OUT, DIRECT> m;
+  m.p = p;
+  m.run(lds);
 }
 
 }  // namespace pararnn
