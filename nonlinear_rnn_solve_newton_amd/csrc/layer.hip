@@ -258,9 +258,7 @@ bool norm_vec(int D, std::initializer_list<const void*> ptrs) {
 // ---------------------------------------------------------------------------
 // 8-bit product
 
-// 256 x 256 of y by 8 waves (64 x 128 each), 128 x 128 by 4 (64 x 64 each),
-// 64 x 64 by 4 (32 x 32 each)
-typedef MatmulShape<4, 2, 4, 8> MatmulLarge;
+// 128 x 128 of y by 4 waves (64 x 64 each), 64 x 64 by 4 (32 x 32 each)
 typedef MatmulShape<2, 2, 4, 4> MatmulMid;
 typedef MatmulShape<2, 2, 2, 2> MatmulSmall;
 constexpr int kCUs = 256;
@@ -275,8 +273,7 @@ template <int MODE, bool E8, int ROWS, bool F32OUT>
 int launch_matmul_shape(const MatmulArgs& p, bool direct, hipStream_t s) {
   if constexpr (MODE != kMulExact) {
     if (direct && ceil_div(p.M, 256) * ceil_div(p.N, 256) >= kCUs)
-      return launch(matmul_kernel<MatmulLarge, MODE, E8, ROWS, F32OUT, true>,
-                    ceil_div(p.M, 256) * ceil_div(p.N, 256), MatmulLarge::NT, s, p);
+      return launch(matmul_large_kernel<MODE, E8, ROWS>, ceil_div(p.M, 256) * ceil_div(p.N, 256), 512, s, p);
   }
   if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= kCUs)
     return launch_matmul<MatmulMid, MODE, E8, ROWS, F32OUT>(p, direct, s);
@@ -461,7 +458,7 @@ extern "C" int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void*
   p.N = o->N;
   p.K = o->K;
   p.KB = static_cast<int>(ceil_div(o->K, 128));
-  p.vec = o->N % 4 == 0 && aligned(y, f32 ? 16 : 8);
+  p.vec = !f32 && o->N % 8 == 0 && aligned(y, 16) ? 8 : o->N % 4 == 0 && aligned(y, f32 ? 16 : 8) ? 4 : 1;
   const bool direct = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
   hipStream_t s = static_cast<hipStream_t>(stream_);
   const int rows = o->w_rows;

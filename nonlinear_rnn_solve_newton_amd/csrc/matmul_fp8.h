@@ -30,7 +30,7 @@ struct MatmulArgs {
   const float* bias;  // [N] or nullptr
   void* y;            // [M][N] bf16 or fp32
   int M, N, K, KB;
-  int vec;            // y and its rows are aligned for 4 columns at a time
+  int vec;            // columns of y that go out at a time, by the alignment of y and its rows: 8, 4 or 1
 };
 
 // 4 columns of y at element i, `left` of them inside the row
@@ -38,7 +38,7 @@ template <bool F32OUT>
 __device__ __forceinline__ void store_row4(void* y, long long i, int left, int vec, const float (&o)[4]) {
   if constexpr (F32OUT) {
     float* q = static_cast<float*>(y) + i;
-    if (vec) {
+    if (vec >= 4) {
       *reinterpret_cast<f32x4*>(q) = f32x4{o[0], o[1], o[2], o[3]};
     } else {
 #pragma unroll
@@ -48,7 +48,7 @@ __device__ __forceinline__ void store_row4(void* y, long long i, int left, int v
   } else {
     bf16* q = static_cast<bf16*>(y) + i;
     const uint32_t lo = pack_bf16(o[0], o[1]), hi = pack_bf16(o[2], o[3]);
-    if (vec) {
+    if (vec >= 4) {
       *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
     } else {
 #pragma unroll
@@ -68,6 +68,34 @@ __device__ __forceinline__ float scale_at(const void* p, long long i) {
     return static_cast<const float*>(p)[i];
   }
 }
+
+// Stores a BM x BN tile of bf16 results through workgroup memory: written as
+// the matrix instructions leave them (4 columns of 16 rows per instruction) a
+// wave would touch 32 bytes of a row at a time, which HBM takes at a quarter
+// of its rate. NT threads; put(row, column, 4 values) fills the tile, then
+// whole rows go out 16 bytes per lane. Chunk c of row m lies at c ^ (m & 15),
+// so that 16 rows written at one column touch different banks.
+template <int BM, int BN, int NT>
+struct TileStore {
+  static constexpr int CH = BN / 8, MASK = (CH < 16 ? CH : 16) - 1;  // 16-byte chunks per row
+  i32x4* lds;
+  __device__ __forceinline__ void put(int m, int n, const float (&o)[4]) {
+    const int c = n >> 3;
+    reinterpret_cast<u32x2*>(lds + m * CH + (c ^ (m & MASK)))[(n >> 2) & 1] =
+        u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+  }
+  __device__ __forceinline__ void flush(void* y, long long m0, int n0, int mrows, int ncols, int N, int tid) {
+    constexpr int RI = NT / CH;  // rows per round
+    const int c = tid % CH, q = tid / CH;
+    uint16_t* base = static_cast<uint16_t*>(y) + m0 * N + n0;
+#pragma unroll
+    for (int i = 0; i < BM / RI; ++i) {
+      const int m = q + i * RI;
+      if (m < mrows && c * 8 < ncols)
+        *reinterpret_cast<i32x4*>(base + static_cast<long long>(m) * N + c * 8) = lds[m * CH + (c ^ (m & MASK))];
+    }
+  }
+};
 
 // 32 e4m3 values widened to bf16, which holds each of them
 __device__ __forceinline__ void widen(const i32x8& v, bf16x8 (&o)[4]) {
@@ -181,15 +209,19 @@ struct Matmul {
   // thread's chunk i: row (tid + NT i) / 8, position tid % 8, column chunk c0
   __device__ __forceinline__ void fetch(int kb, i32x4* sw, i32x4* sa) {
     if constexpr (DIRECT) {
-      const uint32_t v = kb * 128 + c0 * 16 < p.K ? v0 : 0x80000000u;  // extents stay below 2^31 bytes
+      // the row is in the lane's offset, which the extent is checked against;
+      // the column's block, the uniform offset, is not. Extents stay below 2^31.
+      const bool in = kb * 128 + c0 * 16 < p.K;
 #pragma unroll
       for (int i = 0; i < LN; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(sw + wave * 64 + NT * i), 16, v,
-                                                 kb * 128 + i * (NT / 8) * p.K, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(sw + wave * 64 + NT * i), 16,
+                                                 in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u,
+                                                 kb * 128, 0, 0);
 #pragma unroll
       for (int i = 0; i < LM; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sa + wave * 64 + NT * i), 16, v,
-                                                 kb * 128 + i * (NT / 8) * p.K, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sa + wave * 64 + NT * i), 16,
+                                                 in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u,
+                                                 kb * 128, 0, 0);
     } else {
       const uint8_t* abase = p.a + static_cast<long long>(m0) * p.K;
       const uint8_t* wbase = p.w + static_cast<long long>(n0) * p.K;
@@ -313,6 +345,8 @@ struct Matmul {
       i32x4* n = lds + (1 - (kb & 1)) * HALF;
       step(kb, c, c + BN * 8, n, n + BN * 8);
     }
+    const bool whole = !F32OUT && p.vec == 8;  // the last step ended with a barrier
+    TileStore<BM, BN, NT> st{lds};
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       const int n = n0 + wn + 16 * i + 4 * g;
@@ -322,12 +356,16 @@ struct Matmul {
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
         const long long m = m0 + wm + 16 * j + r;
-        if (m >= p.M || n >= p.N) continue;
         float o[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
-        store_row4<F32OUT>(p.y, m * p.N + n, p.N - n, p.vec, o);
+        if (whole) st.put(wm + 16 * j + r, n - n0, o);
+        else if (m < p.M && n < p.N) store_row4<F32OUT>(p.y, m * p.N + n, p.N - n, p.vec, o);
       }
+    }
+    if (whole) {
+      __syncthreads();
+      st.flush(p.y, m0, n0, mrows, p.N - n0, p.N, tid);
     }
   }
 };
@@ -338,6 +376,282 @@ __global__ void __launch_bounds__(S::NT) matmul_kernel(const MatmulArgs p) {
   Matmul<S, MODE, E8, ROWS, F32OUT, DIRECT> m;
   m.p = p;
   m.run(lds);
+}
+
+// ---------------------------------------------------------------------------
+// Large products: 256 x 256 of y by 8 waves (4 along n, 2 along m; 64 x 128
+// each), two waves per SIMD. What bounds it is the time from the issue of a
+// block's loads to their arrival, about a step and a half of products, and
+// workgroup memory holds two blocks only. So a step has two halves: the first
+// multiplies the wave's w rows by the first half of its a rows, the second by
+// the other half. After the first half nobody needs this block's w and first
+// a rows any more (w's stay in registers), and their place takes the block
+// after the next; the place of the second a rows is taken one half later.
+// Every load so has a step and a half to arrive, and the waits count the loads
+// that may still be on their way.
+template <int MODE, bool E8, int ROWS>
+struct MatmulLarge {
+  static constexpr int BN = 256, BM = 256, NT = 512, TN = 4, TM = 8;
+  // 16-byte chunks of one buffer: w, then the first and the second a rows of both waves along m
+  static constexpr int OX0 = BN * 8, OX1 = OX0 + BM * 4, BUF = OX1 + BM * 4;
+  static constexpr int SB = MODE == kMulE8m0 ? 1 : 4;      // bytes of a scale in workgroup memory
+  static constexpr int SCH = 256 * SB;  // bytes of 256 scales: two buffers for a, two for w
+  static constexpr int NWL = 4, NXL = 2;  // loads per thread: w, half of a
+  typedef __attribute__((address_space(3))) void lds_void;
+
+  MatmulArgs p;
+  int tid, wave, r, g, m0, n0, wni, wmi;
+  __amdgpu_buffer_rsrc_t rsa, rsw;
+  uint32_t v0;
+  int c16;                 // the thread's column within a block, bytes
+  f32x4 acc[TN][TM];
+  i32x8 fw[TN];
+  uint32_t vs;  // scale on its way: of row tid (first half of the threads), of a column or block of w (second)
+  f32x4 d[MODE == kMulE8m0 ? 1 : TN];  // products not yet scaled: of row tile dj, by ds
+
+  __device__ __forceinline__ void load_w(int kb, i32x4* buf) {
+    const bool in = kb * 128 + c16 < p.K;
+    const int so = kb < p.KB ? kb * 128 : 0;
+#pragma unroll
+    for (int i = 0; i < NWL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(buf + wave * 64 + NT * i), 16,
+                                               in ? v0 + static_cast<uint32_t>(i * 64) * p.K : 0x80000000u, so, 0, 0);
+  }
+  // rows 64 half + (0..63) of both 128-row parts
+  __device__ __forceinline__ void load_a(int kb, int half, i32x4* buf) {
+    const bool in = kb * 128 + c16 < p.K;
+    const int so = kb < p.KB ? kb * 128 : 0;
+#pragma unroll
+    for (int i = 0; i < NXL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(buf + (half ? OX1 : OX0) + wave * 64 + NT * i), 16,
+                                               in ? v0 + static_cast<uint32_t>(i * 128 + half * 64) * p.K : 0x80000000u,
+                                               so, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t raw_scale(const void* q, long long i) {
+    if constexpr (MODE == kMulE8m0) return static_cast<const uint8_t*>(q)[i];
+    else return __float_as_uint(scale_at<E8>(q, i));
+  }
+  __device__ __forceinline__ void load_scales(int kb) {
+    const int k = min(kb, p.KB - 1), t = tid & 255;
+    const void* q = p.sa;
+    long long at = static_cast<long long>(k) * p.M + min(m0 + t, p.M - 1);
+    if (tid >= 256) {
+      q = p.sw;
+      at = ROWS == 1 ? min(n0 + t, p.N - 1) : min(n0 + (t & 3) * 64, p.N - 1) / 128;
+      at = at * p.KB + k;
+    }
+    vs = raw_scale(q, at);
+  }
+  // row 16 j + r of a wave's rows lies at 8 r + j, so that a lane's 8 scales
+  // are consecutive; e8m0 column 16 i + r of w at 4 r + i, fp32 columns in
+  // order; scales of whole blocks at the number of the wave along n
+  __device__ __forceinline__ void land_scales(int kb, char* scales) {
+    const int t = tid & 255;
+    const int pa = (t & 128) + (t & 15) * 8 + ((t >> 4) & 7);
+    const int pw = ROWS == 128 ? (t & 3) : MODE == kMulE8m0 ? (t & 192) + (t & 15) * 4 + ((t >> 4) & 3) : t;
+    char* to = scales + ((tid < 256 ? 0 : 2) + (kb & 1)) * SCH;
+    const int at = tid < 256 ? pa : pw;
+    if constexpr (SB == 1) reinterpret_cast<uint8_t*>(to)[at] = static_cast<uint8_t>(vs);
+    else reinterpret_cast<uint32_t*>(to)[at] = vs;
+  }
+
+  // acc of row tile j += d * its scale * the columns' scales
+  __device__ __forceinline__ void scale_add(int j, float sj, const uint32_t (&csw)[ROWS == 128 ? 1 : SB == 1 ? 1 : 16]) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        acc[i][j][v] = fmaf(d[i][v], sj * __uint_as_float(csw[ROWS == 128 ? 0 : 4 * i + v]), acc[i][j][v]);
+  }
+  // the products up to here are issued before what follows: keeps the
+  // compiler from moving them behind the next barrier
+  __device__ __forceinline__ void pin(int j) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i) __asm__ volatile("" : "+v"(acc[i][j]));
+  }
+  // 4 row tiles of the wave by its 4 column tiles. With fp32 scales the
+  // products of a row tile are scaled and added under those of the next.
+  template <int HALF>
+  __device__ __forceinline__ void products(const i32x4* __restrict__ x, const i32x4 (&sc)[SB == 1 ? 1 : 2],
+                                           const uint32_t (&csw)[ROWS == 128 ? 1 : SB == 1 ? 1 : 16]) {
+    const int b0 = (wmi * 64 + r) * 8 + (g ^ (r & 7)), b1 = (wmi * 64 + r) * 8 + ((g + 4) ^ (r & 7));
+    i32x4 lo = x[b0], hi = x[b1];
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const int j = HALF * 4 + jj;
+      const i32x8 fa = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      if (jj < 3) {
+        lo = x[b0 + 128 * (jj + 1)];
+        hi = x[b1 + 128 * (jj + 1)];
+      }
+      if constexpr (MODE == kMulE8m0) {
+        const int sj = sc[0][HALF];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) mfma_e8(acc[i][j], fw[i], fa, static_cast<int>(csw[0]), i, sj, jj);
+        pin(j);
+      } else {
+        f32x4 dn[TN];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+          dn[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[i], fa, z, 0, 0, 0, 0, 0, 0);
+        }
+        if (j > 0) {
+          scale_add(j - 1, __int_as_float(sc[(j - 1) / 4][(j - 1) % 4]), csw);
+          pin(j - 1);
+        }
+#pragma unroll
+        for (int i = 0; i < TN; ++i) d[i] = dn[i];
+        if (j == TM - 1) scale_add(j, __int_as_float(sc[1][3]), csw);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // the instruction takes the byte of a scale register as an immediate; a
+  // block's scale is in byte 0 of its register whatever the column tile
+  static __device__ __forceinline__ void mfma_e8(f32x4& c, const i32x8& w, const i32x8& a, int sw, int i, int sa, int j) {
+#define PARARNN_MFMA(I, J) \
+  c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, ROWS == 128 ? 0 : I, sw, J, sa)
+#define PARARNN_MFMA_J(I) \
+  if (j == 0) PARARNN_MFMA(I, 0); else if (j == 1) PARARNN_MFMA(I, 1); else if (j == 2) PARARNN_MFMA(I, 2); else PARARNN_MFMA(I, 3)
+    if (i == 0) { PARARNN_MFMA_J(0); } else if (i == 1) { PARARNN_MFMA_J(1); } else if (i == 2) { PARARNN_MFMA_J(2); } else { PARARNN_MFMA_J(3); }
+#undef PARARNN_MFMA_J
+#undef PARARNN_MFMA
+  }
+
+  // Orders workgroup memory between the waves, and only that: unlike a fence
+  // it leaves the loads into it that are counted separately on their way.
+  static __device__ __forceinline__ void hand_over() {
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __asm__ volatile("" ::: "memory");
+  }
+
+  // One block. rd and wr are the same memory, and so are rs and ws: restrict
+  // says that what is written (by the loads into workgroup memory, which the
+  // compiler would otherwise wait for) does not change what is still read
+  // before the next barrier. The offsets of the buffers are opaque, so that
+  // nothing read in one step is taken for known in a later one.
+  __device__ __forceinline__ void step(int kb, const i32x4* __restrict__ rd, i32x4* __restrict__ wr,
+                                       const char* __restrict__ rs, char* __restrict__ ws) {
+    int cur = (kb & 1) * BUF;
+    __asm__ volatile("" : "+s"(cur));
+    const int nxt = BUF - cur;
+    // first half: w and the first a rows of this block have arrived, and the
+    // next block's scales; 8 newer loads may not have
+    __builtin_amdgcn_s_waitcnt(0x0f78);
+    land_scales(kb + 1, ws);
+    hand_over();
+    load_scales(kb + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    load_a(kb + 1, 1, wr + nxt);
+    i32x4 sc[SB == 1 ? 1 : 2];
+    uint32_t csw[ROWS == 128 ? 1 : SB == 1 ? 1 : 16];
+    {
+      const char* sa = rs + (kb & 1) * SCH;
+      const char* sw = rs + (2 + (kb & 1)) * SCH;
+      if constexpr (SB == 1) {
+        const i32x2 t = *reinterpret_cast<const i32x2*>(sa + wmi * 128 + r * 8);
+        sc[0] = i32x4{t.x, t.y, 0, 0};
+      } else {
+        sc[0] = *reinterpret_cast<const i32x4*>(sa + (wmi * 128 + r * 8) * 4);
+        sc[1] = *reinterpret_cast<const i32x4*>(sa + (wmi * 128 + r * 8) * 4 + 16);
+      }
+      if constexpr (ROWS == 128) {
+        if constexpr (SB == 1) csw[0] = static_cast<uint8_t>(sw[wni]);
+        else csw[0] = reinterpret_cast<const uint32_t*>(sw)[wni];
+      } else if constexpr (SB == 1) {
+        csw[0] = *reinterpret_cast<const uint32_t*>(sw + wni * 64 + r * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const i32x4 t = *reinterpret_cast<const i32x4*>(sw + (wni * 64 + 16 * i + 4 * g) * 4);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) csw[4 * i + v] = static_cast<uint32_t>(t[v]);
+        }
+      }
+    }
+    const int b0 = (wni * 64 + r) * 8 + (g ^ (r & 7)), b1 = (wni * 64 + r) * 8 + ((g + 4) ^ (r & 7));
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+      fw[i] = __builtin_shufflevector(rd[cur + b0 + 128 * i], rd[cur + b1 + 128 * i], 0, 1, 2, 3, 4, 5, 6, 7);
+    products<0>(rd + cur + OX0, sc, csw);
+    // second half: the other a rows have arrived; again 8 newer loads may not have
+    __builtin_amdgcn_s_waitcnt(0x0f78);
+    hand_over();
+    load_w(kb + 2, wr + cur);
+    load_a(kb + 2, 0, wr + cur);
+    products<1>(rd + cur + OX1, sc, csw);
+  }
+
+  __device__ __forceinline__ void run(i32x4* lds, char* scales) {
+    tid = threadIdx.x;
+    const int lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    r = lane & 15;
+    g = lane >> 4;
+    wni = wave & 3;
+    wmi = wave >> 2;
+    int tm, tn;
+    tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &tm, &tn);
+    m0 = tm * BM;
+    n0 = tn * BN;
+    const int q0 = tid >> 3;
+    c16 = ((tid & 7) ^ (q0 & 7)) * 16;
+    v0 = static_cast<uint32_t>(q0) * p.K + c16;
+    rsa = make_rsrc(p.a + static_cast<long long>(m0) * p.K, static_cast<uint32_t>(min(p.M - m0, BM)) * p.K);
+    rsw = make_rsrc(p.w + static_cast<long long>(n0) * p.K, static_cast<uint32_t>(min(p.N - n0, BN)) * p.K);
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    load_scales(0);
+    land_scales(0, scales);
+    load_w(0, lds);
+    load_a(0, 0, lds);
+    load_scales(1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_a(0, 1, lds);
+    load_w(1, lds + BUF);
+    load_a(1, 0, lds + BUF);
+    for (int kb = 0; kb < p.KB; ++kb) step(kb, lds, lds, scales, scales);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into workgroup memory outlives the products
+    const bool whole = p.vec == 8;
+    TileStore<BM, BN, NT> st{lds};
+    if (whole) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int n = n0 + wni * 64 + 16 * i + 4 * g;
+      float bv[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const long long m = m0 + wmi * 128 + 16 * j + r;
+        float o[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
+        if (whole) st.put(wmi * 128 + 16 * j + r, n - n0, o);
+        else if (m < p.M && n < p.N) store_row4<false>(p.y, m * p.N + n, p.N - n, p.vec, o);
+      }
+    }
+    if (whole) {
+      __syncthreads();
+      st.flush(p.y, m0, n0, p.M - m0, p.N - n0, p.N, tid);
+    }
+  }
+};
+
+template <int MODE, bool E8, int ROWS>
+__global__ void __launch_bounds__(512) matmul_large_kernel(const MatmulArgs p) {
+  typedef MatmulLarge<MODE, E8, ROWS> M;
+  // one array: what the compiler derives from several would replace what restrict says
+  __shared__ i32x4 lds[2 * M::BUF + 4 * M::SCH / 16];
+  M m;
+  m.p = p;
+  m.run(lds, reinterpret_cast<char*>(lds + 2 * M::BUF));
 }
 
 }  // namespace pararnn
