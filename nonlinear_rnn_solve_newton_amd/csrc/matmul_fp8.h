@@ -607,8 +607,11 @@ struct MatmulLarge {
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // in the order that the steps count them in; the bias waits in workgroup memory
+    float* s_bias = reinterpret_cast<float*>(scales + 4 * SCH);
+    const float bias = p.bias && tid < 256 && n0 + tid < p.N ? p.bias[n0 + tid] : 0.0f;
     load_scales(0);
-    land_scales(0, scales);
+    const uint32_t vs0 = vs;
     load_w(0, lds);
     load_a(0, 0, lds);
     load_scales(1);
@@ -616,6 +619,11 @@ struct MatmulLarge {
     load_a(0, 1, lds);
     load_w(1, lds + BUF);
     load_a(1, 0, lds + BUF);
+    const uint32_t vs1 = vs;
+    vs = vs0;
+    land_scales(0, scales);
+    vs = vs1;
+    if (tid < 256) s_bias[tid] = bias;
     for (int kb = 0; kb < p.KB; ++kb) step(kb, lds, lds, scales, scales);
     __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into workgroup memory outlives the products
     const bool whole = p.vec == 8;
@@ -624,9 +632,7 @@ struct MatmulLarge {
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       const int n = n0 + wni * 64 + 16 * i + 4 * g;
-      float bv[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
+      const f32x4 bv = *reinterpret_cast<const f32x4*>(s_bias + (n - n0));
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
         const long long m = m0 + wmi * 128 + 16 * j + r;
@@ -648,7 +654,7 @@ template <int MODE, bool E8, int ROWS>
 __global__ void __launch_bounds__(512) matmul_large_kernel(const MatmulArgs p) {
   typedef MatmulLarge<MODE, E8, ROWS> M;
   // one array: what the compiler derives from several would replace what restrict says
-  __shared__ i32x4 lds[2 * M::BUF + 4 * M::SCH / 16];
+  __shared__ i32x4 lds[2 * M::BUF + 4 * M::SCH / 16 + 64];
   M m;
   m.p = p;
   m.run(lds, reinterpret_cast<char*>(lds + 2 * M::BUF));
