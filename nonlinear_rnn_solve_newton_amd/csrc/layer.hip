@@ -459,6 +459,7 @@ extern "C" int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void*
   p.K = o->K;
   p.KB = static_cast<int>(ceil_div(o->K, 128));
   p.vec = !f32 && o->N % 8 == 0 && aligned(y, 16) ? 8 : o->N % 4 == 0 && aligned(y, f32 ? 16 : 8) ? 4 : 1;
+  p.stream = 2.0 * p.M * p.N > 256.0 * 1024 * 1024;
   const bool direct = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
   hipStream_t s = static_cast<hipStream_t>(stream_);
   const int rows = o->w_rows;

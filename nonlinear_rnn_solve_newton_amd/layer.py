@@ -16,6 +16,7 @@ wrong type, shape or placement raises PararnnError. There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import re
 from typing import Optional
 
@@ -99,11 +100,6 @@ def lib():
     return _lib
 
 
-def _check(status: int, what: str):
-    if status != 0:
-        raise PararnnError(f"{what} failed: {status} ({strerror(status)})")
-
-
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -135,8 +131,22 @@ def _first(t, name: str, dims: int) -> torch.device:
     return t.device
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _launch(what: str, device: torch.device, *args):
+    """The C call on torch's current stream of the tensors' device, which is
+    made current for it where it is not."""
+    i = device.index
+    fn = getattr(lib(), what)
+    if _get_device() == i:
+        st = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, _raw_stream(i))
+    if st != 0:
+        raise PararnnError(f"{what} failed: {st} ({strerror(st)})")
 
 
 def _workspace(ws, need: int, device):
@@ -151,6 +161,16 @@ def _workspace(ws, need: int, device):
 
 # ---------------------------------------------------------------------------
 # gated linear recurrence
+
+@functools.lru_cache(maxsize=1024)
+def _gated_bytes(adjoint: int, B: int, L: int, D: int, dtype: int, c: float) -> int:
+    return lib().pararnn_gated_workspace_bytes(adjoint, ctypes.byref(GatedOpts(B, L, D, dtype, c, None, None)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _saved_rows(L: int) -> int:
+    return lib().pararnn_gated_saved_rows(L)
+
 
 def _gated_opts(u, lam, c, lengths, reset):
     dev = _first(u, "u", 4)
@@ -182,17 +202,15 @@ def gated_scan(u: torch.Tensor, lam: torch.Tensor, *, c: float = 8.0, h0: Option
     _dev(h0, "h0", torch.float32, (B, D), dev)
     if out is None:
         out = torch.empty(B, L, D, dtype=u.dtype, device=dev)
-    _dev(out, "out", u.dtype, (B, L, D), dev)
-    need = lib().pararnn_gated_workspace_bytes(0, ctypes.byref(o))
-    ws = _workspace(ws, need, dev)
+    else:
+        _dev(out, "out", u.dtype, (B, L, D), dev)
+    ws = _workspace(ws, _gated_bytes(0, B, L, D, o.dtype, c), dev)
     hT = torch.empty(B, D, dtype=torch.float32, device=dev)
-    saved = (torch.empty(lib().pararnn_gated_saved_rows(L), B, D, dtype=torch.float32, device=dev)
+    saved = (torch.empty(_saved_rows(L), B, D, dtype=torch.float32, device=dev)
              if save else None)
-    with torch.cuda.device(dev):
-        st = lib().pararnn_gated_scan(_ptr(u), _ptr(lam), _ptr(h0), _ptr(out), _ptr(hT), _ptr(saved), _ptr(ws),
-                                      ws.numel(), ctypes.byref(o), _stream(dev))
-    _check(st, "pararnn_gated_scan")
-    return dict(h=out, hT=hT, saved=saved, ws=ws)
+    _launch("pararnn_gated_scan", dev, _ptr(u), _ptr(lam), _ptr(h0), _ptr(out), _ptr(hT), _ptr(saved), _ptr(ws),
+            ws.numel(), ctypes.byref(o))
+    return {"h": out, "hT": hT, "saved": saved, "ws": ws}
 
 
 def gated_scan_adjoint(u: torch.Tensor, lam: torch.Tensor, dh: torch.Tensor, saved: torch.Tensor, *,
@@ -204,22 +222,19 @@ def gated_scan_adjoint(u: torch.Tensor, lam: torch.Tensor, dh: torch.Tensor, sav
     Returns dict(du [B][L][3][D] in u's type, dlam [D], dh0 [B][D], ws)."""
     o, dev, B, L, D = _gated_opts(u, lam, c, lengths, reset)
     _dev(dh, "dh", u.dtype, (B, L, D), dev)
-    _dev(saved, "saved", torch.float32, (lib().pararnn_gated_saved_rows(L), B, D), dev)
+    _dev(saved, "saved", torch.float32, (_saved_rows(L), B, D), dev)
     if saved is None:
         raise PararnnError("the adjoint needs the states saved by gated_scan(save=True)")
     _dev(dhT, "dhT", torch.float32, (B, D), dev)
     if du is None:
         du = torch.empty(B, L, 3, D, dtype=u.dtype, device=dev)
-    _dev(du, "du", u.dtype, (B, L, 3, D), dev)
-    need = lib().pararnn_gated_workspace_bytes(1, ctypes.byref(o))
-    ws = _workspace(ws, need, dev)
+    else:
+        _dev(du, "du", u.dtype, (B, L, 3, D), dev)
+    ws = _workspace(ws, _gated_bytes(1, B, L, D, o.dtype, c), dev)
     dlam = torch.empty(D, dtype=torch.float32, device=dev) if want_dlam else None
     dh0 = torch.empty(B, D, dtype=torch.float32, device=dev) if want_dh0 else None
-    with torch.cuda.device(dev):
-        st = lib().pararnn_gated_scan_adjoint(_ptr(u), _ptr(lam), _ptr(saved), _ptr(dh), _ptr(dhT), _ptr(du),
-                                              _ptr(dlam), _ptr(dh0), _ptr(ws), ws.numel(), ctypes.byref(o),
-                                              _stream(dev))
-    _check(st, "pararnn_gated_scan_adjoint")
+    _launch("pararnn_gated_scan_adjoint", dev, _ptr(u), _ptr(lam), _ptr(saved), _ptr(dh), _ptr(dhT), _ptr(du),
+            _ptr(dlam), _ptr(dh0), _ptr(ws), ws.numel(), ctypes.byref(o))
     return dict(du=du, dlam=dlam, dh0=dh0, ws=ws)
 
 
@@ -243,11 +258,10 @@ def gated_step(u: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *, c: fl
     _dev(slots, "slots", torch.int32, (B,), dev)
     if out is None:
         out = torch.empty(B, D, dtype=u.dtype, device=dev)
-    _dev(out, "out", u.dtype, (B, D), dev)
-    with torch.cuda.device(dev):
-        st = lib().pararnn_gated_step(_ptr(u), _ptr(lam), _ptr(slots), _ptr(state), _ptr(out), B, D, S,
-                                      _DTYPE[u.dtype], c, _stream(dev))
-    _check(st, "pararnn_gated_step")
+    else:
+        _dev(out, "out", u.dtype, (B, D), dev)
+    _launch("pararnn_gated_step", dev, _ptr(u), _ptr(lam), _ptr(slots), _ptr(state), _ptr(out), B, D, S,
+            _DTYPE[u.dtype], c)
     return out
 
 
@@ -282,10 +296,8 @@ def norm_residual(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.
         scale = torch.empty(-(-D // BLOCK), N, dtype=scale_dtype, device=dev)
     s = x if residual is None else torch.empty_like(x)
     o = NormOpts(N, D, _DTYPE[x.dtype], out, eps)
-    with torch.cuda.device(dev):
-        st = lib().pararnn_norm_residual(_ptr(x), _ptr(residual), _ptr(w), None if s is x else _ptr(s), _ptr(y),
-                                         _ptr(scale), ctypes.byref(o), _stream(dev))
-    _check(st, "pararnn_norm_residual")
+    _launch("pararnn_norm_residual", dev, _ptr(x), _ptr(residual), _ptr(w), None if s is x else _ptr(s), _ptr(y),
+            _ptr(scale), ctypes.byref(o))
     return dict(y=y, s=s, scale=scale)
 
 
@@ -307,10 +319,8 @@ def norm_residual_adjoint(s: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, *,
         ws = _workspace(ws, lib().pararnn_norm_workspace_bytes(ctypes.byref(o)), dev)
         dw = torch.empty(D, dtype=torch.float32, device=dev)
     dx = torch.empty_like(s)
-    with torch.cuda.device(dev):
-        st = lib().pararnn_norm_residual_adjoint(_ptr(s), _ptr(w), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw), _ptr(ws),
-                                                 0 if ws is None else ws.numel(), ctypes.byref(o), _stream(dev))
-    _check(st, "pararnn_norm_residual_adjoint")
+    _launch("pararnn_norm_residual_adjoint", dev, _ptr(s), _ptr(w), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw),
+            _ptr(ws), 0 if ws is None else ws.numel(), ctypes.byref(o))
     return dict(dx=dx, dw=dw, ws=ws)
 
 
@@ -373,10 +383,8 @@ def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Ten
         raise PararnnError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
     if out is None:
         out = torch.empty(M, N, dtype=out_dtype, device=dev)
-    _dev(out, "out", out_dtype, (M, N), dev)
+    else:
+        _dev(out, "out", out_dtype, (M, N), dev)
     o = MatmulOpts(M, N, K, rows, _SCALE[sa.dtype], _DTYPE[out_dtype])
-    with torch.cuda.device(dev):
-        st = lib().pararnn_matmul_fp8(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _ptr(bias), _ptr(out), ctypes.byref(o),
-                                      _stream(dev))
-    _check(st, "pararnn_matmul_fp8")
+    _launch("pararnn_matmul_fp8", dev, _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _ptr(bias), _ptr(out), ctypes.byref(o))
     return out
