@@ -46,7 +46,7 @@ typedef struct {
  * 0 for invalid options. Host-only. */
 size_t pararnn_gated_workspace_bytes(int32_t adjoint, const pararnn_gated_opts* o);
 
-/* Number of saved states per channel: one in front of every 128 steps. */
+/* Number of saved states per channel: one in front of every 96 steps. */
 int32_t pararnn_gated_saved_rows(int32_t L);
 
 /* Forward: h, and optionally hT, the state after each row's last step, and

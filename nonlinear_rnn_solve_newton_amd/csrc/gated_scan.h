@@ -14,16 +14,18 @@
 //
 // Both are linear scans, bound by HBM: bf16 moves 8 bytes per element forward
 // (u in, h out) and 14 back (u and dh in, du out). The states between the
-// chunks of 128 steps (4 / 128 bytes per element) are what the forward pass
+// chunks of 96 steps (4 / 96 bytes per element) are what the forward pass
 // leaves for the adjoint, which rebuilds the others from u, in 32 bits: less
 // to move than the states themselves, and not rounded to bf16.
 #pragma once
+
+#include <type_traits>
 
 #include "layer_common.h"
 
 namespace pararnn {
 
-constexpr int kGatedSave = 128;  // steps between two saved states
+constexpr int kGatedSave = 96;  // steps between two saved states: an adjoint chunk
 
 struct GatedArgs {
   const void* u;            // [B][L][3][D]
@@ -46,35 +48,29 @@ struct GatedArgs {
   float c;
 };
 
-// Gate values of one step: v = 1 - a^2 = -expm1(2 log a) by its series where
-// it is small (1 - a^2 itself would lose the digits that the subtraction
-// cancels), m = sqrt(v) and 1/m from one reciprocal square root, 0 for both
-// where v is 0. beta2: -c softplus(lam) log2(e).
+// Gate values of one step; y = log2 a = beta2 r with beta2 = -c softplus(lam) log2(e).
+// v = 1 - a^2 = 1 - 2^(2y): where it is under 0.22 (2y ln 2 > -0.25) by y q(y), q of
+// degree 4 through the Chebyshev points (relative error 1.2e-8), since the
+// subtraction would cancel its digits; above, the cancellation costs 2 bits.
 struct GateVal {
-  float r, i, a, m, im;
+  float r, i, a, v;
 };
 __device__ __forceinline__ GateVal gate_values(float ur, float ui, float beta2) {
   GateVal g;
   g.r = sigm(ur);
   g.i = sigm(ui);
-  const float y = beta2 * g.r;  // log2 a
+  const float y = beta2 * g.r;
   g.a = __builtin_amdgcn_exp2f(y);
-  const float w = y * -1.3862943611198906f;  // -2 log a >= 0
-  float p = 1.0f / 5040.0f;  // (1 - exp(-w)) / w
-  p = fmaf(p, w, -1.0f / 720.0f);
-  p = fmaf(p, w, 1.0f / 120.0f);
-  p = fmaf(p, w, -1.0f / 24.0f);
-  p = fmaf(p, w, 1.0f / 6.0f);
-  p = fmaf(p, w, -0.5f);
-  p = fmaf(p, w, 1.0f);
-  // from 0.25 on the cancellation costs under 2 bits; below it the series'
-  // next term is under 2^-28
-  const float v = w < 0.25f ? p * w : fmaf(-g.a, g.a, 1.0f);
-  const float rs = __builtin_amdgcn_rsqf(v);
-  g.im = v < 1.17549435e-38f ? 0.0f : rs;
-  g.m = v * g.im;
+  float q = -0.0384703129529953f;
+  q = fmaf(q, y, -0.15323998034000397f);
+  q = fmaf(q, y, -0.44399136304855347f);
+  q = fmaf(q, y, -0.9609050750732422f);
+  q = fmaf(q, y, -1.3862943649291992f);
+  g.v = y > -0.18033688f ? q * y : fmaf(-g.a, g.a, 1.0f);
   return g;
 }
+constexpr float kNoInput = 9.0e18f;  // 1/m from here on: m = 0
+__device__ __forceinline__ float decay_log2(float lam, float c) { return -1.4426950408889634f * c * softplus(lam); }
 
 // Affine transforms x -> A x + b of C channels. RST: a transform that begins a
 // document (anywhere inside) holds A = -0 and drops what comes before it
@@ -112,6 +108,15 @@ struct Lin {
       x[c] = (RST && __float_as_uint(A[c]) == kResetA) ? b[c] : y;
     }
   }
+  __device__ __forceinline__ Lin shfl_down(int delta) const {
+    Lin r;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      r.A[c] = __shfl_down(A[c], delta, 64);
+      r.b[c] = __shfl_down(b[c], delta, 64);
+    }
+    return r;
+  }
   __device__ __forceinline__ Lin shfl_up(int delta) const {
     Lin r;
 #pragma unroll
@@ -124,98 +129,95 @@ struct Lin {
 };
 
 // The carry into a chunk. Chunks (counted in scan order) form groups of
-// `group`. A chunk publishes its own transform as soon as it has it, except
-// the last of a group, which publishes the state at its end: the next group's
-// start. A chunk so waits for its group's start and for the transforms of the
-// chunks before it in the group, and composes them in order: the chain of
-// waits has one link per group, not per chunk, and the order of the sums does
-// not depend on timing, so results repeat bit for bit. Tickets are taken
-// chunk by chunk, so whatever a workgroup waits for has started before it.
-// Words carry their tag (1: written) in the high half.
-template <int C, bool RST>
-__device__ __forceinline__ void chunk_carry(const GatedArgs& p, long long slots, long long chan, int cs, int q,
-                                            const Lin<C, RST>& tot, float (&x)[C]) {
+// `group` <= kMaxGroup. A chunk publishes its own transform as soon as it has
+// it, except the last of a group, which publishes the state at its end: the
+// next group's start. A chunk so waits for its group's start and for the
+// transforms of the chunks before it in the group, reads them all at once and
+// composes them in order: the chain of waits has one link per group, not per
+// chunk, and the order of the sums does not depend on timing, so results
+// repeat bit for bit. Tickets are taken chunk by chunk, so whatever a
+// workgroup waits for has started before it. Words carry their tag (1:
+// written) in the high half. Called by one wave, a channel per lane: tot is
+// the chunk's transform, x the state before the first chunk; returns the
+// state before chunk q.
+constexpr int kMaxGroup = 8;
+template <bool RST>
+__device__ __forceinline__ float chunk_carry(const GatedArgs& p, long long slots, long long chan, int q,
+                                             const Lin<1, RST>& tot, float x) {
   const int grp = q / p.group, j = q - grp * p.group;
   const bool last = j == p.group - 1;
   if (!last && q < p.nchunks - 1) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      desc_put(p.agg + static_cast<long long>(q) * 2 * slots + chan + c * cs, 1u, tot.A[c]);
-      desc_put(p.agg + (static_cast<long long>(q) * 2 + 1) * slots + chan + c * cs, 1u, tot.b[c]);
-    }
+    desc_put(p.agg + static_cast<long long>(q) * 2 * slots + chan, 1u, tot.A[0]);
+    desc_put(p.agg + (static_cast<long long>(q) * 2 + 1) * slots + chan, 1u, tot.b[0]);
   }
-  Lin<C, RST> m;  // chunks before this one in the group, composed from the first on
-  m.set_identity();
-  for (int i = q - j; i < q; ++i) {
-    unsigned long long wa[C], wb[C];
-    while (true) {
-      bool ok = true;
+  unsigned long long wa[kMaxGroup - 1], wb[kMaxGroup - 1], wx = 0ull;
+  while (true) {
+    const unsigned long long* at = p.agg + static_cast<long long>(q - j) * 2 * slots + chan;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        wa[c] = desc_get(p.agg + static_cast<long long>(i) * 2 * slots + chan + c * cs);
-        wb[c] = desc_get(p.agg + (static_cast<long long>(i) * 2 + 1) * slots + chan + c * cs);
-        ok = ok && desc_ok(wa[c], 1u) && desc_ok(wb[c], 1u);
+    for (int s = 0; s < kMaxGroup - 1; ++s) {
+      if (s < j) {
+        wa[s] = desc_get(const_cast<unsigned long long*>(at) + 2 * s * slots);
+        wb[s] = desc_get(const_cast<unsigned long long*>(at) + (2 * s + 1) * slots);
       }
-      if (ok) break;
-      __builtin_amdgcn_s_sleep(1);
     }
-    Lin<C, RST> e;
+    if (grp > 0) wx = desc_get(p.carry + static_cast<long long>(grp) * slots + chan);
+    bool ok = grp == 0 || desc_ok(wx, 1u);
 #pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = desc_val(wa[c]); e.b[c] = desc_val(wb[c]); }
-    e.after(m);
-    m = e;
+    for (int s = 0; s < kMaxGroup - 1; ++s)
+      if (s < j) ok = ok && desc_ok(wa[s], 1u) && desc_ok(wb[s], 1u);
+    if (ok) break;
+    __builtin_amdgcn_s_sleep(1);
   }
-  if (grp > 0) {
-    unsigned long long w[C];
-    while (true) {
-      bool ok = true;
+  float v[1] = {grp > 0 ? desc_val(wx) : x};
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        w[c] = desc_get(p.carry + static_cast<long long>(grp) * slots + chan + c * cs);
-        ok = ok && desc_ok(w[c], 1u);
-      }
-      if (ok) break;
-      __builtin_amdgcn_s_sleep(1);
+  for (int s = 0; s < kMaxGroup - 1; ++s) {
+    if (s < j) {
+      Lin<1, RST> e;
+      e.A[0] = desc_val(wa[s]);
+      e.b[0] = desc_val(wb[s]);
+      e.apply(v);
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = desc_val(w[c]);
   }
-  m.apply(x);
   if (last && q < p.nchunks - 1) {
-    float y[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) y[c] = x[c];
+    float y[1] = {v[0]};
     tot.apply(y);
-#pragma unroll
-    for (int c = 0; c < C; ++c) desc_put(p.carry + static_cast<long long>(grp + 1) * slots + chan + c * cs, 1u, y[c]);
+    desc_put(p.carry + static_cast<long long>(grp + 1) * slots + chan, 1u, y[0]);
   }
+  return v[0];
 }
 
-// A workgroup of W waves covers LD * C channels (LD = 64 / LL lanes along D)
-// and CL = W * LL * T steps: T steps in series per lane, a shuffle scan over
-// the LL lane groups, an LDS scan over the waves, chunk_carry over the chunks.
+// A workgroup covers LD * C channels (LD = 64 / LL lanes along D) and
+// CL = W * LL * T steps: T steps in series per lane, a shuffle scan over the
+// LL lane groups, an LDS scan over the W waves, chunk_carry over the chunks.
+// The first wave takes the carry. It parks its steps in workgroup memory
+// meanwhile: the words it polls would otherwise cost every wave registers.
 template <class UT, int C, int T, int W, int LL, int OCC, bool RST>
 __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs p) {
   constexpr int LD = 64 / LL, CW = LD * C, CL = W * LL * T;
-  __shared__ float s_A[W][CW], s_b[W][CW], s_carry[CW];
+  static_assert(CW <= 64, "one wave takes the carry, a channel per lane");
+  constexpr int NP = 2 * T * C / 4;  // 16-byte pieces that a lane parks
+  static_assert(T * C % 4 == 0, "whole pieces");
+  __shared__ float s_A[W][CW], s_b[W][CW], s_start[W][CW], s_beta[CW];
+  __shared__ f32x4 s_park[NP][64];
   __shared__ unsigned int s_ticket;
 
-  const int tid = threadIdx.x;
-  const int lane = tid & 63, wave = tid >> 6;
-  const int ld = lane % LD, ll = lane / LD;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   unsigned int ticket = blockIdx.x;
   if (p.nchunks > 1) {
     if (tid == 0) s_ticket = atomicAdd(p.ctr, 1u);
     __syncthreads();
-    ticket = s_ticket;
+    ticket = __builtin_amdgcn_readfirstlane(s_ticket);
   }
   const unsigned int ntiles = static_cast<unsigned int>(p.B) * p.ntiles_d;
   const int chunk = static_cast<int>(ticket / ntiles);
   const int tile = static_cast<int>(ticket - static_cast<unsigned int>(chunk) * ntiles);
   const int b = tile / p.ntiles_d;
-  const int d0 = (tile - b * p.ntiles_d) * CW + ld * C;
+  const int dt0 = (tile - b * p.ntiles_d) * CW;
+
+  const int ld = lane % LD, ll = lane / LD;
+  const int d0 = dt0 + ld * C;
   const bool dv = d0 < p.D;
-  const int dc = dv ? d0 : 0;
   const int lt0 = (wave * LL + ll) * T;
   const int l0 = chunk * CL + lt0;
   const int len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
@@ -234,30 +236,30 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
   for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int g = 0; g < 3; ++g) uu[t][g].load(ru, vu0 + t * ustep, static_cast<uint32_t>(g) * gstep);
-
+  bool cut[RST ? T : 1];  // document starts
+  if constexpr (RST) {
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      cut[t] = p.reset[static_cast<long long>(b) * p.L + min(l0 + t, p.L - 1)] != 0;
+  }
+  if (tid < CW) s_beta[tid] = decay_log2(p.lam[min(dt0 + tid, p.D - 1)], p.c);
+  __syncthreads();
   float beta2[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) beta2[c] = -1.4426950408889634f * p.c * softplus(p.lam[dc + c]);
+  for (int c = 0; c < C; ++c) beta2[c] = s_beta[ld * C + c];
 
-  float A[T][C], x[T][C];  // x: input of the step, then nothing else
+  // the steps' transforms; those past the length are the identity
+  const bool ragged = (chunk + 1) * static_cast<long long>(CL) > len;
+  float A[T][C], x[T][C];
 #pragma unroll
   for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const GateVal g = gate_values(uu[t][0].get(c), uu[t][1].get(c), beta2[c]);
-      A[t][c] = g.a;
-      x[t][c] = g.m * (g.i * uu[t][2].get(c));
+      A[t][c] = RST && cut[t] ? __uint_as_float(kResetA) : g.a;
+      x[t][c] = __builtin_amdgcn_sqrtf(g.v) * (g.i * uu[t][2].get(c));
     }
-  if constexpr (RST) {
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool cut = l0 + t < p.L && p.reset[static_cast<long long>(b) * p.L + min(l0 + t, p.L - 1)] != 0;
-#pragma unroll
-      for (int c = 0; c < C; ++c) A[t][c] = cut ? __uint_as_float(kResetA) : A[t][c];
-    }
-  }
-  const bool ragged = (chunk + 1) * static_cast<long long>(CL) > len;
-  if (ragged) {  // steps past the length: identity
+  if (ragged) {
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -296,84 +298,124 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
     }
   }
   __syncthreads();
-  if (wave == 0 && ll == 0) {
-    float v[C];
+  if (wave == 0) {
+    float* flat_A = &A[0][0];
+    float* flat_x = &x[0][0];
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = (dv && p.h0) ? p.h0[static_cast<long long>(b) * p.D + dc + c] : 0.0f;
-    if (dv && p.nchunks > 1) {
-      Lin<C, RST> tot;
-      tot.set_identity();
+    for (int i = 0; i < NP / 2; ++i) {
+      s_park[i][lane] = f32x4{flat_A[4 * i], flat_A[4 * i + 1], flat_A[4 * i + 2], flat_A[4 * i + 3]};
+      s_park[NP / 2 + i][lane] = f32x4{flat_x[4 * i], flat_x[4 * i + 1], flat_x[4 * i + 2], flat_x[4 * i + 3]};
+    }
+    if (lane < CW) {
+      const bool in = dt0 + lane < p.D;
+      const long long bd = static_cast<long long>(b) * p.D + dt0 + lane;
+      float v[1] = {in && p.h0 ? p.h0[bd] : 0.0f};
+      if (p.nchunks > 1) {
+        Lin<1, RST> tot;
+        tot.set_identity();
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          Lin<1, RST> e;
+          e.A[0] = s_A[w][lane];
+          e.b[0] = s_b[w][lane];
+          e.after(tot);
+          tot = e;
+        }
+        v[0] = chunk_carry<RST>(p, static_cast<long long>(p.B) * p.ntiles_d * CW,
+                                static_cast<long long>(tile) * CW + lane, chunk, tot, v[0]);
+      }
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        Lin<C, RST> e;
-#pragma unroll
-        for (int c = 0; c < C; ++c) { e.A[c] = s_A[w][ld * C + c]; e.b[c] = s_b[w][ld * C + c]; }
-        e.after(tot);
-        tot = e;
+        s_start[w][lane] = v[0];
+        Lin<1, RST> e;
+        e.A[0] = s_A[w][lane];
+        e.b[0] = s_b[w][lane];
+        e.apply(v);
       }
-      chunk_carry<C, RST>(p, static_cast<long long>(p.B) * p.ntiles_d * CW, static_cast<long long>(tile) * CW + ld,
-                          LD, chunk, tot, v);
+      if (p.hT && in && chunk == p.nchunks - 1) p.hT[bd] = v[0];
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) s_carry[ld * C + c] = v[c];
+    for (int i = 0; i < NP / 2; ++i) {
+      // volatile: read back, not kept in registers after all
+      const f32x4 va = *static_cast<const volatile f32x4*>(&s_park[i][lane]);
+      const f32x4 vx = *static_cast<const volatile f32x4*>(&s_park[NP / 2 + i][lane]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        flat_A[4 * i + k] = va[k];
+        flat_x[4 * i + k] = vx[k];
+      }
+    }
   }
   __syncthreads();
-
   float h[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) h[c] = s_carry[ld * C + c];
-  for (int w = 0; w < wave; ++w) {
-    Lin<C, RST> e;
-#pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = s_A[w][ld * C + c]; e.b[c] = s_b[w][ld * C + c]; }
-    e.apply(h);
-  }
+  for (int c = 0; c < C; ++c) h[c] = s_start[wave][ld * C + c];
   if constexpr (LL > 1) excl.apply(h);
   if (p.saved && dv && l0 % kGatedSave == 0 && l0 < p.L)
     st_f32<C>(p.saved + (static_cast<long long>(l0 / kGatedSave) * p.B + b) * p.D + d0, h);
 
+  auto put_out = [&](auto full) {
 #pragma unroll
-  for (int t = 0; t < T; ++t) {
-    Lin<C, RST> e;
+    for (int t = 0; t < T; ++t) {
+      Lin<C, RST> e;
 #pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = A[t][c]; e.b[c] = x[t][c]; }
-    e.apply(h);
-    float o[C];
+      for (int c = 0; c < C; ++c) { e.A[c] = A[t][c]; e.b[c] = x[t][c]; }
+      e.apply(h);
+      float o[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = (ragged && l0 + t >= len) ? 0.0f : h[c];
-    buf_st<UT, C>(rh, vh0 + t * gstep, 0u, o);  // dropped past L or D
-  }
-  if (p.hT && dv && chunk == p.nchunks - 1 && wave == W - 1 && ll == LL - 1)
-    st_f32<C>(p.hT + static_cast<long long>(b) * p.D + d0, h);
+      for (int c = 0; c < C; ++c) o[c] = (!decltype(full)::value && l0 + t >= len) ? 0.0f : h[c];
+      buf_st<UT, C>(rh, vh0 + t * gstep, 0u, o);  // dropped past L or D
+    }
+  };
+  if (ragged) put_out(std::false_type{});
+  else put_out(std::true_type{});
 }
 
+// Packed values stay packed: without this the compiler keeps the unpacked ones
+// of their first use in registers for the second.
+template <int C>
+__device__ __forceinline__ void keep_packed(URaw<bf16, C>& u) {
+#pragma unroll
+  for (int i = 0; i < URaw<bf16, C>::NW; ++i) __asm__ volatile("" : "+v"(u.w[i]));
+}
+template <int C>
+__device__ __forceinline__ void keep_packed(URaw<float, C>&) {}
+
 // The adjoint of one chunk of CL = kGatedSave steps: a scan forward from the
-// saved state for the h_{t-1}, and the scan backward for mu, on the same lanes.
+// saved state for the h_{t-1}, and the scan backward for mu, on the same
+// lanes.
 template <class UT, int C, int T, int W, int LL, int OCC, bool RST>
 __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedArgs p) {
   constexpr int LD = 64 / LL, CW = LD * C, CL = W * LL * T, NSEG = W * LL;
   static_assert(CL == kGatedSave, "a chunk starts at a saved state");
-  __shared__ float s_A[W][CW], s_b[W][CW], s_B[W][CW], s_m[W][CW], s_carry[CW];
+  static_assert(CW <= 64, "one wave takes the carry, a channel per lane");
+  // transforms of the waves, forward (A, b) and backward (B, m); what enters them
+  __shared__ float s_A[W][CW], s_b[W][CW], s_B[W][CW], s_m[W][CW], s_h[W][CW], s_mu[W][CW], s_beta[CW];
   __shared__ float s_dl[NSEG][CW];
+  constexpr int NP = 5 * T * C / 4;  // 16-byte pieces that a lane of the first wave parks
+  static_assert(T * C % 4 == 0, "whole pieces");
+  __shared__ f32x4 s_park[NP][64];
+  __shared__ Lin<C, RST> s_fx[W][LL > 1 ? 64 : 1], s_bx[W][LL > 1 ? 64 : 1];
   __shared__ unsigned int s_ticket;
 
-  const int tid = threadIdx.x;
-  const int lane = tid & 63, wave = tid >> 6;
-  const int ld = lane % LD, ll = lane / LD;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   unsigned int ticket = blockIdx.x;
   if (p.nchunks > 1) {
     if (tid == 0) s_ticket = atomicAdd(p.ctr, 1u);
     __syncthreads();
-    ticket = s_ticket;
+    ticket = __builtin_amdgcn_readfirstlane(s_ticket);
   }
   const unsigned int ntiles = static_cast<unsigned int>(p.B) * p.ntiles_d;
   const int rchunk = static_cast<int>(ticket / ntiles);
   const int chunk = p.nchunks - 1 - rchunk;  // taken from the end of L
   const int tile = static_cast<int>(ticket - static_cast<unsigned int>(rchunk) * ntiles);
   const int b = tile / p.ntiles_d;
-  const int d0 = (tile - b * p.ntiles_d) * CW + ld * C;
+  const int dt0 = (tile - b * p.ntiles_d) * CW;
+
+  const int ld = lane % LD, ll = lane / LD;
+  const int d0 = dt0 + ld * C;
   const bool dv = d0 < p.D;
-  const int dc = dv ? d0 : 0;
   const int lt0 = (wave * LL + ll) * T;
   const int l0 = chunk * CL + lt0;
   const int len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
@@ -395,33 +437,36 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
     for (int g = 0; g < 3; ++g) uu[t][g].load(ru, vu0 + t * ustep, static_cast<uint32_t>(g) * gstep);
     gg[t].load(rdh, vh0 + t * gstep, 0u);
   }
-  float beta[C], beta2[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    beta[c] = -p.c * softplus(p.lam[dc + c]);
-    beta2[c] = 1.4426950408889634f * beta[c];
-  }
-
-  float A[T][C], bb[T][C], dh[T][C];  // transform of the step; bb later holds h_{t-1}
-  GateVal gv[T][C];
-#pragma unroll
-  for (int t = 0; t < T; ++t)
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      gv[t][c] = gate_values(uu[t][0].get(c), uu[t][1].get(c), beta2[c]);
-      A[t][c] = gv[t][c].a;
-      bb[t][c] = gv[t][c].m * (gv[t][c].i * uu[t][2].get(c));
-      dh[t][c] = gg[t].get(c);
-    }
+  bool cut[RST ? T : 1];
   if constexpr (RST) {
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const bool cut = l0 + t < p.L && p.reset[static_cast<long long>(b) * p.L + min(l0 + t, p.L - 1)] != 0;
+    for (int t = 0; t < T; ++t)
+      cut[t] = p.reset[static_cast<long long>(b) * p.L + min(l0 + t, p.L - 1)] != 0;
+  }
+  if (tid < CW) s_beta[tid] = decay_log2(p.lam[min(dt0 + tid, p.D - 1)], p.c);
+  __syncthreads();
+  float beta2[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) A[t][c] = cut ? __uint_as_float(kResetA) : A[t][c];
+  for (int c = 0; c < C; ++c) beta2[c] = s_beta[ld * C + c];
+
+  const bool ragged = (chunk + 1) * static_cast<long long>(CL) > len;
+  // per step: its transform (bb later holds h_{t-1}), r, i and 1/m; x and dh stay packed
+  float A[T][C], bb[T][C], gr[T][C], gi[T][C], im[T][C];
+  // the steps one after the other: interleaved, their intermediates would not fit the registers
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const GateVal g = gate_values(uu[t][0].get(c), uu[t][1].get(c), beta2[c]);
+      gr[t][c] = g.r;
+      gi[t][c] = g.i;
+      // 1/m is kept finite (2^63 for v = 0): where v is 0, so are r or beta, and with them what 1/m multiplies
+      im[t][c] = __builtin_amdgcn_rsqf(fmaxf(g.v, 1.17549435e-38f));
+      A[t][c] = RST && cut[t] ? __uint_as_float(kResetA) : g.a;
+      bb[t][c] = g.v * im[t][c] * (g.i * uu[t][2].get(c));
     }
   }
-  const bool ragged = (chunk + 1) * static_cast<long long>(CL) > len;
   if (ragged) {
 #pragma unroll
     for (int t = 0; t < T; ++t)
@@ -429,7 +474,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
       for (int c = 0; c < C; ++c) {
         A[t][c] = l0 + t < len ? A[t][c] : 1.0f;
         bb[t][c] = l0 + t < len ? bb[t][c] : 0.0f;
-        dh[t][c] = l0 + t < len ? dh[t][c] : 0.0f;
+        if (c == 0 && l0 + t >= len) gg[t].zero();
       }
   }
 
@@ -448,37 +493,30 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
     Lin<C, RST> e;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      const bool none = RST && __float_as_uint(A[t][c]) == kResetA;
       e.A[c] = A[t][c];
-      e.b[c] = (RST && __float_as_uint(A[t][c]) == kResetA) ? 0.0f : A[t][c] * dh[t][c];
+      e.b[c] = none ? 0.0f : A[t][c] * gg[t].get(c);
     }
     if (t < T - 1) e.after(bw);
     bw = e;
   }
-  Lin<C, RST> fx, bx;  // what precedes the lane in either direction, within the wave
-  fx.set_identity();
-  bx.set_identity();
   if constexpr (LL > 1) {
 #pragma unroll
     for (int off = 1; off < LL; off *= 2) {
       const Lin<C, RST> prev = fw.shfl_up(off * LD);
       if (ll >= off) fw.after(prev);
-      Lin<C, RST> next;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        next.A[c] = __shfl_down(bw.A[c], off * LD, 64);
-        next.b[c] = __shfl_down(bw.b[c], off * LD, 64);
-      }
+      const Lin<C, RST> next = bw.shfl_down(off * LD);
       if (ll < LL - off) bw.after(next);
     }
-    const Lin<C, RST> prev = fw.shfl_up(LD);
-    if (ll > 0) fx = prev;
-    Lin<C, RST> next;
+    // what precedes the lane within the wave, in either direction, waits in
+    // workgroup memory for the carry: registers are short
+    s_fx[wave][lane] = fw;
+    s_bx[wave][lane] = bw;
+  }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      next.A[c] = __shfl_down(bw.A[c], LD, 64);
-      next.b[c] = __shfl_down(bw.b[c], LD, 64);
-    }
-    if (ll < LL - 1) bx = next;
+  for (int t = 0; t < T; ++t) {
+    keep_packed<C>(uu[t][2]);
+    keep_packed<C>(gg[t]);
   }
   if (ll == LL - 1) {
 #pragma unroll
@@ -495,39 +533,68 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
     }
   }
   __syncthreads();
-  if (wave == 0 && ll == 0) {
-    float v[C];
+  if (wave == 0) {
+    float* const flat[5] = {&A[0][0], &bb[0][0], &gr[0][0], &gi[0][0], &im[0][0]};
+    constexpr int N4 = T * C / 4;
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = (dv && p.dhT) ? p.dhT[static_cast<long long>(b) * p.D + dc + c] : 0.0f;
-    if (dv && p.nchunks > 1) {
-      Lin<C, RST> tot;
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+      for (int i = 0; i < N4; ++i)
+        s_park[k * N4 + i][lane] = f32x4{flat[k][4 * i], flat[k][4 * i + 1], flat[k][4 * i + 2], flat[k][4 * i + 3]};
+    if (lane < CW) {
+      const bool in = dt0 + lane < p.D;
+      const long long bd = static_cast<long long>(b) * p.D + dt0 + lane;
+      float h[1] = {in ? p.saved[static_cast<long long>(chunk) * p.B * p.D + bd] : 0.0f};
+      float v[1] = {in && p.dhT ? p.dhT[bd] : 0.0f};
+      Lin<1, RST> tot;
       tot.set_identity();
 #pragma unroll
-      for (int w = W - 1; w >= 0; --w) {
-        Lin<C, RST> e;
-#pragma unroll
-        for (int c = 0; c < C; ++c) { e.A[c] = s_B[w][ld * C + c]; e.b[c] = s_m[w][ld * C + c]; }
+      for (int w = 0; w < W; ++w) {
+        s_h[w][lane] = h[0];
+        Lin<1, RST> e;
+        e.A[0] = s_A[w][lane];
+        e.b[0] = s_b[w][lane];
+        e.apply(h);
+        e.A[0] = s_B[W - 1 - w][lane];
+        e.b[0] = s_m[W - 1 - w][lane];
         e.after(tot);
         tot = e;
       }
-      chunk_carry<C, RST>(p, static_cast<long long>(p.B) * p.ntiles_d * CW, static_cast<long long>(tile) * CW + ld,
-                          LD, rchunk, tot, v);
+      if (p.nchunks > 1)
+        v[0] = chunk_carry<RST>(p, static_cast<long long>(p.B) * p.ntiles_d * CW,
+                                static_cast<long long>(tile) * CW + lane, rchunk, tot, v[0]);
+#pragma unroll
+      for (int w = W - 1; w >= 0; --w) {
+        s_mu[w][lane] = v[0];
+        Lin<1, RST> e;
+        e.A[0] = s_B[w][lane];
+        e.b[0] = s_m[w][lane];
+        e.apply(v);
+      }
+      if (p.dh0 && in && chunk == 0) p.dh0[bd] = v[0];
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) s_carry[ld * C + c] = v[c];
-  }
-  // meanwhile the others rebuild their states from the saved one
-  float h[C];
+    for (int k = 0; k < 5; ++k)
 #pragma unroll
-  for (int c = 0; c < C; ++c) h[c] = 0.0f;
-  if (dv) ld_f32<C>(p.saved + (static_cast<long long>(chunk) * p.B + b) * p.D + d0, h);
-  for (int w = 0; w < wave; ++w) {
-    Lin<C, RST> e;
+      for (int i = 0; i < N4; ++i) {
+        // volatile: read back, not kept in registers after all
+        const f32x4 v = *static_cast<const volatile f32x4*>(&s_park[k * N4 + i][lane]);
 #pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = s_A[w][ld * C + c]; e.b[c] = s_b[w][ld * C + c]; }
-    e.apply(h);
+        for (int q = 0; q < 4; ++q) flat[k][4 * i + q] = v[q];
+      }
   }
-  if constexpr (LL > 1) fx.apply(h);
+  __syncthreads();
+  float h[C], mu[C], dl[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    h[c] = s_h[wave][ld * C + c];
+    mu[c] = s_mu[wave][ld * C + c];
+    dl[c] = 0.0f;
+  }
+  if constexpr (LL > 1) {
+    if (ll > 0) s_fx[wave][lane - LD].apply(h);
+    if (ll < LL - 1) s_bx[wave][lane + LD].apply(mu);
+  }
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     Lin<C, RST> e;
@@ -538,56 +605,45 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
 #pragma unroll
     for (int c = 0; c < C; ++c) bb[t][c] = prev[c];
   }
-  __syncthreads();
-  float mu[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) mu[c] = s_carry[ld * C + c];
-  for (int w = W - 1; w > wave; --w) {
-    Lin<C, RST> e;
-#pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = s_B[w][ld * C + c]; e.b[c] = s_m[w][ld * C + c]; }
-    e.apply(mu);
-  }
-  if constexpr (LL > 1) bx.apply(mu);
 
-  float dl[C];
+  auto put_out = [&](auto full) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) dl[c] = 0.0f;
+    for (int t = T - 1; t >= 0; --t) {
+      __builtin_amdgcn_sched_barrier(0);
+      const bool on = decltype(full)::value || l0 + t < len;
+      float o[3][C];
 #pragma unroll
-  for (int t = T - 1; t >= 0; --t) {
-    const bool on = !ragged || l0 + t < len;
-    float o[3][C];
+      for (int c = 0; c < C; ++c) {
+        const bool ct = RST && __float_as_uint(A[t][c]) == kResetA;
+        // a itself, also where the transform holds the mark of a document start
+        const float at = RST ? __builtin_amdgcn_exp2f(beta2[c] * gr[t][c]) : A[t][c];
+        const float r = gr[t][c], i = gi[t][c], g = mu[c] + gg[t].get(c);
+        const float prev = ct ? 0.0f : bb[t][c];
+        const float ix = i * uu[t][2].get(c), gx = im[t][c] < kNoInput ? g * __builtin_amdgcn_rcpf(im[t][c]) : 0.0f;
+        const float ga = g * at;
+        const float dla = ga * fmaf(-ix * at, im[t][c], prev);
+        dl[c] = on ? fmaf(dla, r, dl[c]) : dl[c];
+        o[0][c] = on ? dla * (0.6931471805599453f * beta2[c]) * fmaf(-r, r, r) : 0.0f;
+        o[1][c] = on ? gx * (ix * (1.0f - i)) : 0.0f;
+        o[2][c] = on ? gx * i : 0.0f;
+        mu[c] = ct ? 0.0f : (on ? ga : mu[c]);
+      }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const GateVal v = gv[t][c];
-      const float xv = uu[t][2].get(c), g = mu[c] + dh[t][c];
-      const bool cut = RST && __float_as_uint(A[t][c]) == kResetA;
-      const float prev = cut ? 0.0f : bb[t][c];
-      const float ix = v.i * xv, gm = g * v.m;
-      const float dla = g * v.a * fmaf(-ix * v.a, v.im, prev);
-      dl[c] = on ? fmaf(dla, v.r, dl[c]) : dl[c];
-      o[0][c] = on ? dla * beta[c] * fmaf(-v.r, v.r, v.r) : 0.0f;
-      o[1][c] = on ? gm * (ix * (1.0f - v.i)) : 0.0f;
-      o[2][c] = on ? gm * v.i : 0.0f;
-      mu[c] = cut ? 0.0f : (on ? v.a * g : mu[c]);
+      for (int g = 0; g < 3; ++g)
+        buf_st<UT, C, kBufNT>(rdu, vu0 + t * ustep, static_cast<uint32_t>(g) * gstep, o[g]);
     }
-#pragma unroll
-    for (int g = 0; g < 3; ++g)
-      buf_st<UT, C, kBufNT>(rdu, vu0 + t * ustep, static_cast<uint32_t>(g) * gstep, o[g]);
-  }
-  if (p.dh0 && dv && l0 == 0) st_f32<C>(p.dh0 + static_cast<long long>(b) * p.D + d0, mu);
-  if (p.dl_part) {  // summed over the lane groups in order
+  };
+  if (ragged) put_out(std::false_type{});
+  else put_out(std::true_type{});
+  if (p.dl_part) {  // the lane groups' sums of dlog a r, added in order
 #pragma unroll
     for (int c = 0; c < C; ++c) s_dl[wave * LL + ll][ld * C + c] = dl[c];
     __syncthreads();
-    if (wave == 0 && ll == 0 && dv) {
-      float s[C];
+    if (wave == 0 && lane < CW && dt0 + lane < p.D) {
+      float v = 0.0f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) s[c] = 0.0f;
-      for (int k = 0; k < NSEG; ++k)
-#pragma unroll
-        for (int c = 0; c < C; ++c) s[c] += s_dl[k][ld * C + c];
-      st_f32<C>(p.dl_part + (static_cast<long long>(chunk) * p.B + b) * p.D + d0, s);
+      for (int k = 0; k < NSEG; ++k) v += s_dl[k][lane];
+      p.dl_part[(static_cast<long long>(chunk) * p.B + b) * p.D + dt0 + lane] = v;
     }
   }
 }
@@ -647,8 +703,8 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const UT* u, const floa
   ld_f32<C>(sp, sv);
 #pragma unroll
   for (int q = 0; q < C; ++q) {
-    const GateVal g = gate_values(ur.get(q), ui.get(q), -1.4426950408889634f * c * softplus(lv[q]));
-    sv[q] = fmaf(g.a, sv[q], g.m * (g.i * ux.get(q)));
+    const GateVal g = gate_values(ur.get(q), ui.get(q), decay_log2(lv[q], c));
+    sv[q] = fmaf(g.a, sv[q], __builtin_amdgcn_sqrtf(g.v) * (g.i * ux.get(q)));
     o[q] = live ? sv[q] : 0.0f;
   }
   if (live) st_f32<C>(sp, sv);

@@ -59,28 +59,41 @@ int pick_c(int cmax, int D, size_t es, std::initializer_list<const void*> typed,
 // ---------------------------------------------------------------------------
 // gated scan
 
-// Launch shapes: C channels per lane, T steps per lane, LL lane groups; 8 waves
+// Launch shapes: C channels per lane, T steps per lane, LL lane groups, W
+// waves, OCC waves per SIMD that the registers must allow
 template <class UT, int C> struct ScanShape;
-template <> struct ScanShape<bf16, 4> { static constexpr int T = 8, LL = 4; };
-template <> struct ScanShape<bf16, 2> { static constexpr int T = 16, LL = 2; };
-template <> struct ScanShape<bf16, 1> { static constexpr int T = 32, LL = 1; };
-template <> struct ScanShape<float, 2> { static constexpr int T = 8, LL = 4; };
-template <> struct ScanShape<float, 1> { static constexpr int T = 16, LL = 2; };
-template <int C> struct AdjShape;
-template <> struct AdjShape<2> { static constexpr int T = 8, LL = 2; };
-template <> struct AdjShape<1> { static constexpr int T = 16, LL = 1; };
-constexpr int kWaves = 8;
-constexpr int kScanChunk = 256;
-static_assert(kWaves * AdjShape<2>::T * AdjShape<2>::LL == kGatedSave &&
-              kWaves * AdjShape<1>::T * AdjShape<1>::LL == kGatedSave, "adjoint chunk");
+template <> struct ScanShape<bf16, 4> { static constexpr int T = 8, LL = 4, W = 8, OCC = 4; };
+template <> struct ScanShape<bf16, 2> { static constexpr int T = 16, LL = 2, W = 8, OCC = 4; };
+template <> struct ScanShape<bf16, 1> { static constexpr int T = 32, LL = 1, W = 8, OCC = 4; };
+template <> struct ScanShape<float, 2> { static constexpr int T = 8, LL = 4, W = 8, OCC = 4; };
+template <> struct ScanShape<float, 1> { static constexpr int T = 16, LL = 2, W = 8, OCC = 4; };
+template <class UT, int C> struct AdjShape;
+template <class UT> struct AdjShape<UT, 2> { static constexpr int T = 6, LL = 2, W = 8, OCC = 4; };
+template <class UT> struct AdjShape<UT, 1> { static constexpr int T = 12, LL = 1, W = 8, OCC = 4; };
 
-int scan_cw(int dtype, int C, bool adj) {
-  if (adj) return C == 2 ? 64 / AdjShape<2>::LL * 2 : 64 / AdjShape<1>::LL;
-  if (dtype == PARARNN_BF16)
-    return C == 4 ? 64 / ScanShape<bf16, 4>::LL * 4 : C == 2 ? 64 / ScanShape<bf16, 2>::LL * 2 : 64;
-  return C == 2 ? 64 / ScanShape<float, 2>::LL * 2 : 64 / ScanShape<float, 1>::LL;
+struct ScanGeo {
+  int chunk, cw;
+};
+template <class K, int C> constexpr ScanGeo geo_of() { return {K::T * K::LL * K::W, 64 / K::LL * C}; }
+constexpr int scan_cmax(int dtype, bool adj) { return adj ? 2 : dtype == PARARNN_BF16 ? 4 : 2; }
+ScanGeo scan_geo(int dtype, int C, bool adj) {
+  const bool h = dtype == PARARNN_BF16;
+  if (adj) {
+    if (C == 2) return h ? geo_of<AdjShape<bf16, 2>, 2>() : geo_of<AdjShape<float, 2>, 2>();
+    return h ? geo_of<AdjShape<bf16, 1>, 1>() : geo_of<AdjShape<float, 1>, 1>();
+  }
+  if (C == 4) return geo_of<ScanShape<bf16, 4>, 4>();
+  if (C == 2) return h ? geo_of<ScanShape<bf16, 2>, 2>() : geo_of<ScanShape<float, 2>, 2>();
+  return h ? geo_of<ScanShape<bf16, 1>, 1>() : geo_of<ScanShape<float, 1>, 1>();
 }
-int scan_cmax(int dtype, bool adj) { return adj ? 2 : dtype == PARARNN_BF16 ? 4 : 2; }
+constexpr int kMaxScanChunk = 512;
+
+// Chunks per group (chunk_carry): with many tiles per chunk row the chunk
+// before has long finished when this one asks, and plain hand-over from chunk
+// to chunk is the least work; with few, the chain of waits counts.
+int gated_group(long long tiles_per_row) {
+  return tiles_per_row >= 64 ? 1 : tiles_per_row >= 32 ? 2 : tiles_per_row >= 16 ? 4 : kMaxGroup;
+}
 
 struct GatedLayout {
   size_t ctr = 0, carry = 0, agg = 0, clear_end = 0, part = 0, total = 0;
@@ -89,11 +102,11 @@ struct GatedLayout {
 
 GatedLayout gated_layout(const pararnn_gated_opts* o, bool adj, int C) {
   GatedLayout y;
-  const int chunk = adj ? kGatedSave : kScanChunk, cw = scan_cw(o->dtype, C, adj);
-  y.nchunks = static_cast<int>(ceil_div(o->L, chunk));
-  y.ntiles_d = static_cast<int>(ceil_div(o->D, cw));
-  const size_t slots = static_cast<size_t>(o->B) * y.ntiles_d * cw;
-  y.group = 8;
+  const ScanGeo g = scan_geo(o->dtype, C, adj);
+  y.nchunks = static_cast<int>(ceil_div(o->L, g.chunk));
+  y.ntiles_d = static_cast<int>(ceil_div(o->D, g.cw));
+  const size_t slots = static_cast<size_t>(o->B) * y.ntiles_d * g.cw;
+  y.group = gated_group(static_cast<long long>(o->B) * y.ntiles_d);
   size_t off = 0;
   if (y.nchunks > 1) {
     off = round_up(sizeof(uint32_t));
@@ -112,15 +125,15 @@ GatedLayout gated_layout(const pararnn_gated_opts* o, bool adj, int C) {
 bool gated_ok(const pararnn_gated_opts* o, bool adj) {
   if (!o || o->B < 1 || o->L < 1 || o->D < 1) return false;
   if (!(o->c > 0.0f) || !isfinite(o->c)) return false;
-  if (o->L > 2147483647 - 2 * kScanChunk) return false;  // step numbers of a last partial chunk
+  if (o->L > 2147483647 - 2 * kMaxScanChunk) return false;  // step numbers of a last partial chunk
   if (static_cast<double>(o->B) * o->L * o->D * 12 > 9.0e18) return false;
   for (int C = 1; C <= scan_cmax(o->dtype, adj); C *= 2) {
-    const double wgs = static_cast<double>(o->B) * ceil_div(o->D, scan_cw(o->dtype, C, adj)) *
-                       ceil_div(o->L, adj ? kGatedSave : kScanChunk);
+    const ScanGeo g = scan_geo(o->dtype, C, adj);
+    const double wgs = static_cast<double>(o->B) * ceil_div(o->D, g.cw) * ceil_div(o->L, g.chunk);
     if (wgs > 2.0e9) return false;
   }
   // one chunk is addressed with 32-bit offsets below 2^31
-  return static_cast<double>(kScanChunk) * 3 * o->D * 4 < 2147483648.0;
+  return static_cast<double>(kMaxScanChunk) * 3 * o->D * 4 < 2147483648.0;
 }
 bool dtype_ok(int dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF16; }
 
@@ -130,16 +143,16 @@ int launch_gated(const GatedArgs& a, bool adj, hipStream_t s) {
   const GatedArgs& b = a;
   if (adj) {
     if constexpr (C <= 2) {
-      using K = AdjShape<C>;
-      return launch(gated_adjoint_kernel<UT, C, K::T, kWaves, K::LL, 2, RST>, grid, 64 * kWaves, s, b);
+      using K = AdjShape<UT, C>;
+      return launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST>, grid, 64 * K::W, s, b);
     }
     return PARARNN_EUNSUPPORTED;
   }
   if constexpr (C == 4 && sizeof(UT) == 4) return PARARNN_EUNSUPPORTED;
   else {
     using K = ScanShape<UT, C>;
-    static_assert(K::T * K::LL * kWaves == kScanChunk, "chunk");
-    return launch(gated_scan_kernel<UT, C, K::T, kWaves, K::LL, 4, RST>, grid, 64 * kWaves, s, b);
+    static_assert(K::T * K::LL * K::W <= kMaxScanChunk && kGatedSave % K::T == 0, "chunk");
+    return launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST>, grid, 64 * K::W, s, b);
   }
 }
 template <class UT>
