@@ -41,6 +41,7 @@ struct GatedArgs {
   void* du;                 // [B][L][3][D]
   float* dh0;               // [B][D] or nullptr
   float* dl_part;           // [nchunks][B][D] partial sums of dlog a r, or nullptr
+  float* dlam;              // [D], where there is one partial sum per channel
   unsigned long long* carry;  // [ngroups][slots] states at the groups' starts
   unsigned long long* agg;    // [nchunks][2][slots] chunk transforms
   unsigned int* ctr;        // [0] ticket
@@ -128,6 +129,11 @@ struct Lin {
   }
 };
 
+// Parked values are read back, not kept in registers after all: volatile
+__device__ __forceinline__ f32x4 read_back(const f32x4* p) {
+  return *(const volatile __attribute__((address_space(3))) f32x4*)p;
+}
+
 // The carry into a chunk. Chunks (counted in scan order) form groups of
 // `group` <= kMaxGroup. A chunk publishes its own transform as soon as it has
 // it, except the last of a group, which publishes the state at its end: the
@@ -189,22 +195,23 @@ __device__ __forceinline__ float chunk_carry(const GatedArgs& p, long long slots
 // A workgroup covers LD * C channels (LD = 64 / LL lanes along D) and
 // CL = W * LL * T steps: T steps in series per lane, a shuffle scan over the
 // LL lane groups, an LDS scan over the W waves, chunk_carry over the chunks.
+// ONE: the whole sequence is one chunk (no ticket, no carry).
 // The first wave takes the carry. It parks its steps in workgroup memory
 // meanwhile: the words it polls would otherwise cost every wave registers.
-template <class UT, int C, int T, int W, int LL, int OCC, bool RST>
+template <class UT, int C, int T, int W, int LL, int OCC, bool RST, bool ONE>
 __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs p) {
   constexpr int LD = 64 / LL, CW = LD * C, CL = W * LL * T;
   static_assert(CW <= 64, "one wave takes the carry, a channel per lane");
   constexpr int NP = 2 * T * C / 4;  // 16-byte pieces that a lane parks
   static_assert(T * C % 4 == 0, "whole pieces");
   __shared__ float s_A[W][CW], s_b[W][CW], s_start[W][CW], s_beta[CW];
-  __shared__ f32x4 s_park[NP][64];
+  __shared__ f32x4 s_park[ONE ? 1 : NP][64];
   __shared__ unsigned int s_ticket;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   unsigned int ticket = blockIdx.x;
-  if (p.nchunks > 1) {
+  if (!ONE && p.nchunks > 1) {
     if (tid == 0) s_ticket = atomicAdd(p.ctr, 1u);
     __syncthreads();
     ticket = __builtin_amdgcn_readfirstlane(s_ticket);
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
     float* flat_A = &A[0][0];
     float* flat_x = &x[0][0];
 #pragma unroll
-    for (int i = 0; i < NP / 2; ++i) {
+    for (int i = 0; i < (ONE ? 0 : NP / 2); ++i) {
       s_park[i][lane] = f32x4{flat_A[4 * i], flat_A[4 * i + 1], flat_A[4 * i + 2], flat_A[4 * i + 3]};
       s_park[NP / 2 + i][lane] = f32x4{flat_x[4 * i], flat_x[4 * i + 1], flat_x[4 * i + 2], flat_x[4 * i + 3]};
     }
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
       const bool in = dt0 + lane < p.D;
       const long long bd = static_cast<long long>(b) * p.D + dt0 + lane;
       float v[1] = {in && p.h0 ? p.h0[bd] : 0.0f};
-      if (p.nchunks > 1) {
+      if constexpr (!ONE) {
         Lin<1, RST> tot;
         tot.set_identity();
 #pragma unroll
@@ -335,10 +342,8 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
       if (p.hT && in && chunk == p.nchunks - 1) p.hT[bd] = v[0];
     }
 #pragma unroll
-    for (int i = 0; i < NP / 2; ++i) {
-      // volatile: read back, not kept in registers after all
-      const f32x4 va = *static_cast<const volatile f32x4*>(&s_park[i][lane]);
-      const f32x4 vx = *static_cast<const volatile f32x4*>(&s_park[NP / 2 + i][lane]);
+    for (int i = 0; i < (ONE ? 0 : NP / 2); ++i) {
+      const f32x4 va = read_back(&s_park[i][lane]), vx = read_back(&s_park[NP / 2 + i][lane]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         flat_A[4 * i + k] = va[k];
@@ -384,24 +389,24 @@ __device__ __forceinline__ void keep_packed(URaw<float, C>&) {}
 // The adjoint of one chunk of CL = kGatedSave steps: a scan forward from the
 // saved state for the h_{t-1}, and the scan backward for mu, on the same
 // lanes.
-template <class UT, int C, int T, int W, int LL, int OCC, bool RST>
+template <class UT, int C, int T, int W, int LL, int OCC, bool RST, bool ONE>
 __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedArgs p) {
   constexpr int LD = 64 / LL, CW = LD * C, CL = W * LL * T, NSEG = W * LL;
-  static_assert(CL == kGatedSave, "a chunk starts at a saved state");
+  static_assert(ONE || CL == kGatedSave, "a chunk starts at a saved state");
   static_assert(CW <= 64, "one wave takes the carry, a channel per lane");
   // transforms of the waves, forward (A, b) and backward (B, m); what enters them
   __shared__ float s_A[W][CW], s_b[W][CW], s_B[W][CW], s_m[W][CW], s_h[W][CW], s_mu[W][CW], s_beta[CW];
   __shared__ float s_dl[NSEG][CW];
   constexpr int NP = 5 * T * C / 4;  // 16-byte pieces that a lane of the first wave parks
   static_assert(T * C % 4 == 0, "whole pieces");
-  __shared__ f32x4 s_park[NP][64];
+  __shared__ f32x4 s_park[ONE ? 1 : NP][64];
   __shared__ Lin<C, RST> s_fx[W][LL > 1 ? 64 : 1], s_bx[W][LL > 1 ? 64 : 1];
   __shared__ unsigned int s_ticket;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   unsigned int ticket = blockIdx.x;
-  if (p.nchunks > 1) {
+  if (!ONE && p.nchunks > 1) {
     if (tid == 0) s_ticket = atomicAdd(p.ctr, 1u);
     __syncthreads();
     ticket = __builtin_amdgcn_readfirstlane(s_ticket);
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
-      for (int i = 0; i < N4; ++i)
+      for (int i = 0; i < (ONE ? 0 : N4); ++i)
         s_park[k * N4 + i][lane] = f32x4{flat[k][4 * i], flat[k][4 * i + 1], flat[k][4 * i + 2], flat[k][4 * i + 3]};
     if (lane < CW) {
       const bool in = dt0 + lane < p.D;
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
         e.after(tot);
         tot = e;
       }
-      if (p.nchunks > 1)
+      if constexpr (!ONE)
         v[0] = chunk_carry<RST>(p, static_cast<long long>(p.B) * p.ntiles_d * CW,
                                 static_cast<long long>(tile) * CW + lane, rchunk, tot, v[0]);
 #pragma unroll
@@ -576,9 +581,8 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
-      for (int i = 0; i < N4; ++i) {
-        // volatile: read back, not kept in registers after all
-        const f32x4 v = *static_cast<const volatile f32x4*>(&s_park[k * N4 + i][lane]);
+      for (int i = 0; i < (ONE ? 0 : N4); ++i) {
+        const f32x4 v = read_back(&s_park[k * N4 + i][lane]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) flat[k][4 * i + q] = v[q];
       }
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
   };
   if (ragged) put_out(std::false_type{});
   else put_out(std::true_type{});
-  if (p.dl_part) {  // the lane groups' sums of dlog a r, added in order
+  if (p.dl_part || p.dlam) {  // the lane groups' sums of dlog a r, added in order
 #pragma unroll
     for (int c = 0; c < C; ++c) s_dl[wave * LL + ll][ld * C + c] = dl[c];
     __syncthreads();
@@ -643,7 +647,9 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
       float v = 0.0f;
 #pragma unroll
       for (int k = 0; k < NSEG; ++k) v += s_dl[k][lane];
-      p.dl_part[(static_cast<long long>(chunk) * p.B + b) * p.D + dt0 + lane] = v;
+      const int d = dt0 + lane;
+      if (p.dlam) p.dlam[d] = -p.c * sigm(p.lam[d]) * v;
+      else p.dl_part[(static_cast<long long>(chunk) * p.B + b) * p.D + d] = v;
     }
   }
 }

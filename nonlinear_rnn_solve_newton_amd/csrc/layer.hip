@@ -62,31 +62,42 @@ int pick_c(int cmax, int D, size_t es, std::initializer_list<const void*> typed,
 // Launch shapes: C channels per lane, T steps per lane, LL lane groups, W
 // waves, OCC waves per SIMD that the registers must allow
 template <class UT, int C> struct ScanShape;
-template <> struct ScanShape<bf16, 4> { static constexpr int T = 8, LL = 4, W = 8, OCC = 4; };
-template <> struct ScanShape<bf16, 2> { static constexpr int T = 16, LL = 2, W = 8, OCC = 4; };
-template <> struct ScanShape<bf16, 1> { static constexpr int T = 32, LL = 1, W = 8, OCC = 4; };
+template <> struct ScanShape<bf16, 2> { static constexpr int T = 12, LL = 2, W = 8, OCC = 5; };
+template <> struct ScanShape<bf16, 1> { static constexpr int T = 24, LL = 1, W = 8, OCC = 4; };
 template <> struct ScanShape<float, 2> { static constexpr int T = 8, LL = 4, W = 8, OCC = 4; };
 template <> struct ScanShape<float, 1> { static constexpr int T = 16, LL = 2, W = 8, OCC = 4; };
 template <class UT, int C> struct AdjShape;
 template <class UT> struct AdjShape<UT, 2> { static constexpr int T = 6, LL = 2, W = 8, OCC = 4; };
 template <class UT> struct AdjShape<UT, 1> { static constexpr int T = 12, LL = 1, W = 8, OCC = 4; };
 
+// Small problems, where latency counts: the whole sequence in one workgroup of
+// 16 waves, so that there is no carry between chunks, nothing to clear and one
+// launch per pass. It reads only 4 C channels of a row.
+struct SmallShape { static constexpr int T = 4, LL = 16, W = 16, OCC = 4; };
+constexpr int kSmallSteps = SmallShape::T * SmallShape::LL * SmallShape::W;
+// B * D up to which it is taken: at 64 channels of 1024 steps 10 and 11 us per pass against 14 and
+// 18, at 1024 channels 20 and 32 against 14 and 18 (every line of HBM is read by 8 workgroups)
+constexpr int kSmallChannels = 256;
+bool gated_small(const pararnn_gated_opts* o) {
+  return o->L <= kSmallSteps && static_cast<long long>(o->B) * o->D <= kSmallChannels;
+}
+
 struct ScanGeo {
   int chunk, cw;
 };
 template <class K, int C> constexpr ScanGeo geo_of() { return {K::T * K::LL * K::W, 64 / K::LL * C}; }
-constexpr int scan_cmax(int dtype, bool adj) { return adj ? 2 : dtype == PARARNN_BF16 ? 4 : 2; }
-ScanGeo scan_geo(int dtype, int C, bool adj) {
-  const bool h = dtype == PARARNN_BF16;
+constexpr int kScanMaxC = 2;
+ScanGeo scan_geo(const pararnn_gated_opts* o, int C, bool adj) {
+  const bool h = o->dtype == PARARNN_BF16;
+  if (gated_small(o)) return C == 2 ? geo_of<SmallShape, 2>() : geo_of<SmallShape, 1>();
   if (adj) {
     if (C == 2) return h ? geo_of<AdjShape<bf16, 2>, 2>() : geo_of<AdjShape<float, 2>, 2>();
     return h ? geo_of<AdjShape<bf16, 1>, 1>() : geo_of<AdjShape<float, 1>, 1>();
   }
-  if (C == 4) return geo_of<ScanShape<bf16, 4>, 4>();
   if (C == 2) return h ? geo_of<ScanShape<bf16, 2>, 2>() : geo_of<ScanShape<float, 2>, 2>();
   return h ? geo_of<ScanShape<bf16, 1>, 1>() : geo_of<ScanShape<float, 1>, 1>();
 }
-constexpr int kMaxScanChunk = 512;
+constexpr int kMaxScanChunk = kSmallSteps;
 
 // Chunks per group (chunk_carry): with many tiles per chunk row the chunk
 // before has long finished when this one asks, and plain hand-over from chunk
@@ -98,15 +109,17 @@ int gated_group(long long tiles_per_row) {
 struct GatedLayout {
   size_t ctr = 0, carry = 0, agg = 0, clear_end = 0, part = 0, total = 0;
   int nchunks = 0, ntiles_d = 0, group = 1;
+  bool direct = false;  // a channel's steps are all in one workgroup: it writes dlam itself
 };
 
 GatedLayout gated_layout(const pararnn_gated_opts* o, bool adj, int C) {
   GatedLayout y;
-  const ScanGeo g = scan_geo(o->dtype, C, adj);
+  const ScanGeo g = scan_geo(o, C, adj);
   y.nchunks = static_cast<int>(ceil_div(o->L, g.chunk));
   y.ntiles_d = static_cast<int>(ceil_div(o->D, g.cw));
   const size_t slots = static_cast<size_t>(o->B) * y.ntiles_d * g.cw;
   y.group = gated_group(static_cast<long long>(o->B) * y.ntiles_d);
+  y.direct = adj && y.nchunks * static_cast<long long>(o->B) == 1;
   size_t off = 0;
   if (y.nchunks > 1) {
     off = round_up(sizeof(uint32_t));
@@ -117,8 +130,8 @@ GatedLayout gated_layout(const pararnn_gated_opts* o, bool adj, int C) {
   }
   y.clear_end = off;
   y.part = off;
-  if (adj) off = round_up(off + sizeof(float) * y.nchunks * static_cast<size_t>(o->B) * o->D);
-  y.total = off > kAlign ? off : kAlign;
+  if (adj && !y.direct) off = round_up(off + sizeof(float) * y.nchunks * static_cast<size_t>(o->B) * o->D);
+  y.total = off;
   return y;
 }
 
@@ -127,8 +140,8 @@ bool gated_ok(const pararnn_gated_opts* o, bool adj) {
   if (!(o->c > 0.0f) || !isfinite(o->c)) return false;
   if (o->L > 2147483647 - 2 * kMaxScanChunk) return false;  // step numbers of a last partial chunk
   if (static_cast<double>(o->B) * o->L * o->D * 12 > 9.0e18) return false;
-  for (int C = 1; C <= scan_cmax(o->dtype, adj); C *= 2) {
-    const ScanGeo g = scan_geo(o->dtype, C, adj);
+  for (int C = 1; C <= kScanMaxC; C *= 2) {
+    const ScanGeo g = scan_geo(o, C, adj);
     const double wgs = static_cast<double>(o->B) * ceil_div(o->D, g.cw) * ceil_div(o->L, g.chunk);
     if (wgs > 2.0e9) return false;
   }
@@ -138,34 +151,34 @@ bool gated_ok(const pararnn_gated_opts* o, bool adj) {
 bool dtype_ok(int dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF16; }
 
 template <class UT, int C, bool RST>
-int launch_gated(const GatedArgs& a, bool adj, hipStream_t s) {
+int launch_gated(const GatedArgs& a, bool adj, bool small, hipStream_t s) {
   const long long grid = static_cast<long long>(a.B) * a.ntiles_d * a.nchunks;
   const GatedArgs& b = a;
+  if (small) {
+    using K = SmallShape;
+    return adj ? launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, true>, grid, 64 * K::W, s, b)
+               : launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, true>, grid, 64 * K::W, s, b);
+  }
   if (adj) {
-    if constexpr (C <= 2) {
-      using K = AdjShape<UT, C>;
-      return launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST>, grid, 64 * K::W, s, b);
-    }
-    return PARARNN_EUNSUPPORTED;
+    using K = AdjShape<UT, C>;
+    return launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, false>, grid, 64 * K::W, s, b);
   }
-  if constexpr (C == 4 && sizeof(UT) == 4) return PARARNN_EUNSUPPORTED;
-  else {
-    using K = ScanShape<UT, C>;
-    static_assert(K::T * K::LL * K::W <= kMaxScanChunk && kGatedSave % K::T == 0, "chunk");
-    return launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST>, grid, 64 * K::W, s, b);
-  }
+  using K = ScanShape<UT, C>;
+  static_assert(K::T * K::LL * K::W <= kMaxScanChunk && kGatedSave % K::T == 0, "chunk");
+  // document starts take registers of their own
+  return launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, RST ? 4 : K::OCC, RST, false>, grid, 64 * K::W, s, b);
 }
 template <class UT>
-int launch_gated_c(int C, const GatedArgs& a, bool adj, hipStream_t s) {
+int launch_gated_c(int C, const GatedArgs& a, bool adj, bool small, hipStream_t s) {
   const bool r = a.reset != nullptr;
-  if (C == 4) return r ? launch_gated<UT, 4, true>(a, adj, s) : launch_gated<UT, 4, false>(a, adj, s);
-  if (C == 2) return r ? launch_gated<UT, 2, true>(a, adj, s) : launch_gated<UT, 2, false>(a, adj, s);
-  return r ? launch_gated<UT, 1, true>(a, adj, s) : launch_gated<UT, 1, false>(a, adj, s);
+  if (C == 2) return r ? launch_gated<UT, 2, true>(a, adj, small, s) : launch_gated<UT, 2, false>(a, adj, small, s);
+  return r ? launch_gated<UT, 1, true>(a, adj, small, s) : launch_gated<UT, 1, false>(a, adj, small, s);
 }
 
 int gated(bool adj, GatedArgs& a, float* dlam, void* ws, size_t ws_bytes, const pararnn_gated_opts* o, int C,
           hipStream_t stream) {
   const GatedLayout y = gated_layout(o, adj, C);
+  if (y.total && !ws) return PARARNN_EINVAL;
   if (ws_bytes < y.total) return PARARNN_EWORKSPACE;
   if (!aligned(ws, kAlign)) return PARARNN_EUNSUPPORTED;
   char* w = static_cast<char*>(ws);
@@ -174,7 +187,8 @@ int gated(bool adj, GatedArgs& a, float* dlam, void* ws, size_t ws_bytes, const 
   a.carry = reinterpret_cast<unsigned long long*>(w + y.carry);
   a.agg = reinterpret_cast<unsigned long long*>(w + y.agg);
   a.ctr = reinterpret_cast<unsigned int*>(w + y.ctr);
-  if (dlam) a.dl_part = reinterpret_cast<float*>(w + y.part);
+  if (dlam && y.direct) a.dlam = dlam;
+  else if (dlam) a.dl_part = reinterpret_cast<float*>(w + y.part);
   a.B = o->B;
   a.L = o->L;
   a.D = o->D;
@@ -186,9 +200,10 @@ int gated(bool adj, GatedArgs& a, float* dlam, void* ws, size_t ws_bytes, const 
     const int rc = clear(w, y.clear_end, stream);
     if (rc) return rc;
   }
-  const int rc = o->dtype == PARARNN_BF16 ? launch_gated_c<bf16>(C, a, adj, stream)
-                                          : launch_gated_c<float>(C, a, adj, stream);
-  if (rc || !dlam) return rc;
+  const bool small = gated_small(o);
+  const int rc = o->dtype == PARARNN_BF16 ? launch_gated_c<bf16>(C, a, adj, small, stream)
+                                          : launch_gated_c<float>(C, a, adj, small, stream);
+  if (rc || !dlam || y.direct) return rc;
   return launch(column_sum_kernel, ceil_div(o->D, kSumCols), kSumCols * kSumGroups, stream,
                 static_cast<const float*>(a.dl_part), dlam, static_cast<long long>(y.nchunks) * o->B,
                 static_cast<int>(o->D), a.lam, o->c);
@@ -303,14 +318,17 @@ int launch_matmul_rows(const MatmulArgs& p, int rows, bool direct, hipStream_t s
 
 using namespace pararnn;
 
-extern "C" size_t pararnn_gated_workspace_bytes(int32_t adjoint, const pararnn_gated_opts* o) {
-  if ((adjoint != 0 && adjoint != 1) || !gated_ok(o, adjoint != 0) || !dtype_ok(o->dtype)) return 0;
+extern "C" int32_t pararnn_gated_workspace_bytes(int32_t adjoint, const pararnn_gated_opts* o, size_t* bytes) {
+  if ((adjoint != 0 && adjoint != 1) || !bytes || !gated_ok(o, adjoint != 0)) return PARARNN_EINVAL;
+  if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
   size_t n = 0;
-  for (int C = 1; C <= scan_cmax(o->dtype, adjoint != 0); C *= 2) {
+  for (int C = 1; C <= kScanMaxC; C *= 2) {
+    if (o->D % C) continue;
     const size_t t = gated_layout(o, adjoint != 0, C).total;
     n = t > n ? t : n;
   }
-  return n;
+  *bytes = n;
+  return PARARNN_OK;
 }
 
 extern "C" int32_t pararnn_gated_saved_rows(int32_t L) {
@@ -320,10 +338,10 @@ extern "C" int32_t pararnn_gated_saved_rows(int32_t L) {
 extern "C" int32_t pararnn_gated_scan(const void* u, const float* lam, const float* h0, void* h, float* hT,
                                       float* saved, void* ws, size_t ws_bytes, const pararnn_gated_opts* o,
                                       void* stream) {
-  if (!gated_ok(o, false) || !u || !lam || !h || !ws) return PARARNN_EINVAL;
+  if (!gated_ok(o, false) || !u || !lam || !h) return PARARNN_EINVAL;
   if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
   const size_t es = o->dtype == PARARNN_BF16 ? 2 : 4;
-  const int C = pick_c(scan_cmax(o->dtype, false), o->D, es, {u, h}, {hT, saved});
+  const int C = pick_c(kScanMaxC, o->D, es, {u, h}, {hT, saved});
   if (!C || !aligned(lam, 4) || !aligned(h0, 4) || !aligned(o->lengths, 4)) return PARARNN_EUNSUPPORTED;
   GatedArgs a;
   memset(&a, 0, sizeof(a));
@@ -339,10 +357,10 @@ extern "C" int32_t pararnn_gated_scan(const void* u, const float* lam, const flo
 extern "C" int32_t pararnn_gated_scan_adjoint(const void* u, const float* lam, const float* saved, const void* dh,
                                               const float* dhT, void* du, float* dlam, float* dh0, void* ws,
                                               size_t ws_bytes, const pararnn_gated_opts* o, void* stream) {
-  if (!gated_ok(o, true) || !u || !lam || !saved || !dh || !du || !ws) return PARARNN_EINVAL;
+  if (!gated_ok(o, true) || !u || !lam || !saved || !dh || !du) return PARARNN_EINVAL;
   if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
   const size_t es = o->dtype == PARARNN_BF16 ? 2 : 4;
-  const int C = pick_c(scan_cmax(o->dtype, true), o->D, es, {u, dh, du}, {saved, dh0});
+  const int C = pick_c(kScanMaxC, o->D, es, {u, dh, du}, {saved, dh0});
   if (!C || !aligned(lam, 4) || !aligned(dhT, 4) || !aligned(dlam, 4) || !aligned(o->lengths, 4))
     return PARARNN_EUNSUPPORTED;
   GatedArgs a;

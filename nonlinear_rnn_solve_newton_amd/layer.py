@@ -22,7 +22,7 @@ from typing import Optional
 
 import torch
 
-from .binding import BF16, F32, PKG, PararnnError, alloc_workspace, strerror
+from .binding import BF16, F32, PKG, PararnnError, strerror
 
 LIB_PATH = PKG / "libpararnn_layer.so"
 HEADER = PKG.parent / "include" / "pararnn_layer.h"
@@ -76,8 +76,8 @@ def lib():
         L = ctypes.CDLL(str(LIB_PATH))
         P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
         G = ctypes.POINTER(GatedOpts)
-        L.pararnn_gated_workspace_bytes.argtypes = [I32, G]
-        L.pararnn_gated_workspace_bytes.restype = SZ
+        L.pararnn_gated_workspace_bytes.argtypes = [I32, G, ctypes.POINTER(SZ)]
+        L.pararnn_gated_workspace_bytes.restype = I32
         L.pararnn_gated_saved_rows.argtypes = [I32]
         L.pararnn_gated_saved_rows.restype = I32
         L.pararnn_gated_scan.argtypes = [P, P, P, P, P, P, P, SZ, G, P]
@@ -104,15 +104,18 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _dev(t: Optional[torch.Tensor], name: str, dtype, shape, device):
-    """Checks an argument that may be None; dtype None takes any."""
+def _dev(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, device: torch.device):
+    """Checks an argument that may be None."""
     if t is None:
+        return
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise PararnnError(f"{name} must be a device tensor")
     if t.device != device:
         raise PararnnError(f"{name} must be on {device}, got {t.device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -150,13 +153,14 @@ def _launch(what: str, device: torch.device, *args):
 
 
 def _workspace(ws, need: int, device):
-    if need == 0:
-        raise PararnnError("invalid sizes or options")
+    """The workspace of a call and its size: the caller's, a new one, or none."""
     if ws is None:
-        return alloc_workspace(need, device)
+        if need == 0:
+            return None, 0
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     if not ws.is_cuda or ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
         raise PararnnError("ws must be a contiguous uint8 tensor on the inputs' device")
-    return ws
+    return ws, ws.numel()
 
 
 # ---------------------------------------------------------------------------
@@ -164,7 +168,12 @@ def _workspace(ws, need: int, device):
 
 @functools.lru_cache(maxsize=1024)
 def _gated_bytes(adjoint: int, B: int, L: int, D: int, dtype: int, c: float) -> int:
-    return lib().pararnn_gated_workspace_bytes(adjoint, ctypes.byref(GatedOpts(B, L, D, dtype, c, None, None)))
+    n = ctypes.c_size_t()
+    st = lib().pararnn_gated_workspace_bytes(adjoint, ctypes.byref(GatedOpts(B, L, D, dtype, c, None, None)),
+                                             ctypes.byref(n))
+    if st != 0:
+        raise PararnnError(f"pararnn_gated_workspace_bytes failed: {st} ({strerror(st)})")
+    return n.value
 
 
 @functools.lru_cache(maxsize=1024)
@@ -204,12 +213,12 @@ def gated_scan(u: torch.Tensor, lam: torch.Tensor, *, c: float = 8.0, h0: Option
         out = torch.empty(B, L, D, dtype=u.dtype, device=dev)
     else:
         _dev(out, "out", u.dtype, (B, L, D), dev)
-    ws = _workspace(ws, _gated_bytes(0, B, L, D, o.dtype, c), dev)
+    ws, nws = _workspace(ws, _gated_bytes(0, B, L, D, o.dtype, c), dev)
     hT = torch.empty(B, D, dtype=torch.float32, device=dev)
     saved = (torch.empty(_saved_rows(L), B, D, dtype=torch.float32, device=dev)
              if save else None)
     _launch("pararnn_gated_scan", dev, _ptr(u), _ptr(lam), _ptr(h0), _ptr(out), _ptr(hT), _ptr(saved), _ptr(ws),
-            ws.numel(), ctypes.byref(o))
+            nws, ctypes.byref(o))
     return {"h": out, "hT": hT, "saved": saved, "ws": ws}
 
 
@@ -230,12 +239,12 @@ def gated_scan_adjoint(u: torch.Tensor, lam: torch.Tensor, dh: torch.Tensor, sav
         du = torch.empty(B, L, 3, D, dtype=u.dtype, device=dev)
     else:
         _dev(du, "du", u.dtype, (B, L, 3, D), dev)
-    ws = _workspace(ws, _gated_bytes(1, B, L, D, o.dtype, c), dev)
+    ws, nws = _workspace(ws, _gated_bytes(1, B, L, D, o.dtype, c), dev)
     dlam = torch.empty(D, dtype=torch.float32, device=dev) if want_dlam else None
     dh0 = torch.empty(B, D, dtype=torch.float32, device=dev) if want_dh0 else None
     _launch("pararnn_gated_scan_adjoint", dev, _ptr(u), _ptr(lam), _ptr(saved), _ptr(dh), _ptr(dhT), _ptr(du),
-            _ptr(dlam), _ptr(dh0), _ptr(ws), ws.numel(), ctypes.byref(o))
-    return dict(du=du, dlam=dlam, dh0=dh0, ws=ws)
+            _ptr(dlam), _ptr(dh0), _ptr(ws), nws, ctypes.byref(o))
+    return {"du": du, "dlam": dlam, "dh0": dh0, "ws": ws}
 
 
 def gated_step(u: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *, c: float = 8.0,
@@ -268,6 +277,11 @@ def gated_step(u: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *, c: fl
 # ---------------------------------------------------------------------------
 # norm
 
+@functools.lru_cache(maxsize=1024)
+def _norm_bytes(N: int, D: int, dtype: int) -> int:
+    return lib().pararnn_norm_workspace_bytes(ctypes.byref(NormOpts(N, D, dtype, NORM_SAME, 0.0)))
+
+
 def norm_residual(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
                   scale_dtype: Optional[torch.dtype] = None) -> dict:
     """s = x + residual, y = s / sqrt(mean(s^2) + eps) * w over the last of the
@@ -298,7 +312,7 @@ def norm_residual(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.
     o = NormOpts(N, D, _DTYPE[x.dtype], out, eps)
     _launch("pararnn_norm_residual", dev, _ptr(x), _ptr(residual), _ptr(w), None if s is x else _ptr(s), _ptr(y),
             _ptr(scale), ctypes.byref(o))
-    return dict(y=y, s=s, scale=scale)
+    return {"y": y, "s": s, "scale": scale}
 
 
 def norm_residual_adjoint(s: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, *, ds: Optional[torch.Tensor] = None,
@@ -314,14 +328,17 @@ def norm_residual_adjoint(s: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, *,
     _dev(dy, "dy", s.dtype, (N, D), dev)
     _dev(ds, "ds", s.dtype, (N, D), dev)
     o = NormOpts(N, D, _DTYPE[s.dtype], NORM_SAME, eps)
-    dw = None
+    dw, nws = None, 0
     if want_dw:
-        ws = _workspace(ws, lib().pararnn_norm_workspace_bytes(ctypes.byref(o)), dev)
+        need = _norm_bytes(N, D, o.dtype)
+        if need == 0:
+            raise PararnnError("invalid sizes (norm_residual takes at most 16384 columns)")
+        ws, nws = _workspace(ws, need, dev)
         dw = torch.empty(D, dtype=torch.float32, device=dev)
     dx = torch.empty_like(s)
     _launch("pararnn_norm_residual_adjoint", dev, _ptr(s), _ptr(w), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw),
-            _ptr(ws), 0 if ws is None else ws.numel(), ctypes.byref(o))
-    return dict(dx=dx, dw=dw, ws=ws)
+            _ptr(ws), nws, ctypes.byref(o))
+    return {"dx": dx, "dw": dw, "ws": ws}
 
 
 # ---------------------------------------------------------------------------
@@ -373,7 +390,7 @@ def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Ten
     KB = -(-K // BLOCK)
     if not isinstance(sa, torch.Tensor) or sa.dtype not in _SCALE:
         raise PararnnError("sa must be float32 or float8_e8m0fnu")
-    _dev(sa, "sa", None, (KB, M), dev)
+    _dev(sa, "sa", sa.dtype, (KB, M), dev)
     if not isinstance(sw, torch.Tensor):
         raise PararnnError("sw must be a device tensor")
     rows = 1 if N > 1 and sw.shape == (N, KB) else BLOCK
