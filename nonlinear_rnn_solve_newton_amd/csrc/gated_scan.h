@@ -129,6 +129,24 @@ struct Lin {
   }
 };
 
+// The document starts among a lane's T steps, bit t for step t. The wave's
+// steps begin at l and are read a byte per lane; a step at or past len is none.
+template <int T, int LL, bool RST>
+__device__ __forceinline__ uint32_t document_starts(const GatedArgs& p, int b, int l, int len, int lane) {
+  static_assert(T <= 32 && T * LL <= 64, "a byte per lane");
+  if constexpr (RST) {
+    const bool in = lane < T * LL && l + lane < len;
+    const unsigned char v = in ? p.reset[static_cast<long long>(b) * p.L + l + lane] : 0;
+    const unsigned long long all = __ballot(v != 0);
+    return static_cast<uint32_t>(all >> (lane / (64 / LL) * T)) & static_cast<uint32_t>((1ull << T) - 1);
+  }
+  return 0u;
+}
+template <bool RST>
+__device__ __forceinline__ float marked(float a, uint32_t cuts, int t) {
+  return RST && (cuts >> t & 1u) ? __uint_as_float(kResetA) : a;
+}
+
 // Parked values are read back, not kept in registers after all: volatile
 __device__ __forceinline__ f32x4 read_back(const f32x4* p) {
   return *(const volatile __attribute__((address_space(3))) f32x4*)p;
@@ -243,12 +261,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
   for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int g = 0; g < 3; ++g) uu[t][g].load(ru, vu0 + t * ustep, static_cast<uint32_t>(g) * gstep);
-  bool cut[RST ? T : 1];  // document starts
-  if constexpr (RST) {
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      cut[t] = p.reset[static_cast<long long>(b) * p.L + min(l0 + t, p.L - 1)] != 0;
-  }
+  const uint32_t cuts = document_starts<T, LL, RST>(p, b, chunk * CL + wave * LL * T, len, lane);
   if (tid < CW) s_beta[tid] = decay_log2(p.lam[min(dt0 + tid, p.D - 1)], p.c);
   __syncthreads();
   float beta2[C];
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const GateVal g = gate_values(uu[t][0].get(c), uu[t][1].get(c), beta2[c]);
-      A[t][c] = RST && cut[t] ? __uint_as_float(kResetA) : g.a;
+      A[t][c] = g.a;
       x[t][c] = __builtin_amdgcn_sqrtf(g.v) * (g.i * uu[t][2].get(c));
     }
   if (ragged) {
@@ -282,7 +295,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
   for (int t = 0; t < T; ++t) {
     Lin<C, RST> e;
 #pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = A[t][c]; e.b[c] = x[t][c]; }
+    for (int c = 0; c < C; ++c) { e.A[c] = marked<RST>(A[t][c], cuts, t); e.b[c] = x[t][c]; }
     if (t) e.after(acc);
     acc = e;
   }
@@ -364,7 +377,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
     for (int t = 0; t < T; ++t) {
       Lin<C, RST> e;
 #pragma unroll
-      for (int c = 0; c < C; ++c) { e.A[c] = A[t][c]; e.b[c] = x[t][c]; }
+      for (int c = 0; c < C; ++c) { e.A[c] = marked<RST>(A[t][c], cuts, t); e.b[c] = x[t][c]; }
       e.apply(h);
       float o[C];
 #pragma unroll
@@ -442,12 +455,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
     for (int g = 0; g < 3; ++g) uu[t][g].load(ru, vu0 + t * ustep, static_cast<uint32_t>(g) * gstep);
     gg[t].load(rdh, vh0 + t * gstep, 0u);
   }
-  bool cut[RST ? T : 1];
-  if constexpr (RST) {
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-      cut[t] = p.reset[static_cast<long long>(b) * p.L + min(l0 + t, p.L - 1)] != 0;
-  }
+  const uint32_t cuts = document_starts<T, LL, RST>(p, b, chunk * CL + wave * LL * T, len, lane);
   if (tid < CW) s_beta[tid] = decay_log2(p.lam[min(dt0 + tid, p.D - 1)], p.c);
   __syncthreads();
   float beta2[C];
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
       gi[t][c] = g.i;
       // 1/m is kept finite (2^63 for v = 0): where v is 0, so are r or beta, and with them what 1/m multiplies
       im[t][c] = __builtin_amdgcn_rsqf(fmaxf(g.v, 1.17549435e-38f));
-      A[t][c] = RST && cut[t] ? __uint_as_float(kResetA) : g.a;
+      A[t][c] = g.a;
       bb[t][c] = g.v * im[t][c] * (g.i * uu[t][2].get(c));
     }
   }
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
   for (int t = 0; t < T; ++t) {
     Lin<C, RST> e;
 #pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = A[t][c]; e.b[c] = bb[t][c]; }
+    for (int c = 0; c < C; ++c) { e.A[c] = marked<RST>(A[t][c], cuts, t); e.b[c] = bb[t][c]; }
     if (t) e.after(fw);
     fw = e;
   }
@@ -498,9 +506,8 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
     Lin<C, RST> e;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const bool none = RST && __float_as_uint(A[t][c]) == kResetA;
-      e.A[c] = A[t][c];
-      e.b[c] = none ? 0.0f : A[t][c] * gg[t].get(c);
+      e.A[c] = marked<RST>(A[t][c], cuts, t);
+      e.b[c] = RST && (cuts >> t & 1u) ? 0.0f : A[t][c] * gg[t].get(c);
     }
     if (t < T - 1) e.after(bw);
     bw = e;
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
     Lin<C, RST> e;
     float prev[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) { e.A[c] = A[t][c]; e.b[c] = bb[t][c]; prev[c] = h[c]; }
+    for (int c = 0; c < C; ++c) { e.A[c] = marked<RST>(A[t][c], cuts, t); e.b[c] = bb[t][c]; prev[c] = h[c]; }
     e.apply(h);
 #pragma unroll
     for (int c = 0; c < C; ++c) bb[t][c] = prev[c];
@@ -618,9 +625,8 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
       float o[3][C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const bool ct = RST && __float_as_uint(A[t][c]) == kResetA;
-        // a itself, also where the transform holds the mark of a document start
-        const float at = RST ? __builtin_amdgcn_exp2f(beta2[c] * gr[t][c]) : A[t][c];
+        const bool ct = RST && (cuts >> t & 1u);
+        const float at = A[t][c];
         const float r = gr[t][c], i = gi[t][c], g = mu[c] + gg[t].get(c);
         const float prev = ct ? 0.0f : bb[t][c];
         const float ix = i * uu[t][2].get(c), gx = im[t][c] < kNoInput ? g * __builtin_amdgcn_rcpf(im[t][c]) : 0.0f;

@@ -103,7 +103,7 @@ constexpr int kMaxScanChunk = kSmallSteps;
 // before has long finished when this one asks, and plain hand-over from chunk
 // to chunk is the least work; with few, the chain of waits counts.
 int gated_group(long long tiles_per_row) {
-  return tiles_per_row >= 64 ? 1 : tiles_per_row >= 32 ? 2 : tiles_per_row >= 16 ? 4 : kMaxGroup;
+  return tiles_per_row >= 128 ? 1 : tiles_per_row >= 64 ? 2 : tiles_per_row >= 16 ? 4 : kMaxGroup;
 }
 
 struct GatedLayout {
