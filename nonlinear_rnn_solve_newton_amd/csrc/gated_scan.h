@@ -27,6 +27,19 @@ namespace pararnn {
 
 constexpr int kGatedSave = 96;  // steps between two saved states: an adjoint chunk
 
+// n / d for n < 2^31 by a multiplication: m = ceil(2^(31 + s) / d), s = ceil(log2 d)
+struct FastDiv {
+  uint32_t m, s;
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> (31 + s));
+  }
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return FastDiv{static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), s};
+}
+
 struct GatedArgs {
   const void* u;            // [B][L][3][D]
   const float* lam;         // [D]
@@ -44,7 +57,10 @@ struct GatedArgs {
   float* dlam;              // [D], where there is one partial sum per channel
   unsigned long long* carry;  // [ngroups][slots] states at the groups' starts
   unsigned long long* agg;    // [nchunks][2][slots] chunk transforms
-  unsigned int* ctr;        // [0] ticket
+  unsigned int* ctr;        // ticket counters
+  int parts_log2;           // how many of them
+  unsigned int run;         // tiles per counter
+  FastDiv by_run, by_row;   // division by run and by ntiles_d
   int B, L, D, nchunks, ntiles_d, group;
   float c;
 };
@@ -147,6 +163,41 @@ __device__ __forceinline__ float marked(float a, uint32_t cuts, int t) {
   return RST && (cuts >> t & 1u) ? __uint_as_float(kResetA) : a;
 }
 
+// Which tile (batch row, channels) and chunk a workgroup works on. The tiles
+// are dealt out in `parts` equal runs, each with a ticket counter of its own (a
+// counter that 512 workgroups ask at once costs the last of them 3 us); within
+// a run the tickets go chunk by chunk. Workgroup i takes a ticket of run
+// i % parts (the last run may be short: its spare tickets are of no tile). Chunks of a tile depend on
+// earlier ones of that tile only, so whatever a workgroup waits for has
+// started before it.
+struct TilePos {
+  int chunk, tile, b, dt0;
+};
+constexpr int kTicketStride = 64;  // counters 256 bytes apart
+struct Tickets {
+  unsigned int part;
+  __device__ __forceinline__ explicit Tickets(const GatedArgs& p) { part = blockIdx.x & ((1u << p.parts_log2) - 1u); }
+  // by one thread; with one chunk nothing waits, and the order is that of the workgroups
+  __device__ __forceinline__ unsigned int take(const GatedArgs& p) const {
+    return p.nchunks > 1 ? atomicAdd(p.ctr + part * kTicketStride, 1u) : blockIdx.x >> p.parts_log2;
+  }
+  __device__ __forceinline__ bool fill(const GatedArgs& p, unsigned int chunk, unsigned int tile, int cw, TilePos* at) const {
+    at->chunk = static_cast<int>(chunk);
+    at->tile = static_cast<int>(tile);
+    at->b = static_cast<int>(p.by_row.div(tile));
+    at->dt0 = static_cast<int>(tile - static_cast<unsigned int>(at->b) * p.ntiles_d) * cw;
+    return tile < static_cast<unsigned int>(p.B) * p.ntiles_d;
+  }
+  // one chunk: workgroup i has tile i
+  __device__ __forceinline__ void one(const GatedArgs& p, unsigned int i, int cw, TilePos* at) const {
+    fill(p, 0u, i, cw, at);
+  }
+  __device__ __forceinline__ bool place(const GatedArgs& p, unsigned int ticket, int cw, TilePos* at) const {
+    const unsigned int chunk = p.by_run.div(ticket);
+    return fill(p, chunk, part * p.run + (ticket - chunk * p.run), cw, at);
+  }
+};
+
 // Parked values are read back, not kept in registers after all: volatile
 __device__ __forceinline__ f32x4 read_back(const f32x4* p) {
   return *(const volatile __attribute__((address_space(3))) f32x4*)p;
@@ -228,17 +279,16 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_scan_kernel(const GatedArgs
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  unsigned int ticket = blockIdx.x;
-  if (!ONE && p.nchunks > 1) {
-    if (tid == 0) s_ticket = atomicAdd(p.ctr, 1u);
+  Tickets q(p);
+  TilePos at;
+  if constexpr (ONE) {
+    q.one(p, blockIdx.x, CW, &at);
+  } else {
+    if (tid == 0) s_ticket = q.take(p);
     __syncthreads();
-    ticket = __builtin_amdgcn_readfirstlane(s_ticket);
+    if (!q.place(p, __builtin_amdgcn_readfirstlane(s_ticket), CW, &at)) return;
   }
-  const unsigned int ntiles = static_cast<unsigned int>(p.B) * p.ntiles_d;
-  const int chunk = static_cast<int>(ticket / ntiles);
-  const int tile = static_cast<int>(ticket - static_cast<unsigned int>(chunk) * ntiles);
-  const int b = tile / p.ntiles_d;
-  const int dt0 = (tile - b * p.ntiles_d) * CW;
+  const int chunk = at.chunk, tile = at.tile, b = at.b, dt0 = at.dt0;
 
   const int ld = lane % LD, ll = lane / LD;
   const int d0 = dt0 + ld * C;
@@ -418,29 +468,27 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  unsigned int ticket = blockIdx.x;
-  if (!ONE && p.nchunks > 1) {
-    if (tid == 0) s_ticket = atomicAdd(p.ctr, 1u);
-    __syncthreads();
-    ticket = __builtin_amdgcn_readfirstlane(s_ticket);
-  }
-  const unsigned int ntiles = static_cast<unsigned int>(p.B) * p.ntiles_d;
-  const int rchunk = static_cast<int>(ticket / ntiles);
-  const int chunk = p.nchunks - 1 - rchunk;  // taken from the end of L
-  const int tile = static_cast<int>(ticket - static_cast<unsigned int>(rchunk) * ntiles);
-  const int b = tile / p.ntiles_d;
-  const int dt0 = (tile - b * p.ntiles_d) * CW;
-
   const int ld = lane % LD, ll = lane / LD;
-  const int d0 = dt0 + ld * C;
-  const bool dv = d0 < p.D;
   const int lt0 = (wave * LL + ll) * T;
+  const uint32_t gstep = static_cast<uint32_t>(p.D * sizeof(UT)), ustep = 3 * gstep;
+  constexpr uint32_t kOOB = 0x80000000u;
+
+  Tickets q(p);
+  TilePos at;
+  if constexpr (ONE) {
+    q.one(p, blockIdx.x, CW, &at);
+  } else {
+    if (tid == 0) s_ticket = q.take(p);
+    __syncthreads();
+    if (!q.place(p, __builtin_amdgcn_readfirstlane(s_ticket), CW, &at)) return;
+  }
+  const int rchunk = at.chunk, chunk = p.nchunks - 1 - rchunk;  // taken from the end of L
+  const int tile = at.tile, b = at.b, dt0 = at.dt0, d0 = dt0 + ld * C;
+  const bool dv = d0 < p.D;
   const int l0 = chunk * CL + lt0;
   const int len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
   const long long wrow = static_cast<long long>(b) * p.L + static_cast<long long>(chunk) * CL;
-  const uint32_t gstep = static_cast<uint32_t>(p.D * sizeof(UT)), ustep = 3 * gstep;
   const uint32_t rows = static_cast<uint32_t>(min(p.L - chunk * CL, CL));
-  constexpr uint32_t kOOB = 0x80000000u;
   const uint32_t vd = static_cast<uint32_t>(d0 * sizeof(UT));
   const uint32_t vu0 = dv ? static_cast<uint32_t>(lt0) * ustep + vd : kOOB;
   const uint32_t vh0 = dv ? static_cast<uint32_t>(lt0) * gstep + vd : kOOB;

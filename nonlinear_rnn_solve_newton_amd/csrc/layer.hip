@@ -17,6 +17,7 @@
 namespace pararnn {
 namespace {
 
+constexpr int kCUs = 256;
 constexpr size_t kAlign = 256;
 size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -63,7 +64,7 @@ int pick_c(int cmax, int D, size_t es, std::initializer_list<const void*> typed,
 // waves, OCC waves per SIMD that the registers must allow
 template <class UT, int C> struct ScanShape;
 template <> struct ScanShape<bf16, 2> { static constexpr int T = 12, LL = 2, W = 8, OCC = 5; };
-template <> struct ScanShape<bf16, 1> { static constexpr int T = 24, LL = 1, W = 8, OCC = 4; };
+template <> struct ScanShape<bf16, 1> { static constexpr int T = 16, LL = 1, W = 8, OCC = 4; };
 template <> struct ScanShape<float, 2> { static constexpr int T = 8, LL = 4, W = 8, OCC = 4; };
 template <> struct ScanShape<float, 1> { static constexpr int T = 16, LL = 2, W = 8, OCC = 4; };
 template <class UT, int C> struct AdjShape;
@@ -98,6 +99,12 @@ ScanGeo scan_geo(const pararnn_gated_opts* o, int C, bool adj) {
   return h ? geo_of<ScanShape<bf16, 1>, 1>() : geo_of<ScanShape<float, 1>, 1>();
 }
 constexpr int kMaxScanChunk = kSmallSteps;
+// Ticket counters: 8 for up to this many tickets, else 2. 8 keep the
+// workgroups that start together from queueing at one counter (5 x 1237 x 1000
+// 29 -> 24 us forward, 51 -> 42 us back); where many rounds follow each other
+// that is a small share, and 2 runs keep neighbouring channels together
+// (1 x 65536 x 2048: 230 and 418 us against 240 and 438).
+constexpr long long kFewTickets = 3072;
 
 // Chunks per group (chunk_carry): with many tiles per chunk row the chunk
 // before has long finished when this one asks, and plain hand-over from chunk
@@ -108,7 +115,7 @@ int gated_group(long long tiles_per_row) {
 
 struct GatedLayout {
   size_t ctr = 0, carry = 0, agg = 0, clear_end = 0, part = 0, total = 0;
-  int nchunks = 0, ntiles_d = 0, group = 1;
+  int nchunks = 0, ntiles_d = 0, group = 1, parts_log2 = 0;
   bool direct = false;  // a channel's steps are all in one workgroup: it writes dlam itself
 };
 
@@ -121,8 +128,10 @@ GatedLayout gated_layout(const pararnn_gated_opts* o, bool adj, int C) {
   y.group = gated_group(static_cast<long long>(o->B) * y.ntiles_d);
   y.direct = adj && y.nchunks * static_cast<long long>(o->B) == 1;
   size_t off = 0;
+  const long long ntiles = static_cast<long long>(o->B) * y.ntiles_d;
+  while (y.parts_log2 < (ntiles * y.nchunks <= kFewTickets ? 3 : 1) && (1 << y.parts_log2) < ntiles) ++y.parts_log2;
   if (y.nchunks > 1) {
-    off = round_up(sizeof(uint32_t));
+    off = round_up(sizeof(uint32_t) * (kTicketStride << y.parts_log2));
     y.carry = off;
     off = round_up(off + sizeof(uint64_t) * slots * (ceil_div(y.nchunks, y.group) + 1));
     y.agg = off;
@@ -143,7 +152,7 @@ bool gated_ok(const pararnn_gated_opts* o, bool adj) {
   for (int C = 1; C <= kScanMaxC; C *= 2) {
     const ScanGeo g = scan_geo(o, C, adj);
     const double wgs = static_cast<double>(o->B) * ceil_div(o->D, g.cw) * ceil_div(o->L, g.chunk);
-    if (wgs > 2.0e9) return false;
+    if (wgs > 1.5e9) return false;
   }
   // one chunk is addressed with 32-bit offsets below 2^31
   return static_cast<double>(kMaxScanChunk) * 3 * o->D * 4 < 2147483648.0;
@@ -152,7 +161,8 @@ bool dtype_ok(int dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF16;
 
 template <class UT, int C, bool RST>
 int launch_gated(const GatedArgs& a, bool adj, bool small, hipStream_t s) {
-  const long long grid = static_cast<long long>(a.B) * a.ntiles_d * a.nchunks;
+  const long long grid = static_cast<long long>(a.B) * a.ntiles_d;
+  const long long all = (static_cast<long long>(a.run) << a.parts_log2) * a.nchunks;
   const GatedArgs& b = a;
   if (small) {
     using K = SmallShape;
@@ -161,12 +171,12 @@ int launch_gated(const GatedArgs& a, bool adj, bool small, hipStream_t s) {
   }
   if (adj) {
     using K = AdjShape<UT, C>;
-    return launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, false>, grid, 64 * K::W, s, b);
+    return launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, false>, all, 64 * K::W, s, b);
   }
   using K = ScanShape<UT, C>;
   static_assert(K::T * K::LL * K::W <= kMaxScanChunk && kGatedSave % K::T == 0, "chunk");
   // document starts take registers of their own
-  return launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, RST ? 4 : K::OCC, RST, false>, grid, 64 * K::W, s, b);
+  return launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, RST ? 4 : K::OCC, RST, false>, all, 64 * K::W, s, b);
 }
 template <class UT>
 int launch_gated_c(int C, const GatedArgs& a, bool adj, bool small, hipStream_t s) {
@@ -195,6 +205,10 @@ int gated(bool adj, GatedArgs& a, float* dlam, void* ws, size_t ws_bytes, const 
   a.nchunks = y.nchunks;
   a.ntiles_d = y.ntiles_d;
   a.group = y.group;
+  a.parts_log2 = y.parts_log2;
+  a.run = static_cast<unsigned>(ceil_div(static_cast<long long>(o->B) * y.ntiles_d, 1 << y.parts_log2));
+  a.by_run = fast_div(a.run);
+  a.by_row = fast_div(static_cast<unsigned>(y.ntiles_d));
   a.c = o->c;
   if (y.clear_end) {
     const int rc = clear(w, y.clear_end, stream);
@@ -289,7 +303,6 @@ bool norm_vec(int D, std::initializer_list<const void*> ptrs) {
 // 128 x 128 of y by 4 waves (64 x 64 each), 64 x 64 by 4 (32 x 32 each)
 typedef MatmulShape<2, 2, 4, 4> MatmulMid;
 typedef MatmulShape<2, 2, 2, 2> MatmulSmall;
-constexpr int kCUs = 256;
 
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT>
 int launch_matmul(const MatmulArgs& p, bool direct, hipStream_t s) {
