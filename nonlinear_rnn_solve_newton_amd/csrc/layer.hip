@@ -300,24 +300,54 @@ bool norm_vec(int D, std::initializer_list<const void*> ptrs) {
 // ---------------------------------------------------------------------------
 // 8-bit product
 
-// 128 x 128 of y by 4 waves (64 x 64 each), 64 x 64 by 4 (32 x 32 each)
-typedef MatmulShape<2, 2, 4, 4> MatmulMid;
-typedef MatmulShape<2, 2, 2, 2> MatmulSmall;
+// 128 x 128 of y by 4 waves (64 x 64 each), 64 x 64 by 4 (32 x 32 each), and
+// the same with the blocks of K dealt out to 2 or 4 such groups
+typedef MatmulShape<2, 2, 4, 4, 1> MatmulMid;
+typedef MatmulShape<2, 2, 2, 2, 1> MatmulSmall;
+typedef MatmulShape<2, 2, 2, 2, 2> MatmulSplit2;
+typedef MatmulShape<2, 2, 2, 2, 4> MatmulSplit4;
 
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT>
 int launch_matmul(const MatmulArgs& p, bool direct, hipStream_t s) {
   const long long grid = ceil_div(p.M, S::BM) * ceil_div(p.N, S::BN);
-  return direct ? launch(matmul_kernel<S, MODE, E8, ROWS, F32OUT, true>, grid, S::NT, s, p)
-                : launch(matmul_kernel<S, MODE, E8, ROWS, F32OUT, false>, grid, S::NT, s, p);
+  return direct ? launch(matmul_kernel<S, MODE, E8, ROWS, F32OUT, true>, grid, S::NT * S::KS, s, p)
+                : launch(matmul_kernel<S, MODE, E8, ROWS, F32OUT, false>, grid, S::NT * S::KS, s, p);
 }
+template <int MODE, bool E8, int ROWS, bool F32OUT, int MT, int NT, int UN>
+int launch_matmul_few(const MatmulArgs& p, hipStream_t s) {
+  constexpr int M8 = MODE == kMulE8m0 ? kMulScale : MODE;
+  return launch(matmul_few_kernel<M8, E8, ROWS, F32OUT, MT, NT, UN>, ceil_div(p.N, 16 * NT), 512, s, p);
+}
+
 template <int MODE, bool E8, int ROWS, bool F32OUT>
 int launch_matmul_shape(const MatmulArgs& p, bool direct, hipStream_t s) {
+  if (direct && p.M <= 64) {
+    // as many columns per workgroup as leave every CU one (each workgroup reads
+    // all of a): 16 x 16384 x 4096 takes 12.8 us with 64 columns, 16.7 with 32
+    const long long n16 = ceil_div(p.N, 16);
+    if (n16 >= 4 * kCUs)
+      return p.M <= 16   ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 4, 1>(p, s)
+             : p.M <= 32 ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 4, 1>(p, s)
+                         : launch_matmul_few<MODE, E8, ROWS, F32OUT, 4, 4, 1>(p, s);
+    if (p.M <= 16) return launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 1, 4>(p, s);
+    if (p.M <= 32) return launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 1, 2>(p, s);
+    return launch_matmul_few<MODE, E8, ROWS, F32OUT, 4, 1, 2>(p, s);
+  }
   if constexpr (MODE != kMulExact) {
     if (direct && ceil_div(p.M, 256) * ceil_div(p.N, 256) >= kCUs)
       return launch(matmul_large_kernel<MODE, E8, ROWS>, ceil_div(p.M, 256) * ceil_div(p.N, 256), 512, s, p);
   }
   if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= kCUs)
     return launch_matmul<MatmulMid, MODE, E8, ROWS, F32OUT>(p, direct, s);
+  // too few tiles for every CU: what counts is the number of steps, each as
+  // long as its loads take. 256 x 4096 x 4096 takes 18.5 us in one group of
+  // waves, 14.2 in two, 12.4 in four; where the loads go through registers
+  // four groups run short of them (777 x 1000 x 1333, fp32: 16.4, 14.7, 24.5)
+  if (ceil_div(p.M, 64) * ceil_div(p.N, 64) <= kCUs && p.KB >= 4)
+    return direct ? launch(matmul_kernel<MatmulSplit4, MODE, E8, ROWS, F32OUT, true>,
+                           ceil_div(p.M, 64) * ceil_div(p.N, 64), 1024, s, p)
+                  : launch(matmul_kernel<MatmulSplit2, MODE, E8, ROWS, F32OUT, false>,
+                           ceil_div(p.M, 64) * ceil_div(p.N, 64), 512, s, p);
   return launch_matmul<MatmulSmall, MODE, E8, ROWS, F32OUT>(p, direct, s);
 }
 template <int MODE, bool E8, bool F32OUT>

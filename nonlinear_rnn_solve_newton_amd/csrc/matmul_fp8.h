@@ -177,11 +177,12 @@ __device__ __forceinline__ void tile_of(unsigned int id, unsigned int ntm, unsig
   *tn = static_cast<int>(u / gm);
 }
 
-// The shape of a tile: waves along n and m, 16 x 16 tiles per wave along n and m
-template <int WN_, int WM_, int TN_, int TM_>
+// The shape of a tile: waves along n and m, 16 x 16 tiles per wave along n and
+// m; KS groups of such waves, each with every KS-th block of K
+template <int WN_, int WM_, int TN_, int TM_, int KS_>
 struct MatmulShape {
-  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_;
-  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, NT = 64 * WN * WM;
+  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, KS = KS_;
+  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, NT = 64 * WN * WM;  // NT: threads of a group
 };
 
 // BM x BN of y per workgroup. Each step brings 128 columns of both operands
@@ -194,7 +195,7 @@ struct MatmulShape {
 // columns that start at a multiple of that) or 1.
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT, bool DIRECT>
 struct Matmul {
-  static constexpr int BN = S::BN, BM = S::BM, NT = S::NT, TN = S::TN, TM = S::TM;
+  static constexpr int BN = S::BN, BM = S::BM, NT = S::NT, TN = S::TN, TM = S::TM, KS = S::KS;
   static constexpr int LN = BN * 8 / NT, LM = BM * 8 / NT;  // 16-byte chunks per thread
   static_assert(TN * 16 <= 64, "one scale block of w per wave");
   static_assert(NT % 64 == 0, "a thread's rows share their low 3 bits");
@@ -219,16 +220,17 @@ struct Matmul {
       // the row is in the lane's offset, which the extent is checked against;
       // the column's block, the uniform offset, is not. Extents stay below 2^31.
       const bool in = kb * 128 + c0 * 16 < p.K;
+      const int so = kb < p.KB ? kb * 128 : 0;
 #pragma unroll
       for (int i = 0; i < LN; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(sw + wave * 64 + NT * i), 16,
                                                  in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u,
-                                                 kb * 128, 0, 0);
+                                                 so, 0, 0);
 #pragma unroll
       for (int i = 0; i < LM; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sa + wave * 64 + NT * i), 16,
                                                  in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u,
-                                                 kb * 128, 0, 0);
+                                                 so, 0, 0);
     } else {
       const uint8_t* abase = p.a + static_cast<long long>(m0) * p.K;
       const uint8_t* wbase = p.w + static_cast<long long>(n0) * p.K;
@@ -256,7 +258,8 @@ struct Matmul {
     if constexpr (MODE == kMulE8m0) return static_cast<const uint8_t*>(q)[i];
     else return scale_at<E8>(q, i);
   }
-  __device__ __forceinline__ void scales(int kb) {
+  __device__ __forceinline__ void scales(int k) {
+    const int kb = min(k, p.KB - 1);
 #pragma unroll
     for (int j = 0; j < TM; ++j)
       fsa[j] = scale_of(p.sa, static_cast<long long>(kb) * p.M + min(m0 + wm + 16 * j + r, p.M - 1));
@@ -280,13 +283,14 @@ struct Matmul {
     for (int j = 0; j < TM; ++j) csa[j] = fsa[j];
 #pragma unroll
     for (int i = 0; i < NSW; ++i) csw[i] = fsw[i];
-    if (kb + 1 < p.KB) {
-      fetch(kb + 1, nw, na);
-      scales(kb + 1);
+    if (kb + KS < p.KB + KS - 1) {  // another group may have a block where this one has none
+      fetch(kb + KS, nw, na);
+      scales(kb + KS);
     }
     // lane's two chunks of a row of its tile 0; tile i: 128 i further
     const int bw0 = (wn + r) * 8 + (g ^ (r & 7)), bw1 = (wn + r) * 8 + ((g + 4) ^ (r & 7));
     const int ba0 = (wm + r) * 8 + (g ^ (r & 7)), ba1 = (wm + r) * 8 + ((g + 4) ^ (r & 7));
+    if (kb < p.KB) {
     Frag<MODE> fw[TN];
 #pragma unroll
     for (int i = 0; i < TN; ++i) fw[i].set(cw[bw0 + 128 * i], cw[bw1 + 128 * i]);
@@ -313,14 +317,18 @@ struct Matmul {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (kb + 1 < p.KB) land(nw, na);
+    }
+    if (kb + KS < p.KB + KS - 1) land(nw, na);
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the loads into workgroup memory are done
     __syncthreads();
   }
 
   __device__ __forceinline__ void run(i32x4* lds) {
     constexpr int HALF = (BN + BM) * 8;
-    tid = threadIdx.x;
+    const int kg = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / NT);  // the wave's group
+    i32x4* const all = lds;
+    lds += kg * 2 * HALF;
+    tid = static_cast<int>(threadIdx.x) - kg * NT;
     const int lane = tid & 63;
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     r = lane & 15;
@@ -342,18 +350,44 @@ struct Matmul {
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    fetch(0, lds, lds + BN * 8);
-    scales(0);
+    fetch(kg, lds, lds + BN * 8);
+    scales(kg);
     land(lds, lds + BN * 8);
     __builtin_amdgcn_s_waitcnt(0x0f70);
     __syncthreads();
-    for (int kb = 0; kb < p.KB; ++kb) {
-      i32x4* c = lds + (kb & 1) * HALF;
-      i32x4* n = lds + (1 - (kb & 1)) * HALF;
-      step(kb, c, c + BN * 8, n, n + BN * 8);
+    int odd = 0;  // every group takes as many steps as the first
+    for (int kb = 0; kb < p.KB; kb += KS, odd ^= 1) {
+      i32x4* c = lds + odd * HALF;
+      i32x4* n = lds + (1 - odd) * HALF;
+      step(kb + kg, c, c + BN * 8, n, n + BN * 8);
+    }
+    if constexpr (KS > 1) {  // the groups' sums, joined in order
+      f32x4* sum = reinterpret_cast<f32x4*>(all);
+      constexpr int PER = TN * TM * NT;
+      static_assert((KS - 1) * PER <= KS * 2 * HALF, "the sums fit where the blocks were");
+      if (kg > 0) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j) sum[(kg - 1) * PER + (i * TM + j) * NT + tid] = acc[i][j];
+      }
+      __syncthreads();
+      if (kg == 0) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int k = 0; k < KS - 1; ++k) acc[i][j] += sum[k * PER + (i * TM + j) * NT + tid];
+      }
+      __syncthreads();
     }
     const bool whole = !F32OUT && p.vec == 8;  // the last step ended with a barrier
-    TileStore<BM, BN, NT> st{lds};
+    TileStore<BM, BN, NT> st{all};
+    if (kg > 0) {
+      if (whole) __syncthreads();
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       const int n = n0 + wn + 16 * i + 4 * g;
@@ -378,8 +412,8 @@ struct Matmul {
 };
 
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT, bool DIRECT>
-__global__ void __launch_bounds__(S::NT) matmul_kernel(const MatmulArgs p) {
-  __shared__ i32x4 lds[2 * (S::BN + S::BM) * 8];
+__global__ void __launch_bounds__(S::NT * S::KS) matmul_kernel(const MatmulArgs p) {
+  __shared__ i32x4 lds[S::KS * 2 * (S::BN + S::BM) * 8];
   Matmul<S, MODE, E8, ROWS, F32OUT, DIRECT> m;
   m.p = p;
   m.run(lds);
@@ -665,6 +699,111 @@ __global__ void __launch_bounds__(512) matmul_large_kernel(const MatmulArgs p) {
   M m;
   m.p = p;
   m.run(lds, reinterpret_cast<char*>(lds + 2 * M::BUF));
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (up to 16 MT): the product is the time it takes to read w. A
+// workgroup of 8 waves takes 16 NT columns of y; its waves take the 128-blocks
+// of K in turn, straight from HBM into registers (nothing of w is used twice),
+// and their sums are joined in order through workgroup memory. UN blocks are
+// in flight per wave.
+template <int MODE, bool E8, int ROWS, bool F32OUT, int MT, int NT, int UN>
+__global__ void __launch_bounds__(512) matmul_few_kernel(const MatmulArgs p) {
+  constexpr int W = 8;
+  __shared__ f32x4 s_acc[W][NT * MT][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = static_cast<int>(blockIdx.x) * 16 * NT;
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // rows past the end read row 0 of their tile, and are not stored
+  const uint8_t* wp[NT];
+  const uint8_t* ap[MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) wp[i] = p.w + static_cast<long long>(min(n0 + 16 * i + r, p.N - 1)) * p.K;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) ap[j] = p.a + static_cast<long long>(min(16 * j + r, p.M - 1)) * p.K;
+
+  // the two 16-byte chunks g and g + 4 of a row's block; past column K zeros (K is a multiple of 16)
+  auto ld = [&](const uint8_t* row, int kb, i32x4& lo, i32x4& hi) {
+    const int k0 = kb * 128 + 16 * g, k1 = k0 + 64;
+    const i32x4 z = {0, 0, 0, 0};
+    lo = k0 < p.K ? *reinterpret_cast<const i32x4*>(row + k0) : z;
+    hi = k1 < p.K ? *reinterpret_cast<const i32x4*>(row + k1) : z;
+  };
+  for (int kb0 = wave * UN; kb0 < p.KB; kb0 += W * UN) {
+    i32x4 wl[UN][NT], wh[UN][NT], al[UN][MT], ah[UN][MT];
+    float sa[UN][MT], sw[UN][ROWS == 128 ? 1 : NT * 4];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int kb = kb0 + u;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) ld(wp[i], kb, wl[u][i], wh[u][i]);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int kb = kb0 + u, k = min(kb, p.KB - 1);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        ld(ap[j], kb, al[u][j], ah[u][j]);
+        sa[u][j] = scale_at<E8>(p.sa, static_cast<long long>(k) * p.M + min(16 * j + r, p.M - 1));
+      }
+      if constexpr (ROWS == 128) {
+        sw[u][0] = scale_at<E8>(p.sw, static_cast<long long>(min(n0, p.N - 1) / 128) * p.KB + k);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i)
+          sw[u][i] = scale_at<E8>(p.sw, static_cast<long long>(min(n0 + 16 * (i / 4) + 4 * g + i % 4, p.N - 1)) * p.KB + k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      Frag<MODE> fa[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) fa[j].set(al[u][j], ah[u][j]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        Frag<MODE> fw;
+        fw.set(wl[u][i], wh[u][i]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const f32x4 d = tile_product<MODE>(fw, fa[j]);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            // a block past the end adds nothing, whatever its (clamped) scale is
+            const float s = sa[u][j] * sw[u][ROWS == 128 ? 0 : 4 * i + v];
+            acc[i][j][v] = kb0 + u < p.KB ? fmaf(d[v], s, acc[i][j][v]) : acc[i][j][v];
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) s_acc[wave][i * MT + j][lane] = acc[i][j];
+  __syncthreads();
+  // wave w joins tiles w, w + 8, ...
+#pragma unroll
+  for (int t0 = 0; t0 < NT * MT; t0 += W) {
+    const int t = t0 + wave;
+    if (t >= NT * MT) break;
+    const int i = t / MT, j = t % MT;
+    const int n = n0 + 16 * i + 4 * g, m = 16 * j + r;
+    f32x4 v = s_acc[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += s_acc[w][t][lane];
+    if (m < p.M && n < p.N) {
+      float o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[q] = v[q] + (p.bias && n + q < p.N ? p.bias[n + q] : 0.0f);
+      store_row4<F32OUT>(p.y, static_cast<long long>(m) * p.N + n, p.N - n, p.vec, o);
+    }
+  }
 }
 
 }  // namespace pararnn
