@@ -238,15 +238,25 @@ NormShape norm_shape(int D) {
   if (D <= 1024) return {64, 2};
   if (D <= 2048) return {256, 1};
   if (D <= 4096) return {256, 2};
-  if (D <= 8192) return {256, 4};
+  if (D <= 8192) return {512, 2};
   return {1024, 2};
 }
 int norm_rows(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
 
-// workgroups of the adjoint: each leaves one partial row of dw
+// Workgroups of the adjoint, each of which leaves one partial row of dw: what
+// the CUs hold at once (4 waves per SIMD; 32768 x 4096 takes 307 us with half
+// as many, 205 with all)
 long long norm_adjoint_grid(const pararnn_norm_opts* o) {
-  const long long rounds = ceil_div(o->N, norm_rows(norm_shape(o->D).tpr));
-  return rounds < 512 ? rounds : 512;
+  const NormShape k = norm_shape(o->D);
+  const long long rounds = ceil_div(o->N, norm_rows(k.tpr)), room = kCUs * 16 / (k.tpr < 256 ? 4 : k.tpr / 64);
+  return rounds < room ? rounds : room;
+}
+
+// Tensors that together are larger than the last-level cache are read and
+// written past it (32768 x 4096 to 8 bits: 173 -> 161 us); smaller ones may be
+// there from the operator before, and are for the one behind.
+bool norm_stream(const pararnn_norm_opts* o, int bytes_per_element) {
+  return static_cast<double>(o->N) * o->D * bytes_per_element >= 256.0 * 1024 * 1024;
 }
 
 bool norm_ok(const pararnn_norm_opts* o) {
@@ -261,32 +271,36 @@ int norm_dispatch(int D, F go) {
                                     : go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
   if (k.tpr == 256) {
     if (k.nv == 1) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-    if (k.nv == 2) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
   }
+  if (k.tpr == 512) return go(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
   return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
 
 template <class XT, int OUT, bool VEC>
-int launch_norm(const NormArgs& a, hipStream_t s) {
+int launch_norm(const NormArgs& a, bool stream, hipStream_t s) {
   return norm_dispatch<XT, VEC>(a.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     long long grid = ceil_div(a.N, TPR < 256 ? 256 / TPR : 1);
     if (grid > 8192) grid = 8192;
-    return launch(norm_kernel<XT, TPR, NV, OUT, VEC>, grid, TPR < 256 ? 256 : TPR, s, a);
+    const int block = TPR < 256 ? 256 : TPR;
+    return stream && VEC ? launch(norm_kernel<XT, TPR, NV, OUT, VEC, VEC>, grid, block, s, a)
+                         : launch(norm_kernel<XT, TPR, NV, OUT, VEC, false>, grid, block, s, a);
   });
 }
 template <class XT, bool VEC>
-int launch_norm_out(int out, const NormArgs& a, hipStream_t s) {
-  return out == kNormSame  ? launch_norm<XT, kNormSame, VEC>(a, s)
-         : out == kNormFp8 ? launch_norm<XT, kNormFp8, VEC>(a, s)
-                           : launch_norm<XT, kNormFp8Pow2, VEC>(a, s);
+int launch_norm_out(int out, const NormArgs& a, bool stream, hipStream_t s) {
+  return out == kNormSame  ? launch_norm<XT, kNormSame, VEC>(a, stream, s)
+         : out == kNormFp8 ? launch_norm<XT, kNormFp8, VEC>(a, stream, s)
+                           : launch_norm<XT, kNormFp8Pow2, VEC>(a, stream, s);
 }
 template <class XT, bool VEC>
-int launch_norm_adjoint(const NormArgs& a, long long grid, hipStream_t s) {
+int launch_norm_adjoint(const NormArgs& a, long long grid, bool stream, hipStream_t s) {
   return norm_dispatch<XT, VEC>(a.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    return launch(norm_adjoint_kernel<XT, TPR, NV, VEC>, grid, TPR < 256 ? 256 : TPR, s, a);
+    const int block = TPR < 256 ? 256 : TPR;
+    return stream && VEC ? launch(norm_adjoint_kernel<XT, TPR, NV, VEC, VEC>, grid, block, s, a)
+                         : launch(norm_adjoint_kernel<XT, TPR, NV, VEC, false>, grid, block, s, a);
   });
 }
 
@@ -463,11 +477,12 @@ extern "C" int32_t pararnn_norm_residual(const void* x, const void* residual, co
   a.N = o->N;
   a.D = o->D;
   a.eps = o->eps;
+  const bool stream = norm_stream(o, static_cast<int>(es) * 3 + 1);
   hipStream_t st = static_cast<hipStream_t>(stream_);
   const bool vec = norm_vec(o->D, {x, residual, w, s, y});
   if (o->dtype == PARARNN_BF16)
-    return vec ? launch_norm_out<bf16, true>(o->out, a, st) : launch_norm_out<bf16, false>(o->out, a, st);
-  return vec ? launch_norm_out<float, true>(o->out, a, st) : launch_norm_out<float, false>(o->out, a, st);
+    return vec ? launch_norm_out<bf16, true>(o->out, a, stream, st) : launch_norm_out<bf16, false>(o->out, a, stream, st);
+  return vec ? launch_norm_out<float, true>(o->out, a, stream, st) : launch_norm_out<float, false>(o->out, a, stream, st);
 }
 
 extern "C" size_t pararnn_norm_workspace_bytes(const pararnn_norm_opts* o) {
@@ -496,14 +511,15 @@ extern "C" int32_t pararnn_norm_residual_adjoint(const void* s, const float* w, 
   a.N = o->N;
   a.D = o->D;
   a.eps = o->eps;
+  const bool stream = norm_stream(o, static_cast<int>(es) * 4);
   hipStream_t st = static_cast<hipStream_t>(stream_);
   const bool vec = norm_vec(o->D, {s, w, dy, ds, dx});
   const long long grid = norm_adjoint_grid(o);
   int rc;
   if (o->dtype == PARARNN_BF16)
-    rc = vec ? launch_norm_adjoint<bf16, true>(a, grid, st) : launch_norm_adjoint<bf16, false>(a, grid, st);
+    rc = vec ? launch_norm_adjoint<bf16, true>(a, grid, stream, st) : launch_norm_adjoint<bf16, false>(a, grid, stream, st);
   else
-    rc = vec ? launch_norm_adjoint<float, true>(a, grid, st) : launch_norm_adjoint<float, false>(a, grid, st);
+    rc = vec ? launch_norm_adjoint<float, true>(a, grid, stream, st) : launch_norm_adjoint<float, false>(a, grid, stream, st);
   if (rc || !dw) return rc;
   return launch(column_sum_kernel, ceil_div(o->D, kSumCols), kSumCols * kSumGroups, st,
                 static_cast<const float*>(a.dw_part), dw, grid, static_cast<int>(o->D),
@@ -532,7 +548,7 @@ extern "C" int32_t pararnn_matmul_fp8(const void* a, const void* sa, const void*
   p.N = o->N;
   p.K = o->K;
   p.KB = static_cast<int>(ceil_div(o->K, 128));
-  p.vec = !f32 && o->N % 8 == 0 && aligned(y, 16) ? 8 : o->N % 4 == 0 && aligned(y, f32 ? 16 : 8) ? 4 : 1;
+  p.vec = !f32 && o->N % 8 == 0 && o->N <= (1 << 22) && aligned(y, 16) ? 8 : o->N % 4 == 0 && aligned(y, f32 ? 16 : 8) ? 4 : 1;
   p.stream = 2.0 * p.M * p.N > 256.0 * 1024 * 1024;
   const bool direct = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
   hipStream_t s = static_cast<hipStream_t>(stream_);

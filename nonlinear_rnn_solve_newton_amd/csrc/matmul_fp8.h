@@ -90,15 +90,17 @@ struct TileStore {
   __device__ __forceinline__ void flush(void* y, long long m0, int n0, int mrows, int ncols, int N, int stream, int tid) {
     constexpr int RI = NT / CH;  // rows per round
     const int c = tid % CH, q = tid / CH;
-    uint16_t* base = static_cast<uint16_t*>(y) + m0 * N + n0;
+    // rows past the tile's last are past the extent, columns past N are not sent
+    const __amdgpu_buffer_rsrc_t to =
+        make_rsrc(static_cast<uint16_t*>(y) + m0 * N + n0, static_cast<uint32_t>((min(mrows, BM) - 1) * N + min(ncols, BN)) * 2);
 #pragma unroll
     for (int i = 0; i < BM / RI; ++i) {
       const int m = q + i * RI;
-      if (m < mrows && c * 8 < ncols) {
-        i32x4* to = reinterpret_cast<i32x4*>(base + static_cast<long long>(m) * N + c * 8);
+      if (c * 8 < ncols) {
         const i32x4 v = lds[m * CH + (c ^ (m & MASK))];
-        if (stream) __builtin_nontemporal_store(v, to);
-        else *to = v;
+        const uint32_t at = static_cast<uint32_t>(m * N + c * 8) * 2;
+        if (stream) __builtin_amdgcn_raw_buffer_store_b128(v, to, at, 0, kBufNT);
+        else __builtin_amdgcn_raw_buffer_store_b128(v, to, at, 0, 0);
       }
     }
   }

@@ -36,16 +36,28 @@ struct NormArgs {
 
 // 8 consecutive columns starting at d: one wide access where every row is
 // aligned for it (VEC), else single elements up to D; columns past D read 0
-template <class XT, bool VEC>
+// STREAM: past the caches
+template <bool STREAM, class V>
+__device__ __forceinline__ V ld_vec(const V* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+template <bool STREAM, class V>
+__device__ __forceinline__ void st_vec(V* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+template <class XT, bool VEC, bool STREAM = false>
 __device__ __forceinline__ void ld8(const XT* p, int d, int D, float (&v)[8]) {
   if constexpr (VEC) {
     if (d < D) {
       if constexpr (sizeof(XT) == 4) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(p + d), b = *reinterpret_cast<const f32x4*>(p + d + 4);
+        const f32x4 a = ld_vec<STREAM>(reinterpret_cast<const f32x4*>(p + d));
+        const f32x4 b = ld_vec<STREAM>(reinterpret_cast<const f32x4*>(p + d + 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
       } else {
-        const i32x4 a = *reinterpret_cast<const i32x4*>(p + d);
+        const i32x4 a = ld_vec<STREAM>(reinterpret_cast<const i32x4*>(p + d));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[2 * i] = bf16_lo(static_cast<uint32_t>(a[i]));
@@ -64,18 +76,18 @@ __device__ __forceinline__ void ld8(const XT* p, int d, int D, float (&v)[8]) {
     }
   }
 }
-template <class XT, bool VEC>
+template <class XT, bool VEC, bool STREAM>
 __device__ __forceinline__ void st8(XT* p, int d, int D, const float (&v)[8]) {
   if constexpr (VEC) {
     if (d < D) {
       if constexpr (sizeof(XT) == 4) {
-        *reinterpret_cast<f32x4*>(p + d) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4*>(p + d + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        st_vec<STREAM>(reinterpret_cast<f32x4*>(p + d), f32x4{v[0], v[1], v[2], v[3]});
+        st_vec<STREAM>(reinterpret_cast<f32x4*>(p + d + 4), f32x4{v[4], v[5], v[6], v[7]});
       } else {
         i32x4 a;
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = static_cast<int>(pack_bf16(v[2 * i], v[2 * i + 1]));
-        *reinterpret_cast<i32x4*>(p + d) = a;
+        st_vec<STREAM>(reinterpret_cast<i32x4*>(p + d), a);
       }
     }
   } else {
@@ -114,7 +126,7 @@ __device__ __forceinline__ void row_sum(float (&v)[NS], float* lds, int tid) {
 }
 
 // A workgroup takes 256 / TPR rows at a time (1 where TPR is 256 or more); OUT: kNorm*
-template <class XT, int TPR, int NV, int OUT, bool VEC>
+template <class XT, int TPR, int NV, int OUT, bool VEC, bool STREAM>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormArgs p) {
   constexpr int BT = TPR < 256 ? 256 : TPR, RW = BT / TPR;
   __shared__ float s_sum[BT / 64];
@@ -131,19 +143,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormA
     float s[NV][8];
     float ss[1] = {0.0f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) ld8<XT, VEC>(static_cast<const XT*>(p.x) + at, 8 * (t + TPR * k), p.D, s[k]);
+    for (int k = 0; k < NV; ++k) ld8<XT, VEC, STREAM>(static_cast<const XT*>(p.x) + at, 8 * (t + TPR * k), p.D, s[k]);
     if (p.residual) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         float r[8];
-        ld8<XT, VEC>(static_cast<const XT*>(p.residual) + at, 8 * (t + TPR * k), p.D, r);
+        ld8<XT, VEC, STREAM>(static_cast<const XT*>(p.residual) + at, 8 * (t + TPR * k), p.D, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[k][i] += r[i];
       }
     }
     if (p.s && on) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) st8<XT, VEC>(static_cast<XT*>(p.s) + at, 8 * (t + TPR * k), p.D, s[k]);
+      for (int k = 0; k < NV; ++k) st8<XT, VEC, STREAM>(static_cast<XT*>(p.s) + at, 8 * (t + TPR * k), p.D, s[k]);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -157,7 +169,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormA
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[k][i] = s[k][i] * rstd * wv[k][i];
       if constexpr (OUT == kNormSame) {
-        if (on) st8<XT, VEC>(static_cast<XT*>(p.y) + at, d, p.D, s[k]);
+        if (on) st8<XT, VEC, STREAM>(static_cast<XT*>(p.y) + at, d, p.D, s[k]);
       } else {
         // the block's largest magnitude, by bits: a NaN counts as the largest
         uint32_t m = 0;
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormA
         q1 = __builtin_amdgcn_cvt_pk_fp8_f32(s[k][6] * inv, s[k][7] * inv, q1, true);
         uint8_t* q = static_cast<uint8_t*>(p.y) + at + d;
         if constexpr (VEC) {
-          if (on && d < p.D) *reinterpret_cast<i32x2*>(q) = i32x2{q0, q1};
+          if (on && d < p.D) st_vec<STREAM>(reinterpret_cast<i32x2*>(q), i32x2{q0, q1});
         } else if (on) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -198,7 +210,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormA
 
 // dx per row; dw summed in registers over the workgroup's rows, one partial
 // row per workgroup for column_sum_kernel
-template <class XT, int TPR, int NV, bool VEC>
+template <class XT, int TPR, int NV, bool VEC, bool STREAM>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_adjoint_kernel(const NormArgs p) {
   constexpr int BT = TPR < 256 ? 256 : TPR, RW = BT / TPR;
   __shared__ float s_sum[2 * (BT / 64)];
@@ -220,8 +232,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_adjoint_kernel(con
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      ld8<XT, VEC>(static_cast<const XT*>(p.x) + at, 8 * (t + TPR * k), p.D, s[k]);
-      ld8<XT, VEC>(static_cast<const XT*>(p.dy) + at, 8 * (t + TPR * k), p.D, g[k]);
+      ld8<XT, VEC, STREAM>(static_cast<const XT*>(p.x) + at, 8 * (t + TPR * k), p.D, s[k]);
+      ld8<XT, VEC, STREAM>(static_cast<const XT*>(p.dy) + at, 8 * (t + TPR * k), p.D, g[k]);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -239,14 +251,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_adjoint_kernel(con
       float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-      if (p.ds) ld8<XT, VEC>(static_cast<const XT*>(p.ds) + at, d, p.D, o);
+      if (p.ds) ld8<XT, VEC, STREAM>(static_cast<const XT*>(p.ds) + at, d, p.D, o);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = s[k][i] * rstd;
         o[i] = fmaf(rstd, fmaf(-n, mean, g[k][i] * wv[k][i]), o[i]);
         if (on) dw[k][i] = fmaf(g[k][i], n, dw[k][i]);
       }
-      if (on) st8<XT, VEC>(static_cast<XT*>(p.dx) + at, d, p.D, o);
+      if (on) st8<XT, VEC, STREAM>(static_cast<XT*>(p.dx) + at, d, p.D, o);
     }
   }
   if (!p.dw_part) return;
