@@ -321,6 +321,22 @@ typedef MatmulShape<2, 2, 2, 2, 1> MatmulSmall;
 typedef MatmulShape<2, 2, 2, 2, 2> MatmulSplit2;
 typedef MatmulShape<2, 2, 2, 2, 4> MatmulSplit4;
 
+// Which large tile: 256 x 256 (4), 256 x 192 (3), or neither (0). One
+// workgroup fills a CU, so the time is the rounds it takes over the CUs times
+// a round's. In units of a 128-block on 16 columns per wave (0.4 us) a round
+// of 64 tn columns takes tn KB and 20 for its beginning and end, and one of
+// two 128 x 128 tiles per CU 2.7 KB and 14 (measured at 8192 x 8192 x 8192,
+// 32768 x 16384 x 4096 and 4096 x 6144 x 2048).
+int large_tile(const MatmulArgs& p) {
+  const long long tm = ceil_div(p.M, 256);
+  const double kb = p.KB;
+  const double mid = ceil_div(ceil_div(p.M, 128) * ceil_div(p.N, 128), 2 * kCUs) * (2.7 * kb + 14.0);
+  const double l4 = ceil_div(tm * ceil_div(p.N, 256), kCUs) * (4.0 * kb + 20.0);
+  const double l3 = ceil_div(tm * ceil_div(p.N, 192), kCUs) * (3.0 * kb + 20.0);
+  if (mid < l4 && mid < l3) return 0;
+  return l4 <= l3 ? 4 : 3;
+}
+
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT>
 int launch_matmul(const MatmulArgs& p, bool direct, hipStream_t s) {
   const long long grid = ceil_div(p.M, S::BM) * ceil_div(p.N, S::BN);
@@ -348,8 +364,11 @@ int launch_matmul_shape(const MatmulArgs& p, bool direct, hipStream_t s) {
     return launch_matmul_few<MODE, E8, ROWS, F32OUT, 4, 1, 2>(p, s);
   }
   if constexpr (MODE != kMulExact) {
-    if (direct && ceil_div(p.M, 256) * ceil_div(p.N, 256) >= kCUs)
-      return launch(matmul_large_kernel<MODE, E8, ROWS>, ceil_div(p.M, 256) * ceil_div(p.N, 256), 512, s, p);
+    const int tn = direct ? large_tile(p) : 0;
+    if (tn == 4)
+      return launch(matmul_large_kernel<4, MODE, E8, ROWS>, ceil_div(p.M, 256) * ceil_div(p.N, 256), 512, s, p);
+    if (tn == 3)
+      return launch(matmul_large_kernel<3, MODE, E8, ROWS>, ceil_div(p.M, 256) * ceil_div(p.N, 192), 512, s, p);
   }
   if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= kCUs)
     return launch_matmul<MatmulMid, MODE, E8, ROWS, F32OUT>(p, direct, s);

@@ -74,30 +74,33 @@ __device__ __forceinline__ float scale_at(const void* p, long long i) {
 // the matrix instructions leave them (4 columns of 16 rows per instruction) a
 // wave would touch 32 bytes of a row at a time, which HBM takes at a quarter
 // of its rate. NT threads; put(row, column, 4 values) fills the tile, then
-// whole rows go out 16 bytes per lane. Chunk c of row m lies at c ^ (m & 15),
-// so that 16 rows written at one column touch different banks.
+// whole rows go out 16 bytes per lane. So that 16 rows written at one column
+// touch different banks, chunk c of row m lies at c ^ (m & 15) where a row is
+// a power of two of chunks, and rows are one chunk longer where it is not.
 template <int BM, int BN, int NT>
 struct TileStore {
-  static constexpr int CH = BN / 8, MASK = (CH < 16 ? CH : 16) - 1;  // 16-byte chunks per row
+  static constexpr int CH = BN / 8;  // 16-byte chunks per row
+  static constexpr bool POW2 = (CH & (CH - 1)) == 0;
+  static constexpr int MASK = POW2 ? (CH < 16 ? CH : 16) - 1 : 0, ROW = POW2 ? CH : CH + 1;
+  static constexpr int CHUNKS = BM * ROW;
   i32x4* lds;
   __device__ __forceinline__ void put(int m, int n, const float (&o)[4]) {
     const int c = n >> 3;
-    reinterpret_cast<u32x2*>(lds + m * CH + (c ^ (m & MASK)))[(n >> 2) & 1] =
+    reinterpret_cast<u32x2*>(lds + m * ROW + (c ^ (m & MASK)))[(n >> 2) & 1] =
         u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
   }
   // stream: y is larger than the last-level cache and so is not kept in L2,
   // where it would displace the operands (2 % of the time of a 1 GB result)
   __device__ __forceinline__ void flush(void* y, long long m0, int n0, int mrows, int ncols, int N, int stream, int tid) {
-    constexpr int RI = NT / CH;  // rows per round
-    const int c = tid % CH, q = tid / CH;
     // rows past the tile's last are past the extent, columns past N are not sent
     const __amdgpu_buffer_rsrc_t to =
         make_rsrc(static_cast<uint16_t*>(y) + m0 * N + n0, static_cast<uint32_t>((min(mrows, BM) - 1) * N + min(ncols, BN)) * 2);
+    static_assert(BM * CH % NT == 0, "whole rounds");
 #pragma unroll
-    for (int i = 0; i < BM / RI; ++i) {
-      const int m = q + i * RI;
+    for (int i = 0; i < BM * CH / NT; ++i) {
+      const int e = tid + NT * i, m = e / CH, c = e % CH;
       if (c * 8 < ncols) {
-        const i32x4 v = lds[m * CH + (c ^ (m & MASK))];
+        const i32x4 v = lds[m * ROW + (c ^ (m & MASK))];
         const uint32_t at = static_cast<uint32_t>(m * N + c * 8) * 2;
         if (stream) __builtin_amdgcn_raw_buffer_store_b128(v, to, at, 0, kBufNT);
         else __builtin_amdgcn_raw_buffer_store_b128(v, to, at, 0, 0);
@@ -422,8 +425,8 @@ __global__ void __launch_bounds__(S::NT * S::KS) matmul_kernel(const MatmulArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Large products: 256 x 256 of y by 8 waves (4 along n, 2 along m; 64 x 128
-// each), two waves per SIMD. What bounds it is the time from the issue of a
+// Large products: 256 rows by 64 TN columns of y by 8 waves (4 along n, 2
+// along m; 16 TN x 128 each), two waves per SIMD. What bounds it is the time from the issue of a
 // block's loads to their arrival, about a step and a half of products, and
 // workgroup memory holds two blocks only. So a step has two halves: the first
 // multiplies the wave's w rows by the first half of its a rows, the second by
@@ -432,14 +435,20 @@ __global__ void __launch_bounds__(S::NT * S::KS) matmul_kernel(const MatmulArgs 
 // after the next; the place of the second a rows is taken one half later.
 // Every load so has a step and a half to arrive, and the waits count the loads
 // that may still be on their way.
-template <int MODE, bool E8, int ROWS>
+template <int TN, int MODE, bool E8, int ROWS>
 struct MatmulLarge {
-  static constexpr int BN = 256, BM = 256, NT = 512, TN = 4, TM = 8;
+  static constexpr int BN = 64 * TN, BM = 256, NT = 512, TM = 8, WC = 16 * TN;
   // 16-byte chunks of one buffer: w, then the first and the second a rows of both waves along m
   static constexpr int OX0 = BN * 8, OX1 = OX0 + BM * 4, BUF = OX1 + BM * 4;
   static constexpr int SB = MODE == kMulE8m0 ? 1 : 4;      // bytes of a scale in workgroup memory
   static constexpr int SCH = 256 * SB;  // bytes of 256 scales: two buffers for a, two for w
-  static constexpr int NWL = 4, NXL = 2;  // loads per thread: w, half of a
+  static constexpr int NWL = TN, NXL = 2;  // loads per thread: w, half of a
+  // loads that may be on their way when a half step begins: this or the next
+  // block's second a rows, and w and the first a rows of the next block
+  static constexpr int WAIT = 0x0f70 | (NWL + 2 * NXL);
+  // a lane's scales of w: with one per block, 64 columns are in one block, 48 may be in two
+  static constexpr int NB = TN == 4 ? 1 : TN, NSC = ROWS == 128 ? NB : SB == 1 ? 1 : 4 * TN;
+  static constexpr int TILE_BUF = TileStore<BM, BN, NT>::CHUNKS, LDS = 2 * BUF > TILE_BUF ? 2 * BUF : TILE_BUF;
   typedef __attribute__((address_space(3))) void lds_void;
 
   MatmulArgs p;
@@ -480,31 +489,32 @@ struct MatmulLarge {
     long long at = static_cast<long long>(k) * p.M + min(m0 + t, p.M - 1);
     if (tid >= 256) {
       q = p.sw;
-      at = ROWS == 1 ? min(n0 + t, p.N - 1) : min(n0 + (t & 3) * 64, p.N - 1) / 128;
+      at = ROWS == 1 ? min(n0 + t, p.N - 1) : min(n0 + (t & 15) * 16, p.N - 1) / 128;
       at = at * p.KB + k;
     }
     vs = raw_scale(q, at);
   }
   // row 16 j + r of a wave's rows lies at 8 r + j, so that a lane's 8 scales
-  // are consecutive; e8m0 column 16 i + r of w at 4 r + i, fp32 columns in
-  // order; scales of whole blocks at the number of the wave along n
+  // are consecutive; e8m0 column 16 i + r of a wave's columns at 4 r + i, fp32
+  // columns in order; with one scale per block, those of 16 columns each
   __device__ __forceinline__ void land_scales(int kb, char* scales) {
     const int t = tid & 255;
     const int pa = (t & 128) + (t & 15) * 8 + ((t >> 4) & 7);
-    const int pw = ROWS == 128 ? (t & 3) : MODE == kMulE8m0 ? (t & 192) + (t & 15) * 4 + ((t >> 4) & 3) : t;
+    const int pw = ROWS == 128 ? t & 15 : MODE == kMulE8m0 ? t / WC * 64 + (t & 15) * 4 + t % WC / 16 : t;
     char* to = scales + ((tid < 256 ? 0 : 2) + (kb & 1)) * SCH;
     const int at = tid < 256 ? pa : pw;
+    if (tid >= 256 && t >= BN) return;
     if constexpr (SB == 1) reinterpret_cast<uint8_t*>(to)[at] = static_cast<uint8_t>(vs);
     else reinterpret_cast<uint32_t*>(to)[at] = vs;
   }
 
   // acc of row tile j += d * its scale * the columns' scales
-  __device__ __forceinline__ void scale_add(int j, float sj, const uint32_t (&csw)[ROWS == 128 ? 1 : SB == 1 ? 1 : 16]) {
+  __device__ __forceinline__ void scale_add(int j, float sj, const uint32_t (&csw)[NSC]) {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        acc[i][j][v] = fmaf(d[i][v], sj * __uint_as_float(csw[ROWS == 128 ? 0 : 4 * i + v]), acc[i][j][v]);
+        acc[i][j][v] = fmaf(d[i][v], sj * __uint_as_float(csw[ROWS == 128 ? i % NB : 4 * i + v]), acc[i][j][v]);
   }
   // the products up to here are issued before what follows: keeps the
   // compiler from moving them behind the next barrier
@@ -516,7 +526,7 @@ struct MatmulLarge {
   // products of a row tile are scaled and added under those of the next.
   template <int HALF>
   __device__ __forceinline__ void products(const i32x4* __restrict__ x, const i32x4 (&sc)[SB == 1 ? 1 : 2],
-                                           const uint32_t (&csw)[ROWS == 128 ? 1 : SB == 1 ? 1 : 16]) {
+                                           const uint32_t (&csw)[NSC]) {
     const int b0 = (wmi * 64 + r) * 8 + (g ^ (r & 7)), b1 = (wmi * 64 + r) * 8 + ((g + 4) ^ (r & 7));
     i32x4 lo = x[b0], hi = x[b1];
 #pragma unroll
@@ -530,7 +540,7 @@ struct MatmulLarge {
       if constexpr (MODE == kMulE8m0) {
         const int sj = sc[0][HALF];
 #pragma unroll
-        for (int i = 0; i < TN; ++i) mfma_e8(acc[i][j], fw[i], fa, static_cast<int>(csw[0]), i, sj, jj);
+        for (int i = 0; i < TN; ++i) mfma_e8(acc[i][j], fw[i], fa, static_cast<int>(csw[ROWS == 128 ? i % NB : 0]), i, sj, jj);
         pin(j);
       } else {
         f32x4 dn[TN];
@@ -584,14 +594,14 @@ struct MatmulLarge {
     const int nxt = BUF - cur;
     // first half: w and the first a rows of this block have arrived, and the
     // next block's scales; 8 newer loads may not have
-    __builtin_amdgcn_s_waitcnt(0x0f78);
+    __builtin_amdgcn_s_waitcnt(WAIT);
     land_scales(kb + 1, ws);
     hand_over();
     load_scales(kb + 2);
     __builtin_amdgcn_sched_barrier(0);
     load_a(kb + 1, 1, wr + nxt);
     i32x4 sc[SB == 1 ? 1 : 2];
-    uint32_t csw[ROWS == 128 ? 1 : SB == 1 ? 1 : 16];
+    uint32_t csw[NSC];
     {
       const char* sa = rs + (kb & 1) * SCH;
       const char* sw = rs + (2 + (kb & 1)) * SCH;
@@ -603,26 +613,29 @@ struct MatmulLarge {
         sc[1] = *reinterpret_cast<const i32x4*>(sa + (wmi * 128 + r * 8) * 4 + 16);
       }
       if constexpr (ROWS == 128) {
-        if constexpr (SB == 1) csw[0] = static_cast<uint8_t>(sw[wni]);
-        else csw[0] = reinterpret_cast<const uint32_t*>(sw)[wni];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          if constexpr (SB == 1) csw[i] = static_cast<uint8_t>(sw[wni * TN + i]);
+          else csw[i] = reinterpret_cast<const uint32_t*>(sw)[wni * TN + i];
+        }
       } else if constexpr (SB == 1) {
         csw[0] = *reinterpret_cast<const uint32_t*>(sw + wni * 64 + r * 4);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const i32x4 t = *reinterpret_cast<const i32x4*>(sw + (wni * 64 + 16 * i + 4 * g) * 4);
+        for (int i = 0; i < TN; ++i) {
+          const i32x4 t = *reinterpret_cast<const i32x4*>(sw + (wni * WC + 16 * i + 4 * g) * 4);
 #pragma unroll
           for (int v = 0; v < 4; ++v) csw[4 * i + v] = static_cast<uint32_t>(t[v]);
         }
       }
     }
-    const int b0 = (wni * 64 + r) * 8 + (g ^ (r & 7)), b1 = (wni * 64 + r) * 8 + ((g + 4) ^ (r & 7));
+    const int b0 = (wni * WC + r) * 8 + (g ^ (r & 7)), b1 = (wni * WC + r) * 8 + ((g + 4) ^ (r & 7));
 #pragma unroll
     for (int i = 0; i < TN; ++i)
       fw[i] = __builtin_shufflevector(rd[cur + b0 + 128 * i], rd[cur + b1 + 128 * i], 0, 1, 2, 3, 4, 5, 6, 7);
     products<0>(rd + cur + OX0, sc, csw);
-    // second half: the other a rows have arrived; again 8 newer loads may not have
-    __builtin_amdgcn_s_waitcnt(0x0f78);
+    // second half: the other a rows have arrived; again WAIT's newer loads may not have
+    __builtin_amdgcn_s_waitcnt(WAIT);
     hand_over();
     load_w(kb + 2, wr + cur);
     load_a(kb + 2, 0, wr + cur);
@@ -652,7 +665,7 @@ struct MatmulLarge {
       for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // in the order that the steps count them in; the bias waits in workgroup memory
     float* s_bias = reinterpret_cast<float*>(scales + 4 * SCH);
-    const float bias = p.bias && tid < 256 && n0 + tid < p.N ? p.bias[n0 + tid] : 0.0f;
+    const float bias = p.bias && tid < BN && n0 + tid < p.N ? p.bias[n0 + tid] : 0.0f;
     load_scales(0);
     const uint32_t vs0 = vs;
     load_w(0, lds);
@@ -666,7 +679,7 @@ struct MatmulLarge {
     vs = vs0;
     land_scales(0, scales);
     vs = vs1;
-    if (tid < 256) s_bias[tid] = bias;
+    if (tid < BN) s_bias[tid] = bias;
     for (int kb = 0; kb < p.KB; ++kb) step(kb, lds, lds, scales, scales);
     __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into workgroup memory outlives the products
     const bool whole = p.vec == 8;
@@ -674,7 +687,7 @@ struct MatmulLarge {
     if (whole) __syncthreads();
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
-      const int n = n0 + wni * 64 + 16 * i + 4 * g;
+      const int n = n0 + wni * WC + 16 * i + 4 * g;
       const f32x4 bv = *reinterpret_cast<const f32x4*>(s_bias + (n - n0));
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
@@ -693,14 +706,14 @@ struct MatmulLarge {
   }
 };
 
-template <int MODE, bool E8, int ROWS>
+template <int TN, int MODE, bool E8, int ROWS>
 __global__ void __launch_bounds__(512) matmul_large_kernel(const MatmulArgs p) {
-  typedef MatmulLarge<MODE, E8, ROWS> M;
+  typedef MatmulLarge<TN, MODE, E8, ROWS> M;
   // one array: what the compiler derives from several would replace what restrict says
-  __shared__ i32x4 lds[2 * M::BUF + 4 * M::SCH / 16 + 64];
+  __shared__ i32x4 lds[M::LDS + 4 * M::SCH / 16 + 64];
   M m;
   m.p = p;
-  m.run(lds, reinterpret_cast<char*>(lds + 2 * M::BUF));
+  m.run(lds, reinterpret_cast<char*>(lds + M::LDS));
 }
 
 // ---------------------------------------------------------------------------
