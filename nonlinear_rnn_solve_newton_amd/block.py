@@ -1,0 +1,104 @@
+"""A recurrent layer out of the library's operators, for training, prefill and
+decoding:
+
+  s = x + residual                      (the new residual stream)
+  y = rms_norm(s) * norm_w              in 8 bits, a scale per row and 128 columns
+  u = y W^T + bias                      8-bit product: the gate inputs [B][L][G][D]
+  h = recurrence(u)                     gated scan, or the Newton solve of a
+                                        ParaGRU / ParaLSTM cell
+
+`RecurrentBlock` keeps the weights as the product takes them (8 bits, laid out
+once) and runs the calls in order on torch's current stream. The backward pass
+of the gated cell goes straight through the roundings to 8 bits; its two
+products with the weights (dy = du W and dW = du^T y) are plain matrix products
+in bf16.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import binding, layer
+from .binding import PararnnError
+
+GATES = {"gated": 3, "gru": 3, "lstm": 4}
+
+
+class RecurrentBlock:
+    """norm_w [E] fp32, w [G*D][E] (any float type; quantized here), bias [G*D]
+    fp32 or None; coef: lam [D] for the gated cell, the recurrent coefficients
+    a [G][D] for "gru" and "lstm". x and residual have E columns."""
+
+    def __init__(self, cell: str, norm_w: torch.Tensor, w: torch.Tensor, coef: torch.Tensor, *,
+                 bias: Optional[torch.Tensor] = None, c: float = 8.0, eps: float = 1e-6, iters: int = 3,
+                 scale_dtype: torch.dtype = torch.float8_e8m0fnu):
+        if cell not in GATES:
+            raise PararnnError(f"cell must be one of {sorted(GATES)}, got {cell!r}")
+        G = GATES[cell]
+        if w.dim() != 2 or w.shape[0] % G or w.shape[1] != norm_w.shape[0]:
+            raise PararnnError(f"w must be [{G}*D][{norm_w.shape[0]}], got {tuple(w.shape)}")
+        self.cell, self.G, self.D, self.E = cell, G, w.shape[0] // G, w.shape[1]
+        self.norm_w, self.coef, self.bias = norm_w, coef, bias
+        self.c, self.eps, self.iters, self.scale_dtype = c, eps, iters, scale_dtype
+        self.w8, self.sw = layer.quantize_weight(w, scale_dtype=scale_dtype)
+        self._w16 = None
+
+    def gates(self, x: torch.Tensor, residual: Optional[torch.Tensor]):
+        """Gate inputs u [..., G, D] bf16 and the new residual s of rows x [..., E]."""
+        rows = x.reshape(-1, self.E)
+        n = layer.norm_residual(rows, self.norm_w, residual=None if residual is None else residual.reshape(-1, self.E),
+                                eps=self.eps, scale_dtype=self.scale_dtype)
+        u = layer.matmul_fp8(n["y"], n["scale"], self.w8, self.sw, bias=self.bias)
+        return u.view(*x.shape[:-1], self.G, self.D), n["s"].view(x.shape)
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, state=None,
+                lengths: Optional[torch.Tensor] = None, reset: Optional[torch.Tensor] = None,
+                train: bool = False) -> dict:
+        """x, residual [B][L][E] bf16. state: h0 [B][D] (gated, gru) or (c0, h0)
+        (lstm), None for zero; lengths and reset as in layer.gated_scan (gated
+        cell only). Returns dict(h [B][L][D], s [B][L][E], state after the last
+        step, ctx for backward with train=True)."""
+        u, s = self.gates(x, residual)
+        if self.cell == "gated":
+            r = layer.gated_scan(u, self.coef, c=self.c, h0=state, lengths=lengths, reset=reset, save=train)
+            ctx = (u, s, r["saved"], lengths, reset) if train else None
+            return {"h": r["h"], "s": s, "state": r["hT"], "ctx": ctx}
+        if lengths is not None or reset is not None or train:
+            raise PararnnError("lengths, reset and train are for the gated cell")
+        if self.cell == "gru":
+            r = binding.solve("gru", u, self.coef, h0=state, iters=self.iters)
+            return {"h": r["h"], "s": s, "state": r["h"][:, -1].contiguous(), "ctx": None}
+        c0, h0 = state if state is not None else (None, None)
+        r = binding.solve("lstm", u, self.coef, c0=c0, h0=h0, iters=self.iters)
+        return {"h": r["h"], "s": s, "state": (r["c"][:, -1].contiguous(), r["h"][:, -1].contiguous()), "ctx": None}
+
+    def backward(self, ctx, dh: torch.Tensor, ds: Optional[torch.Tensor] = None,
+                 dstate: Optional[torch.Tensor] = None) -> dict:
+        """Gradients of the gated cell's forward call for dh = dL/dh [B][L][D], ds =
+        dL/ds [B][L][E] and dstate = dL/dstate [B][D]: dict(dx (of x and of the
+        residual), dnorm_w, dw, dbias, dcoef, dstate0)."""
+        u, s, saved, lengths, reset = ctx
+        a = layer.gated_scan_adjoint(u, self.coef, dh, saved, c=self.c, dhT=dstate, lengths=lengths, reset=reset,
+                                     want_dh0=True)
+        du = a["du"].view(-1, self.G * self.D)
+        if self._w16 is None:  # the weights' values in bf16, as dy = du W takes them
+            full = layer.scale_values(self.sw).repeat_interleave(128, 0)[:self.G * self.D]
+            full = full.repeat_interleave(128, 1)[:, :self.E]
+            self._w16 = (self.w8.float() * full).to(torch.bfloat16)
+        rows = s.reshape(-1, self.E)
+        y = layer.norm_residual(rows, self.norm_w, eps=self.eps)["y"]
+        n = layer.norm_residual_adjoint(rows, self.norm_w, du @ self._w16, eps=self.eps,
+                                        ds=None if ds is None else ds.reshape(-1, self.E))
+        return {"dx": n["dx"].view(s.shape), "dnorm_w": n["dw"], "dw": du.t() @ y,
+                "dbias": du.sum(dim=0, dtype=torch.float32), "dcoef": a["dlam"], "dstate0": a["dh0"]}
+
+    def step(self, x: torch.Tensor, residual: Optional[torch.Tensor], state: torch.Tensor, *,
+             slots: Optional[torch.Tensor] = None):
+        """One token of each of B requests, x and residual [B][E]; the gated
+        cell's states are the rows slots[b] of the pool `state` [S][D] and are
+        updated in place. Returns (h [B][D], s [B][E])."""
+        if self.cell != "gated":
+            raise PararnnError("step is for the gated cell; give forward a sequence of one step")
+        u, s = self.gates(x, residual)
+        return layer.gated_step(u, self.coef, state, c=self.c, slots=slots), s

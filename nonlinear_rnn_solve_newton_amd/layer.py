@@ -373,6 +373,15 @@ def quantize_weight(w: torch.Tensor, *, rows: int = 128, scale_dtype: torch.dtyp
     return q, sw.contiguous()
 
 
+def scale_values(scale: torch.Tensor) -> torch.Tensor:
+    """The fp32 values of scales of either type."""
+    if scale.dtype == torch.float32:
+        return scale
+    b = scale.view(torch.uint8).to(torch.int32)
+    v = torch.ldexp(torch.ones_like(b, dtype=torch.float32), b - 127)
+    return torch.where(b == 255, torch.full_like(v, float("nan")), v)
+
+
 def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, *,
                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
