@@ -43,7 +43,8 @@ typedef struct {
 } pararnn_gated_opts;
 
 /* Workspace of pararnn_gated_scan (adjoint = 0) or _adjoint (adjoint = 1) into
- * *bytes; it may be 0, and ws then NULL. Host-only. */
+ * *bytes, enough with and without lengths and reset; it may be 0, and ws then
+ * NULL. Host-only. */
 int32_t pararnn_gated_workspace_bytes(int32_t adjoint, const pararnn_gated_opts* o, size_t* bytes);
 
 /* Number of saved states per channel: one in front of every 96 steps. */

@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
 // out[d] = f(d) * sum of `rows` partial rows, in a fixed order: kSumGroups
 // interleaved row groups per column, then the groups in turn.
 // lam: f = -c s(lam[d]); nullptr: f = 1.
-constexpr int kSumCols = 64, kSumGroups = 16;
+constexpr int kSumCols = 32, kSumGroups = 32;
 static __global__ void __launch_bounds__(kSumCols * kSumGroups)
 column_sum_kernel(const float* part, float* out, long long rows, int D, const float* lam, float c) {
   __shared__ float s_sum[kSumGroups][kSumCols];
