@@ -51,7 +51,8 @@ int32_t pararnn_gated_workspace_bytes(int32_t adjoint, const pararnn_gated_opts*
 int32_t pararnn_gated_saved_rows(int32_t L);
 
 /* Forward: h, and optionally hT, the state after each row's last step, and
- * saved [saved_rows(L)][B][D] fp32, the states the adjoint starts from. */
+ * saved [saved_rows(L)][B][D] fp32, the states the adjoint starts from (those
+ * past a row's length may stay unwritten). */
 int32_t pararnn_gated_scan(const void* u, const float* lam, const float* h0, void* h, float* hT, float* saved,
                            void* ws, size_t ws_bytes, const pararnn_gated_opts* o, void* stream);
 

@@ -52,6 +52,11 @@ def run(x, train=True, **kw):
     return out
 
 
+def pad_mask(x):
+    """[B][L], true at the steps of a row."""
+    return torch.arange(x["u"].shape[1])[None] < x["lengths"][:, None]
+
+
 def close(got, want, what):
     v, e = want
     tol = e + (R.BF16_EPS * (np.abs(v) + e) if got.dtype == torch.bfloat16 else 0.0) + R.TINY
@@ -89,6 +94,20 @@ def test_each_mask_alone(masks):
     say(f"gated scan masks={masks}")
     x = draw(4, 700, 72, "bf16", 5, masks)
     check(x, run(x))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("masks", ["lengths", "both"])
+def test_lengths_at_chunk_borders(masks, dtype):
+    """Rows that end at, before and behind the border of a chunk in either
+    direction; the padding behind them holds NaN."""
+    say(f"gated scan {dtype} masks={masks}, lengths at chunk borders")
+    lengths = torch.tensor([800, 0, 1, 95, 96, 97, 191, 192, 193, 256, 257, 384, 385, 799], dtype=torch.int32)
+    x = draw(len(lengths), 800, 68, dtype, 23, masks)
+    x["lengths"] = lengths
+    got = run({**x, "u": x["u"].where(pad_mask(x)[:, :, None, None], float("nan")),
+               "dh": x["dh"].where(pad_mask(x)[:, :, None], float("nan"))})
+    check(x, got)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
