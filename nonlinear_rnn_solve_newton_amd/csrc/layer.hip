@@ -354,18 +354,26 @@ int launch_matmul_few(const MatmulArgs& p, hipStream_t s) {
 
 template <int MODE, bool E8, int ROWS, bool F32OUT>
 int launch_matmul_shape(const MatmulArgs& p, bool direct, hipStream_t s) {
-  if (direct && p.M <= 64) {
-    // as many columns per workgroup as leave every CU one (each workgroup reads
-    // all of a): 16 x 16384 x 4096 takes 12.8 us with 64 columns, 16.7 with 32
-    const long long n16 = ceil_div(p.N, 16);
-    if (n16 >= 4 * kCUs)
-      return p.M <= 16   ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 4, 1>(p, s)
-             : p.M <= 32 ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 4, 1>(p, s)
-                         : launch_matmul_few<MODE, E8, ROWS, F32OUT, 4, 4, 1>(p, s);
-    if (p.M <= 16) return launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 1, 4>(p, s);
-    if (p.M <= 32) return launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 1, 2>(p, s);
-    return launch_matmul_few<MODE, E8, ROWS, F32OUT, 4, 1, 2>(p, s);
+  // Few rows: each workgroup reads all of a, so it takes as many columns as
+  // leave a workgroup for most CUs (16 x 12288 x 4096: 11.9 us with 64 columns,
+  // 15.0 with 16; 32 x 8192 x 4096: 12.3 with 32, 14.9 with 16, 14.8 with 64).
+  // With 33 to 64 rows that is too much to read as soon as the CUs take turns:
+  // 64 x 4096 x 4096 takes 11.7 us in tiles (bf16) against 13.3, and fp32
+  // results, whose tiles cost twice the instructions, 16.3 against 13.5, but
+  // 64 x 8192 x 4096 18.6 against 25.0.
+  const long long n16 = ceil_div(p.N, 16);
+  if (direct && p.M <= 32) {
+    if (n16 >= 3 * kCUs)
+      return p.M <= 16 ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 4, 1>(p, s)
+                       : launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 4, 1>(p, s);
+    if (n16 >= 2 * kCUs)
+      return p.M <= 16 ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 2, 2>(p, s)
+                       : launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 2, 2>(p, s);
+    return p.M <= 16 ? launch_matmul_few<MODE, E8, ROWS, F32OUT, 1, 1, 4>(p, s)
+                     : launch_matmul_few<MODE, E8, ROWS, F32OUT, 2, 1, 2>(p, s);
   }
+  if (direct && p.M <= 64 && n16 <= (F32OUT ? kCUs : kCUs / 2))
+    return launch_matmul_few<MODE, E8, ROWS, F32OUT, 4, 1, 2>(p, s);
   if constexpr (MODE != kMulExact) {
     const int tn = direct ? large_tile(p) : 0;
     if (tn == 4)

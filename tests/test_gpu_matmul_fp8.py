@@ -68,6 +68,19 @@ def test_many_tiles(scale, M, N, K):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("out", list(OUT))
+@pytest.mark.parametrize("scale,rows", [("f32", 128), ("f32", 1), ("e8m0", 128), ("e8m0", 1)])
+@pytest.mark.parametrize("M,N", [(1, 8210), (16, 8192), (17, 8210), (1, 12301), (16, 12300), (32, 12300), (64, 2050),
+                                 (50, 4100)])
+def test_few_rows_of_wide_products(M, N, scale, rows, out):
+    """One to four times 16 rows, 16 to 64 columns per workgroup, the last one partly past the end."""
+    K = 1296
+    say(f"matmul {M}x{N}x{K} {scale} rows={rows} -> {out}")
+    a, sa, w, sw, bias = draw(M, N, K, scale, rows, M + N)
+    got = layer.matmul_fp8(*(t.cuda() for t in (a, sa, w, sw)), bias=bias.cuda(), out_dtype=OUT[out])
+    check(a, sa, w, sw, bias, rows, out, got)
+
+
 @pytest.mark.parametrize("N", [4140, 4152, 4097])
 @pytest.mark.parametrize("scale,rows", [("f32", 128), ("f32", 1), ("e8m0", 128), ("e8m0", 1)])
 def test_enough_tiles_for_every_cu(scale, rows, N):
