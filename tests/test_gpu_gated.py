@@ -75,7 +75,7 @@ def check(x, got, c=8.0):
 
 
 # one step, tiny, odd widths (one channel per lane), widths of 2 mod 4, sizes
-# around the chunks of 112 to 256 steps and the tiles of 32 and 64 channels
+# around the chunks of 96 to 256 steps and the tiles of 32 and 64 channels
 SHAPES = [(1, 1, 1), (2, 2, 3), (3, 5, 64), (1, 127, 65), (2, 128, 6), (2, 129, 4), (1, 256, 32), (1, 257, 100),
           (3, 511, 62), (2, 1000, 33), (1, 2500, 8), (5, 300, 130)]
 
