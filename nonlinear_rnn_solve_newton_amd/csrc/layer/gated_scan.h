@@ -22,7 +22,7 @@
 // 110 us back (470 MB, 4.3 TB/s), 1 x 65536 x 2048 takes 213 us forward (5.0
 // TB/s), against 5.5 TB/s that a plain stream of that mix reaches. Between them
 // lie the arithmetic (34 vector instructions per element forward, 65 back: half
-// of the issue slots, and more as the transcendental ones take four), the
+// of the issue slots, and a fifth more as the transcendental ones take two), the
 // launch that clears the carries (5 us) and, where few chunks are in flight,
 // the wait for the carry (2 us per group of chunks).
 #pragma once
