@@ -67,11 +67,8 @@ template <> struct ScanShape<bf16, 2> { static constexpr int T = 12, LL = 2, W =
 template <> struct ScanShape<bf16, 1> { static constexpr int T = 16, LL = 1, W = 8, OCC = 4; };
 template <> struct ScanShape<float, 2> { static constexpr int T = 8, LL = 4, W = 8, OCC = 4; };
 template <> struct ScanShape<float, 1> { static constexpr int T = 16, LL = 2, W = 8, OCC = 4; };
-template <class UT, int C, bool RST> struct AdjShape { static constexpr int T = 6, LL = 2, W = 8, OCC = 4; };
-template <class UT, bool RST> struct AdjShape<UT, 1, RST> { static constexpr int T = 12, LL = 1, W = 8, OCC = 4; };
-// the compiler spills fp32 pairs without document starts in the wide shape, and with them in this
-// one: 8 x 4096 x 1024 takes 224 us wide and 189 us here without starts, 180 and 196 us with
-template <> struct AdjShape<float, 2, false> { static constexpr int T = 6, LL = 4, W = 4, OCC = 4; };
+template <int C> struct AdjShape { static constexpr int T = 6, LL = 2, W = 8, OCC = 4; };
+template <> struct AdjShape<1> { static constexpr int T = 12, LL = 1, W = 8, OCC = 4; };
 
 // Small problems, where latency counts: the whole sequence in one workgroup of
 // 16 waves, so that there is no carry between chunks, nothing to clear and one
@@ -93,10 +90,7 @@ constexpr int kScanMaxC = 2;
 ScanGeo scan_geo(const pararnn_gated_opts* o, int C, bool adj) {
   const bool h = o->dtype == PARARNN_BF16;
   if (gated_small(o)) return C == 2 ? geo_of<SmallShape, 2>() : geo_of<SmallShape, 1>();
-  if (adj) {
-    if (C == 1) return geo_of<AdjShape<bf16, 1, false>, 1>();
-    return h || o->reset ? geo_of<AdjShape<bf16, 2, true>, 2>() : geo_of<AdjShape<float, 2, false>, 2>();
-  }
+  if (adj) return C == 2 ? geo_of<AdjShape<2>, 2>() : geo_of<AdjShape<1>, 1>();
   if (C == 2) return h ? geo_of<ScanShape<bf16, 2>, 2>() : geo_of<ScanShape<float, 2>, 2>();
   return h ? geo_of<ScanShape<bf16, 1>, 1>() : geo_of<ScanShape<float, 1>, 1>();
 }
@@ -172,7 +166,7 @@ int launch_gated(const GatedArgs& a, bool adj, bool small, hipStream_t s) {
                : launch(gated_scan_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, true>, grid, 64 * K::W, s, b);
   }
   if (adj) {
-    using K = AdjShape<UT, C, RST>;
+    using K = AdjShape<C>;
     return launch(gated_adjoint_kernel<UT, C, K::T, K::W, K::LL, K::OCC, RST, false>, all, 64 * K::W, s, b);
   }
   using K = ScanShape<UT, C>;
@@ -409,15 +403,10 @@ extern "C" int32_t pararnn_gated_workspace_bytes(int32_t adjoint, const pararnn_
   if ((adjoint != 0 && adjoint != 1) || !bytes || !gated_ok(o, adjoint != 0)) return PARARNN_EINVAL;
   if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
   size_t n = 0;
-  pararnn_gated_opts q = *o;
-  const uint8_t start = 0;
-  for (const uint8_t* reset : {static_cast<const uint8_t*>(nullptr), &start}) {  // enough for calls with and without
-    q.reset = reset;
-    for (int C = 1; C <= kScanMaxC; C *= 2) {
-      if (o->D % C) continue;
-      const size_t t = gated_layout(&q, adjoint != 0, C).total;
-      n = t > n ? t : n;
-    }
+  for (int C = 1; C <= kScanMaxC; C *= 2) {
+    if (o->D % C) continue;
+    const size_t t = gated_layout(o, adjoint != 0, C).total;
+    n = t > n ? t : n;
   }
   *bytes = n;
   return PARARNN_OK;
