@@ -13,7 +13,9 @@
  * an error other than PARARNN_EHIP, inputs and outputs that do not alias
  * (except where a call says "in place"). Sums, states and statistics are held
  * in 32 bits; results are rounded once, to nearest even. Repeated calls give
- * the same bits.
+ * the same bits. Sizes whose launch would have 2^32 threads or more (512 for
+ * 32 or 64 channels of a row and 96 to 256 steps of a scan, one for 1 to 4
+ * channels of a step, 256 or 512 for a tile of a product) are PARARNN_EINVAL.
  */
 #ifndef PARARNN_LAYER_H
 #define PARARNN_LAYER_H

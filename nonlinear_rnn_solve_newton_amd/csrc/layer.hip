@@ -24,8 +24,13 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int check_hip(hipError_t e) { return e == hipSuccess ? PARARNN_OK : PARARNN_EHIP; }
 
+// A launch's size in threads is a 32-bit number: a larger one would run as its
+// low 32 bits (8388609 workgroups of 512 as one), without an error.
+constexpr long long kMaxThreads = 4294967295LL;
+
 template <typename F, typename... Args>
 int launch(F kernel, long long grid, int block, hipStream_t s, Args... args) {
+  if (grid > kMaxThreads / block) return PARARNN_EINVAL;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(block), 0, s, args...);
   return check_hip(hipGetLastError());
 }
@@ -147,8 +152,10 @@ bool gated_ok(const pararnn_gated_opts* o, bool adj) {
   if (static_cast<double>(o->B) * o->L * o->D * 12 > 9.0e18) return false;
   for (int C = 1; C <= kScanMaxC; C *= 2) {
     const ScanGeo g = scan_geo(o, C, adj);
-    const double wgs = static_cast<double>(o->B) * ceil_div(o->D, g.cw) * ceil_div(o->L, g.chunk);
-    if (wgs > 1.5e9) return false;
+    // workgroups of 512 threads, two equal runs of tiles (as many tickets as this have two counters)
+    const long long tiles = static_cast<long long>(o->B) * ceil_div(o->D, g.cw);
+    const double wgs = static_cast<double>(tiles == 1 ? 1 : tiles + tiles % 2) * ceil_div(o->L, g.chunk);
+    if (wgs > static_cast<double>(kMaxThreads / 512)) return false;
   }
   // one chunk is addressed with 32-bit offsets below 2^31
   return static_cast<double>(kMaxScanChunk) * 3 * o->D * 4 < 2147483648.0;
@@ -465,7 +472,6 @@ extern "C" int32_t pararnn_gated_step(const void* u, const float* lam, const int
   const int C = pick_c(4, D, es, {u, h}, {lam, state});
   if (!C || !aligned(slots, 4)) return PARARNN_EUNSUPPORTED;
   const long long blocks = ceil_div(static_cast<long long>(B) * (D / C), 256);
-  if (blocks > 2000000000LL) return PARARNN_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream_);
   auto go = [&](auto kernel, auto* up, auto* hp) { return launch(kernel, blocks, 256, s, up, lam, slots, state, hp, B, D, S, c); };
   if (dtype == PARARNN_BF16) {

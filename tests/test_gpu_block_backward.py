@@ -1,0 +1,113 @@
+"""RecurrentBlock.backward term by term against 64 bits: every element of each
+gradient, each product at the inputs it got, with masks, carried states and
+without the optional arguments; padding that holds NaN; weights that change;
+other streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+from nonlinear_rnn_solve_newton_amd import layer
+from nonlinear_rnn_solve_newton_amd.binding import PararnnError
+from nonlinear_rnn_solve_newton_amd.block import RecurrentBlock
+from tests import layer_reference as R
+from tests.helpers import say
+from tests.test_gpu_block import inputs, make
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def within(got, want, tol, what):
+    """got (its own rounding included in the bound) within tol of want, element by element."""
+    if got.dtype == torch.bfloat16:
+        tol = tol + R.BF16_EPS * (np.abs(want) + tol)
+    err = np.abs(f64(got) - want)
+    assert (err <= tol + R.TINY).all(), f"{what}: {int((~(err <= tol + R.TINY)).sum())} of {err.size} outside"
+
+
+def product(a, b):
+    """a b of float64 arrays and its bound in fp32 sums of any order (one rounding per term at most)."""
+    return a @ b, R.U * (a.shape[1] + 1) * (np.abs(a) @ np.abs(b))
+
+
+def weights(blk):
+    """Values of the block's 8-bit weights, exact in float64."""
+    n = blk.G * blk.D
+    full = layer.scale_values(blk.sw).repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :blk.E]
+    return f64(blk.w8.float()) * f64(full)
+
+
+def check_backward(blk, f, b, dh, ds=None, dstate=None, lengths=None, reset=None, state=None):
+    """Gradients b of blk.forward's result f: the recurrence's from the gate inputs
+    that the layer made, then the products and the norm's at the rounded values
+    that they take (the recurrence's gradient and the norm's output, both bf16)."""
+    opt = lambda t: None if t is None else t.cpu().numpy()  # noqa: E731
+    u, s = f["ctx"][0], f["s"]
+    rec = R.gated(f64(u), f64(blk.coef), c=blk.c, h0=None if state is None else f64(state), lengths=opt(lengths),
+                  reset=opt(reset), dh=f64(dh), dhT=None if dstate is None else f64(dstate))
+    within(b["dcoef"], *rec["dlam"], "dcoef")
+    within(b["dstate0"], *rec["dh0"], "dstate0")
+    saved = f["ctx"][2]
+    a = layer.gated_scan_adjoint(u, blk.coef, dh, saved, c=blk.c, dhT=dstate, lengths=lengths, reset=reset)
+    within(a["du"], *rec["du"], "du")
+    du = f64(a["du"]).reshape(-1, blk.G * blk.D)
+    on = np.ones(s.shape[:2], bool) if lengths is None else np.arange(s.shape[1])[None] < opt(lengths)[:, None]
+    on = on.reshape(-1)
+    rows = f64(s).reshape(-1, blk.E)[on]
+    y = f64(layer.norm_residual(s.reshape(-1, blk.E), blk.norm_w, eps=blk.eps)["y"])[on]
+    within(b["dw"], *product(du[on].T, y), "dw")
+    want = du[on].sum(0)
+    within(b["dbias"], want, R.U * on.sum() * np.abs(du[on]).sum(0), "dbias")
+    # dy: weights and the product rounded to bf16
+    w = weights(blk)
+    dy, e = product(du[on], w)
+    e = e + R.BF16_EPS * (np.abs(du[on]) @ np.abs(w))
+    e = e + R.BF16_EPS * (np.abs(dy) + e)
+    nw = f64(blk.norm_w)
+    dsr = None if ds is None else f64(ds).reshape(-1, blk.E)[on]
+    n = R.norm_adjoint(rows, nw, dy, dsr, eps=blk.eps)
+    rstd = 1.0 / np.sqrt((rows * rows).mean(1, keepdims=True) + blk.eps)
+    nrm, ew = np.abs(rows * rstd), np.abs(nw) * e
+    within(b["dx"].reshape(-1, blk.E)[torch.from_numpy(on).cuda()], n["dx"][0],
+           n["dx"][1] + 1.01 * rstd * (ew + nrm * (ew * nrm).mean(1, keepdims=True)), "dx")
+    within(b["dnorm_w"], n["dw"][0], n["dw"][1] + 1.01 * (e * nrm).sum(0), "dnorm_w")
+    return on
+
+
+@pytest.mark.parametrize("scale", [torch.float32, torch.float8_e8m0fnu])
+@pytest.mark.parametrize("case", ["plain", "ds", "state", "masks"])
+def test_every_gradient(case, scale):
+    say(f"block backward: {case}, {scale}")
+    B, L, E, D = 3, 150, 200, 72
+    blk = make("gated", E, D, scale_dtype=scale)
+    x, res = inputs(B, L, E)
+    g = torch.Generator().manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    dh, ds, kw, state, dstate = n(B, L, D).bfloat16(), None, {}, None, None
+    if case != "plain":
+        ds = n(B, L, E).bfloat16()
+    if case in ("state", "masks"):
+        state, dstate = n(B, D), n(B, D)
+    if case == "masks":
+        kw = dict(lengths=torch.tensor([150, 97, 0], dtype=torch.int32).cuda(),
+                  reset=(torch.rand(B, L, generator=g) < 0.05).cuda())
+    f = blk.forward(x, res, state=state, train=True, **kw)
+    b = blk.backward(f["ctx"], dh, ds, dstate)
+    check_backward(blk, f, b, dh, ds, dstate, state=state, **kw)
+
+
+def test_without_a_bias_or_a_residual():
+    say("block backward without bias and residual")
+    B, L, E, D = 2, 60, 136, 40
+    full = make("gated", E, D)
+    blk = RecurrentBlock("gated", full.norm_w, torch.randn(3 * D, E, generator=torch.Generator().manual_seed(3)).cuda(),
+                         full.coef)
+    x, _ = inputs(B, L, E)
+    dh = torch.randn(B, L, D, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    f = blk.forward(x, train=True)
+    check_backward(blk, f, blk.backward(f["ctx"], dh), dh)
