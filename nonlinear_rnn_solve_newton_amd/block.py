@@ -77,7 +77,9 @@ class RecurrentBlock:
                  dstate: Optional[torch.Tensor] = None) -> dict:
         """Gradients of the gated cell's forward call for dh = dL/dh [B][L][D], ds =
         dL/ds [B][L][E] and dstate = dL/dstate [B][D]: dict(dx (of x and of the
-        residual), dnorm_w, dw, dbias, dcoef, dstate0)."""
+        residual), dnorm_w, dw, dbias, dcoef, dstate0). Steps past a row's length
+        (whatever x, the residual and dh hold there) add nothing to the gradients
+        of the weights, and their dx is ds."""
         u, s, saved, lengths, reset = ctx
         a = layer.gated_scan_adjoint(u, self.coef, dh, saved, c=self.c, dhT=dstate, lengths=lengths, reset=reset,
                                      want_dh0=True)
@@ -86,6 +88,11 @@ class RecurrentBlock:
             full = layer.scale_values(self.sw).repeat_interleave(128, 0)[:self.G * self.D]
             full = full.repeat_interleave(128, 1)[:, :self.E]
             self._w16 = (self.w8.float() * full).to(torch.bfloat16)
+        if lengths is not None:
+            # padding may hold anything, and the sums over the rows would take 0 x NaN from it:
+            # rows of ones there (finite also with eps 0) add the zeros that du holds
+            off = torch.arange(s.shape[1], device=s.device) >= lengths[:, None]
+            s = s.masked_fill(off[:, :, None], 1.0)
         rows = s.reshape(-1, self.E)
         y = layer.norm_residual(rows, self.norm_w, eps=self.eps)["y"]
         n = layer.norm_residual_adjoint(rows, self.norm_w, du @ self._w16, eps=self.eps,

@@ -111,3 +111,32 @@ def test_without_a_bias_or_a_residual():
     dh = torch.randn(B, L, D, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
     f = blk.forward(x, train=True)
     check_backward(blk, f, blk.backward(f["ctx"], dh), dh)
+
+
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_padding_may_hold_anything(bad, eps):
+    """Steps past a row's length do not reach the weights' gradients, whatever x,
+    the residual and dh hold there."""
+    say(f"block backward, {bad} in the padding, eps {eps}")
+    B, L, E, D = 3, 130, 128, 64
+    blk = make("gated", E, D, eps=eps)
+    x, res = inputs(B, L, E)
+    g = torch.Generator().manual_seed(5)
+    dh = torch.randn(B, L, D, generator=g).bfloat16().cuda()
+    ds = torch.randn(B, L, E, generator=g).bfloat16().cuda()
+    lengths = torch.tensor([130, 33, 0], dtype=torch.int32).cuda()
+    on = torch.arange(L).cuda()[None] < lengths[:, None]
+
+    def grads(fill):
+        xx, rr, dd = (torch.where(on[:, :, None], t, torch.tensor(fill, dtype=t.dtype).cuda()) for t in (x, res, dh))
+        f = blk.forward(xx, rr, lengths=lengths, train=True)
+        return f, blk.backward(f["ctx"], dd, ds), dd
+
+    f, got, dd = grads(bad)
+    _, want, _ = grads(1.0)
+    for k in ("dnorm_w", "dw", "dbias", "dcoef", "dstate0"):
+        assert torch.isfinite(got[k]).all() and torch.equal(got[k], want[k]), k
+    assert torch.equal(got["dx"][on], want["dx"][on])
+    assert torch.equal(got["dx"][~on], ds[~on])  # s = x + residual there too, and nothing else uses it
+    check_backward(blk, f, got, dd, ds, lengths=lengths)
