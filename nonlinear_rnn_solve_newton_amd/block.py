@@ -7,8 +7,9 @@ decoding:
   h = recurrence(u)                     gated scan, or the Newton solve of a
                                         ParaGRU / ParaLSTM cell
 
-`RecurrentBlock` keeps the weights as the product takes them (8 bits, laid out
-once) and runs the calls in order on torch's current stream. The backward pass
+`RecurrentBlock` keeps the weights as the product takes them (w8 and sw of
+layer.quantize_weight, which may be replaced or written between calls) and
+runs the calls in order on torch's current stream. The backward pass
 of the gated cell goes straight through the roundings to 8 bits; its two
 products with the weights (dy = du W and dW = du^T y) are plain matrix products
 in bf16.
@@ -42,7 +43,21 @@ class RecurrentBlock:
         self.norm_w, self.coef, self.bias = norm_w, coef, bias
         self.c, self.eps, self.iters, self.scale_dtype = c, eps, iters, scale_dtype
         self.w8, self.sw = layer.quantize_weight(w, scale_dtype=scale_dtype)
-        self._w16 = None
+
+    def _weights16(self) -> torch.Tensor:
+        """The 8-bit weights' values in bf16, as dy = du W takes them. Made by each
+        backward pass: a copy that is kept would miss new weights, and other streams
+        and graphs than the one that made it would have to wait for it."""
+        q = self.w8.to(torch.bfloat16)  # exact
+        scale = self.sw.float().repeat_interleave(layer.BLOCK, 0)[:q.shape[0]]
+        whole = self.E // layer.BLOCK
+        cols = whole * layer.BLOCK
+        if whole:  # one fp32 product each, rounded once, in place
+            v = q[:, :cols].unflatten(1, (whole, layer.BLOCK))
+            torch.mul(v, scale[:, :whole, None], out=v)
+        if cols < self.E:
+            torch.mul(q[:, cols:], scale[:, whole:], out=q[:, cols:])
+        return q
 
     def gates(self, x: torch.Tensor, residual: Optional[torch.Tensor]):
         """Gate inputs u [..., G, D] bf16 and the new residual s of rows x [..., E]."""
@@ -84,10 +99,6 @@ class RecurrentBlock:
         a = layer.gated_scan_adjoint(u, self.coef, dh, saved, c=self.c, dhT=dstate, lengths=lengths, reset=reset,
                                      want_dh0=True)
         du = a["du"].view(-1, self.G * self.D)
-        if self._w16 is None:  # the weights' values in bf16, as dy = du W takes them
-            full = layer.scale_values(self.sw).repeat_interleave(128, 0)[:self.G * self.D]
-            full = full.repeat_interleave(128, 1)[:, :self.E]
-            self._w16 = (self.w8.float() * full).to(torch.bfloat16)
         if lengths is not None:
             # padding may hold anything, and the sums over the rows would take 0 x NaN from it:
             # rows of ones there (finite also with eps 0) add the zeros that du holds
@@ -95,7 +106,7 @@ class RecurrentBlock:
             s = s.masked_fill(off[:, :, None], 1.0)
         rows = s.reshape(-1, self.E)
         y = layer.norm_residual(rows, self.norm_w, eps=self.eps)["y"]
-        n = layer.norm_residual_adjoint(rows, self.norm_w, du @ self._w16, eps=self.eps,
+        n = layer.norm_residual_adjoint(rows, self.norm_w, du @ self._weights16(), eps=self.eps,
                                         ds=None if ds is None else ds.reshape(-1, self.E))
         return {"dx": n["dx"].view(s.shape), "dnorm_w": n["dw"], "dw": du.t() @ y,
                 "dbias": du.sum(dim=0, dtype=torch.float32), "dcoef": a["dlam"], "dstate0": a["dh0"]}

@@ -140,3 +140,86 @@ def test_padding_may_hold_anything(bad, eps):
     assert torch.equal(got["dx"][on], want["dx"][on])
     assert torch.equal(got["dx"][~on], ds[~on])  # s = x + residual there too, and nothing else uses it
     check_backward(blk, f, got, dd, ds, lengths=lengths)
+
+
+def weights_of(seed, n, E):
+    return torch.randn(n, E, generator=torch.Generator().manual_seed(seed)).cuda() / E ** 0.5
+
+
+def test_gradients_follow_the_weights():
+    """A training loop sets new 8-bit weights between its steps, in new tensors or
+    in place: the next backward takes them."""
+    say("block backward after an update of the weights")
+    B, L, E, D = 2, 50, 200, 40
+    x, res = inputs(B, L, E)
+    dh = torch.randn(B, L, D, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    blk = make("gated", E, D)
+    for k in range(3):
+        if k == 1:
+            blk.w8, blk.sw = layer.quantize_weight(weights_of(7, 3 * D, E), scale_dtype=blk.scale_dtype)
+        if k == 2:
+            w8, sw = layer.quantize_weight(weights_of(8, 3 * D, E), scale_dtype=blk.scale_dtype)
+            blk.w8.copy_(w8)
+            blk.sw.view(torch.uint8).copy_(sw.view(torch.uint8))
+        f = blk.forward(x, res, train=True)
+        check_backward(blk, f, blk.backward(f["ctx"], dh), dh)
+
+
+# 32768 rows of 24 columns: the sum of dbias over many workgroups
+@pytest.mark.parametrize("B,L,E,D", [(4, 1024, 256, 128), (16, 2048, 128, 8)])
+def test_first_backward_in_a_graph(B, L, E, D):
+    """A captured backward leaves nothing behind that an eager one before the
+    first replay would read, and every replay gives the eager result."""
+    say(f"block backward, captured first, {B}x{L}x{E}x{D}")
+    blk, ref = make("gated", E, D), make("gated", E, D)
+    x, res = inputs(B, L, E)
+    dh = torch.randn(B, L, D, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+
+    def step(b):
+        f = b.forward(x, res, train=True)
+        return b.backward(f["ctx"], dh)
+
+    want = step(ref)  # also warms the libraries up
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(ref)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = step(blk)
+    eager = step(blk)
+    for k in want:
+        assert torch.equal(eager[k], want[k]), f"eager before a replay: {k}"
+    for i in range(4):
+        for v in got.values():
+            v.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for k in want:
+            assert torch.equal(got[k], want[k]), f"replay {i}: {k}"
+        step(ref)
+        torch.cuda.synchronize()
+
+
+def test_backward_on_two_streams():
+    """The first backward on one stream, the next on another that knows nothing of it."""
+    say("block backward on two streams")
+    B, L, E, D = 2, 64, 256, 128
+    blk, ref = make("gated", E, D), make("gated", E, D)
+    x, res = inputs(B, L, E)
+    dh = torch.randn(B, L, D, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    f = blk.forward(x, res, train=True)
+    want = ref.backward(ref.forward(x, res, train=True)["ctx"], dh)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    out = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            out.append(blk.backward(f["ctx"], dh))
+    torch.cuda.synchronize()
+    for b in out:
+        for k in want:
+            assert torch.equal(b[k], want[k]), k
+    assert not any(isinstance(v, torch.Tensor) and v.dtype == torch.bfloat16 for v in vars(blk).values())
