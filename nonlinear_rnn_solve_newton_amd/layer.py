@@ -367,19 +367,15 @@ def quantize_weight(w: torch.Tensor, *, rows: int = 128, scale_dtype: torch.dtyp
         m, e = torch.frexp(scale)
         e = torch.where(m == 0.5, e - 1, e)
         sw = torch.where(torch.isfinite(scale), e + 127, 255).to(torch.uint8).view(scale_dtype)
-        scale = torch.ldexp(torch.ones_like(scale), e)
+        scale = scale_values(sw)  # torch.ldexp on the card is a power, and good to an ulp only
     q = (v / scale[:, None, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
     q = q.reshape(nb * rows, kb * BLOCK)[:N, :K].contiguous().view(torch.float8_e4m3fn)
     return q, sw.contiguous()
 
 
 def scale_values(scale: torch.Tensor) -> torch.Tensor:
-    """The fp32 values of scales of either type."""
-    if scale.dtype == torch.float32:
-        return scale
-    b = scale.view(torch.uint8).to(torch.int32)
-    v = torch.ldexp(torch.ones_like(b, dtype=torch.float32), b - 127)
-    return torch.where(b == 255, torch.full_like(v, float("nan")), v)
+    """The fp32 values of scales of either type (exact: every e8m0 value is one)."""
+    return scale.float()
 
 
 def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, *,
