@@ -361,7 +361,8 @@ def quantize_weight(w: torch.Tensor, *, rows: int = 128, scale_dtype: torch.dtyp
     N, K = w.shape
     nb, kb = -(-N // rows), -(-K // BLOCK)
     v = torch.nn.functional.pad(w.float(), (0, kb * BLOCK - K, 0, nb * rows - N)).view(nb, rows, kb, BLOCK)
-    scale = v.abs().amax(dim=(1, 3)).clamp_min(2.0 ** -100) / 448.0
+    scale = v.abs().amax(dim=(1, 3)).clamp_min(2.0 ** -100)
+    scale = scale / scale.new_full((), 448.0)  # by a Python number the card multiplies by a rounded reciprocal
     sw = scale
     if scale_dtype != torch.float32:
         m, e = torch.frexp(scale)

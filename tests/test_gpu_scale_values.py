@@ -1,5 +1,6 @@
 """Scales as values: powers of two are exact, and weights are laid out the same
 on the card and on the host."""
+import numpy as np
 import pytest
 import torch
 
@@ -35,3 +36,20 @@ def test_weights_at_ties_of_their_8_bits():
         assert torch.equal(sw.cpu().view(torch.uint8)[:, 0].int(), torch.arange(27, 227).int()), dev
         got = w8.cpu().view(torch.uint8)
         assert torch.equal(got, want), f"{dev}: {int((got != want).sum())} of {want.numel()} differ"
+
+
+@pytest.mark.parametrize("scale_dtype", [torch.float32, torch.float8_e8m0fnu])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_the_same_layout_on_host_and_card(rows, scale_dtype):
+    """max / 448 is a correctly rounded quotient on both."""
+    say(f"quantize_weight on host and card, rows={rows}")
+    g = torch.Generator().manual_seed(1)
+    w = torch.randn(700, 900, generator=g) * torch.exp(3 * torch.randn(700, 1, generator=g))
+    a, sa = layer.quantize_weight(w, rows=rows, scale_dtype=scale_dtype)
+    b, sb = layer.quantize_weight(w.cuda(), rows=rows, scale_dtype=scale_dtype)
+    assert torch.equal(sa.view(torch.uint8), sb.cpu().view(torch.uint8))
+    assert torch.equal(a.view(torch.uint8), b.cpu().view(torch.uint8))
+    if scale_dtype == torch.float32:
+        p = torch.nn.functional.pad(w.abs(), (0, 124, 0, -700 % rows)).view(-1, rows, 8, 128)
+        want = p.amax(dim=(1, 3)).numpy() / np.float32(448)
+        assert np.array_equal(sa.numpy(), want)
