@@ -59,21 +59,37 @@ class RecurrentBlock:
             torch.mul(q[:, cols:], scale[:, whole:], out=q[:, cols:])
         return q
 
+    def _rows(self, t, name: str, lead) -> torch.Tensor:
+        """t [*lead][E] as rows of E. As many elements in another shape would be other rows."""
+        if not isinstance(t, torch.Tensor) or t.shape != (*lead, self.E):
+            raise PararnnError(f"{name} must be a tensor of shape {(*lead, self.E)}, got "
+                               f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
+        return t.reshape(-1, self.E)
+
+    def _dims(self, x, n: int):
+        if not isinstance(x, torch.Tensor) or x.dim() != n:
+            raise PararnnError(f"x must be a tensor of {n} dimensions, the last of {self.E} columns")
+
     def gates(self, x: torch.Tensor, residual: Optional[torch.Tensor]):
         """Gate inputs u [..., G, D] bf16 and the new residual s of rows x [..., E]."""
-        rows = x.reshape(-1, self.E)
-        n = layer.norm_residual(rows, self.norm_w, residual=None if residual is None else residual.reshape(-1, self.E),
-                                eps=self.eps, scale_dtype=self.scale_dtype)
+        lead = x.shape[:-1] if isinstance(x, torch.Tensor) else ()
+        rows = self._rows(x, "x", lead)
+        if residual is not None:
+            residual = self._rows(residual, "residual", lead)
+        n = layer.norm_residual(rows, self.norm_w, residual=residual, eps=self.eps, scale_dtype=self.scale_dtype)
         u = layer.matmul_fp8(n["y"], n["scale"], self.w8, self.sw, bias=self.bias)
         return u.view(*x.shape[:-1], self.G, self.D), n["s"].view(x.shape)
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, state=None,
                 lengths: Optional[torch.Tensor] = None, reset: Optional[torch.Tensor] = None,
                 train: bool = False) -> dict:
-        """x, residual [B][L][E] bf16. state: h0 [B][D] (gated, gru) or (c0, h0)
-        (lstm), None for zero; lengths and reset as in layer.gated_scan (gated
-        cell only). Returns dict(h [B][L][D], s [B][L][E], state after the last
+        """x, residual [B][L][E] bf16 (without train fp32 too). state: h0 [B][D]
+        (gated, gru) or (c0, h0) (lstm), None for zero; lengths and reset as in
+        layer.gated_scan (gated cell only). Returns dict(h [B][L][D], s [B][L][E], state after the last
         step, ctx for backward with train=True)."""
+        self._dims(x, 3)
+        if train and x.dtype != torch.bfloat16:
+            raise PararnnError(f"training takes x and residual in bfloat16, got {x.dtype}")
         u, s = self.gates(x, residual)
         if self.cell == "gated":
             r = layer.gated_scan(u, self.coef, c=self.c, h0=state, lengths=lengths, reset=reset, save=train)
@@ -95,7 +111,11 @@ class RecurrentBlock:
         residual), dnorm_w, dw, dbias, dcoef, dstate0). Steps past a row's length
         (whatever x, the residual and dh hold there) add nothing to the gradients
         of the weights, and their dx is ds."""
+        if ctx is None:
+            raise PararnnError("backward needs the ctx of forward(train=True)")
         u, s, saved, lengths, reset = ctx
+        if ds is not None:
+            ds = self._rows(ds, "ds", s.shape[:-1])
         a = layer.gated_scan_adjoint(u, self.coef, dh, saved, c=self.c, dhT=dstate, lengths=lengths, reset=reset,
                                      want_dh0=True)
         du = a["du"].view(-1, self.G * self.D)
@@ -106,8 +126,7 @@ class RecurrentBlock:
             s = s.masked_fill(off[:, :, None], 1.0)
         rows = s.reshape(-1, self.E)
         y = layer.norm_residual(rows, self.norm_w, eps=self.eps)["y"]
-        n = layer.norm_residual_adjoint(rows, self.norm_w, du @ self._weights16(), eps=self.eps,
-                                        ds=None if ds is None else ds.reshape(-1, self.E))
+        n = layer.norm_residual_adjoint(rows, self.norm_w, du @ self._weights16(), eps=self.eps, ds=ds)
         return {"dx": n["dx"].view(s.shape), "dnorm_w": n["dw"], "dw": du.t() @ y,
                 "dbias": du.sum(dim=0, dtype=torch.float32), "dcoef": a["dlam"], "dstate0": a["dh0"]}
 
@@ -118,5 +137,6 @@ class RecurrentBlock:
         updated in place. Returns (h [B][D], s [B][E])."""
         if self.cell != "gated":
             raise PararnnError("step is for the gated cell; give forward a sequence of one step")
+        self._dims(x, 2)
         u, s = self.gates(x, residual)
         return layer.gated_step(u, self.coef, state, c=self.c, slots=slots), s

@@ -223,3 +223,41 @@ def test_backward_on_two_streams():
         for k in want:
             assert torch.equal(b[k], want[k]), k
     assert not any(isinstance(v, torch.Tensor) and v.dtype == torch.bfloat16 for v in vars(blk).values())
+
+
+def test_refused_shapes_and_types():
+    """As many elements in another order are not the same rows, and a training
+    pass is refused where its backward would be."""
+    say("block: refused shapes")
+    B, L, E, D = 3, 5, 128, 64
+    blk = make("gated", E, D)
+    x, res = inputs(B, L, E)
+    f = blk.forward(x, res, train=True)
+    dh = torch.zeros(B, L, D, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(4, D, device="cuda")
+    bad = [
+        lambda: blk.forward(x, res.transpose(0, 1).contiguous()),
+        lambda: blk.forward(x, res.view(B * L, E)),
+        lambda: blk.forward(x.view(B, 2 * L, E // 2), res.view(B, 2 * L, E // 2)),
+        lambda: blk.forward(x.view(B * L, E)),
+        lambda: blk.forward(x[0, 0]),
+        lambda: blk.forward(x.cpu()),
+        lambda: blk.forward(None),
+        lambda: blk.forward(x, [1.0]),
+        lambda: blk.forward(x.float(), res.float(), train=True),
+        lambda: blk.step(x[:, 0].contiguous(), res[:, 0].t().contiguous(), pool),
+        lambda: blk.step(x, res, pool),
+        lambda: blk.backward(f["ctx"], dh, torch.zeros(L, B, E, dtype=torch.bfloat16, device="cuda")),
+        lambda: blk.backward(f["ctx"], dh, torch.zeros(B * L, E, dtype=torch.bfloat16, device="cuda")),
+        lambda: blk.backward(f["ctx"], dh, torch.zeros(B, L, E, device="cuda")),
+        lambda: blk.backward(f["ctx"], dh.transpose(0, 1).contiguous()),
+        lambda: blk.backward(blk.forward(x, res)["ctx"], dh),
+    ]
+    for i, c in enumerate(bad):
+        with pytest.raises(PararnnError):
+            c()
+            raise AssertionError(f"refusal {i} did not come")
+    # rows of any strides are taken, and fp32 rows without train
+    t = torch.empty(L, B, E, dtype=torch.bfloat16, device="cuda").transpose(0, 1).copy_(res)
+    assert torch.equal(blk.forward(x, t)["s"], f["s"])
+    assert blk.forward(x.float(), res.float())["s"].dtype == torch.float32
