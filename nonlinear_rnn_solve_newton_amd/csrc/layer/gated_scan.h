@@ -565,8 +565,9 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
       const GateVal g = gate_values(uu[t][0].get(c), uu[t][1].get(c), beta2[c]);
       gr[t][c] = g.r;
       gi[t][c] = g.i;
-      // 1/m is kept finite (2^63 for v = 0): where v is 0, so are r or beta, and with them what 1/m multiplies
-      im[t][c] = __builtin_amdgcn_rsqf(fmaxf(g.v, 1.17549435e-38f));
+      // 1/m is kept finite (2^63 for v = 0): where v is 0, so are r or beta, and with them what 1/m multiplies.
+      // v is +0 or more; as an integer a NaN is larger than every number and stays one
+      im[t][c] = __builtin_amdgcn_rsqf(__uint_as_float(max(__float_as_uint(g.v), 0x00800000u)));
       A[t][c] = g.a;
       bb[t][c] = g.v * im[t][c] * (g.i * uu[t][2].get(c));
     }
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(64 * W, OCC) gated_adjoint_kernel(const GatedA
         const float at = A[t][c];
         const float r = gr[t][c], i = gi[t][c], g = mu[c] + gg[t].get(c);
         const float prev = ct ? 0.0f : bb[t][c];
-        const float ix = i * uu[t][2].get(c), gx = im[t][c] < kNoInput ? g * __builtin_amdgcn_rcpf(im[t][c]) : 0.0f;
+        const float ix = i * uu[t][2].get(c), gx = im[t][c] >= kNoInput ? 0.0f : g * __builtin_amdgcn_rcpf(im[t][c]);
         const float ga = g * at;
         const float dla = ga * fmaf(-ix * at, im[t][c], prev);
         dl[c] = on ? fmaf(dla, r, dl[c]) : dl[c];
