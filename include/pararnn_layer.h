@@ -94,8 +94,8 @@ typedef struct {
 /* Forward: y, and optionally s (NULL: not written), from one pass. y is made
  * from the sum before its rounding to `dtype`. With an 8-bit y every 128
  * columns of a row share scale = max(max|y|, 2^-100) / 448, or the next power
- * of two at or above that, and hold y / scale rounded to nearest even; a block
- * with an infinity or a NaN stands for NaN. */
+ * of two at or above that, and hold y / scale (the fp32 quotient) rounded to
+ * nearest even; a block with an infinity or a NaN stands for NaN. */
 int32_t pararnn_norm_residual(const void* x, const void* residual, const float* w, void* s, void* y, void* scale,
                               const pararnn_norm_opts* o, void* stream);
 
