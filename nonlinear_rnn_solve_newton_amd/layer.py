@@ -158,7 +158,7 @@ def _workspace(ws, need: int, device):
         if need == 0:
             return None, 0
         return torch.empty(need, dtype=torch.uint8, device=device), need
-    if not ws.is_cuda or ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
         raise PararnnError("ws must be a contiguous uint8 tensor on the inputs' device")
     return ws, ws.numel()
 
@@ -190,7 +190,7 @@ def _gated_opts(u, lam, c, lengths, reset):
         raise PararnnError(f"u must be float32 or bfloat16, got {u.dtype}")
     _dev(lam, "lam", torch.float32, (D,), dev)
     _dev(lengths, "lengths", torch.int32, (B,), dev)
-    if reset is not None and reset.dtype == torch.bool:
+    if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
         reset = reset.view(torch.uint8)
     _dev(reset, "reset", torch.uint8, (B, L), dev)
     o = GatedOpts(B, L, D, _DTYPE[u.dtype], c, _ptr(lengths), _ptr(reset))
@@ -352,7 +352,7 @@ def quantize_weight(w: torch.Tensor, *, rows: int = 128, scale_dtype: torch.dtyp
     float8_e4m3fn, sw [ceil(N/rows)][ceil(K/128)]) with scale = max(max|w|,
     2^-100) / 448 over each rows x 128 block (rows 128 or 1), or the next power
     of two at or above it for scale_dtype float8_e8m0fnu. Works on any device."""
-    if w.dim() != 2 or not w.is_floating_point():
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or not w.is_floating_point():
         raise PararnnError("w must be a floating-point matrix [N][K]")
     if rows not in (1, BLOCK):
         raise PararnnError(f"rows must be 1 or {BLOCK}, got {rows}")
