@@ -7,6 +7,7 @@ import torch
 
 from nonlinear_rnn_solve_newton_amd import layer
 from tests import layer_reference as R
+from tests import test_gpu_norm as N
 from tests.helpers import say
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +81,23 @@ def test_second_round_of_workgroups(D):
     for sl in parts(N):
         p = layer.norm_residual(x[sl], w, residual=r[sl])
         assert torch.equal(whole["y"][sl], p["y"]) and torch.equal(whole["s"][sl], p["s"])
+
+
+# widths that are not whole vectors of 8, one for each launch shape that the narrower tests leave out
+@pytest.mark.parametrize("D", [777, 3001, 16383])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_odd_widths(dtype, D):
+    say(f"norm and adjoint {dtype} 5x{D}")
+    x = N.draw(5, D, dtype, D)
+    d = {k: v.cuda() for k, v in x.items()}
+    want = R.norm(*(N.f64(x[k]) for k in ("x", "w", "residual")))
+    r = layer.norm_residual(d["x"], d["w"], residual=d["residual"])
+    N.close(r["s"], want["s"], "s")
+    N.close(r["y"], want["y"], "y")
+    for scale in N.SC:
+        q = layer.norm_residual(d["x"], d["w"], residual=d["residual"], scale_dtype=N.SC[scale])
+        N.check_fp8(q, want["y"], scale)
+    a = layer.norm_residual_adjoint(d["x"], d["w"], d["dy"], ds=d["ds"])
+    want = R.norm_adjoint(*(N.f64(x[k]) for k in ("x", "w", "dy", "ds")))
+    N.close(a["dx"], want["dx"], "dx")
+    N.close(a["dw"], want["dw"], "dw")
