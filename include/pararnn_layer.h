@@ -116,10 +116,13 @@ int32_t pararnn_norm_residual_adjoint(const void* s, const float* w, const void*
  * a [M][K], sa [ceil(K/128)][M] (as norm_residual writes them), w [N][K],
  * sw [ceil(N/w_rows)][ceil(K/128)], bias [N] fp32 or NULL, y [M][N].
  * With N = G*D this makes the gate inputs u [B*L][G][D] of the recurrences.
- * A bf16 y is computed with the 8-bit matrix instructions, which round the
- * products they add to about 2^-16 of the largest; an fp32 y from exact
- * products. K % 16 == 0 with 16-byte aligned a and w selects the widest
- * accesses.
+ * A bf16 y is computed with the 8-bit matrix instructions, which cut products to
+ * multiples of 2^-13 of the power of two of the largest of eight neighbours
+ * (along k) before they add them in fp32: at most 2^-10.2 of the sum of the
+ * products' magnitudes, 1e-6 to 1e-5 of it for operands of one size. An fp32 y
+ * comes from exact products. Scales whose product is below 2^-126 or 2^128 and
+ * above are outside what the scaling in fp32 holds. K % 16 == 0 with 16-byte
+ * aligned a and w selects the widest accesses.
  */
 typedef enum { PARARNN_SCALE_F32 = 0, PARARNN_SCALE_E8M0 = 1 } pararnn_scale_type;
 

@@ -80,8 +80,11 @@ template <> struct AdjShape<1> { static constexpr int T = 12, LL = 1, W = 8, OCC
 // launch per pass. It reads only 4 C channels of a row.
 struct SmallShape { static constexpr int T = 4, LL = 16, W = 16, OCC = 4; };
 constexpr int kSmallSteps = SmallShape::T * SmallShape::LL * SmallShape::W;
-// B * D up to which it is taken: at 64 channels of 1024 steps 10 and 11 us per pass against 14 and
-// 18, at 1024 channels 20 and 32 against 14 and 18 (every line of HBM is read by 8 workgroups)
+// B * D up to which it is taken. 1024 steps, forward and adjoint, against chunks with their clear (fp32,
+// on the device): 64 channels 5.8 and 11.1 us against 8.9 and 13.8, 256 6.7 and 15.6 against 9.2 and
+// 14.3, 512 9.3 and 21.2 against 9.4 and 15.0, 1024 18 and 30 against 10 and 16 (every line of HBM is
+// read by 8 workgroups). In bf16 the adjoint's side turns earlier (128 channels 11.6 against 12.1, 256
+// 16.7 against 12.5), and up to 96 steps, one chunk, it is 10 against 7 us.
 constexpr int kSmallChannels = 256;
 bool gated_small(const pararnn_gated_opts* o) {
   return o->L <= kSmallSteps && static_cast<long long>(o->B) * o->D <= kSmallChannels;

@@ -8,12 +8,23 @@
 // and one fp32 scale of a covers them. Both operands take their 32 bytes of a
 // 128-block per lane in the same order, so any order does.
 //
-// The 8-bit matrix instructions round the products that they add to about 2^-16
-// of the largest (measured: 1.5e-5 of the result for Gaussian values, in the
-// 16x16x128, 32x32x64 and 16x16x32 forms alike). That is far below the rounding
-// of a bf16 result (2^-8). An fp32 result keeps its digits: its operands are
-// widened to bf16, which holds every e4m3 value, and multiplied in that type,
-// whose sums are good to 1e-8.
+// The 8-bit matrix instructions add their products eight at a time (k in
+// order), each cut toward zero to a multiple of 2^-13 of the power of two of the
+// largest of the eight; the sums of eight, and the running sum where the
+// instruction carries it (e8m0 scales), are added in fp32 (measured in the
+// 16x16x128 form that is used here). A result is so off by at most 7 x 2^-13 =
+// 2^-10.2 of the sum of its products' magnitudes. Measured, of that sum, at K =
+// 128 and 4096: Gaussian operands 2.2e-6 and 3.7e-7 root mean square, 1.2e-5 and
+// 1.5e-6 at most; operands spread over many powers of two (Gaussian times exp of
+// twice a Gaussian) 3.5e-5 and 1.6e-5, 2.4e-4 and 1e-4 at most; positive ones of
+// one size 4e-7 to 1e-6, over 2^20 products as over 2^12. A bf16 result takes
+// it: for Gaussian operands it is a hundredth of the result's own rounding (root
+// mean square) and turns one in five hundred of them; it exceeds that rounding
+// where products over many powers of two cancel. An fp32 result keeps its
+// digits: its operands are widened to bf16, which holds every e4m3 value, and
+// multiplied in that type, whose sums are good to 1e-8.
+// The product of two scales is formed in fp32 in all but the e8m0 tiles: scales
+// that multiply to less than 2^-126 lose digits, to 2^128 or more are infinite.
 #pragma once
 
 #include <type_traits>
@@ -438,7 +449,8 @@ __global__ void __launch_bounds__(S::NT * S::KS) matmul_kernel(const MatmulArgs 
 // after the next; the place of the second a rows is taken one half later.
 // Every load so has a step and a half to arrive, and the waits count the loads
 // that may still be on their way. 32768 x 16384 x 4096 with e8m0 scales takes
-// 1.83 ms (2400 TFLOP/s), 4096 x 6144 x 2048 with fp32 scales 60.7 us (1700);
+// 1.84 to 1.92 ms (2290 to 2390 TFLOP/s, by the box), 4096 x 6144 x 2048 with
+// fp32 scales 61 to 66 us (1570 to 1690);
 // with 32 or 16 blocks of K, what a tile costs before its first product and
 // behind its last (5 us) is a sixth to a third of its time.
 template <int TN, int MODE, bool E8, int ROWS>
@@ -741,7 +753,7 @@ __global__ void __launch_bounds__(512) matmul_few_kernel(const MatmulArgs p) {
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // rows past the end read row 0 of their tile, and are not stored
+  // rows past the end read the last row, and are not stored
   const uint8_t* wp[NT];
   const uint8_t* ap[MT];
 #pragma unroll

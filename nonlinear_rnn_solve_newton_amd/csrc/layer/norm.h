@@ -38,8 +38,6 @@ struct NormArgs {
   float eps;
 };
 
-// 8 consecutive columns starting at d: one wide access where every row is
-// aligned for it (VEC), else single elements up to D; columns past D read 0
 // STREAM: past the caches
 template <bool STREAM, class V>
 __device__ __forceinline__ V ld_vec(const V* p) {
@@ -51,6 +49,8 @@ __device__ __forceinline__ void st_vec(V* p, V v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, p);
   else *p = v;
 }
+// 8 consecutive columns starting at d: one wide access where every row is
+// aligned for it (VEC), else single elements up to D; columns past D read 0
 template <class XT, bool VEC, bool STREAM = false>
 __device__ __forceinline__ void ld8(const XT* p, int d, int D, float (&v)[8]) {
   if constexpr (VEC) {
