@@ -37,6 +37,8 @@ class RecurrentBlock:
         if cell not in GATES:
             raise PararnnError(f"cell must be one of {sorted(GATES)}, got {cell!r}")
         G = GATES[cell]
+        if not all(isinstance(t, torch.Tensor) for t in (norm_w, w, coef)) or norm_w.dim() != 1:
+            raise PararnnError("norm_w, w and coef must be tensors, norm_w of one dimension")
         if w.dim() != 2 or w.shape[0] % G or w.shape[1] != norm_w.shape[0]:
             raise PararnnError(f"w must be [{G}*D][{norm_w.shape[0]}], got {tuple(w.shape)}")
         self.cell, self.G, self.D, self.E = cell, G, w.shape[0] // G, w.shape[1]
