@@ -22,7 +22,7 @@ def check(x, got, c=8.0):
         close(got[k], (v, 5 * e if k == "dlam" else e), k)
 
 
-# tiles per chunk row: 800 (groups of 1, over 3072 tickets), 100 (groups of 2), 20 (4), 6 and fewer (8)
+# tiles per chunk row: 800 (groups of 1, two ticket counters), 100 (groups of 2), 20 (4), 6 and fewer (8)
 SHAPES = [(800, 800, 2), (800, 800, 3), (100, 1100, 4), (100, 1100, 5), (20, 900, 50), (3, 1500, 101), (1, 3000, 1),
           (2, 1025, 6)]
 
