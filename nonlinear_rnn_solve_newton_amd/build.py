@@ -18,6 +18,8 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libpararnn.so"
 # the operators of the layer around the solver (include/pararnn_layer.h)
 LAYER_LIB = PKG / "libpararnn_layer.so"
+# the operators of a delta-rule layer (include/pararnn_delta.h)
+DELTA_LIB = PKG / "libpararnn_delta.so"
 # measurement kernels for the device ceilings bench.py reports (not the solver)
 CEIL_LIB = PKG / "libceilings.so"
 ARCH = "gfx950"
@@ -53,6 +55,7 @@ def build_one(src: Path, out: Path, verbose: bool = False, extra_flags=(), host_
 def build(verbose: bool = False, extra_flags=()) -> Path:
     build_one(CSRC / "ceilings.hip", CEIL_LIB, verbose, extra_flags)
     build_one(CSRC / "layer.hip", LAYER_LIB, verbose, extra_flags)
+    build_one(CSRC / "delta.hip", DELTA_LIB, verbose, extra_flags)
     return build_one(CSRC / "pararnn.hip", LIB, verbose, extra_flags)
 
 

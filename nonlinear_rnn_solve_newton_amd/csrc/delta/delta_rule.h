@@ -1,0 +1,1146 @@
+// delta_rule.h -- gated delta rule over chunks of 64 steps, its adjoint, and
+// its single-token step. Per value head, with S [dk][dv], unit q and k, decay a
+// and write strength b (0 < b < 1):
+//   S_t = a S_{t-1} + k b (v - a S_{t-1}^T k)^T,   o_t = scale S_t^T q.
+//
+// Within a chunk, with G_i the sum of log a over its first i steps, S0 the state
+// in front of it and E_ij = exp(G_i - G_j) (zero where a document starts in
+// between), the read values are X = V - diag(e^G) K S0 and
+//   y = T X,  T = (1 + strictly lower(E_ij k_i.k_j b_j))^-1   (v less what k reads)
+//   O = scale e^G Q S0 + P y,   P = lower(scale E_ij q_i.k_j b_j)
+//   S1 = e^G_64 S0 + K^T (e^(G_64 - G) b y).
+// |T_ij| <= b_j <= 1: it is a product of contractions between two unit keys. T
+// is inverted by substitution in blocks of 16 and joined, never by its series,
+// whose terms reach C(63, 31) for equal keys.
+//
+// delta_prep_kernel makes T, P and the rows' factors of all chunks at once;
+// delta_scan_kernel carries the state, a wave per 16 columns of dv, which do not
+// depend on each other. The adjoint carries dS back the same way,
+//   dY = P^T dO + e^(G_64 - G) b K dS1,  dX = T^T dY = dV,
+//   dS0 = e^G_64 dS1 + (scale e^G Q)^T dO - (e^G K)^T dX,
+// and delta_grad_kernel takes the rest of all chunks at once:
+//   dQ = scale e^G dO S0^T + D0 K,               D0_ij = scale E_ij b_j dO_i.y_j (i >= j)
+//   dK read = D1 K - e^G dX S0^T,                D1_ij = -E_ij b_j dX_i.y_j      (i > j)
+//   dK written = D0^T Q + D1^T K + e^(G_64 - G) b y dS1^T
+//   dG_i = q_i.dQ_i + k_i.(dK read)_i - k_i.(dK written)_i,  + <S1, dS1> at the last
+//   b dL/db = k.(dK written),  which a gate's gradient (1 - b) b dL/db takes as it is.
+#pragma once
+
+#include "delta_common.h"
+
+namespace pararnn {
+
+constexpr int kDeltaChunk = 64;
+
+struct DeltaView {  // [B][L][..], packed from the third dimension on; strides in elements
+  const void* p;
+  long long batch, token;
+};
+
+struct DeltaArgs {
+  DeltaView q, k, v, gates;
+  DeltaView gq, gk, gv, dgates;  // adjoint: outputs (gradients of q, k, v and the gates)
+  const float* lam;              // [HV]
+  const float* s0;               // [B][HV][dk][dv] or nullptr: the state in front; adjoint: dsT
+  float* sT;                     // the state behind, or nullptr; adjoint: ds0
+  void* o;                       // [B][L][HV][dv]; adjoint: dO
+  const int* lengths;
+  const uint8_t* reset;
+  bf16x8* frags;                 // per chunk and value head: planes of T and P as operands
+  float* rows;                   // per chunk and value head: kRows x 64 factors
+  float* states;                 // saved: [B HV][chunks][dk][dv] the state in front of each chunk, or nullptr
+  float* ys;                     // saved: [B HV][chunks][64][dv] y
+  float* dstates;                // adjoint: [B HV][chunks][dk][dv] dS behind each chunk
+  float* dxs;                    // adjoint: [B HV][chunks][64][dv] dX
+  float* dlam_part;              // adjoint: [HV][B chunks]
+  int B, L, H, HV, dk, dv, nc;
+  float c, eps, scale;
+  int wide_qk, wide_v, wide_dqk, wide_dv, wide_o;  // rows whose 8 elements take 16-byte accesses: a multiple of 8 of them
+};
+
+// factors of a chunk's rows
+enum { kRowX = 0, kRowO = 1, kRowS = 2, kRowWhole = 3, kRowK = 4, kRowQ = 5, kRowB = 6, kRowG = 7, kRowR = 8,
+       kRowSeg = 9, kRows = 10 };
+
+// Blocks (16 rows x 32 inner indexes) of a lower triangular 64 x 64 operand,
+// and of its transpose, that are not zero: 6 of 8
+constexpr int kTriBlocks = 6;
+__host__ __device__ constexpr int low_block(int i, int kb) { return i < 2 ? i : 2 + 2 * (i - 2) + kb; }
+__host__ __device__ constexpr int up_block(int j, int kb) { return j < 2 ? 2 * j + kb : 4 + (j - 2); }
+// planes per chunk: T, then P
+template <class UT, bool ADJ>
+struct DeltaFrags {
+  static constexpr int NT = 3, NP = ADJ ? 3 : DeltaPlanes<UT>::NO;
+  static constexpr int T = kTriBlocks * NT * 64, P = kTriBlocks * NP * 64, ALL = T + P;
+};
+
+__device__ __forceinline__ int delta_len(const DeltaArgs& p, int b) {
+  return p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
+}
+template <class UT>
+__device__ __forceinline__ const UT* at(const DeltaView& v, int b, long long t) {
+  return static_cast<const UT*>(v.p) + b * v.batch + t * v.token;
+}
+template <class UT>
+__device__ __forceinline__ UT* out_at(const DeltaView& v, int b, long long t) {
+  return static_cast<UT*>(const_cast<void*>(v.p)) + b * v.batch + t * v.token;
+}
+
+// 16 x 16 x 16 product in fp32: A from workgroup memory (row m, columns 4 g ..),
+// B as a result tile holds it
+__device__ __forceinline__ f32x4 mul16(const float* a, const f32x4& b, f32x4 c) {
+  const f32x4 x = *reinterpret_cast<const f32x4*>(a);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s], b[s], c, 0, 0, 0);
+  return c;
+}
+
+// A workgroup per chunk and value head: row factors, T and P (ADJ: their
+// transposes) as operands of the scan, in memory order of its reads.
+template <class UT, int DK, bool ADJ>
+__global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
+  typedef DeltaFrags<UT, ADJ> F;
+  constexpr int NP = DeltaPlanes<UT>::NP, KB = DK / 32, ROW = 68;
+  __shared__ float sm[64 * ROW], sp[64 * ROW], st[64 * ROW];
+  __shared__ float sg[64], sb[64], sseg[64], srk[64], srq[64];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
+  const int ch = blockIdx.x % p.nc, bh = blockIdx.x / p.nc, b = bh / p.HV, hv = bh % p.HV, h = hv / (p.HV / p.H);
+  const int t0 = ch * kDeltaChunk, len = delta_len(p, b);
+  if (t0 >= len) return;
+  const int n = min(len - t0, kDeltaChunk);
+  float* rows = p.rows + (static_cast<long long>(bh) * p.nc + ch) * (kRows * 64);
+
+  // products of the wave's 16 rows of k and q with the keys up to them
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float nk = 0.0f, nq = 0.0f;
+  {
+    const int i = 16 * w + m;
+    const UT* kr = at<UT>(p.k, b, t0 + min(i, n - 1)) + h * p.dk;
+    const UT* qr = at<UT>(p.q, b, t0 + min(i, n - 1)) + h * p.dk;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int d = 32 * kb + 8 * g;
+      const Raw8<UT> rk = load_raw8<UT>(kr, d, p.dk, i < n, p.wide_qk), rq = load_raw8<UT>(qr, d, p.dk, i < n, p.wide_qk);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        nk = fmaf(rk.at(e), rk.at(e), nk);
+        nq = fmaf(rq.at(e), rq.at(e), nq);
+      }
+      bf16x8 ak[NP], aq[NP];
+      planes_of(rk, ak);
+      planes_of(rq, aq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+          const int r = 16 * j + m;
+          bf16x8 bk[NP];
+          planes_of(load_raw8<UT>(at<UT>(p.k, b, t0 + min(r, n - 1)) + h * p.dk, d, p.dk, r < n, p.wide_qk), bk);
+          mma<NP, NP>(kk[j], ak, bk);
+          mma<NP, NP>(qk[j], aq, bk);
+        }
+    }
+  }
+  nk += __shfl_xor(nk, 16, 64);
+  nk += __shfl_xor(nk, 32, 64);
+  nq += __shfl_xor(nq, 16, 64);
+  nq += __shfl_xor(nq, 32, 64);
+  if (g == 0) {
+    srk[16 * w + m] = 1.0f / sqrtf(nk + p.eps);
+    srq[16 * w + m] = 1.0f / sqrtf(nq + p.eps);
+  }
+  if (w == 0) {  // the gates: a lane per step
+    const int i = lane;
+    const bool on = i < n;
+    const UT* gp = at<UT>(p.gates, b, t0 + min(i, n - 1)) + hv;
+    const float r = on ? sigm(load1(gp)) : 0.0f, beta = on ? sigm(load1(gp + p.HV)) : 0.0f;
+    const float coef = -p.c * softplus(p.lam[hv]);
+    float G = on ? coef * r : 0.0f;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const float u = __shfl_up(G, o, 64);
+      if (i >= o) G += u;
+    }
+    const bool start = on && p.reset && p.reset[static_cast<long long>(b) * p.L + t0 + i] != 0;
+    const unsigned long long starts = __ballot(start);
+    const int seg = __popcll(starts & (~0ull >> (63 - i)));
+    sg[i] = G;
+    sb[i] = beta;
+    sseg[i] = static_cast<float>(seg);
+    rows[kRowB * 64 + i] = beta;
+    rows[kRowG * 64 + i] = G;
+    rows[kRowR * 64 + i] = r;
+    rows[kRowSeg * 64 + i] = static_cast<float>(seg);
+  }
+  __syncthreads();
+  constexpr float kLog2e = 1.4426950408889634f;
+  if (w == 1) {
+    const int i = lane;
+    const float G = sg[i], Ge = sg[63], se = sseg[63];
+    const float gamma = sseg[i] == 0.0f ? __builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
+    const float tail = sseg[i] == se ? __builtin_amdgcn_exp2f((Ge - G) * kLog2e) : 0.0f;
+    rows[kRowX * 64 + i] = gamma * srk[i];
+    rows[kRowO * 64 + i] = p.scale * gamma * srq[i];
+    rows[kRowS * 64 + i] = tail * srk[i] * sb[i];
+    rows[kRowWhole * 64 + i] = se == 0.0f ? __builtin_amdgcn_exp2f(Ge * kLog2e) : 0.0f;
+    rows[kRowK * 64 + i] = srk[i];
+    rows[kRowQ * 64 + i] = srq[i];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = 16 * j + m;
+    const float Gc = sg[c], sc = sseg[c], kc = srk[c] * sb[c];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * w + 4 * g + e;
+      const bool low = i >= c && sseg[i] == sc;
+      const float d = low ? __builtin_amdgcn_exp2f((sg[i] - Gc) * kLog2e) * kc : 0.0f;
+      sm[i * ROW + c] = low && i > c ? d * srk[i] * kk[j][e] : 0.0f;
+      sp[i * ROW + c] = low ? p.scale * d * srq[i] * qk[j][e] : 0.0f;
+      if (j > w) st[i * ROW + c] = 0.0f;
+    }
+  }
+  __syncthreads();
+  if (w == 0) {  // the four diagonal blocks: lane (m, g) solves column m of block g
+    float x[16];
+    const float* a = sm + 16 * g * ROW + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == m ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j4 = 0; j4 < i; j4 += 4) {
+        const f32x4 r = *reinterpret_cast<const f32x4*>(a + i * ROW + j4);
+#pragma unroll
+        for (int j = j4; j < i && j < j4 + 4; ++j) v = fmaf(-r[j - j4], x[j], v);
+      }
+      x[i] = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st[(16 * g + i) * ROW + 16 * g + m] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int d = 1; d < 4; ++d) {  // the blocks below: T_ij = -T_ii (sum of M_ik T_kj over j <= k < i)
+    if (w >= d) {
+      const int j = w - d;
+      f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = j; k < w; ++k) {
+        f32x4 t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = st[(16 * k + 4 * g + e) * ROW + 16 * j + m];
+        s = mul16(sm + (16 * w + m) * ROW + 16 * k + 4 * g, t, s);
+      }
+      const f32x4 r = mul16(st + (16 * w + m) * ROW + 16 * w + 4 * g, s, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st[(16 * w + 4 * g + e) * ROW + 16 * j + m] = -r[e];
+    }
+    __syncthreads();
+  }
+  bf16x8* out = p.frags + (static_cast<long long>(bh) * p.nc + ch) * F::ALL;
+  for (int item = w; item < 2 * kTriBlocks; item += 4) {
+    const int id = item % kTriBlocks;
+    const float* src = item < kTriBlocks ? st : sp;
+    int i, kb;
+    if constexpr (ADJ) {
+      i = id < 4 ? id / 2 : id - 2;
+      kb = id < 4 ? id % 2 : 1;
+    } else {
+      i = id < 2 ? id : 2 + (id - 2) / 2;
+      kb = id < 2 ? 0 : (id - 2) % 2;
+    }
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = 32 * kb + (e < 4 ? 0 : 16) + 4 * g + (e & 3), r = 16 * i + m;
+      x[e] = ADJ ? src[c * ROW + r] : src[r * ROW + c];
+    }
+    bf16x8 o[3];
+    if (item < kTriBlocks) {
+      split8<3>(x, o);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) out[(id * 3 + pl) * 64 + lane] = o[pl];
+    } else {
+      split8<F::NP>(x, o);
+#pragma unroll
+      for (int pl = 0; pl < F::NP; ++pl) out[F::T + (id * F::NP + pl) * 64 + lane] = o[pl];
+    }
+  }
+}
+
+// What a chunk brings into workgroup memory for the scans
+template <class UT, int DK, bool ADJ>
+struct DeltaBuf {
+  static constexpr int NP = DeltaPlanes<UT>::NP;
+  typedef DeltaFrags<UT, ADJ> F;
+  DeltaTile<DK, NP> k, q;
+  bf16x8 frags[F::ALL];
+  float rows[4 * 64];
+};
+
+// The scans' common part: which columns a wave has, and the way of a chunk
+// from memory to workgroup memory, through registers, one chunk ahead
+template <class UT, int DK, int NC, int NW, bool ADJ>
+struct DeltaScan {
+  static constexpr int NP = DeltaPlanes<UT>::NP, NT = 64 * NW, RT = DK / 16, KB = DK / 32;
+  typedef DeltaFrags<UT, ADJ> F;
+  typedef DeltaBuf<UT, DK, ADJ> Buf;
+  static constexpr int NBUF = 2 * sizeof(Buf) <= 160 * 1024 ? 2 : 1;
+  static constexpr int TP = 64 * DK / 8 / NT, FP = (F::ALL + NT - 1) / NT, VP = 256 / NT;
+  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0, "whole rounds");
+
+  const DeltaArgs& p;
+  int tid, lane, w, m, g, b, hv, h, bh, col0, len, nch;
+  bool idle;
+  Raw8<UT> rk[TP], rq[TP];
+  bf16x8 rf[FP];
+  float rv[VP];
+  float vv[NC][4][4];  // the chunk's rows of v (dO), as a result tile holds them
+
+  __device__ __forceinline__ explicit DeltaScan(const DeltaArgs& a) : p(a) {
+    tid = threadIdx.x;
+    lane = tid & 63;
+    w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    m = lane & 15;
+    g = lane >> 4;
+    // the slices of a head follow each other on one XCD, whose L2 holds its chunk
+    const int nsl = (p.dv + 16 * NC * NW - 1) / (16 * NC * NW);
+    const int x = blockIdx.x % 8, l = blockIdx.x / 8;
+    bh = (l / nsl) * 8 + x;
+    idle = bh >= p.B * p.HV;
+    bh = idle ? 0 : bh;
+    b = bh / p.HV;
+    hv = bh % p.HV;
+    h = hv / (p.HV / p.H);
+    col0 = ((l % nsl) * NW + w) * 16 * NC;
+    len = delta_len(p, b);
+    nch = (len + kDeltaChunk - 1) / kDeltaChunk;
+  }
+  __device__ __forceinline__ int col(int cc) const { return col0 + 16 * cc + m; }
+  __device__ __forceinline__ void fetch(int ch, const void* vbase, long long vbatch, long long vtoken) {
+    const int t0 = ch * kDeltaChunk, n = min(len - t0, kDeltaChunk);
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {
+      const int e = tid + NT * i, row = e / (DK / 8), d = e % (DK / 8) * 8;
+      const long long t = t0 + min(row, n - 1);
+      rk[i] = load_raw8<UT>(at<UT>(p.k, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk);
+      rq[i] = load_raw8<UT>(at<UT>(p.q, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk);
+    }
+    const long long id = static_cast<long long>(bh) * p.nc + ch;
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+      if (tid + NT * i < F::ALL) rf[i] = p.frags[id * F::ALL + tid + NT * i];
+#pragma unroll
+    for (int i = 0; i < VP; ++i) rv[i] = p.rows[id * (kRows * 64) + tid + NT * i];
+    const UT* v = static_cast<const UT*>(vbase) + b * vbatch + static_cast<long long>(t0) * vtoken + static_cast<long long>(hv) * p.dv;
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * i + 4 * g + r;
+          vv[cc][i][r] = row < n && col(cc) < p.dv ? load1(v + row * vtoken + col(cc)) : 0.0f;
+        }
+  }
+  __device__ __forceinline__ void land(Buf& to) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {
+      const int e = tid + NT * i, row = e / (DK / 8), d = e % (DK / 8) * 8;
+      to.k.put(row, d, rk[i]);
+      to.q.put(row, d, rq[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+      if (tid + NT * i < F::ALL) to.frags[tid + NT * i] = rf[i];
+#pragma unroll
+    for (int i = 0; i < VP; ++i) to.rows[tid + NT * i] = rv[i];
+  }
+  __device__ __forceinline__ f32x4 row4(const Buf& u, int kind, int i) const {
+    return *reinterpret_cast<const f32x4*>(&u.rows[kind * 64 + 16 * i + 4 * g]);
+  }
+  // [dk][dv] fp32 matrices as the wave's tiles
+  __device__ __forceinline__ void load_state(const float* s, f32x4 (&S)[NC][RT]) const {
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * t + 4 * g + r;
+          S[cc][t][r] = s && row < p.dk && col(cc) < p.dv ? s[static_cast<long long>(row) * p.dv + col(cc)] : 0.0f;
+        }
+  }
+  __device__ __forceinline__ void store_state(float* s, const f32x4 (&S)[NC][RT]) const {
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+      if (col(cc) < p.dv) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * t + 4 * g + r;
+            if (row < p.dk) s[static_cast<long long>(row) * p.dv + col(cc)] = S[cc][t][r];
+          }
+      }
+  }
+  __device__ __forceinline__ void store_rows(float* y, const f32x4 (&Y)[NC][4]) const {
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+      if (col(cc) < p.dv) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[static_cast<long long>(16 * i + 4 * g + r) * p.dv + col(cc)] = Y[cc][i][r];
+      }
+  }
+};
+
+template <class UT, int DK, int NC, int NW>
+__global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaArgs p) {
+  typedef DeltaScan<UT, DK, NC, NW, false> D;
+  typedef typename D::Buf Buf;
+  constexpr int NP = D::NP, NO = DeltaPlanes<UT>::NO, RT = D::RT, KB = D::KB;
+  __shared__ Buf buf[D::NBUF];
+  D s(p);
+  if (s.idle) return;
+  const int m = s.m, g = s.g;
+  f32x4 S[NC][RT];
+  const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
+  float v[NC][4][4];
+  UT* const ob = static_cast<UT*>(p.o) + (static_cast<long long>(s.b) * p.L * p.HV + s.hv) * p.dv;
+  const long long orow = static_cast<long long>(p.HV) * p.dv;
+  if (s.nch > 0) {
+    s.fetch(0, p.v.p, p.v.batch, p.v.token);
+    s.land(buf[0]);
+  }
+  __syncthreads();
+  for (int ch = 0; ch < s.nch; ++ch) {
+    Buf& u = buf[D::NBUF == 2 ? ch & 1 : 0];
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[cc][i][r] = s.vv[cc][i][r];
+    if (ch + 1 < s.nch) s.fetch(ch + 1, p.v.p, p.v.batch, p.v.token);
+    const long long id = static_cast<long long>(s.bh) * p.nc + ch;
+    if (p.states) s.store_state(p.states + id * p.dk * p.dv, S);
+
+    f32x4 ks[NC][4], qs[NC][4];
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ks[cc][i] = qs[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      bf16x8 sb[NC][3];
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x8 a[NP];
+        u.k.rows(i, kb, m, g, a);
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(ks[cc][i], a, sb[cc]);
+        u.q.rows(i, kb, m, g, a);
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NP, NO>(qs[cc][i], a, sb[cc]);
+      }
+    }
+    bf16x8 xb[NC][2][3];
+    f32x4 y[NC][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 xg = s.row4(u, kRowX, i);
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ks[cc][i][r] = fmaf(-xg[r], ks[cc][i][r], v[cc][i][r]);
+    }
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(ks[cc][2 * kb], ks[cc][2 * kb + 1], xb[cc][kb]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) y[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb <= i / 2; ++kb) {
+        bf16x8 a[3];
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) a[pl] = u.frags[(low_block(i, kb) * 3 + pl) * 64 + s.lane];
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<3, 3>(y[cc][i], a, xb[cc][kb]);
+      }
+    }
+    if (p.ys) s.store_rows(p.ys + id * kDeltaChunk * p.dv, y);
+    // the output
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+    const int t0 = ch * kDeltaChunk, last = min(p.L - t0, kDeltaChunk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 og = s.row4(u, kRowO, i);
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) qs[cc][i] *= og;
+#pragma unroll
+      for (int kb = 0; kb <= i / 2; ++kb) {
+        bf16x8 a[NO];
+#pragma unroll
+        for (int pl = 0; pl < NO; ++pl) a[pl] = u.frags[D::F::T + (low_block(i, kb) * NO + pl) * 64 + s.lane];
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NO, NO>(qs[cc][i], a, xb[cc][kb]);
+      }
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+        if (s.col(cc) < p.dv) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * i + 4 * g + r;
+            if (row < last) store1(ob + (t0 + row) * orow + s.col(cc), qs[cc][i][r]);
+          }
+        }
+    }
+    // the state
+    const float whole = u.rows[kRowWhole * 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 sg = s.row4(u, kRowS, i);
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) y[cc][i] *= sg;
+    }
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) S[cc][t] *= whole;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        bf16x8 a[NP];
+        u.k.columns(t, kb, m, g, a);
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(S[cc][t], a, xb[cc][kb]);
+      }
+    }
+    if constexpr (D::NBUF == 1) __syncthreads();
+    if (ch + 1 < s.nch) s.land(buf[D::NBUF == 2 ? (ch + 1) & 1 : 0]);
+    __syncthreads();
+  }
+  if (p.sT) s.store_state(p.sT + at_state, S);
+  // rows behind the last chunk of the sequence
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+    if (s.col(cc) < p.dv)
+      for (long long t = static_cast<long long>(s.nch) * kDeltaChunk + g; t < p.L; t += 4)
+        store1(ob + t * orow + s.col(cc), 0.0f);
+}
+
+// dS from the last chunk to the first; p.s0 is dsT and p.sT is ds0
+template <class UT, int DK, int NC, int NW>
+__global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaArgs p) {
+  typedef DeltaScan<UT, DK, NC, NW, true> D;
+  typedef typename D::Buf Buf;
+  constexpr int NP = D::NP, RT = D::RT, KB = D::KB;
+  __shared__ Buf buf[D::NBUF];
+  D s(p);
+  if (s.idle) return;
+  const int m = s.m, g = s.g;
+  f32x4 S[NC][RT];
+  const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
+  const long long orow = static_cast<long long>(p.HV) * p.dv;
+  float v[NC][4][4];
+  if (s.nch > 0) {
+    s.fetch(s.nch - 1, p.o, p.L * orow, orow);
+    s.land(buf[D::NBUF == 2 ? (s.nch - 1) & 1 : 0]);
+  }
+  __syncthreads();
+  for (int ch = s.nch - 1; ch >= 0; --ch) {
+    Buf& u = buf[D::NBUF == 2 ? ch & 1 : 0];
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[cc][i][r] = s.vv[cc][i][r];
+    if (ch > 0) s.fetch(ch - 1, p.o, p.L * orow, orow);
+    const long long id = static_cast<long long>(s.bh) * p.nc + ch;
+    s.store_state(p.dstates + id * p.dk * p.dv, S);
+
+    f32x4 y[NC][4];
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      bf16x8 sb[NC][3];
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x8 a[NP];
+        u.k.rows(i, kb, m, g, a);
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(y[cc][i], a, sb[cc]);
+      }
+    }
+    bf16x8 xb[NC][2][3];
+    f32x4 x[NC][4];
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const float(&lo)[4] = v[cc][2 * kb], (&hi)[4] = v[cc][2 * kb + 1];
+        split_tiles<NP>(f32x4{lo[0], lo[1], lo[2], lo[3]}, f32x4{hi[0], hi[1], hi[2], hi[3]}, xb[cc][kb]);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 sg = s.row4(u, kRowS, i);
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) y[cc][i] *= sg;
+#pragma unroll
+      for (int kb = i / 2; kb < 2; ++kb) {
+        bf16x8 a[3];
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) a[pl] = u.frags[D::F::T + (up_block(i, kb) * 3 + pl) * 64 + s.lane];
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<3, NP>(y[cc][i], a, xb[cc][kb]);
+      }
+    }
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) x[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = i / 2; kb < 2; ++kb) {
+        bf16x8 a[3];
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) a[pl] = u.frags[(up_block(i, kb) * 3 + pl) * 64 + s.lane];
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<3, 3>(x[cc][i], a, xb[cc][kb]);
+      }
+    }
+    s.store_rows(p.dxs + id * kDeltaChunk * p.dv, x);
+    const float whole = u.rows[kRowWhole * 64];
+    bf16x8 ob[NC][2][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 xg = s.row4(u, kRowX, i), og = s.row4(u, kRowO, i);
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[cc][i][r] *= -xg[r];
+          y[cc][i][r] = og[r] * v[cc][i][r];
+        }
+    }
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        split_tiles<3>(x[cc][2 * kb], x[cc][2 * kb + 1], xb[cc][kb]);
+        split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], ob[cc][kb]);
+      }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) S[cc][t] *= whole;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        bf16x8 a[NP];
+        u.k.columns(t, kb, m, g, a);
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(S[cc][t], a, xb[cc][kb]);
+        u.q.columns(t, kb, m, g, a);
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(S[cc][t], a, ob[cc][kb]);
+      }
+    }
+    if constexpr (D::NBUF == 1) __syncthreads();
+    if (ch > 0) s.land(buf[D::NBUF == 2 ? (ch - 1) & 1 : 0]);
+    __syncthreads();
+  }
+  if (p.sT) s.store_state(p.sT + at_state, S);
+}
+
+// A workgroup per chunk and head of q and k: the gradients of q, k, v and the
+// gates. Wave (i, f): the chunk's 16 rows i, columns f of two halves of dk.
+template <class UT, int DK>
+struct DeltaGradLds {
+  static constexpr int NP = DeltaPlanes<UT>::NP, RT = DK / 16;
+  typedef DeltaTile<DK, NP> Tile;
+  struct Stage {  // 32 columns of dv, in the order of the operands' reads
+    bf16x8 s[RT * 3 * 64], ds[RT * 3 * 64], y[4 * 3 * 64], x[4 * 3 * 64], o[4 * NP * 64];
+  };
+  static constexpr bool APART = sizeof(Stage) + 2 * sizeof(Tile) <= 120 * 1024;  // the tiles beside the stage
+  static constexpr int ROW = 68;
+  struct Mats { float d0[64 * ROW], d1[64 * ROW]; };
+  static constexpr size_t a16(size_t x) { return (x + 15) / 16 * 16; }
+  // stage | (d0, d1 on the stage where the tiles lie apart, else behind the tiles)
+  static constexpr size_t kStage = a16(sizeof(Stage)), kTiles = a16(2 * sizeof(Tile));
+  static constexpr size_t TILES = APART ? kStage : 0;
+  static constexpr size_t MATS = APART ? 0 : kTiles;
+  static constexpr size_t BYTES = APART ? kStage + kTiles : (kStage > kTiles + sizeof(Mats) ? kStage : kTiles + sizeof(Mats));
+};
+
+template <class UT, int DK>
+__global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
+  typedef DeltaGradLds<UT, DK> M;
+  typedef typename M::Tile Tile;
+  constexpr int NP = M::NP, RT = M::RT, HT = RT / 2, ROW = M::ROW;
+  static_assert(M::BYTES + 16384 <= 160 * 1024, "fits the workgroup's memory");
+  static_assert(sizeof(typename M::Mats) <= M::kStage || !M::APART, "the matrices fit where the stage was");
+  __shared__ __attribute__((aligned(16))) char lds[M::BYTES];
+  __shared__ float srow[kRows * 64], spart[2][4][64], sdot[8];
+  typename M::Stage& sg = *reinterpret_cast<typename M::Stage*>(lds);
+  Tile& tk = reinterpret_cast<Tile*>(lds + M::TILES)[0];
+  Tile& tq = reinterpret_cast<Tile*>(lds + M::TILES)[1];
+  typename M::Mats& mt = *reinterpret_cast<typename M::Mats*>(lds + M::MATS);
+
+  const int tid = threadIdx.x, lane = tid & 63, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
+  const int w = w8 & 3, f = w8 >> 2, per = p.HV / p.H;
+  const int ch = blockIdx.x % p.nc, b = blockIdx.x / p.nc / p.H, h = blockIdx.x / p.nc % p.H;
+  const int t0 = ch * kDeltaChunk, len = delta_len(p, b), rows_out = min(p.L - t0, kDeltaChunk);
+  if (t0 >= len) {  // no step: zeros
+    for (int i = tid; i < rows_out * p.dk; i += 512) {
+      store1(out_at<UT>(p.gq, b, t0 + i / p.dk) + h * p.dk + i % p.dk, 0.0f);
+      store1(out_at<UT>(p.gk, b, t0 + i / p.dk) + h * p.dk + i % p.dk, 0.0f);
+    }
+    for (int i = tid; i < rows_out * per * p.dv; i += 512)
+      store1(out_at<UT>(p.gv, b, t0 + i / (per * p.dv)) + static_cast<long long>(h) * per * p.dv + i % (per * p.dv), 0.0f);
+    for (int i = tid; i < rows_out * per; i += 512) {
+      UT* to = out_at<UT>(p.dgates, b, t0 + i / per) + h * per + i % per;
+      store1(to, 0.0f);
+      store1(to + p.HV, 0.0f);
+    }
+    if (tid < per && p.dlam_part) p.dlam_part[(static_cast<long long>(h) * per + tid) * p.B * p.nc + b * p.nc + ch] = 0.0f;
+    return;
+  }
+  const int n = min(len - t0, kDeltaChunk);
+  constexpr float kLog2e = 1.4426950408889634f;
+  auto tiles = [&]() {
+    for (int e = tid; e < 64 * DK / 8; e += 512) {
+      const int row = e / (DK / 8), d = e % (DK / 8) * 8;
+      const long long t = t0 + min(row, n - 1);
+      tk.put(row, d, load_raw8<UT>(at<UT>(p.k, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk));
+      tq.put(row, d, load_raw8<UT>(at<UT>(p.q, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk));
+    }
+  };
+  if constexpr (M::APART) tiles();
+
+  f32x4 dq[HT], dk[HT];
+  float qsum[4], ksum[4];  // q.dQ and k.dK over the value heads, of the lane's 4 rows
+#pragma unroll
+  for (int t = 0; t < HT; ++t) dq[t] = dk[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) qsum[r] = ksum[r] = 0.0f;
+
+  for (int hr = 0; hr < per; ++hr) {
+    const int hv = h * per + hr;
+    const long long id = (static_cast<long long>(b) * p.HV + hv) * p.nc + ch;
+    const float* S = p.states + id * p.dk * p.dv;
+    const float* dS = p.dstates + id * p.dk * p.dv;
+    const float* Y = p.ys + id * kDeltaChunk * p.dv;
+    const float* X = p.dxs + id * kDeltaChunk * p.dv;
+    const UT* O = static_cast<const UT*>(p.o) + ((static_cast<long long>(b) * p.L + t0) * p.HV + hv) * p.dv;
+    const long long orow = static_cast<long long>(p.HV) * p.dv;
+    for (int i = tid; i < kRows * 64; i += 512) srow[i] = p.rows[id * (kRows * 64) + i];
+    f32x4 qo[HT], kx[HT], yd[HT], dd[4];
+    float dot = 0.0f;
+#pragma unroll
+    for (int t = 0; t < HT; ++t) qo[t] = kx[t] = yd[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dd[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int nb = (p.dv + 31) / 32;
+    for (int vb = 0; vb < nb; ++vb) {
+      // 8 columns per lane: lane (m, g) of tile t has row 16 t + m, columns 32 vb + 8 g ..
+      const int d = 32 * vb + 8 * g;
+      __syncthreads();
+      if (w8 < RT) {
+        const int r = 16 * w8 + m;
+        const bool on = r < p.dk;
+        const Raw8<float> a = load_raw8<float>(S + static_cast<long long>(on ? r : 0) * p.dv, d, p.dv, on, p.wide_o);
+        const Raw8<float> e = load_raw8<float>(dS + static_cast<long long>(on ? r : 0) * p.dv, d, p.dv, on, p.wide_o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot = fmaf(a.at(i), e.at(i), dot);
+        bf16x8 o[3];
+        planes_of(a, o);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) sg.s[(w8 * 3 + pl) * 64 + lane] = o[pl];
+        planes_of(e, o);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) sg.ds[(w8 * 3 + pl) * 64 + lane] = o[pl];
+      }
+      {
+        const int r = 16 * w + m;
+        const bool on = r < n;
+        const Raw8<float> a = load_raw8<float>((f ? X : Y) + static_cast<long long>(r) * p.dv, d, p.dv, true, p.wide_o);
+        bf16x8 o[3];
+        planes_of(a, o);
+        bf16x8* to = f ? sg.x : sg.y;
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) to[(w * 3 + pl) * 64 + lane] = o[pl];
+        if (f) {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = on ? a.at(i) : 0.0f;
+          if (r < rows_out) store8(out_at<UT>(p.gv, b, t0 + r) + static_cast<long long>(hv) * p.dv, d, p.dv, p.wide_dv, x);
+        } else {
+          planes_of(load_raw8<UT>(O + (on ? r : 0) * orow, d, p.dv, on, p.wide_v), o);
+#pragma unroll
+          for (int pl = 0; pl < NP; ++pl) sg.o[(w * NP + pl) * 64 + lane] = o[pl];
+        }
+      }
+      __syncthreads();
+      bf16x8 ao[NP], ax[3], ay[3], bb[3];
+#pragma unroll
+      for (int pl = 0; pl < NP; ++pl) ao[pl] = sg.o[(w * NP + pl) * 64 + lane];
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        ax[pl] = sg.x[(w * 3 + pl) * 64 + lane];
+        ay[pl] = sg.y[(w * 3 + pl) * 64 + lane];
+      }
+#pragma unroll
+      for (int t = 0; t < HT; ++t) {
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) bb[pl] = sg.s[((f * HT + t) * 3 + pl) * 64 + lane];
+        mma<NP, 3>(qo[t], ao, bb);
+        mma<3, 3>(kx[t], ax, bb);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) bb[pl] = sg.ds[((f * HT + t) * 3 + pl) * 64 + lane];
+        mma<3, 3>(yd[t], ay, bb);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) bb[pl] = sg.y[(j * 3 + pl) * 64 + lane];
+          if (f == 0) mma<NP, 3>(dd[j], ao, bb);
+          else mma<3, 3>(dd[j], ax, bb);
+        }
+    }
+    __syncthreads();  // the stage has been read
+    if constexpr (!M::APART) tiles();
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
+    if (lane == 0) sdot[w8] = dot;
+    // D0 and D1
+    float* to = f ? mt.d1 : mt.d0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = 16 * j + m;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * w + 4 * g + e;
+        const bool low = (f ? i > c : i >= c) && srow[kRowSeg * 64 + i] == srow[kRowSeg * 64 + c];
+        const float x = (f ? -1.0f : p.scale) * srow[kRowB * 64 + c] *
+                        __builtin_amdgcn_exp2f((srow[kRowG * 64 + i] - srow[kRowG * 64 + c]) * kLog2e);
+        to[i * ROW + c] = low ? x * dd[j][e] : 0.0f;
+      }
+    }
+    __syncthreads();
+    f32x4 kr[HT], kw[HT];
+    const float se = srow[kRowSeg * 64 + 63], Ge = srow[kRowG * 64 + 63];
+    float rq[4], rk[4], part[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 16 * w + 4 * g + r;
+      const float gamma = srow[kRowSeg * 64 + i] == 0.0f ? __builtin_amdgcn_exp2f(srow[kRowG * 64 + i] * kLog2e) : 0.0f;
+      const float tail = srow[kRowSeg * 64 + i] == se ? __builtin_amdgcn_exp2f((Ge - srow[kRowG * 64 + i]) * kLog2e) : 0.0f;
+      const float wr = tail * srow[kRowB * 64 + i];
+      rk[r] = srow[kRowK * 64 + i];
+      rq[r] = srow[kRowQ * 64 + i];
+      part[0][r] = part[1][r] = part[2][r] = part[3][r] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < HT; ++t) {
+        qo[t][r] *= p.scale * gamma;
+        kr[t][r] = -gamma * kx[t][r];
+        kw[t][r] = wr * yd[t][r];
+        part[3][r] = fmaf(kw[t][r], rk[r] * tk.at(i, 16 * (f * HT + t) + m), part[3][r]);
+      }
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      bf16x8 c0[3], c1[3], c2[3], c3[3];
+      float x[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // rows of D0 and D1 with the keys' lengths
+        const int c = 32 * kb + (e < 4 ? 0 : 16) + 4 * g + (e & 3), r = 16 * w + m;
+        const float s = srow[kRowK * 64 + c];
+        x[e] = mt.d0[r * ROW + c] * s;
+        y[e] = mt.d1[r * ROW + c] * s;
+      }
+      split8<3>(x, c0);
+      split8<3>(y, c1);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // their columns, with the lengths of q and k
+        const int c = 32 * kb + (e < 4 ? 0 : 16) + 4 * g + (e & 3), r = 16 * w + m;
+        x[e] = mt.d0[c * ROW + r] * srow[kRowQ * 64 + c];
+        y[e] = mt.d1[c * ROW + r] * srow[kRowK * 64 + c];
+      }
+      split8<3>(x, c2);
+      split8<3>(y, c3);
+#pragma unroll
+      for (int t = 0; t < HT; ++t) {
+        bf16x8 bk[NP], bq[NP];
+        tk.columns(f * HT + t, kb, m, g, bk);
+        tq.columns(f * HT + t, kb, m, g, bq);
+        if (kb <= w / 2) {
+          mma<3, NP>(qo[t], c0, bk);
+          mma<3, NP>(kr[t], c1, bk);
+        }
+        if (kb >= w / 2) {
+          mma<3, NP>(kw[t], c2, bq);
+          mma<3, NP>(kw[t], c3, bk);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < HT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * w + 4 * g + r, d = 16 * (f * HT + t) + m;
+        const float qv = rq[r] * tq.at(i, d), kv = rk[r] * tk.at(i, d);
+        part[0][r] = fmaf(qv, qo[t][r], part[0][r]);
+        part[1][r] = fmaf(kv, kr[t][r], part[1][r]);
+        part[2][r] = fmaf(kv, kw[t][r], part[2][r]);
+        dq[t][r] += qo[t][r];
+        dk[t][r] += kr[t][r] + kw[t][r];
+      }
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[k][r] += __shfl_xor(part[k][r], off, 64);
+    if (m == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) spart[f][k][16 * w + 4 * g + r] = part[k][r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 16 * w + 4 * g + r;
+      qsum[r] += spart[0][0][i] + spart[1][0][i];
+      ksum[r] += spart[0][1][i] + spart[1][1][i] + spart[0][2][i] + spart[1][2][i];
+    }
+    if (w8 == 0) {  // the gates: a lane per step
+      const int i = lane;
+      const float a = spart[0][0][i] + spart[1][0][i], br = spart[0][1][i] + spart[1][1][i],
+                  bw = spart[0][2][i] + spart[1][2][i];
+      float last = spart[0][3][i] + spart[1][3][i];
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) last += __shfl_xor(last, off, 64);
+      float ss = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss += sdot[k];
+      last = fmaf(srow[kRowWhole * 64], ss, last);
+      float G = a + br - bw + (i == 63 ? last : 0.0f);
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {  // of log a: the sum over this step and later ones
+        const float u = __shfl_down(G, o, 64);
+        if (i + o < 64) G += u;
+      }
+      // a decay that a document's start hides has no gradient
+      const bool start = i > 0 ? srow[kRowSeg * 64 + i] != srow[kRowSeg * 64 + i - 1] : srow[kRowSeg * 64] != 0.0f;
+      const float dl = start || i >= n ? 0.0f : G;
+      const float r = srow[kRowR * 64 + i], lam = p.lam[hv];
+      if (i < rows_out) {
+        UT* go = out_at<UT>(p.dgates, b, t0 + i) + hv;
+        store1(go, -p.c * softplus(lam) * dl * r * (1.0f - r));
+        store1(go + p.HV, i < n ? bw * (1.0f - srow[kRowB * 64 + i]) : 0.0f);
+      }
+      if (p.dlam_part) {
+        float sum = dl * r;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        if (i == 0) p.dlam_part[static_cast<long long>(hv) * p.B * p.nc + b * p.nc + ch] = sum;
+      }
+    }
+    __syncthreads();
+  }
+  // through the lengths of q and k
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = 16 * w + 4 * g + r;
+    const float rk = srow[kRowK * 64 + i], rq = srow[kRowQ * 64 + i];
+    if (i < rows_out) {
+      UT* qo = out_at<UT>(p.gq, b, t0 + i) + h * p.dk;
+      UT* ko = out_at<UT>(p.gk, b, t0 + i) + h * p.dk;
+#pragma unroll
+      for (int t = 0; t < HT; ++t) {
+        const int d = 16 * (f * HT + t) + m;
+        if (d < p.dk) {
+          store1(qo + d, rq * fmaf(-rq * tq.at(i, d), qsum[r], dq[t][r]));
+          store1(ko + d, rk * fmaf(-rk * tk.at(i, d), ksum[r], dk[t][r]));
+        }
+      }
+    }
+  }
+}
+
+// dlam[hv] = -c s(lam) sum of its chunks' parts, in a fixed order
+__global__ void __launch_bounds__(256) delta_dlam_kernel(const float* part, const float* lam, float* dlam, int n, float c) {
+  __shared__ float s[256];
+  const int hv = blockIdx.x, tid = threadIdx.x;
+  float v = 0.0f;
+  for (int i = tid; i < n; i += 256) v += part[static_cast<long long>(hv) * n + i];
+  s[tid] = v;
+  __syncthreads();
+#pragma unroll
+  for (int o = 128; o >= 1; o >>= 1) {
+    if (tid < o) s[tid] += s[tid + o];
+    __syncthreads();
+  }
+  if (tid == 0) dlam[hv] = -c * sigm(lam[hv]) * s[0];
+}
+
+struct DeltaStepArgs {
+  const void *q, *k, *v, *gates;        // rows of a request, `*_row` elements apart
+  long long q_row, k_row, v_row, g_row;
+  const float* lam;
+  const int* slots;
+  float* state;  // [S][HV][dk][dv]
+  void* o;       // [B][HV][dv]
+  int B, H, HV, dk, dv, S;
+  float c, eps, scale;
+  int wide;      // rows of the state take 16-byte accesses
+};
+
+// One token: a workgroup per request, value head and 32 columns of the state,
+// 4 columns and every 32nd row per thread. o = a S^T q + (q.k) u needs the old
+// state only, so both sums over the rows come from one pass.
+template <class UT>
+__global__ void __launch_bounds__(256) delta_step_kernel(const DeltaStepArgs p) {
+  constexpr int NR = 4;  // rows per thread: dk <= 128
+  __shared__ float sq[128], sk[128];
+  __shared__ f32x4 sum[4][2][8];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int nsl = (p.dv + 31) / 32;
+  const int sl = blockIdx.x % nsl, bh = blockIdx.x / nsl, b = bh / p.HV, hv = bh % p.HV, h = hv / (p.HV / p.H);
+  const int cg = tid & 7, r0 = tid >> 3, col = 32 * sl + 4 * cg;
+  const int slot = p.slots ? p.slots[b] : b;
+  UT* out = static_cast<UT*>(p.o) + (static_cast<long long>(b) * p.HV + hv) * p.dv;
+  if (slot < 0 || slot >= p.S) {  // no request
+    if (tid < 32 && 32 * sl + tid < p.dv) store1(out + 32 * sl + tid, 0.0f);
+    return;
+  }
+  float* S = p.state + (static_cast<long long>(slot) * p.HV + hv) * p.dk * p.dv;
+  f32x4 s[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int r = r0 + 32 * i;
+    s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (r < p.dk) {
+      const float* at = S + static_cast<long long>(r) * p.dv + col;
+      if (p.wide) {
+        if (col < p.dv) s[i] = *reinterpret_cast<const f32x4*>(at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.dv) s[i][e] = at[e];
+      }
+    }
+  }
+  const UT* q = static_cast<const UT*>(p.q) + b * p.q_row + h * p.dk;
+  const UT* k = static_cast<const UT*>(p.k) + b * p.k_row + h * p.dk;
+  const UT* gp = static_cast<const UT*>(p.gates) + b * p.g_row + hv;
+  float qv[2], kv[2], sums[3] = {0.0f, 0.0f, 0.0f};  // q.q, k.k, q.k; every wave has them all
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int d = lane + 64 * i;
+    qv[i] = d < p.dk ? load1(q + d) : 0.0f;
+    kv[i] = d < p.dk ? load1(k + d) : 0.0f;
+    sums[0] = fmaf(qv[i], qv[i], sums[0]);
+    sums[1] = fmaf(kv[i], kv[i], sums[1]);
+    sums[2] = fmaf(qv[i], kv[i], sums[2]);
+  }
+  const float a = __builtin_amdgcn_exp2f(-p.c * softplus(p.lam[hv]) * sigm(load1(gp)) * 1.4426950408889634f);
+  const float beta = sigm(load1(gp + p.HV));
+  float vv[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    vv[e] = col + e < p.dv ? load1(static_cast<const UT*>(p.v) + b * p.v_row + static_cast<long long>(hv) * p.dv + col + e) : 0.0f;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) sums[j] += __shfl_xor(sums[j], off, 64);
+  const float rq = 1.0f / sqrtf(sums[0] + p.eps), rk = 1.0f / sqrtf(sums[1] + p.eps);
+  if (w == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sq[lane + 64 * i] = qv[i] * rq;
+      sk[lane + 64 * i] = kv[i] * rk;
+    }
+  }
+  __syncthreads();
+  f32x4 ps = {0.0f, 0.0f, 0.0f, 0.0f}, os = ps;
+  float kr[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const float x = sq[r0 + 32 * i];
+    kr[i] = sk[r0 + 32 * i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ps[e] = fmaf(kr[i], s[i][e], ps[e]);
+      os[e] = fmaf(x, s[i][e], os[e]);
+    }
+  }
+#pragma unroll
+  for (int off = 8; off <= 32; off <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ps[e] += __shfl_xor(ps[e], off, 64);
+      os[e] += __shfl_xor(os[e], off, 64);
+    }
+  if (lane < 8) {
+    sum[w][0][lane] = ps;
+    sum[w][1][lane] = os;
+  }
+  __syncthreads();
+  ps = sum[0][0][cg] + sum[1][0][cg] + sum[2][0][cg] + sum[3][0][cg];
+  os = sum[0][1][cg] + sum[1][1][cg] + sum[2][1][cg] + sum[3][1][cg];
+  f32x4 u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) u[e] = beta * fmaf(-a, ps[e], vv[e]);
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int r = r0 + 32 * i;
+    if (r < p.dk) {
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fmaf(kr[i], u[e], a * s[i][e]);
+      float* at = S + static_cast<long long>(r) * p.dv + col;
+      if (p.wide) {
+        if (col < p.dv) *reinterpret_cast<f32x4*>(at) = x;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.dv) at[e] = x[e];
+      }
+    }
+  }
+  if (r0 == 0) {
+    const float qk = sums[2] * rq * rk;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < p.dv) store1(out + col + e, p.scale * fmaf(a, os[e], qk * u[e]));
+  }
+}
+
+}  // namespace pararnn

@@ -11,29 +11,12 @@
 
 #include "../../include/pararnn_layer.h"
 #include "layer/gated_scan.h"
+#include "layer/host_common.h"
 #include "layer/matmul_fp8.h"
 #include "layer/norm.h"
 
 namespace pararnn {
 namespace {
-
-constexpr int kCUs = 256;
-constexpr size_t kAlign = 256;
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int check_hip(hipError_t e) { return e == hipSuccess ? PARARNN_OK : PARARNN_EHIP; }
-
-// A launch's size in threads is a 32-bit number: a larger one would run as its
-// low 32 bits (8388609 workgroups of 512 as one), without an error.
-constexpr long long kMaxThreads = 4294967295LL;
-
-template <typename F, typename... Args>
-int launch(F kernel, long long grid, int block, hipStream_t s, Args... args) {
-  if (grid > kMaxThreads / block) return PARARNN_EINVAL;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(block), 0, s, args...);
-  return check_hip(hipGetLastError());
-}
 
 // clears n16 16-byte words (a kernel rather than a memset: graphs of the
 // caller's stream capture it)
@@ -163,7 +146,6 @@ bool gated_ok(const pararnn_gated_opts* o, bool adj) {
   // one chunk is addressed with 32-bit offsets below 2^31
   return static_cast<double>(kMaxScanChunk) * 3 * o->D * 4 < 2147483648.0;
 }
-bool dtype_ok(int dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF16; }
 
 template <class UT, int C, bool RST>
 int launch_gated(const GatedArgs& a, bool adj, bool small, hipStream_t s) {

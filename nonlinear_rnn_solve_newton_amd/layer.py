@@ -1,4 +1,5 @@
-"""Operators of the recurrent layer around the solver (libpararnn_layer.so).
+"""Operators of the recurrent layer around the solver (libpararnn_layer.so) and
+of a delta-rule layer (libpararnn_delta.so).
 
   norm_residual   root-mean-square norm with the residual's addition, in the
                   input's type or in 8 bits with scales, and its adjoint
@@ -6,12 +7,16 @@
                   the projection that makes the gate inputs u
   gated_scan      gated linear recurrence over the sequence, its adjoint, and
                   gated_step, its form for single tokens
+  delta_scan      gated delta rule over the sequence, a matrix of state per head,
+                  its adjoint, and delta_step, its form for single tokens
 
 Like `binding`, this module checks tensors, allocates outputs and workspace
 with torch and passes raw device pointers plus torch's current HIP stream to
 the C entry points of include/pararnn_layer.h, whose comments define the
-operators. Every tensor must be contiguous and on the same ROCm device; a
-wrong type, shape or placement raises PararnnError. There is no fallback.
+operators (include/pararnn_delta.h for the delta-rule layer's). Every tensor
+must be contiguous, except where a call says that it takes views, and on the
+same ROCm device; a wrong type, shape or placement raises PararnnError. There is
+no fallback.
 """
 from __future__ import annotations
 
@@ -26,6 +31,8 @@ from .binding import BF16, F32, PKG, PararnnError, strerror
 
 LIB_PATH = PKG / "libpararnn_layer.so"
 HEADER = PKG.parent / "include" / "pararnn_layer.h"
+DELTA_LIB_PATH = PKG / "libpararnn_delta.so"
+DELTA_HEADER = PKG.parent / "include" / "pararnn_delta.h"
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -60,9 +67,18 @@ NORM_SAME, NORM_FP8, NORM_FP8_E8M0 = 0, 1, 2
 BLOCK = 128  # columns that share a scale
 
 
-def header_functions() -> list[str]:
-    """Names of the functions declared in include/pararnn_layer.h."""
-    return re.findall(r"^\s*[a-z_0-9]+\s+(pararnn_[a-z_0-9]+)\s*\(", HEADER.read_text(), re.M)
+class View(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class DeltaOpts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "L", "H", "HV", "dk", "dv", "dtype")] + [
+        (n, ctypes.c_float) for n in ("c", "eps", "scale")] + [("lengths", ctypes.c_void_p), ("reset", ctypes.c_void_p)]
+
+
+def header_functions(header=HEADER) -> list[str]:
+    """Names of the functions declared in include/pararnn_layer.h (or pararnn_delta.h)."""
+    return re.findall(r"^\s*[a-z_0-9]+\s+(pararnn_[a-z_0-9]+)\s*\(", header.read_text(), re.M)
 
 
 _lib = None
@@ -98,6 +114,28 @@ def lib():
         L.pararnn_matmul_fp8.restype = I32
         _lib = L
     return _lib
+
+
+_delta = None
+
+
+def delta_lib():
+    global _delta
+    if _delta is None:
+        if not DELTA_LIB_PATH.exists():
+            raise PararnnError(f"{DELTA_LIB_PATH} is not built; run __graft_entry__.build() first")
+        L = ctypes.CDLL(str(DELTA_LIB_PATH))
+        P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        D, V = ctypes.POINTER(DeltaOpts), ctypes.POINTER(View)
+        L.pararnn_delta_workspace_bytes.argtypes = [I32, D, ctypes.POINTER(SZ)]
+        L.pararnn_delta_saved_bytes.argtypes = [D, ctypes.POINTER(SZ)]
+        L.pararnn_delta_scan.argtypes = [V, V, V, V, P, P, P, P, P, P, SZ, D, P]
+        L.pararnn_delta_scan_adjoint.argtypes = [V, V, V, V, P, P, P, P, V, V, V, V, P, P, P, SZ, D, P]
+        L.pararnn_delta_step.argtypes = [V, V, V, V, P, P, P, P, I32, D, P]
+        for n in header_functions(DELTA_HEADER):
+            getattr(L, n).restype = I32
+        _delta = L
+    return _delta
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -141,8 +179,15 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def _launch(what: str, device: torch.device, *args):
     """The C call on torch's current stream of the tensors' device, which is
     made current for it where it is not."""
+    _run(getattr(lib(), what), what, device, args)
+
+
+def _launch_delta(what: str, device: torch.device, *args):
+    _run(getattr(delta_lib(), what), what, device, args)
+
+
+def _run(fn, what, device, args):
     i = device.index
-    fn = getattr(lib(), what)
     if _get_device() == i:
         st = fn(*args, _raw_stream(i))
     else:
@@ -410,4 +455,157 @@ def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Ten
         _dev(out, "out", out_dtype, (M, N), dev)
     o = MatmulOpts(M, N, K, rows, _SCALE[sa.dtype], _DTYPE[out_dtype])
     _launch("pararnn_matmul_fp8", dev, _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _ptr(bias), _ptr(out), ctypes.byref(o))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# gated delta rule
+
+def _view(t, name: str, dtype, shape: tuple, device) -> View:
+    """A tensor [B][L][...] (or [B][...] of a step) that is packed from its third
+    (second) dimension on; its rows and tokens may lie further apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PararnnError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise PararnnError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    lead = len(shape) - 2  # [B] or [B][L]
+    size, stride = t.shape, t.stride()
+    n = size[-1] * size[-2]
+    packed = (size[-1] == 1 or stride[-1] == 1) and (size[-2] == 1 or stride[-2] == size[-1])
+    token = stride[1] if lead == 2 and size[1] > 1 else n
+    batch = stride[0] if size[0] > 1 else token * (size[1] if lead == 2 else 1)
+    if not packed or token < n or batch < (token * (size[1] - 1) + n if lead == 2 else n):
+        raise PararnnError(f"{name} must be packed in its last two dimensions, its rows and tokens apart")
+    return View(t.data_ptr(), batch, token)
+
+
+def _delta_opts(q, k, v, gates, lam, c, eps, scale, lead, lengths=None, reset=None):
+    """Options, views and device of a call; lead: dimensions in front of the heads."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (gates, "gates")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise PararnnError(f"{name} must be a device tensor")
+        if t.dim() != lead + 2:
+            raise PararnnError(f"{name} must have {lead + 2} dimensions, got {t.dim()}")
+    if q.dtype not in _DTYPE:
+        raise PararnnError(f"q must be float32 or bfloat16, got {q.dtype}")
+    dev, at = q.device, tuple(q.shape[:lead])
+    H, dk = q.shape[lead:]
+    HV, dv = v.shape[lead:]
+    if 0 in q.shape or 0 in v.shape or HV % H:
+        raise PararnnError("q, k and v must not be empty, and v's heads a multiple of q's")
+    views = tuple(_view(t, n, q.dtype, (*at, *s), dev) for t, n, s in (
+        (q, "q", (H, dk)), (k, "k", (H, dk)), (v, "v", (HV, dv)), (gates, "gates", (2, HV))))
+    _dev(lam, "lam", torch.float32, (HV,), dev)
+    if lam is None:
+        raise PararnnError("lam must be a device tensor")
+    B, L = at[0], at[1] if lead == 2 else 1
+    _dev(lengths, "lengths", torch.int32, (B,), dev)
+    if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
+        reset = reset.view(torch.uint8)
+    _dev(reset, "reset", torch.uint8, (B, L), dev)
+    o = DeltaOpts(B, L, H, HV, dk, dv, _DTYPE[q.dtype], c, eps, dk ** -0.5 if scale is None else scale,
+                  _ptr(lengths), _ptr(reset))
+    return o, views, dev
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_bytes(kind: int, B: int, L: int, H: int, HV: int, dk: int, dv: int, dtype: int) -> int:
+    """Workspace of the forward (0) and the adjoint (1), bytes of `saved` (2)."""
+    n = ctypes.c_size_t()
+    o = DeltaOpts(B, L, H, HV, dk, dv, dtype, 1.0, 1.0, 1.0, None, None)
+    L_ = delta_lib()
+    st = (L_.pararnn_delta_saved_bytes(ctypes.byref(o), ctypes.byref(n)) if kind == 2
+          else L_.pararnn_delta_workspace_bytes(kind, ctypes.byref(o), ctypes.byref(n)))
+    if st != 0:
+        raise PararnnError(f"invalid sizes (dk at most 128, dv at most 512): {st} ({strerror(st)})")
+    return n.value
+
+
+def delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.Tensor, lam: torch.Tensor, *,
+               c: float = 8.0, eps: float = 1e-6, scale: Optional[float] = None, s0: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None, reset: Optional[torch.Tensor] = None, save: bool = False,
+               out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> dict:
+    """S_t = a S_{t-1} + k b (v - a S_{t-1}^T k)^T, o_t = scale S_t^T q for unit q
+    and k; log a = -c softplus(lam) s(gate_0), b = s(gate_1).
+
+    q, k [B][L][H][dk] (any lengths; made unit here), v [B][L][HV][dv] and gates
+    [B][L][2][HV], all bf16 or all fp32, views whose last two dimensions are
+    packed (columns of one product, say); value head v takes head v // (HV // H) of
+    q and k. lam [HV] fp32, s0 [B][HV][dk][dv] fp32 or None (zero), lengths and
+    reset as in gated_scan; scale None: dk^-1/2. dk at most 128, dv at most 512.
+    Returns dict(o [B][L][HV][dv], sT [B][HV][dk][dv] fp32 state after the last
+    step, saved (with save=True, for the adjoint), ws).
+    """
+    o, views, dev = _delta_opts(q, k, v, gates, lam, c, eps, scale, 2, lengths, reset)
+    B, L, H, HV, dk, dv = o.B, o.L, o.H, o.HV, o.dk, o.dv
+    _dev(s0, "s0", torch.float32, (B, HV, dk, dv), dev)
+    if out is None:
+        out = torch.empty(B, L, HV, dv, dtype=q.dtype, device=dev)
+    else:
+        _dev(out, "out", q.dtype, (B, L, HV, dv), dev)
+    ws, nws = _workspace(ws, _delta_bytes(0, B, L, H, HV, dk, dv, o.dtype), dev)
+    sT = torch.empty(B, HV, dk, dv, dtype=torch.float32, device=dev)
+    saved = (torch.empty(_delta_bytes(2, B, L, H, HV, dk, dv, o.dtype), dtype=torch.uint8, device=dev)
+             if save else None)
+    _launch_delta("pararnn_delta_scan", dev, *map(ctypes.byref, views), _ptr(lam), _ptr(s0), _ptr(out), _ptr(sT),
+                  _ptr(saved), _ptr(ws), nws, ctypes.byref(o))
+    return {"o": out, "sT": sT, "saved": saved, "ws": ws}
+
+
+def delta_scan_adjoint(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.Tensor, lam: torch.Tensor,
+                       do: torch.Tensor, saved: torch.Tensor, *, c: float = 8.0, eps: float = 1e-6,
+                       scale: Optional[float] = None, dsT: Optional[torch.Tensor] = None,
+                       lengths: Optional[torch.Tensor] = None, reset: Optional[torch.Tensor] = None,
+                       want_dlam: bool = True, want_ds0: bool = False, out: Optional[dict] = None,
+                       ws: Optional[torch.Tensor] = None) -> dict:
+    """Adjoint of delta_scan for do = dL/do [B][L][HV][dv] (q's type) and dsT =
+    dL/dsT [B][HV][dk][dv] fp32 or None; `saved` and the options are those of the
+    forward call. out: a dict of tensors or views dq, dk, dv, dgates to write to.
+    Returns dict(dq, dk, dv, dgates in the inputs' shapes and type, dlam [HV], ds0
+    [B][HV][dk][dv] fp32, ws)."""
+    o, views, dev = _delta_opts(q, k, v, gates, lam, c, eps, scale, 2, lengths, reset)
+    B, L, H, HV, dk, dv = o.B, o.L, o.H, o.HV, o.dk, o.dv
+    _dev(do, "do", q.dtype, (B, L, HV, dv), dev)
+    _dev(saved, "saved", torch.uint8, (_delta_bytes(2, B, L, H, HV, dk, dv, o.dtype),), dev)
+    if saved is None or do is None:
+        raise PararnnError("the adjoint needs do and the states saved by delta_scan(save=True)")
+    _dev(dsT, "dsT", torch.float32, (B, HV, dk, dv), dev)
+    g = {}
+    for n, t in (("dq", q), ("dk", k), ("dv", v), ("dgates", gates)):
+        g[n] = (out or {}).get(n)
+        if g[n] is None:
+            g[n] = torch.empty(t.shape, dtype=q.dtype, device=dev)
+    outs = tuple(_view(g[n], n, q.dtype, t.shape, dev) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dgates", gates)))
+    ws, nws = _workspace(ws, _delta_bytes(1, B, L, H, HV, dk, dv, o.dtype), dev)
+    dlam = torch.empty(HV, dtype=torch.float32, device=dev) if want_dlam else None
+    ds0 = torch.empty(B, HV, dk, dv, dtype=torch.float32, device=dev) if want_ds0 else None
+    _launch_delta("pararnn_delta_scan_adjoint", dev, *map(ctypes.byref, views), _ptr(lam), _ptr(saved), _ptr(do),
+                  _ptr(dsT), *map(ctypes.byref, outs), _ptr(dlam), _ptr(ds0), _ptr(ws), nws, ctypes.byref(o))
+    return {**g, "dlam": dlam, "ds0": ds0, "ws": ws}
+
+
+def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.Tensor, lam: torch.Tensor,
+               state: torch.Tensor, *, c: float = 8.0, eps: float = 1e-6, scale: Optional[float] = None,
+               slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One step for each of B requests, q, k [B][H][dk], v [B][HV][dv], gates
+    [B][2][HV] (views as in delta_scan): updates the entries slots[b] (int32 [B];
+    None: entry b) of the pool `state` [S][HV][dk][dv] fp32 in place and returns o
+    [B][HV][dv]. A slot outside 0..S-1 (-1, say) is a row without a request: o =
+    0. The slots must differ from each other."""
+    o, views, dev = _delta_opts(q, k, v, gates, lam, c, eps, scale, 1)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise PararnnError("state must be [S][HV][dk][dv]")
+    S = state.shape[0]
+    _dev(state, "state", torch.float32, (S, o.HV, o.dk, o.dv), dev)
+    _dev(slots, "slots", torch.int32, (o.B,), dev)
+    if out is None:
+        out = torch.empty(o.B, o.HV, o.dv, dtype=q.dtype, device=dev)
+    else:
+        _dev(out, "out", q.dtype, (o.B, o.HV, o.dv), dev)
+    _launch_delta("pararnn_delta_step", dev, *map(ctypes.byref, views), _ptr(lam), _ptr(slots), _ptr(state), _ptr(out),
+                  S, ctypes.byref(o))
     return out
