@@ -40,18 +40,18 @@ DeltaSizes delta_sizes(const pararnn_delta_opts* o, bool adj) {
                           ? (adj ? DeltaFrags<bf16, true>::ALL : DeltaFrags<bf16, false>::ALL)
                           : (adj ? DeltaFrags<float, true>::ALL : DeltaFrags<float, false>::ALL);
   return {round_up(chunks * frag * sizeof(bf16x8)), round_up(chunks * kRows * 64 * sizeof(float)),
-          round_up(chunks * o->dk * o->dv * sizeof(float)), round_up(chunks * kDeltaChunk * o->dv * sizeof(float)),
+          chunks * delta_tiles(o->dv) * delta_tiles(o->dk) * 1024, chunks * delta_tiles(o->dv) * 4096,
           round_up(chunks * sizeof(float))};
 }
 
-// packed rows of n elements, heads of d: 16-byte accesses of 8 elements
-bool wide_rows(const void* p, size_t es, long long batch, long long token, int d) {
-  return aligned(p, 16) && d % 8 == 0 && batch * es % 16 == 0 && token * es % 16 == 0;
+// every row and head starts at a multiple of `bytes`
+bool rows_aligned(const pararnn_view* v, size_t es, int d, size_t bytes, int B) {
+  return aligned(v->p, bytes) && d * es % bytes == 0 && v->token * es % bytes == 0 && (B == 1 || v->batch * es % bytes == 0);
 }
-bool wide_rows(const pararnn_view* v, size_t es, int d) { return wide_rows(v->p, es, v->batch, v->token, d); }
 
+constexpr long long kMaxToken = 1 << 22;  // 64 rows within 32-bit offsets
 bool view_ok(const pararnn_view* v, const pararnn_delta_opts* o, long long packed) {
-  if (!v || !v->p || v->token < packed || v->token > (1LL << 40) || v->batch > (1LL << 50)) return false;
+  if (!v || !v->p || v->token < packed || v->token > kMaxToken || v->batch > (1LL << 50)) return false;
   return o->B == 1 || v->batch >= static_cast<long long>(o->L - 1) * v->token + packed;
 }
 bool views_ok(const pararnn_view* q, const pararnn_view* k, const pararnn_view* v, const pararnn_view* g,
@@ -81,31 +81,53 @@ void delta_fill(DeltaArgs& a, const pararnn_view* q, const pararnn_view* k, cons
   a.c = o->c;
   a.eps = o->eps;
   a.scale = o->scale;
-  a.wide_qk = wide_rows(q, es, o->dk) && wide_rows(k, es, o->dk);
-  a.wide_v = wide_rows(v, es, o->dv);
 }
 
-template <class UT, int DK, bool ADJ>
+template <class UT, bool EVEN, int DK, bool ADJ>
 int run_prep(const DeltaArgs& a, hipStream_t s) {
-  return launch(delta_prep_kernel<UT, DK, ADJ>, static_cast<long long>(a.B) * a.HV * a.nc, 256, s, a);
+  return launch(delta_prep_kernel<UT, EVEN, DK, ADJ>, static_cast<long long>(a.B) * a.HV * a.nc, 256, s, a);
 }
 // the scans' grid: every head's slices on one XCD
 long long scan_grid(const DeltaArgs& a, int cols) { return ceil_div(static_cast<long long>(a.B) * a.HV, 8) * 8 * ceil_div(a.dv, cols); }
 
-template <class UT, int DK>
-int run_forward(const DeltaArgs& a, hipStream_t s) {
-  if (const int rc = run_prep<UT, DK, false>(a, s)) return rc;
-  return launch(delta_scan_kernel<UT, DK, 1, 4>, scan_grid(a, 64), 256, s, a);
+struct DeltaForward {
+  template <class UT, int MODE, int DK>
+  static int run(const DeltaArgs& a, const float*, float*, float*, hipStream_t s) {
+    if (const int rc = run_prep<UT, MODE != kOdd, DK, false>(a, s)) return rc;
+    return launch(delta_scan_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), 256, s, a);
+  }
+};
+struct DeltaAdjoint {
+  template <class UT, int MODE, int DK>
+  static int run(DeltaArgs a, const float* dsT, float* ds0, float* dlam, hipStream_t s) {
+    constexpr bool EVEN = MODE != kOdd;
+    if (const int rc = run_prep<UT, EVEN, DK, true>(a, s)) return rc;
+    a.s0 = dsT;
+    a.sT = ds0;
+    if (const int rc = launch(delta_back_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), 256, s, a)) return rc;
+    if (const int rc = launch(delta_grad_kernel<UT, EVEN, DK>, static_cast<long long>(a.B) * a.H * a.nc, 512, s, a)) return rc;
+    if (!dlam) return PARARNN_OK;
+    return launch(delta_dlam_kernel, a.HV, 256, s, static_cast<const float*>(a.dlam_part), a.lam, dlam, a.B * a.nc, a.c);
+  }
+};
+// mode: of bf16 tensors, kDirect where their rows take 16-byte loads of whole chunks, kEven where they start
+// at multiples of 4 bytes
+template <class R>
+int run_delta(const DeltaArgs& a, int mode, const pararnn_delta_opts* o, const float* dsT, float* ds0, float* dlam, hipStream_t s) {
+  const bool small = o->dk <= 64;
+  if (o->dtype != PARARNN_BF16)
+    return small ? R::template run<float, kEven, 64>(a, dsT, ds0, dlam, s) : R::template run<float, kEven, 128>(a, dsT, ds0, dlam, s);
+  if (mode == kDirect)
+    return small ? R::template run<bf16, kDirect, 64>(a, dsT, ds0, dlam, s) : R::template run<bf16, kDirect, 128>(a, dsT, ds0, dlam, s);
+  if (mode == kEven)
+    return small ? R::template run<bf16, kEven, 64>(a, dsT, ds0, dlam, s) : R::template run<bf16, kEven, 128>(a, dsT, ds0, dlam, s);
+  return small ? R::template run<bf16, kOdd, 64>(a, dsT, ds0, dlam, s) : R::template run<bf16, kOdd, 128>(a, dsT, ds0, dlam, s);
 }
-template <class UT, int DK>
-int run_adjoint(DeltaArgs a, const float* dsT, float* ds0, float* dlam, hipStream_t s) {
-  if (const int rc = run_prep<UT, DK, true>(a, s)) return rc;
-  a.s0 = dsT;
-  a.sT = ds0;
-  if (const int rc = launch(delta_back_kernel<UT, DK, 1, 4>, scan_grid(a, 64), 256, s, a)) return rc;
-  if (const int rc = launch(delta_grad_kernel<UT, DK>, static_cast<long long>(a.B) * a.H * a.nc, 512, s, a)) return rc;
-  if (!dlam) return PARARNN_OK;
-  return launch(delta_dlam_kernel, a.HV, 256, s, static_cast<const float*>(a.dlam_part), a.lam, dlam, a.B * a.nc, a.c);
+int delta_mode(const pararnn_view* q, const pararnn_view* k, const pararnn_view* v, const pararnn_delta_opts* o, size_t es) {
+  auto all = [&](size_t bytes) {
+    return rows_aligned(q, es, o->dk, bytes, o->B) && rows_aligned(k, es, o->dk, bytes, o->B) && rows_aligned(v, es, o->dv, bytes, o->B);
+  };
+  return all(16) ? kDirect : all(4) ? kEven : kOdd;
 }
 
 }  // namespace
@@ -152,12 +174,12 @@ extern "C" int32_t pararnn_delta_scan(const pararnn_view* q, const pararnn_view*
   a.frags = reinterpret_cast<bf16x8*>(w);
   a.rows = reinterpret_cast<float*>(w + z.frags);
   if (saved) {
-    a.states = static_cast<float*>(saved);
-    a.ys = reinterpret_cast<float*>(static_cast<char*>(saved) + z.states);
+    a.states = static_cast<f32x4*>(saved);
+    a.ys = reinterpret_cast<f32x4*>(static_cast<char*>(saved) + z.states);
   }
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  if (opts->dtype == PARARNN_BF16) return opts->dk <= 64 ? run_forward<bf16, 64>(a, st) : run_forward<bf16, 128>(a, st);
-  return opts->dk <= 64 ? run_forward<float, 64>(a, st) : run_forward<float, 128>(a, st);
+  const pararnn_view ov = {o, static_cast<int64_t>(opts->L) * opts->HV * opts->dv, static_cast<int64_t>(opts->HV) * opts->dv};
+  a.wide = rows_aligned(&ov, es, opts->dv, 16, opts->B);
+  return run_delta<DeltaForward>(a, delta_mode(q, k, v, opts, es), opts, nullptr, nullptr, nullptr, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int32_t pararnn_delta_scan_adjoint(const pararnn_view* q, const pararnn_view* k, const pararnn_view* v,
@@ -185,25 +207,21 @@ extern "C" int32_t pararnn_delta_scan_adjoint(const pararnn_view* q, const parar
   a.gv = view(dv);
   a.dgates = view(dgates);
   a.o = const_cast<void*>(d_o);
-  a.wide_v = wide_rows(d_o, es, 0, static_cast<long long>(opts->HV) * opts->dv, opts->dv);
-  a.wide_dv = wide_rows(dv, es, opts->dv);
-  a.wide_o = opts->dv % 8 == 0;
+  const pararnn_view ov = {d_o, static_cast<int64_t>(opts->L) * opts->HV * opts->dv, static_cast<int64_t>(opts->HV) * opts->dv};
+  a.wide = rows_aligned(dv, es, opts->dv, 16, opts->B);
   char* w = static_cast<char*>(ws);
   a.frags = reinterpret_cast<bf16x8*>(w);
   w += z.frags;
   a.rows = reinterpret_cast<float*>(w);
   w += z.rows;
-  a.dstates = reinterpret_cast<float*>(w);
+  a.dstates = reinterpret_cast<f32x4*>(w);
   w += z.states;
-  a.dxs = reinterpret_cast<float*>(w);
+  a.dxs = reinterpret_cast<f32x4*>(w);
   w += z.ys;
   a.dlam_part = dlam ? reinterpret_cast<float*>(w) : nullptr;
-  a.states = static_cast<float*>(const_cast<void*>(saved));
-  a.ys = reinterpret_cast<float*>(static_cast<char*>(const_cast<void*>(saved)) + z.states);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  if (opts->dtype == PARARNN_BF16)
-    return opts->dk <= 64 ? run_adjoint<bf16, 64>(a, dsT, ds0, dlam, st) : run_adjoint<bf16, 128>(a, dsT, ds0, dlam, st);
-  return opts->dk <= 64 ? run_adjoint<float, 64>(a, dsT, ds0, dlam, st) : run_adjoint<float, 128>(a, dsT, ds0, dlam, st);
+  a.states = static_cast<f32x4*>(const_cast<void*>(saved));
+  a.ys = reinterpret_cast<f32x4*>(static_cast<char*>(const_cast<void*>(saved)) + z.states);
+  return run_delta<DeltaAdjoint>(a, delta_mode(q, k, &ov, opts, es), opts, dsT, ds0, dlam, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int32_t pararnn_delta_step(const pararnn_view* q, const pararnn_view* k, const pararnn_view* v,

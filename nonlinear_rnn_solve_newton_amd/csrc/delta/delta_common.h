@@ -13,7 +13,9 @@
 // holds column m, rows 4 g to 4 g + 3. The inner index may run in any order that
 // both operands share. Taken as "rows 4 g .. 4 g + 3 of the first tile of 16,
 // then of the second", two results of one product are, lane by lane, an operand
-// of the next: the state and the values of a chunk never leave registers.
+// of the next: the state and the values of a chunk never leave registers. So that
+// those rows are 8 neighbours in memory, tiles of dk and dv come in pairs of 32:
+// row (or column) i of tile t is number delta_label(t, i).
 #pragma once
 
 #include "../layer/layer_common.h"
@@ -22,6 +24,8 @@ namespace pararnn {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ int delta_label(int t, int i) { return 32 * (t >> 1) + 8 * (i >> 2) + 4 * (t & 1) + (i & 3); }
 
 // planes of a tensor of the caller (NP), and those that an output of its type
 // needs of an fp32 factor (NO: 16 bits below bf16's own rounding of 8)
@@ -56,8 +60,21 @@ __device__ __forceinline__ void split_tiles(const f32x4& lo, const f32x4& hi, bf
   split8<N>(x, o);
 }
 
-// c += a b over their planes, the smallest products first; PB: planes of b that
-// count, N: the order kept (products of planes i and j with i + j < N)
+// c[i] += a[i] b over their planes, the smallest products first (N: products of
+// planes i and j with i + j < N); rows of a inside, so that no instruction waits
+// for the one before it
+template <int NA, int NB, int M>
+__device__ __forceinline__ void mma_rows(f32x4 (&c)[M], const bf16x8 (&a)[M][NA], const bf16x8* b) {
+  constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+  for (int s = N - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i)
+      if (i < NA && s - i < NB) {
+#pragma unroll
+        for (int r = 0; r < M; ++r) c[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[r][i], b[s - i], c[r], 0, 0, 0);
+      }
+}
 template <int NA, int NB>
 __device__ __forceinline__ void mma(f32x4& c, const bf16x8* a, const bf16x8* b) {
   constexpr int N = NA > NB ? NA : NB;
@@ -68,50 +85,61 @@ __device__ __forceinline__ void mma(f32x4& c, const bf16x8* a, const bf16x8* b) 
       if (i < NA && s - i < NB) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], c, 0, 0, 0);
 }
 
-// 8 consecutive elements as they lie in memory
-template <class UT> struct Raw8 {
-  f32x4 a, b;
-  __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
-};
-template <> struct Raw8<bf16> {
-  i32x4 a;
-  __device__ __forceinline__ float at(int i) const {
-    const uint32_t w = static_cast<uint32_t>(a[i >> 1]);
-    return i & 1 ? bf16_hi(w) : bf16_lo(w);
-  }
-};
-// elements d .. d + 7 of a row of n; zeros past its end and where `on` is false. wide: the row's start and n
-// are multiples of 16 bytes and of 8.
-template <class UT>
-__device__ __forceinline__ Raw8<UT> load_raw8(const UT* row, int d, int n, bool on, bool wide) {
-  Raw8<UT> v = {};
-  if (!on || d >= n) return v;
-  if (wide) {
-    if constexpr (sizeof(UT) == 4) {
-      v.a = *reinterpret_cast<const f32x4*>(row + d);
-      v.b = *reinterpret_cast<const f32x4*>(row + d + 4);
-    } else {
-      v.a = *reinterpret_cast<const i32x4*>(row + d);
-    }
-    return v;
-  }
+// 8 consecutive elements of a row on their way from memory: loads through a
+// buffer resource, without branches, so that they stay in flight until `planes`
+// takes them. EVEN: every row starts at a multiple of 4 bytes (16-byte loads need
+// no more); else bf16 elements come one by one.
+template <class UT, bool EVEN>
+struct Piece {
+  static constexpr int N = sizeof(UT) == 4 ? 2 : 1;
+  i32x4 v[N];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (d + i < n) {
-      if constexpr (sizeof(UT) == 4) {
-        if (i < 4) v.a[i & 3] = row[d + i];
-        else v.b[i & 3] = row[d + i];
-      } else {
-        v.a[i >> 1] |= static_cast<int>(static_cast<uint32_t>(row[d + i].bits) << (16 * (i & 1)));
-      }
-    }
-  return v;
+    for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * i, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t word(int i) const { return static_cast<uint32_t>(v[i >> 2][i & 3]); }
+};
+template <>
+struct Piece<bf16, false> {
+  uint16_t h[8];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * i, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return static_cast<uint32_t>(h[2 * i]) | static_cast<uint32_t>(h[2 * i + 1]) << 16;
+  }
+};
+// How tensors come into workgroup memory: through registers (odd elements,
+// 4-byte starts), or by 16-byte loads that write there (bf16 rows of whole chunks)
+enum { kOdd = 0, kEven = 1, kDirect = 2 };
+typedef __attribute__((address_space(3))) void lds_any;
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, void* to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_any*)to, 16, off, 0, 0, 0);
 }
-// planes of 8 elements of the caller's type
-__device__ __forceinline__ void planes_of(const Raw8<bf16>& v, bf16x8* o) { o[0] = __builtin_bit_cast(bf16x8, v.a); }
-__device__ __forceinline__ void planes_of(const Raw8<float>& v, bf16x8* o) {
-  const float x[8] = {v.a[0], v.a[1], v.a[2], v.a[3], v.b[0], v.b[1], v.b[2], v.b[3]};
-  split8<3>(x, o);
+constexpr uint32_t kNoLoad = 0x80000000u;  // past every resource's extent: reads zeros
+// planes of the first `count` of a piece's elements, zeros behind them
+template <class UT, bool EVEN>
+__device__ __forceinline__ void planes_of(const Piece<UT, EVEN>& v, int count, bf16x8* o) {
+  if constexpr (sizeof(UT) == 4) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < count ? __uint_as_float(v.word(i)) : 0.0f;
+    split8<3>(x, o);
+  } else {
+    i32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = static_cast<int>(v.word(i) & (2 * i + 1 < count ? 0xffffffffu : 2 * i < count ? 0xffffu : 0u));
+    o[0] = __builtin_bit_cast(bf16x8, w);
+  }
+}
+template <int NP>
+__device__ __forceinline__ float plane_sum(const bf16x8* o, int i) {
+  float v = static_cast<float>(o[0][i]);
+#pragma unroll
+  for (int p = 1; p < NP; ++p) v += static_cast<float>(o[p][i]);
+  return v;
 }
 
 template <class UT>
@@ -124,66 +152,60 @@ __device__ __forceinline__ void store1(UT* p, float v) {
   if constexpr (sizeof(UT) == 4) *p = v;
   else p->bits = static_cast<uint16_t>(pack_bf16(v, v));
 }
-// 8 consecutive elements of a row of n from d on
-template <class UT>
-__device__ __forceinline__ void store8(UT* row, int d, int n, bool wide, const float (&x)[8]) {
-  if (d >= n) return;
-  if (wide) {
-    if constexpr (sizeof(UT) == 4) {
-      *reinterpret_cast<f32x4*>(row + d) = f32x4{x[0], x[1], x[2], x[3]};
-      *reinterpret_cast<f32x4*>(row + d + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    } else {
-      i32x4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = static_cast<int>(pack_bf16(x[2 * i], x[2 * i + 1]));
-      *reinterpret_cast<i32x4*>(row + d) = v;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (d + i < n) store1(row + d + i, x[i]);
-}
-
-// A chunk's rows of q or k in workgroup memory: NP planes of 64 rows, 16
-// elements longer than DK, so that both ways of reading them are spread over
-// the banks.
-template <int DK, int NP>
+// A tile in workgroup memory: NP planes of ROWS rows of COLS bf16. Chunk c (16
+// bytes) of a row lies at c ^ turn(row), so that 16 rows read at one chunk touch
+// all banks, and 4 rows at 4 chunks as well.
+template <int COLS, int NP, int ROWS = 64>
 struct DeltaTile {
-  static constexpr int ROW = DK + 16;
-  __bf16 x[NP][64 * ROW];
-  // operand A, rows of the chunk: row 16 i + m, inner indexes of the block kb of 32 columns
+  static constexpr int CH = COLS / 8;  // chunks per row
+  __bf16 x[NP][ROWS * COLS];
+  static __device__ __forceinline__ int turn(int row) {
+    return COLS >= 128 ? (row & 3) << 2 | (row >> 2 & 3) : COLS == 64 ? (row >> 1 & 1) << 2 | (row >> 2 & 3) : row >> 2 & 3;
+  }
+  static __device__ __forceinline__ int pos(int row, int col) {
+    return row * COLS + (((col >> 3) ^ turn(row)) << 3) + (col & 7);
+  }
+  // operand A (rows) or B (columns): row 16 i + m, inner indexes the block kb of 32 columns
   __device__ __forceinline__ void rows(int i, int kb, int m, int g, bf16x8* o) const {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const __bf16* at = &x[p][(16 * i + m) * ROW + 32 * kb + 4 * g];
-      const u32x2 lo = *reinterpret_cast<const u32x2*>(at), hi = *reinterpret_cast<const u32x2*>(at + 16);
-      o[p] = __builtin_bit_cast(bf16x8, i32x4{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(hi.x),
-                                              static_cast<int>(hi.y)});
-    }
+    for (int p = 0; p < NP; ++p)  // row 16 i + m has m's turn
+      o[p] = *reinterpret_cast<const bf16x8*>(&x[p][(16 * i + m) * COLS + (((4 * kb + g) ^ turn(m)) << 3)]);
   }
-  // operand A (rows) or B (columns): column 16 t + m, inner indexes the rows of the block kb of 32. Transposed
-  // reads: lane m of a group gives the address of 4 columns of row m / 4 and gets 4 rows of column m.
+  // the same of column m of tile t, inner indexes the block kb of 32 rows. Transposed reads: lane m of a group
+  // gives the address of 4 columns of row m / 4 and gets 4 rows of column m.
   __device__ __forceinline__ void columns(int t, int kb, int m, int g, bf16x8* o) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      __bf16* at = &x[p][(32 * kb + 4 * g + (m >> 2)) * ROW + 16 * t + 4 * (m & 3)];
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * ROW));
+      const int at = pos(32 * kb + 4 * g + (m >> 2), 32 * (t >> 1) + 8 * (m & 3) + 4 * (t & 1));  // 16 rows on: the same turn
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)&x[p][at]);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)&x[p][at + 16 * COLS]);
       o[p] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
-  template <class UT>
-  __device__ __forceinline__ void put(int row, int d, const Raw8<UT>& v) {
-    bf16x8 o[NP];
-    planes_of(v, o);
+  // chunk number `slot` as the tile lies: row slot / CH, columns from source(slot) on
+  static __device__ __forceinline__ int source(int slot) { return ((slot % CH) ^ turn(slot / CH)) << 3; }
+  __device__ __forceinline__ void put_slot(int slot, const bf16x8* o) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(&x[p][row * ROW + d]) = o[p];
+    for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(&x[p][slot * 8]) = o[p];
   }
-  __device__ __forceinline__ float at(int row, int d) const {
-    float v = static_cast<float>(x[0][row * ROW + d]);
+  // 4 fp32 values at consecutive columns
+  __device__ __forceinline__ void put4(int row, int col, const f32x4& v) {
+    float r[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int p = 1; p < NP; ++p) v += static_cast<float>(x[p][row * ROW + d]);
+    for (int p = 0; p < NP; ++p) {
+      const uint32_t a = pack_bf16(r[0], r[1]), b = pack_bf16(r[2], r[3]);
+      *reinterpret_cast<u32x2*>(&x[p][pos(row, col)]) = u32x2{a, b};
+      r[0] -= __uint_as_float(a << 16);
+      r[1] -= __uint_as_float(a & 0xffff0000u);
+      r[2] -= __uint_as_float(b << 16);
+      r[3] -= __uint_as_float(b & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ float at(int row, int col) const {
+    const int i = pos(row, col);
+    float v = static_cast<float>(x[0][i]);
+#pragma unroll
+    for (int p = 1; p < NP; ++p) v += static_cast<float>(x[p][i]);
     return v;
   }
 };

@@ -48,14 +48,15 @@ struct DeltaArgs {
   const uint8_t* reset;
   bf16x8* frags;                 // per chunk and value head: planes of T and P as operands
   float* rows;                   // per chunk and value head: kRows x 64 factors
-  float* states;                 // saved: [B HV][chunks][dk][dv] the state in front of each chunk, or nullptr
-  float* ys;                     // saved: [B HV][chunks][64][dv] y
-  float* dstates;                // adjoint: [B HV][chunks][dk][dv] dS behind each chunk
-  float* dxs;                    // adjoint: [B HV][chunks][64][dv] dX
+  // As result tiles lie in registers, per chunk and value head [2 ceil(dv / 32)][tiles of 16 rows][64 lanes]:
+  f32x4* states;                 // saved: the state in front of each chunk (2 ceil(dk / 32) tiles), or nullptr
+  f32x4* ys;                     // saved: y (4 tiles)
+  f32x4* dstates;                // adjoint: dS behind each chunk
+  f32x4* dxs;                    // adjoint: dX
   float* dlam_part;              // adjoint: [HV][B chunks]
   int B, L, H, HV, dk, dv, nc;
   float c, eps, scale;
-  int wide_qk, wide_v, wide_dqk, wide_dv, wide_o;  // rows whose 8 elements take 16-byte accesses: a multiple of 8 of them
+  int wide;                      // rows of bf16 o (adjoint: dV) take 16-byte stores
 };
 
 // factors of a chunk's rows
@@ -74,12 +75,24 @@ struct DeltaFrags {
   static constexpr int T = kTriBlocks * NT * 64, P = kTriBlocks * NP * 64, ALL = T + P;
 };
 
+// tiles of 16 that n rows or columns take, in pairs
+__host__ __device__ constexpr int delta_tiles(int n) { return (n + 31) / 32 * 2; }
 __device__ __forceinline__ int delta_len(const DeltaArgs& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
 }
 template <class UT>
 __device__ __forceinline__ const UT* at(const DeltaView& v, int b, long long t) {
   return static_cast<const UT*>(v.p) + b * v.batch + t * v.token;
+}
+// n rows from step t on, from element d of the `packed` ones of a row
+template <class UT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const DeltaView& v, int b, long long t, int d, int n, int packed) {
+  return make_rsrc(at<UT>(v, b, t) + d, static_cast<uint32_t>((n - 1) * v.token + packed - d) * sizeof(UT));
+}
+// where row `row` of a resource of rows `token` elements apart has its element d; nowhere unless `on`
+template <class UT>
+__device__ __forceinline__ uint32_t offset_of(int row, long long token, int d, bool on) {
+  return on ? static_cast<uint32_t>((row * static_cast<int>(token) + d) * static_cast<int>(sizeof(UT))) : kNoLoad;
 }
 template <class UT>
 __device__ __forceinline__ UT* out_at(const DeltaView& v, int b, long long t) {
@@ -97,7 +110,7 @@ __device__ __forceinline__ f32x4 mul16(const float* a, const f32x4& b, f32x4 c) 
 
 // A workgroup per chunk and value head: row factors, T and P (ADJ: their
 // transposes) as operands of the scan, in memory order of its reads.
-template <class UT, int DK, bool ADJ>
+template <class UT, bool EVEN, int DK, bool ADJ>
 __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
   typedef DeltaFrags<UT, ADJ> F;
   constexpr int NP = DeltaPlanes<UT>::NP, KB = DK / 32, ROW = 68;
@@ -116,27 +129,32 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float nk = 0.0f, nq = 0.0f;
   {
+    const int H = p.H * p.dk;
+    const __amdgpu_buffer_rsrc_t kr = rows_of<UT>(p.k, b, t0, h * p.dk, n, H), qr = rows_of<UT>(p.q, b, t0, h * p.dk, n, H);
     const int i = 16 * w + m;
-    const UT* kr = at<UT>(p.k, b, t0 + min(i, n - 1)) + h * p.dk;
-    const UT* qr = at<UT>(p.q, b, t0 + min(i, n - 1)) + h * p.dk;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      const int d = 32 * kb + 8 * g;
-      const Raw8<UT> rk = load_raw8<UT>(kr, d, p.dk, i < n, p.wide_qk), rq = load_raw8<UT>(qr, d, p.dk, i < n, p.wide_qk);
+      const int d = 32 * kb + 8 * g, count = p.dk - d;
+      Piece<UT, EVEN> rk[4], rq;
+      rq.load(qr, offset_of<UT>(i, p.q.token, d, i < n && count > 0));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) rk[j].load(kr, offset_of<UT>(16 * j + m, p.k.token, d, 16 * j + m < n && count > 0));
+      bf16x8 aq[NP], ak[NP], bk[NP];
+      planes_of(rq, count, aq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j == w) planes_of(rk[j], count, ak);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        nk = fmaf(rk.at(e), rk.at(e), nk);
-        nq = fmaf(rq.at(e), rq.at(e), nq);
+        const float x = plane_sum<NP>(ak, e), y = plane_sum<NP>(aq, e);
+        nk = fmaf(x, x, nk);
+        nq = fmaf(y, y, nq);
       }
-      bf16x8 ak[NP], aq[NP];
-      planes_of(rk, ak);
-      planes_of(rq, aq);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w) {
-          const int r = 16 * j + m;
-          bf16x8 bk[NP];
-          planes_of(load_raw8<UT>(at<UT>(p.k, b, t0 + min(r, n - 1)) + h * p.dk, d, p.dk, r < n, p.wide_qk), bk);
+          planes_of(rk[j], count, bk);
           mma<NP, NP>(kk[j], ak, bk);
           mma<NP, NP>(qk[j], aq, bk);
         }
@@ -268,34 +286,43 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
   }
 }
 
-// What a chunk brings into workgroup memory for the scans
-template <class UT, int DK, bool ADJ>
+// What a chunk brings into workgroup memory for the scans; VC: columns of v
+// (dO) that the workgroup takes. Where the tensors are bf16, a wave leaves its
+// results in the place of its own columns of v, and they go out by whole rows
+// while the next chunk is worked on.
+template <class UT, int DK, int VC, bool ADJ>
 struct DeltaBuf {
   static constexpr int NP = DeltaPlanes<UT>::NP;
   typedef DeltaFrags<UT, ADJ> F;
   DeltaTile<DK, NP> k, q;
+  DeltaTile<VC, NP> v;
   bf16x8 frags[F::ALL];
   float rows[4 * 64];
 };
 
 // The scans' common part: which columns a wave has, and the way of a chunk
-// from memory to workgroup memory, through registers, one chunk ahead
-template <class UT, int DK, int NC, int NW, bool ADJ>
+// from memory to workgroup memory, one chunk ahead: through registers, or direct
+template <class UT, int MODE, int DK, int NC, int NW, bool ADJ>
 struct DeltaScan {
-  static constexpr int NP = DeltaPlanes<UT>::NP, NT = 64 * NW, RT = DK / 16, KB = DK / 32;
+  static constexpr int NP = DeltaPlanes<UT>::NP, NT = 64 * NW, RT = DK / 16, KB = DK / 32, VC = 16 * NC * NW;
+  static constexpr bool DIRECT = MODE == kDirect;
   typedef DeltaFrags<UT, ADJ> F;
-  typedef DeltaBuf<UT, DK, ADJ> Buf;
+  typedef DeltaBuf<UT, DK, VC, ADJ> Buf;
   static constexpr int NBUF = 2 * sizeof(Buf) <= 160 * 1024 ? 2 : 1;
-  static constexpr int TP = 64 * DK / 8 / NT, FP = (F::ALL + NT - 1) / NT, VP = 256 / NT;
-  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0, "whole rounds");
+  static constexpr bool INPLACE = sizeof(UT) == 2;
+  static_assert(!INPLACE || NBUF == 2, "results wait in the other buffer");
+  static constexpr int TP = 64 * DK / 8 / NT, FP = (F::ALL + NT - 1) / NT, VP = 256 / NT, CP = 64 * VC / 8 / NT;
+  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0 && 64 * VC / 8 % NT == 0, "whole rounds");
+  static_assert(NT / (DK / 8) % 16 == 0 && NT / (VC / 8) % 16 == 0, "a thread's slots lie in one column, with one turn");
+  static_assert(F::ALL % 64 == 0, "whole waves");
 
   const DeltaArgs& p;
-  int tid, lane, w, m, g, b, hv, h, bh, col0, len, nch;
+  int tid, lane, w, m, g, b, hv, h, bh, wg0, col0, len, nch;
+  int trow, tcol, vrow, vcol;  // the thread's first slot of q and k, and of v
   bool idle;
-  Raw8<UT> rk[TP], rq[TP];
-  bf16x8 rf[FP];
-  float rv[VP];
-  float vv[NC][4][4];  // the chunk's rows of v (dO), as a result tile holds them
+  Piece<UT, MODE != kOdd> rk[DIRECT ? 1 : TP], rq[DIRECT ? 1 : TP], rv[DIRECT ? 1 : CP];
+  i32x4 rf[DIRECT ? 1 : FP];
+  float rr[VP];
 
   __device__ __forceinline__ explicit DeltaScan(const DeltaArgs& a) : p(a) {
     tid = threadIdx.x;
@@ -304,7 +331,7 @@ struct DeltaScan {
     m = lane & 15;
     g = lane >> 4;
     // the slices of a head follow each other on one XCD, whose L2 holds its chunk
-    const int nsl = (p.dv + 16 * NC * NW - 1) / (16 * NC * NW);
+    const int nsl = (p.dv + VC - 1) / VC;
     const int x = blockIdx.x % 8, l = blockIdx.x / 8;
     bh = (l / nsl) * 8 + x;
     idle = bh >= p.B * p.HV;
@@ -312,49 +339,144 @@ struct DeltaScan {
     b = bh / p.HV;
     hv = bh % p.HV;
     h = hv / (p.HV / p.H);
-    col0 = ((l % nsl) * NW + w) * 16 * NC;
+    wg0 = (l % nsl) * VC;
+    col0 = wg0 / 16 + w * NC;
     len = delta_len(p, b);
     nch = (len + kDeltaChunk - 1) / kDeltaChunk;
+    trow = tid / (DK / 8);
+    tcol = DeltaTile<DK, NP>::source(tid);
+    vrow = tid / (VC / 8);
+    vcol = DeltaTile<VC, NP>::source(tid);
   }
-  __device__ __forceinline__ int col(int cc) const { return col0 + 16 * cc + m; }
-  __device__ __forceinline__ void fetch(int ch, const void* vbase, long long vbatch, long long vtoken) {
+  // the lane's column of v: column m of tile col0 + cc
+  __device__ __forceinline__ int col(int cc) const { return delta_label(col0 + cc, m); }
+  __device__ __forceinline__ void fetch_qk(int ch, const DeltaView& x, DeltaTile<DK, NP>& to, decltype(rk)& r) {
     const int t0 = ch * kDeltaChunk, n = min(len - t0, kDeltaChunk);
+    const __amdgpu_buffer_rsrc_t rs = rows_of<UT>(x, b, t0, h * p.dk, n, p.H * p.dk);
 #pragma unroll
     for (int i = 0; i < TP; ++i) {
-      const int e = tid + NT * i, row = e / (DK / 8), d = e % (DK / 8) * 8;
-      const long long t = t0 + min(row, n - 1);
-      rk[i] = load_raw8<UT>(at<UT>(p.k, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk);
-      rq[i] = load_raw8<UT>(at<UT>(p.q, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk);
+      const int row = trow + NT / (DK / 8) * i;
+      const uint32_t off = offset_of<UT>(row, x.token, tcol, row < n && tcol < p.dk);
+      if constexpr (DIRECT) load_to_lds(rs, &to.x[0][(64 * w + NT * i) * 8], off);
+      else r[i].load(rs, off);
     }
-    const long long id = static_cast<long long>(bh) * p.nc + ch;
-#pragma unroll
-    for (int i = 0; i < FP; ++i)
-      if (tid + NT * i < F::ALL) rf[i] = p.frags[id * F::ALL + tid + NT * i];
-#pragma unroll
-    for (int i = 0; i < VP; ++i) rv[i] = p.rows[id * (kRows * 64) + tid + NT * i];
-    const UT* v = static_cast<const UT*>(vbase) + b * vbatch + static_cast<long long>(t0) * vtoken + static_cast<long long>(hv) * p.dv;
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * i + 4 * g + r;
-          vv[cc][i][r] = row < n && col(cc) < p.dv ? load1(v + row * vtoken + col(cc)) : 0.0f;
-        }
   }
-  __device__ __forceinline__ void land(Buf& to) {
+  __device__ __forceinline__ void fetch_v(int ch, const DeltaView& x, Buf& to) {
+    const int t0 = ch * kDeltaChunk, n = min(len - t0, kDeltaChunk);
+    const __amdgpu_buffer_rsrc_t rs = rows_of<UT>(x, b, t0, hv * p.dv, n, p.HV * p.dv);
 #pragma unroll
-    for (int i = 0; i < TP; ++i) {
-      const int e = tid + NT * i, row = e / (DK / 8), d = e % (DK / 8) * 8;
-      to.k.put(row, d, rk[i]);
-      to.q.put(row, d, rq[i]);
+    for (int i = 0; i < CP; ++i) {
+      const int row = vrow + NT / (VC / 8) * i;
+      const uint32_t off = offset_of<UT>(row, x.token, wg0 + vcol, row < n && wg0 + vcol < p.dv);
+      if constexpr (DIRECT) load_to_lds(rs, &to.v.x[0][(64 * w + NT * i) * 8], off);
+      else rv[i].load(rs, off);
+    }
+  }
+  // the triangular operands [FROM, TO) of FP rounds
+  template <int FROM, int TO>
+  __device__ __forceinline__ void fetch_frags(int ch, Buf& to) {
+    const __amdgpu_buffer_rsrc_t fr = make_rsrc(p.frags + (static_cast<long long>(bh) * p.nc + ch) * F::ALL, F::ALL * 16);
+#pragma unroll
+    for (int i = FROM; i < TO; ++i) {
+      if constexpr (DIRECT) {
+        if (NT * (i + 1) <= F::ALL || 64 * w + NT * i < F::ALL) load_to_lds(fr, &to.frags[64 * w + NT * i], (tid + NT * i) * 16);
+      } else {
+        rf[i] = __builtin_amdgcn_raw_buffer_load_b128(fr, (tid + NT * i) * 16, 0, 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void fetch_rows(int ch) {
+#pragma unroll
+    for (int i = 0; i < VP; ++i)
+      rr[i] = p.rows[(static_cast<long long>(bh) * p.nc + ch) * (kRows * 64) + tid + NT * i];
+  }
+  __device__ __forceinline__ void fetch_all(int ch, const DeltaView& v, Buf& to) {
+    fetch_qk(ch, p.k, to.k, rk);
+    fetch_qk(ch, p.q, to.q, rq);
+    fetch_v(ch, v, to);
+    fetch_frags<0, FP>(ch, to);
+    fetch_rows(ch);
+  }
+  // what came through registers; then the loads that did not are waited for
+  __device__ __forceinline__ void land(Buf& to) {
+    if constexpr (!DIRECT) {
+      bf16x8 o[NP];
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        planes_of(rk[i], p.dk - tcol, o);
+        to.k.put_slot(tid + NT * i, o);
+        planes_of(rq[i], p.dk - tcol, o);
+        to.q.put_slot(tid + NT * i, o);
+      }
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        planes_of(rv[i], p.dv - wg0 - vcol, o);
+        to.v.put_slot(tid + NT * i, o);
+      }
+#pragma unroll
+      for (int i = 0; i < FP; ++i)
+        if (NT * (i + 1) <= F::ALL || tid + NT * i < F::ALL) to.frags[tid + NT * i] = __builtin_bit_cast(bf16x8, rf[i]);
     }
 #pragma unroll
-    for (int i = 0; i < FP; ++i)
-      if (tid + NT * i < F::ALL) to.frags[tid + NT * i] = rf[i];
+    for (int i = 0; i < VP; ++i) to.rows[tid + NT * i] = rr[i];
+    if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  }
+  // The wave's results Y of a chunk, rows of [..][HV][dv] from `to` on: into the place of its columns of v,
+  // to be sent later, or straight to memory
+  __device__ __forceinline__ void result(Buf& u, const DeltaView& to, int t0, int rows, const f32x4 (&Y)[NC][4]) const {
+    if constexpr (INPLACE) {
 #pragma unroll
-    for (int i = 0; i < VP; ++i) to.rows[tid + NT * i] = rv[i];
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            u.v.x[0][u.v.pos(16 * i + 4 * g + r, delta_label(w * NC + cc, m))] = static_cast<__bf16>(Y[cc][i][r]);
+    } else {
+      UT* o = out_at<UT>(to, b, t0) + static_cast<long long>(hv) * p.dv;
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+        if (col(cc) < p.dv) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (16 * i + 4 * g + r < rows) store1(o + (16 * i + 4 * g + r) * to.token + col(cc), Y[cc][i][r]);
+        }
+    }
+  }
+  // A thread takes the slots that it fills (or that its wave's loads fill) with the next chunk of the buffer,
+  // so nobody overwrites what another wave has not taken yet.
+  __device__ __forceinline__ void take(const Buf& u, i32x4 (&v)[CP]) const {
+    if constexpr (INPLACE) {
+#pragma unroll
+      for (int i = 0; i < CP; ++i) v[i] = *reinterpret_cast<const i32x4*>(&u.v.x[0][(tid + NT * i) * 8]);
+      if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): taken, before a load may write there
+    }
+  }
+  __device__ __forceinline__ void send(const i32x4 (&v)[CP], const DeltaView& to, int t0, int rows) const {
+    if constexpr (INPLACE) {
+      const int at = wg0 + vcol, count = p.dv - at;
+      bf16* o = reinterpret_cast<bf16*>(out_at<UT>(to, b, t0)) + static_cast<long long>(hv) * p.dv + at;
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        const int row = vrow + NT / (VC / 8) * i;
+        if (row < rows && count > 0) {
+          if (p.wide) {  // dv is a multiple of 8
+            *reinterpret_cast<i32x4*>(o + row * to.token) = v[i];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < count) o[row * to.token + e].bits = static_cast<uint16_t>(static_cast<uint32_t>(v[i][e >> 1]) >> (16 * (e & 1)));
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void flush(const Buf& u, const DeltaView& to, int t0, int rows) const {
+    i32x4 v[CP] = {};
+    take(u, v);
+    send(v, to, t0, rows);
   }
   __device__ __forceinline__ f32x4 row4(const Buf& u, int kind, int i) const {
     return *reinterpret_cast<const f32x4*>(&u.rows[kind * 64 + 16 * i + 4 * g]);
@@ -367,7 +489,7 @@ struct DeltaScan {
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * t + 4 * g + r;
+          const int row = delta_label(t, 4 * g + r);
           S[cc][t][r] = s && row < p.dk && col(cc) < p.dv ? s[static_cast<long long>(row) * p.dv + col(cc)] : 0.0f;
         }
   }
@@ -379,301 +501,411 @@ struct DeltaScan {
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int row = 16 * t + 4 * g + r;
+            const int row = delta_label(t, 4 * g + r);
             if (row < p.dk) s[static_cast<long long>(row) * p.dv + col(cc)] = S[cc][t][r];
           }
       }
   }
-  __device__ __forceinline__ void store_rows(float* y, const f32x4 (&Y)[NC][4]) const {
+  // N tiles of each of the wave's columns as they lie, n of them per column tile in memory
+  template <int N>
+  __device__ __forceinline__ void store_tiles(f32x4* to, long long id, int n, const f32x4 (&Y)[NC][N]) const {
+    const int nct = delta_tiles(p.dv), c0 = col0;
 #pragma unroll
     for (int cc = 0; cc < NC; ++cc)
-      if (col(cc) < p.dv) {
+      if (c0 + cc < nct) {
+        f32x4* at = to + ((id * nct + c0 + cc) * n) * 64 + lane;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y[static_cast<long long>(16 * i + 4 * g + r) * p.dv + col(cc)] = Y[cc][i][r];
+        for (int t = 0; t < N; ++t)
+          if (t < n) at[t * 64] = Y[cc][t];
       }
   }
 };
 
-template <class UT, int DK, int NC, int NW>
-__global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaArgs p) {
-  typedef DeltaScan<UT, DK, NC, NW, false> D;
-  typedef typename D::Buf Buf;
+// y += a x for a triangular a given by its blocks: lower, or (UP) the transpose
+// of one. XP: planes that x has room for, NB: those that count.
+template <int NA, int NB, int NC, bool UP = false, int XP>
+__device__ __forceinline__ void tri_rows(f32x4 (&y)[NC][4], const bf16x8 (&a)[kTriBlocks][NA], const bf16x8 (&x)[NC][2][XP]) {
+  constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+  for (int s = N - 1; s >= 0; --s)
+#pragma unroll
+    for (int k = 0; k <= s; ++k)
+      if (k < NA && s - k < NB) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (UP ? kb >= i / 2 : kb <= i / 2) {
+#pragma unroll
+              for (int cc = 0; cc < NC; ++cc)
+                y[cc][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[UP ? up_block(i, kb) : low_block(i, kb)][k], x[cc][kb][s - k],
+                                                                   y[cc][i], 0, 0, 0);
+            }
+      }
+}
+
+// TG tiles of the state from t0 on: S += a x over the chunk's rows
+template <int NP, int TG, int NC, int RT>
+__device__ __forceinline__ void state_tiles(f32x4 (&S)[NC][RT], int t0, const bf16x8 (&a)[TG][2][NP], const bf16x8 (&x)[NC][2][3]) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int k = 0; k <= s; ++k)
+      if (k < NP) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int t = 0; t < TG; ++t)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+              S[cc][t0 + t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][kb][k], x[cc][kb][s - k], S[cc][t0 + t], 0, 0, 0);
+      }
+}
+
+// A chunk of the scan. `up` is the chunk's, `top` the next one's, which loads
+// fill meanwhile: restrict is what lets reads of the one pass loads into the other
+// without a wait.
+template <class D, class UT, int DK, int NC>
+__device__ __forceinline__ void delta_scan_chunk(D& s, const DeltaArgs& p, const DeltaView& o, int ch, bool more,
+                                                 typename D::Buf* __restrict__ up, typename D::Buf* __restrict__ top,
+                                                 f32x4 (&S)[NC][D::RT], bf16x8 (&sb)[NC][D::KB][3]) {
   constexpr int NP = D::NP, NO = DeltaPlanes<UT>::NO, RT = D::RT, KB = D::KB;
+  const int m = s.m, g = s.g;
+  typename D::Buf &u = *up, &to = *top;
+  const long long id = static_cast<long long>(s.bh) * p.nc + ch;
+
+  // Each part's operands are read while the part before it runs, and the next chunk's loads are dealt out
+  // over the parts: a wave has its matrix core to itself, and nothing else hides what a read takes. The
+  // compiler keeps to the order between sched_barriers.
+  f32x4 ks[NC][4], qs[NC][4];
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[cc][i] = qs[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  bf16x8 ka[2][4][NP], qa[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][NO], vv[NC][2][NP];
+  i32x4 out[D::CP] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
+  if (ch > 0) s.take(to, out);  // the results of the chunk before, where the next one lands
+  if (p.states) s.template store_tiles<RT>(p.states, id, delta_tiles(p.dk), S);
+  if (more) s.fetch_qk(ch + 1, p.k, to.k, s.rk);
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kb + 1 < KB) u.k.rows(i, kb + 1, m, g, ka[(kb + 1) & 1][i]);
+      else u.q.rows(i, 0, m, g, qa[0][i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) mma_rows<NP, 3>(ks[cc], ka[kb & 1], sb[cc][kb]);
+  }
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) u.v.columns(s.w * NC + cc, kb, m, g, vv[cc][kb]);
+  if (more) s.fetch_qk(ch + 1, p.q, to.q, s.rq);
+  bf16x8 xb[NC][2][3];
+  f32x4 y[NC][4];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    if (kb + 1 < KB) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u.q.rows(i, kb + 1, m, g, qa[(kb + 1) & 1][i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTriBlocks; ++j)
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) ta[j][pl] = u.frags[(j * 3 + pl) * 64 + s.lane];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) mma_rows<NP, NO>(qs[cc], qa[kb & 1], sb[cc][kb]);
+    if (kb < 2) {  // beside q's products
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f32x4 xg = s.row4(u, kRowX, 2 * kb + i);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            ks[cc][2 * kb + i][r] = fmaf(-xg[r], ks[cc][2 * kb + i][r], plane_sum<NP>(vv[cc][kb], 4 * i + r));
+          y[cc][2 * kb + i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        split_tiles<3>(ks[cc][2 * kb], ks[cc][2 * kb + 1], xb[cc][kb]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kTriBlocks; ++j)
+#pragma unroll
+    for (int pl = 0; pl < NO; ++pl) pa[j][pl] = u.frags[D::F::T + (j * NO + pl) * 64 + s.lane];
+  if (ch > 0) s.send(out, o, (ch - 1) * kDeltaChunk, kDeltaChunk);
+  if (more) {
+    s.fetch_v(ch + 1, p.v, to);
+    s.fetch_rows(ch + 1);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  tri_rows<3, 3, NC>(y, ta, xb);
+  constexpr int TG = NP == 1 ? (RT < 4 ? RT : 4) : 2;  // tiles of the state at a time
+  bf16x8 yb[NC][2][3], kc[2][TG][2][NP];
+#pragma unroll
+  for (int t = 0; t < TG; ++t)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) u.k.columns(t, kb, m, g, kc[0][t][kb]);
+  if (more) s.template fetch_frags<0, D::FP / 2>(ch + 1, to);
+  __builtin_amdgcn_sched_barrier(0);
+  if (p.ys) s.template store_tiles<4>(p.ys, id, 4, y);
+  // the output
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x4 og = s.row4(u, kRowO, i);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) qs[cc][i] *= og;
+  }
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+  tri_rows<NO, NO, NC>(qs, pa, xb);
+  // the state
+  const float whole = u.rows[kRowWhole * 64];
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[cc][i] *= s.row4(u, kRowS, i);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], yb[cc][kb]);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) S[cc][t] *= whole;
+  }
+  if (more) s.template fetch_frags<D::FP / 2, D::FP>(ch + 1, to);
+#pragma unroll
+  for (int t0 = 0; t0 < RT; t0 += TG) {
+    if (t0 + TG < RT) {
+#pragma unroll
+      for (int t = 0; t < TG; ++t)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) u.k.columns(t0 + TG + t, kb, m, g, kc[(t0 / TG + 1) & 1][t][kb]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    state_tiles<NP, TG, NC>(S, t0, kc[(t0 / TG) & 1], yb);
+#pragma unroll
+    for (int t = t0; t < t0 + TG; t += 2)
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][t], S[cc][t + 1], sb[cc][t / 2]);
+  }
+  s.result(u, o, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), qs);
+}
+
+template <class UT, int MODE, int DK, int NC, int NW>
+__global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaArgs p) {
+  typedef DeltaScan<UT, MODE, DK, NC, NW, false> D;
+  typedef typename D::Buf Buf;
+  constexpr int RT = D::RT, KB = D::KB;
   __shared__ Buf buf[D::NBUF];
   D s(p);
   if (s.idle) return;
-  const int m = s.m, g = s.g;
   f32x4 S[NC][RT];
   const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
   s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
-  float v[NC][4][4];
-  UT* const ob = static_cast<UT*>(p.o) + (static_cast<long long>(s.b) * p.L * p.HV + s.hv) * p.dv;
-  const long long orow = static_cast<long long>(p.HV) * p.dv;
+  bf16x8 sb[NC][KB][3];
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
+  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
   if (s.nch > 0) {
-    s.fetch(0, p.v.p, p.v.batch, p.v.token);
+    s.fetch_all(0, p.v, buf[0]);
     s.land(buf[0]);
   }
   __syncthreads();
   for (int ch = 0; ch < s.nch; ++ch) {
-    Buf& u = buf[D::NBUF == 2 ? ch & 1 : 0];
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[cc][i][r] = s.vv[cc][i][r];
-    if (ch + 1 < s.nch) s.fetch(ch + 1, p.v.p, p.v.batch, p.v.token);
-    const long long id = static_cast<long long>(s.bh) * p.nc + ch;
-    if (p.states) s.store_state(p.states + id * p.dk * p.dv, S);
-
-    f32x4 ks[NC][4], qs[NC][4];
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ks[cc][i] = qs[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      bf16x8 sb[NC][3];
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf16x8 a[NP];
-        u.k.rows(i, kb, m, g, a);
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(ks[cc][i], a, sb[cc]);
-        u.q.rows(i, kb, m, g, a);
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NP, NO>(qs[cc][i], a, sb[cc]);
-      }
-    }
-    bf16x8 xb[NC][2][3];
-    f32x4 y[NC][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 xg = s.row4(u, kRowX, i);
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ks[cc][i][r] = fmaf(-xg[r], ks[cc][i][r], v[cc][i][r]);
-    }
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(ks[cc][2 * kb], ks[cc][2 * kb + 1], xb[cc][kb]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) y[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int kb = 0; kb <= i / 2; ++kb) {
-        bf16x8 a[3];
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) a[pl] = u.frags[(low_block(i, kb) * 3 + pl) * 64 + s.lane];
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<3, 3>(y[cc][i], a, xb[cc][kb]);
-      }
-    }
-    if (p.ys) s.store_rows(p.ys + id * kDeltaChunk * p.dv, y);
-    // the output
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
-    const int t0 = ch * kDeltaChunk, last = min(p.L - t0, kDeltaChunk);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 og = s.row4(u, kRowO, i);
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) qs[cc][i] *= og;
-#pragma unroll
-      for (int kb = 0; kb <= i / 2; ++kb) {
-        bf16x8 a[NO];
-#pragma unroll
-        for (int pl = 0; pl < NO; ++pl) a[pl] = u.frags[D::F::T + (low_block(i, kb) * NO + pl) * 64 + s.lane];
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NO, NO>(qs[cc][i], a, xb[cc][kb]);
-      }
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc)
-        if (s.col(cc) < p.dv) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = 16 * i + 4 * g + r;
-            if (row < last) store1(ob + (t0 + row) * orow + s.col(cc), qs[cc][i][r]);
-          }
-        }
-    }
-    // the state
-    const float whole = u.rows[kRowWhole * 64];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 sg = s.row4(u, kRowS, i);
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) y[cc][i] *= sg;
-    }
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) S[cc][t] *= whole;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        bf16x8 a[NP];
-        u.k.columns(t, kb, m, g, a);
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(S[cc][t], a, xb[cc][kb]);
-      }
-    }
+    const int at = ch & (D::NBUF - 1), next = (ch + 1) & (D::NBUF - 1);
+    const bool more = ch + 1 < s.nch;
+    delta_scan_chunk<D, UT, DK, NC>(s, p, o, ch, more, &buf[at], &buf[next], S, sb);
     if constexpr (D::NBUF == 1) __syncthreads();
-    if (ch + 1 < s.nch) s.land(buf[D::NBUF == 2 ? (ch + 1) & 1 : 0]);
+    if (more) s.land(buf[next]);
     __syncthreads();
   }
   if (p.sT) s.store_state(p.sT + at_state, S);
+  if (s.nch > 0) {
+    const int t0 = (s.nch - 1) * kDeltaChunk;
+    s.flush(buf[(s.nch - 1) & (D::NBUF - 1)], o, t0, min(p.L - t0, kDeltaChunk));
+  }
   // rows behind the last chunk of the sequence
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
     if (s.col(cc) < p.dv)
-      for (long long t = static_cast<long long>(s.nch) * kDeltaChunk + g; t < p.L; t += 4)
-        store1(ob + t * orow + s.col(cc), 0.0f);
+      for (long long t = static_cast<long long>(s.nch) * kDeltaChunk + s.g; t < p.L; t += 4)
+        store1(out_at<UT>(o, s.b, t) + static_cast<long long>(s.hv) * p.dv + s.col(cc), 0.0f);
 }
 
-// dS from the last chunk to the first; p.s0 is dsT and p.sT is ds0
-template <class UT, int DK, int NC, int NW>
-__global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaArgs p) {
-  typedef DeltaScan<UT, DK, NC, NW, true> D;
-  typedef typename D::Buf Buf;
+// A chunk of the adjoint's scan: as above, from the last to the first. `top` holds
+// the results of chunk ch + 1 (behind: there is one), and then takes chunk ch - 1.
+template <class D, class UT, int DK, int NC>
+__device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const DeltaView& o, int ch, bool more, bool behind,
+                                                 typename D::Buf* __restrict__ up, typename D::Buf* __restrict__ top,
+                                                 f32x4 (&S)[NC][D::RT], bf16x8 (&sb)[NC][D::KB][3]) {
   constexpr int NP = D::NP, RT = D::RT, KB = D::KB;
-  __shared__ Buf buf[D::NBUF];
-  D s(p);
-  if (s.idle) return;
   const int m = s.m, g = s.g;
-  f32x4 S[NC][RT];
-  const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
-  s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
-  const long long orow = static_cast<long long>(p.HV) * p.dv;
-  float v[NC][4][4];
-  if (s.nch > 0) {
-    s.fetch(s.nch - 1, p.o, p.L * orow, orow);
-    s.land(buf[D::NBUF == 2 ? (s.nch - 1) & 1 : 0]);
-  }
-  __syncthreads();
-  for (int ch = s.nch - 1; ch >= 0; --ch) {
-    Buf& u = buf[D::NBUF == 2 ? ch & 1 : 0];
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[cc][i][r] = s.vv[cc][i][r];
-    if (ch > 0) s.fetch(ch - 1, p.o, p.L * orow, orow);
-    const long long id = static_cast<long long>(s.bh) * p.nc + ch;
-    s.store_state(p.dstates + id * p.dk * p.dv, S);
+  typename D::Buf &u = *up, &to = *top;
+  const long long id = static_cast<long long>(s.bh) * p.nc + ch;
 
-    f32x4 y[NC][4];
+  f32x4 y[NC][4], x[NC][4];
 #pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
+  for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) y[cc][i] = x[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  bf16x8 ka[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][3], vb[NC][2][NP];
+  i32x4 out[D::CP] = {};
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      bf16x8 sb[NC][3];
+  for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
+  if (behind) s.take(to, out);
+  s.template store_tiles<RT>(p.dstates, id, delta_tiles(p.dk), S);
+  if (more) s.fetch_qk(ch - 1, p.k, to.k, s.rk);
 #pragma unroll
-      for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc]);
+  for (int kb = 0; kb < KB; ++kb) {
+    if (kb + 1 < KB) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf16x8 a[NP];
-        u.k.rows(i, kb, m, g, a);
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(y[cc][i], a, sb[cc]);
-      }
-    }
-    bf16x8 xb[NC][2][3];
-    f32x4 x[NC][4];
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const float(&lo)[4] = v[cc][2 * kb], (&hi)[4] = v[cc][2 * kb + 1];
-        split_tiles<NP>(f32x4{lo[0], lo[1], lo[2], lo[3]}, f32x4{hi[0], hi[1], hi[2], hi[3]}, xb[cc][kb]);
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 sg = s.row4(u, kRowS, i);
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) y[cc][i] *= sg;
-#pragma unroll
-      for (int kb = i / 2; kb < 2; ++kb) {
-        bf16x8 a[3];
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) a[pl] = u.frags[D::F::T + (up_block(i, kb) * 3 + pl) * 64 + s.lane];
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<3, NP>(y[cc][i], a, xb[cc][kb]);
-      }
-    }
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) x[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int kb = i / 2; kb < 2; ++kb) {
-        bf16x8 a[3];
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) a[pl] = u.frags[(up_block(i, kb) * 3 + pl) * 64 + s.lane];
-#pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<3, 3>(x[cc][i], a, xb[cc][kb]);
-      }
-    }
-    s.store_rows(p.dxs + id * kDeltaChunk * p.dv, x);
-    const float whole = u.rows[kRowWhole * 64];
-    bf16x8 ob[NC][2][3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 xg = s.row4(u, kRowX, i), og = s.row4(u, kRowO, i);
+      for (int i = 0; i < 4; ++i) u.k.rows(i, kb + 1, m, g, ka[(kb + 1) & 1][i]);
+    } else {
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[cc][i][r] *= -xg[r];
-          y[cc][i][r] = og[r] * v[cc][i][r];
-        }
+        for (int k2 = 0; k2 < 2; ++k2) u.v.columns(s.w * NC + cc, k2, m, g, vb[cc][k2]);
+#pragma unroll
+      for (int j = 0; j < kTriBlocks; ++j)
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) pa[j][pl] = u.frags[D::F::T + (j * 3 + pl) * 64 + s.lane];
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) mma_rows<NP, 3>(y[cc], ka[kb & 1], sb[cc][kb]);
+  }
+#pragma unroll
+  for (int j = 0; j < kTriBlocks; ++j)
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl) ta[j][pl] = u.frags[(j * 3 + pl) * 64 + s.lane];
+  if (behind) s.send(out, p.gv, (ch + 1) * kDeltaChunk, min(p.L - (ch + 1) * kDeltaChunk, kDeltaChunk));
+  if (more) s.fetch_qk(ch - 1, p.q, to.q, s.rq);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x4 sg = s.row4(u, kRowS, i);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) y[cc][i] *= sg;
+  }
+  tri_rows<3, NP, NC, true>(y, pa, vb);
+  constexpr int TG = NP == 1 ? 2 : 1;  // tiles of the state at a time
+  bf16x8 xb[NC][2][3], ob[NC][2][3], kc[2][TG][2][NP], qc[2][TG][2][NP];
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+#pragma unroll
+  for (int t = 0; t < TG; ++t)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      u.q.columns(t, kb, m, g, qc[0][t][kb]);
+      u.k.columns(t, kb, m, g, kc[0][t][kb]);
+    }
+  if (more) {
+    s.fetch_v(ch - 1, o, to);
+    s.fetch_rows(ch - 1);
+    s.template fetch_frags<0, D::FP / 2>(ch - 1, to);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  tri_rows<3, 3, NC, true>(x, ta, xb);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x4 og = s.row4(u, kRowO, i);
 #pragma unroll
     for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        split_tiles<3>(x[cc][2 * kb], x[cc][2 * kb + 1], xb[cc][kb]);
-        split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], ob[cc][kb]);
-      }
+      for (int r = 0; r < 4; ++r) y[cc][i][r] = og[r] * plane_sum<NP>(vb[cc][i / 2], 4 * (i & 1) + r);
+  }
+  const float whole = u.rows[kRowWhole * 64];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
+  for (int cc = 0; cc < NC; ++cc) {
 #pragma unroll
-      for (int cc = 0; cc < NC; ++cc) S[cc][t] *= whole;
+    for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], ob[cc][kb]);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        bf16x8 a[NP];
-        u.k.columns(t, kb, m, g, a);
+    for (int t = 0; t < RT; ++t) S[cc][t] *= whole;
+  }
+  if (more) s.template fetch_frags<D::FP / 2, D::FP>(ch - 1, to);
+  __builtin_amdgcn_sched_barrier(0);
+  s.template store_tiles<4>(p.dxs, id, 4, x);
+  s.result(u, p.gv, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), x);
 #pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(S[cc][t], a, xb[cc][kb]);
-        u.q.columns(t, kb, m, g, a);
+  for (int cc = 0; cc < NC; ++cc) {
 #pragma unroll
-        for (int cc = 0; cc < NC; ++cc) mma<NP, 3>(S[cc][t], a, ob[cc][kb]);
-      }
+    for (int i = 0; i < 4; ++i) x[cc][i] *= -s.row4(u, kRowX, i);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) split_tiles<3>(x[cc][2 * kb], x[cc][2 * kb + 1], xb[cc][kb]);
+  }
+#pragma unroll
+  for (int t0 = 0; t0 < RT; t0 += TG) {
+    if (t0 + TG < RT) {
+#pragma unroll
+      for (int t = 0; t < TG; ++t)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          u.q.columns(t0 + TG + t, kb, m, g, qc[(t0 / TG + 1) & 1][t][kb]);
+          u.k.columns(t0 + TG + t, kb, m, g, kc[(t0 / TG + 1) & 1][t][kb]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    state_tiles<NP, TG, NC>(S, t0, qc[(t0 / TG) & 1], ob);
+    state_tiles<NP, TG, NC>(S, t0, kc[(t0 / TG) & 1], xb);
+    const int t = t0 + TG - 2;
+    if (t >= 0 && t % 2 == 0) {
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][t], S[cc][t + 1], sb[cc][t / 2]);
+    }
+  }
+}
+
+// dS from the last chunk to the first; p.s0 is dsT and p.sT is ds0
+template <class UT, int MODE, int DK, int NC, int NW>
+__global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaArgs p) {
+  typedef DeltaScan<UT, MODE, DK, NC, NW, true> D;
+  typedef typename D::Buf Buf;
+  constexpr int RT = D::RT, KB = D::KB;
+  __shared__ Buf buf[D::NBUF];
+  D s(p);
+  if (s.idle) return;
+  f32x4 S[NC][RT];
+  const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
+  bf16x8 sb[NC][KB][3];
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
+  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
+  if (s.nch > 0) {
+    Buf& u = buf[(s.nch - 1) & (D::NBUF - 1)];
+    s.fetch_all(s.nch - 1, o, u);
+    s.land(u);
+  }
+  __syncthreads();
+  for (int ch = s.nch - 1; ch >= 0; --ch) {
+    const int at = ch & (D::NBUF - 1), next = (ch + 1) & (D::NBUF - 1);
+    const bool more = ch > 0;
+    delta_back_chunk<D, UT, DK, NC>(s, p, o, ch, more, ch + 1 < s.nch, &buf[at], &buf[next], S, sb);
     if constexpr (D::NBUF == 1) __syncthreads();
-    if (ch > 0) s.land(buf[D::NBUF == 2 ? (ch - 1) & 1 : 0]);
+    if (more) s.land(buf[next]);
     __syncthreads();
   }
   if (p.sT) s.store_state(p.sT + at_state, S);
+  if (s.nch > 0) s.flush(buf[0], p.gv, 0, min(p.L, kDeltaChunk));
+  // rows behind the last chunk of the sequence
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+    if (s.col(cc) < p.dv)
+      for (long long t = static_cast<long long>(s.nch) * kDeltaChunk + s.g; t < p.L; t += 4)
+        store1(out_at<UT>(p.gv, s.b, t) + static_cast<long long>(s.hv) * p.dv + s.col(cc), 0.0f);
 }
 
 // A workgroup per chunk and head of q and k: the gradients of q, k, v and the
@@ -682,8 +914,10 @@ template <class UT, int DK>
 struct DeltaGradLds {
   static constexpr int NP = DeltaPlanes<UT>::NP, RT = DK / 16;
   typedef DeltaTile<DK, NP> Tile;
-  struct Stage {  // 32 columns of dv, in the order of the operands' reads
-    bf16x8 s[RT * 3 * 64], ds[RT * 3 * 64], y[4 * 3 * 64], x[4 * 3 * 64], o[4 * NP * 64];
+  struct Stage {  // 32 columns of dv, which are the rows of all but dO
+    DeltaTile<DK, 3, 32> s, ds;
+    DeltaTile<64, 3, 32> y, x;
+    DeltaTile<32, NP> o;
   };
   static constexpr bool APART = sizeof(Stage) + 2 * sizeof(Tile) <= 120 * 1024;  // the tiles beside the stage
   static constexpr int ROW = 68;
@@ -696,7 +930,7 @@ struct DeltaGradLds {
   static constexpr size_t BYTES = APART ? kStage + kTiles : (kStage > kTiles + sizeof(Mats) ? kStage : kTiles + sizeof(Mats));
 };
 
-template <class UT, int DK>
+template <class UT, bool EVEN, int DK>
 __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   typedef DeltaGradLds<UT, DK> M;
   typedef typename M::Tile Tile;
@@ -719,8 +953,6 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
       store1(out_at<UT>(p.gq, b, t0 + i / p.dk) + h * p.dk + i % p.dk, 0.0f);
       store1(out_at<UT>(p.gk, b, t0 + i / p.dk) + h * p.dk + i % p.dk, 0.0f);
     }
-    for (int i = tid; i < rows_out * per * p.dv; i += 512)
-      store1(out_at<UT>(p.gv, b, t0 + i / (per * p.dv)) + static_cast<long long>(h) * per * p.dv + i % (per * p.dv), 0.0f);
     for (int i = tid; i < rows_out * per; i += 512) {
       UT* to = out_at<UT>(p.dgates, b, t0 + i / per) + h * per + i % per;
       store1(to, 0.0f);
@@ -732,11 +964,24 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   const int n = min(len - t0, kDeltaChunk);
   constexpr float kLog2e = 1.4426950408889634f;
   auto tiles = [&]() {
-    for (int e = tid; e < 64 * DK / 8; e += 512) {
-      const int row = e / (DK / 8), d = e % (DK / 8) * 8;
-      const long long t = t0 + min(row, n - 1);
-      tk.put(row, d, load_raw8<UT>(at<UT>(p.k, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk));
-      tq.put(row, d, load_raw8<UT>(at<UT>(p.q, b, t) + h * p.dk, d, p.dk, row < n, p.wide_qk));
+    constexpr int N = (64 * DK / 8 + 511) / 512;
+    const __amdgpu_buffer_rsrc_t kr = rows_of<UT>(p.k, b, t0, h * p.dk, n, p.H * p.dk);
+    const __amdgpu_buffer_rsrc_t qr = rows_of<UT>(p.q, b, t0, h * p.dk, n, p.H * p.dk);
+    Piece<UT, EVEN> a[N], c[N];
+    const int row = tid / (DK / 8), d = Tile::source(tid);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = row + 512 / (DK / 8) * i;
+      a[i].load(kr, offset_of<UT>(r, p.k.token, d, r < n && d < p.dk));
+      c[i].load(qr, offset_of<UT>(r, p.q.token, d, r < n && d < p.dk));
+    }
+    bf16x8 o[NP];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      planes_of(a[i], p.dk - d, o);
+      tk.put_slot(tid + 512 * i, o);
+      planes_of(c[i], p.dk - d, o);
+      tq.put_slot(tid + 512 * i, o);
     }
   };
   if constexpr (M::APART) tiles();
@@ -751,12 +996,33 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   for (int hr = 0; hr < per; ++hr) {
     const int hv = h * per + hr;
     const long long id = (static_cast<long long>(b) * p.HV + hv) * p.nc + ch;
-    const float* S = p.states + id * p.dk * p.dv;
-    const float* dS = p.dstates + id * p.dk * p.dv;
-    const float* Y = p.ys + id * kDeltaChunk * p.dv;
-    const float* X = p.dxs + id * kDeltaChunk * p.dv;
-    const UT* O = static_cast<const UT*>(p.o) + ((static_cast<long long>(b) * p.L + t0) * p.HV + hv) * p.dv;
-    const long long orow = static_cast<long long>(p.HV) * p.dv;
+    const int rt = delta_tiles(p.dk), nct = delta_tiles(p.dv);
+    const DeltaView ov = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
+    const __amdgpu_buffer_rsrc_t orr = rows_of<UT>(ov, b, t0, hv * p.dv, n, p.HV * p.dv);
+    // all that a chunk has lies in one run of memory: 32-bit offsets
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.states + id * nct * rt * 64, nct * rt * 1024),
+                                 dsr = make_rsrc(p.dstates + id * nct * rt * 64, nct * rt * 1024),
+                                 yr = make_rsrc(p.ys + id * nct * 4 * 64, nct * 4096),
+                                 xr = make_rsrc(p.dxs + id * nct * 4 * 64, nct * 4096);
+    // the thread's share of a block of 32 columns, one block ahead: waves deal out the tiles
+    constexpr int NS = RT * 2 / 8;
+    i32x4 fs[NS], fd[NS], fy, fx;
+    Piece<UT, EVEN> fo;
+    auto fetch = [&](int vb) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int e = w8 + 8 * i, c = 2 * vb + e / RT, t = e % RT;
+        const uint32_t off = t < rt ? static_cast<uint32_t>((c * rt + t) * 64 + lane) * 16 : kNoLoad;
+        fs[i] = __builtin_amdgcn_raw_buffer_load_b128(sr, off, 0, 0);
+        fd[i] = __builtin_amdgcn_raw_buffer_load_b128(dsr, off, 0, 0);
+      }
+      const uint32_t off = static_cast<uint32_t>(((2 * vb + f) * 4 + w) * 64 + lane) * 16;
+      fy = __builtin_amdgcn_raw_buffer_load_b128(yr, off, 0, 0);
+      fx = __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0);
+      const int row = tid >> 2, d = 32 * vb + sg.o.source(tid);
+      if (f == 0) fo.load(orr, offset_of<UT>(row, ov.token, d, row < n && d < p.dv));
+    };
+    fetch(0);
     for (int i = tid; i < kRows * 64; i += 512) srow[i] = p.rows[id * (kRows * 64) + i];
     f32x4 qo[HT], kx[HT], yd[HT], dd[4];
     float dot = 0.0f;
@@ -766,68 +1032,41 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
     for (int j = 0; j < 4; ++j) dd[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int nb = (p.dv + 31) / 32;
     for (int vb = 0; vb < nb; ++vb) {
-      // 8 columns per lane: lane (m, g) of tile t has row 16 t + m, columns 32 vb + 8 g ..
-      const int d = 32 * vb + 8 * g;
       __syncthreads();
-      if (w8 < RT) {
-        const int r = 16 * w8 + m;
-        const bool on = r < p.dk;
-        const Raw8<float> a = load_raw8<float>(S + static_cast<long long>(on ? r : 0) * p.dv, d, p.dv, on, p.wide_o);
-        const Raw8<float> e = load_raw8<float>(dS + static_cast<long long>(on ? r : 0) * p.dv, d, p.dv, on, p.wide_o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot = fmaf(a.at(i), e.at(i), dot);
-        bf16x8 o[3];
-        planes_of(a, o);
+      for (int i = 0; i < NS; ++i) {
+        const int e = w8 + 8 * i, c = e / RT, t = e % RT;
+        const f32x4 a = __builtin_bit_cast(f32x4, fs[i]), d = __builtin_bit_cast(f32x4, fd[i]);
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) sg.s[(w8 * 3 + pl) * 64 + lane] = o[pl];
-        planes_of(e, o);
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) sg.ds[(w8 * 3 + pl) * 64 + lane] = o[pl];
+        for (int r = 0; r < 4; ++r) dot = fmaf(a[r], d[r], dot);
+        sg.s.put4(16 * c + m, delta_label(t, 4 * g), a);
+        sg.ds.put4(16 * c + m, delta_label(t, 4 * g), d);
       }
-      {
-        const int r = 16 * w + m;
-        const bool on = r < n;
-        const Raw8<float> a = load_raw8<float>((f ? X : Y) + static_cast<long long>(r) * p.dv, d, p.dv, true, p.wide_o);
-        bf16x8 o[3];
-        planes_of(a, o);
-        bf16x8* to = f ? sg.x : sg.y;
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) to[(w * 3 + pl) * 64 + lane] = o[pl];
-        if (f) {
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = on ? a.at(i) : 0.0f;
-          if (r < rows_out) store8(out_at<UT>(p.gv, b, t0 + r) + static_cast<long long>(hv) * p.dv, d, p.dv, p.wide_dv, x);
-        } else {
-          planes_of(load_raw8<UT>(O + (on ? r : 0) * orow, d, p.dv, on, p.wide_v), o);
-#pragma unroll
-          for (int pl = 0; pl < NP; ++pl) sg.o[(w * NP + pl) * 64 + lane] = o[pl];
-        }
+      sg.y.put4(16 * f + m, delta_label(w, 4 * g), __builtin_bit_cast(f32x4, fy));
+      sg.x.put4(16 * f + m, delta_label(w, 4 * g), __builtin_bit_cast(f32x4, fx));
+      if (f == 0) {
+        bf16x8 o[NP];
+        planes_of(fo, p.dv - 32 * vb - sg.o.source(tid), o);
+        sg.o.put_slot(tid, o);
       }
       __syncthreads();
+      if (vb + 1 < nb) fetch(vb + 1);
       bf16x8 ao[NP], ax[3], ay[3], bb[3];
-#pragma unroll
-      for (int pl = 0; pl < NP; ++pl) ao[pl] = sg.o[(w * NP + pl) * 64 + lane];
-#pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        ax[pl] = sg.x[(w * 3 + pl) * 64 + lane];
-        ay[pl] = sg.y[(w * 3 + pl) * 64 + lane];
-      }
+      sg.o.rows(w, 0, m, g, ao);
+      sg.x.columns(w, 0, m, g, ax);
+      sg.y.columns(w, 0, m, g, ay);
 #pragma unroll
       for (int t = 0; t < HT; ++t) {
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) bb[pl] = sg.s[((f * HT + t) * 3 + pl) * 64 + lane];
+        sg.s.columns(f * HT + t, 0, m, g, bb);
         mma<NP, 3>(qo[t], ao, bb);
         mma<3, 3>(kx[t], ax, bb);
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) bb[pl] = sg.ds[((f * HT + t) * 3 + pl) * 64 + lane];
+        sg.ds.columns(f * HT + t, 0, m, g, bb);
         mma<3, 3>(yd[t], ay, bb);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w) {
-#pragma unroll
-          for (int pl = 0; pl < 3; ++pl) bb[pl] = sg.y[(j * 3 + pl) * 64 + lane];
+          sg.y.columns(j, 0, m, g, bb);
           if (f == 0) mma<NP, 3>(dd[j], ao, bb);
           else mma<3, 3>(dd[j], ax, bb);
         }
@@ -869,7 +1108,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
         qo[t][r] *= p.scale * gamma;
         kr[t][r] = -gamma * kx[t][r];
         kw[t][r] = wr * yd[t][r];
-        part[3][r] = fmaf(kw[t][r], rk[r] * tk.at(i, 16 * (f * HT + t) + m), part[3][r]);
+        part[3][r] = fmaf(kw[t][r], rk[r] * tk.at(i, delta_label(f * HT + t, m)), part[3][r]);
       }
     }
 #pragma unroll
@@ -912,7 +1151,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
     for (int t = 0; t < HT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * w + 4 * g + r, d = 16 * (f * HT + t) + m;
+        const int i = 16 * w + 4 * g + r, d = delta_label(f * HT + t, m);
         const float qv = rq[r] * tq.at(i, d), kv = rk[r] * tk.at(i, d);
         part[0][r] = fmaf(qv, qo[t][r], part[0][r]);
         part[1][r] = fmaf(kv, kr[t][r], part[1][r]);
@@ -984,7 +1223,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
       UT* ko = out_at<UT>(p.gk, b, t0 + i) + h * p.dk;
 #pragma unroll
       for (int t = 0; t < HT; ++t) {
-        const int d = 16 * (f * HT + t) + m;
+        const int d = delta_label(f * HT + t, m);
         if (d < p.dk) {
           store1(qo + d, rq * fmaf(-rq * tq.at(i, d), qsum[r], dq[t][r]));
           store1(ko + d, rk * fmaf(-rk * tk.at(i, d), ksum[r], dk[t][r]));
