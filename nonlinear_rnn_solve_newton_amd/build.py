@@ -27,6 +27,9 @@ ARCH = "gfx950"
 COMMON_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-Wall"]
 # no packed fp32 (v_pk_*_f32) instructions in the device code
 DEVICE_FLAGS = ["--cuda-device-only", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+# results of matrix instructions in ordinary registers, where the vector instructions between them are: the
+# delta rule's waves would spend a tenth of their instructions on moves between the two files
+DELTA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 HOST_FLAGS = ["--cuda-host-only", "-fPIC", "-shared"]
 
 
@@ -35,13 +38,15 @@ def hipcc() -> str:
     return str(Path(rocm) / "bin" / "hipcc")
 
 
-def build_one(src: Path, out: Path, verbose: bool = False, extra_flags=(), host_flags=()) -> Path:
+def build_one(src: Path, out: Path, verbose: bool = False, extra_flags=(), host_flags=(),
+              device_flags=()) -> Path:
     """Compile one .hip source into a shared library at `out`; host_flags go to
-    the host pass only (e.g. a sanitizer build of the host code)."""
+    the host pass only (e.g. a sanitizer build of the host code), device_flags to
+    the device pass."""
     tmp = out.with_name(out.name + ".tmp")
     with tempfile.TemporaryDirectory() as td:
         fatbin = Path(td) / (src.stem + ".hipfb")
-        dev = [hipcc(), *COMMON_FLAGS, *DEVICE_FLAGS, *extra_flags, str(src), "-o", str(fatbin)]
+        dev = [hipcc(), *COMMON_FLAGS, *DEVICE_FLAGS, *device_flags, *extra_flags, str(src), "-o", str(fatbin)]
         host = [hipcc(), *COMMON_FLAGS, *HOST_FLAGS, *extra_flags, *host_flags, "-Xclang", "-fcuda-include-gpubinary",
                 "-Xclang", str(fatbin), str(src), "-o", str(tmp)]
         for cmd in (dev, host):
@@ -55,7 +60,7 @@ def build_one(src: Path, out: Path, verbose: bool = False, extra_flags=(), host_
 def build(verbose: bool = False, extra_flags=()) -> Path:
     build_one(CSRC / "ceilings.hip", CEIL_LIB, verbose, extra_flags)
     build_one(CSRC / "layer.hip", LAYER_LIB, verbose, extra_flags)
-    build_one(CSRC / "delta.hip", DELTA_LIB, verbose, extra_flags)
+    build_one(CSRC / "delta.hip", DELTA_LIB, verbose, extra_flags, device_flags=DELTA_FLAGS)
     return build_one(CSRC / "pararnn.hip", LIB, verbose, extra_flags)
 
 

@@ -94,7 +94,7 @@ struct DeltaForward {
   template <class UT, int MODE, int DK>
   static int run(const DeltaArgs& a, const float*, float*, float*, hipStream_t s) {
     if (const int rc = run_prep<UT, MODE != kOdd, DK, false>(a, s)) return rc;
-    return launch(delta_scan_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), 256, s, a);
+    return launch(delta_scan_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), DeltaScan<UT, MODE, DK, 1, 4, false>::THREADS, s, a);
   }
 };
 struct DeltaAdjoint {
@@ -104,7 +104,8 @@ struct DeltaAdjoint {
     if (const int rc = run_prep<UT, EVEN, DK, true>(a, s)) return rc;
     a.s0 = dsT;
     a.sT = ds0;
-    if (const int rc = launch(delta_back_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), 256, s, a)) return rc;
+    if (const int rc = launch(delta_back_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), DeltaScan<UT, MODE, DK, 1, 4, true>::THREADS, s, a))
+      return rc;
     if (const int rc = launch(delta_grad_kernel<UT, EVEN, DK>, static_cast<long long>(a.B) * a.H * a.nc, 512, s, a)) return rc;
     if (!dlam) return PARARNN_OK;
     return launch(delta_dlam_kernel, a.HV, 256, s, static_cast<const float*>(a.dlam_part), a.lam, dlam, a.B * a.nc, a.c);

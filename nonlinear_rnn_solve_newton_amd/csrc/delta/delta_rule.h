@@ -300,32 +300,58 @@ struct DeltaBuf {
   float rows[4 * 64];
 };
 
-// The scans' common part: which columns a wave has, and the way of a chunk
-// from memory to workgroup memory, one chunk ahead: through registers, or direct
+// The scans' common part. NW waves have 16 NC columns of dv each and work on a
+// chunk; NL more waves bring the next one meanwhile and send the results of the
+// one before. A CU takes 25 bytes a cycle from memory, so that a chunk (70 KB)
+// keeps whoever asks for it waiting for 3000 cycles of the 5500 that its products
+// take (with each wave loading its share, 8500). One such wave does where loads
+// write to workgroup memory (kDirect), four where they pass through registers;
+// fp32 needs the registers of two waves for one, and its waves load for
+// themselves.
 template <class UT, int MODE, int DK, int NC, int NW, bool ADJ>
 struct DeltaScan {
-  static constexpr int NP = DeltaPlanes<UT>::NP, NT = 64 * NW, RT = DK / 16, KB = DK / 32, VC = 16 * NC * NW;
-  static constexpr bool DIRECT = MODE == kDirect;
+  static constexpr int NP = DeltaPlanes<UT>::NP, RT = DK / 16, KB = DK / 32, VC = 16 * NC * NW;
+  static constexpr bool DIRECT = MODE == kDirect, INPLACE = sizeof(UT) == 2;
+  static constexpr int NL = DIRECT ? 1 : INPLACE ? 4 : 0, THREADS = 64 * (NW + NL), NT = 64 * (NL ? NL : NW);
   typedef DeltaFrags<UT, ADJ> F;
   typedef DeltaBuf<UT, DK, VC, ADJ> Buf;
   static constexpr int NBUF = 2 * sizeof(Buf) <= 160 * 1024 ? 2 : 1;
-  static constexpr bool INPLACE = sizeof(UT) == 2;
-  static_assert(!INPLACE || NBUF == 2, "results wait in the other buffer");
-  static constexpr int TP = 64 * DK / 8 / NT, FP = (F::ALL + NT - 1) / NT, VP = 256 / NT, CP = 64 * VC / 8 / NT;
-  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0 && 64 * VC / 8 % NT == 0, "whole rounds");
-  static_assert(NT / (DK / 8) % 16 == 0 && NT / (VC / 8) % 16 == 0, "a thread's slots lie in one column, with one turn");
-  static_assert(F::ALL % 64 == 0, "whole waves");
+  static_assert(NL == 0 || NBUF == 2, "a buffer to work on and one to fill");
+  // rounds of the loading threads: chunks of q or k, of v, of the triangular operands, row factors
+  static constexpr int TP = 64 * DK / 8 / NT, CP = 64 * VC / 8 / NT, FP = (F::ALL + NT - 1) / NT, VP = 256 / NT;
+  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0 && 64 * VC / 8 % NT == 0 && F::ALL % 64 == 0, "whole rounds");
+
+  // A tensor's rows of the chunk that is fetched next. Rows behind a row's last step lie past the resource's
+  // extent (a token is at least as long as its packed elements) and so come as zeros: nothing but the
+  // resource changes from chunk to chunk.
+  struct Source {
+    const char* at;      // the chunk's first row
+    long long step;      // bytes from chunk to chunk
+    uint32_t row, tail;  // bytes from row to row, and of a row's elements that may be read
+    __device__ __forceinline__ void set(const DeltaView& v, int b, long long t, int d, int packed, int dir) {
+      row = static_cast<uint32_t>(v.token) * sizeof(UT);
+      at = reinterpret_cast<const char*>(pararnn::at<UT>(v, b, t) + d);
+      step = dir * static_cast<long long>(row) * kDeltaChunk;
+      tail = static_cast<uint32_t>(packed - d) * sizeof(UT);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int n) const { return make_rsrc(at, (n - 1) * row + tail); }
+  };
 
   const DeltaArgs& p;
-  int tid, lane, w, m, g, b, hv, h, bh, wg0, col0, len, nch;
-  int trow, tcol, vrow, vcol;  // the thread's first slot of q and k, and of v
-  bool idle;
+  int lane, w, m, g, b, hv, h, bh, wg0, col0, len, nch;
+  bool idle, loads;
+  // of the loading threads
+  int lt, dir, left;  // number, direction, steps of the chunk that is fetched next
+  Source sk, sq, sv;
+  const bf16x8* fp;
+  const float* rp;
   Piece<UT, MODE != kOdd> rk[DIRECT ? 1 : TP], rq[DIRECT ? 1 : TP], rv[DIRECT ? 1 : CP];
   i32x4 rf[DIRECT ? 1 : FP];
   float rr[VP];
 
-  __device__ __forceinline__ explicit DeltaScan(const DeltaArgs& a) : p(a) {
-    tid = threadIdx.x;
+  // v: the tensor whose columns the waves have; dir: 1 from the first chunk on, -1 from the last
+  __device__ __forceinline__ DeltaScan(const DeltaArgs& a, const DeltaView& v, int dir_) : p(a), dir(dir_) {
+    const int tid = threadIdx.x;
     lane = tid & 63;
     w = __builtin_amdgcn_readfirstlane(tid >> 6);
     m = lane & 15;
@@ -343,59 +369,53 @@ struct DeltaScan {
     col0 = wg0 / 16 + w * NC;
     len = delta_len(p, b);
     nch = (len + kDeltaChunk - 1) / kDeltaChunk;
-    trow = tid / (DK / 8);
-    tcol = DeltaTile<DK, NP>::source(tid);
-    vrow = tid / (VC / 8);
-    vcol = DeltaTile<VC, NP>::source(tid);
+    loads = NL && w >= NW;
+    lt = NL ? tid - 64 * NW : tid;
+    const int first = dir > 0 || nch == 0 ? 0 : nch - 1;
+    left = len - first * kDeltaChunk;
+    sk.set(p.k, b, static_cast<long long>(first) * kDeltaChunk, h * p.dk, p.H * p.dk, dir);
+    sq.set(p.q, b, static_cast<long long>(first) * kDeltaChunk, h * p.dk, p.H * p.dk, dir);
+    sv.set(v, b, static_cast<long long>(first) * kDeltaChunk, hv * p.dv, p.HV * p.dv, dir);
+    fp = p.frags + (static_cast<long long>(bh) * p.nc + first) * F::ALL;
+    rp = p.rows + (static_cast<long long>(bh) * p.nc + first) * (kRows * 64);
   }
   // the lane's column of v: column m of tile col0 + cc
   __device__ __forceinline__ int col(int cc) const { return delta_label(col0 + cc, m); }
-  __device__ __forceinline__ void fetch_qk(int ch, const DeltaView& x, DeltaTile<DK, NP>& to, decltype(rk)& r) {
-    const int t0 = ch * kDeltaChunk, n = min(len - t0, kDeltaChunk);
-    const __amdgpu_buffer_rsrc_t rs = rows_of<UT>(x, b, t0, h * p.dk, n, p.H * p.dk);
+  // a tile of COLS columns, those from d0 on of `cols`
+  template <int COLS, int N, class Regs>
+  __device__ __forceinline__ void fetch_tile(const Source& x, int d0, int cols, DeltaTile<COLS, NP>& to, Regs& r) {
+    constexpr int CH = COLS / 8;
+    const __amdgpu_buffer_rsrc_t rs = x.rows(min(left, kDeltaChunk));
 #pragma unroll
-    for (int i = 0; i < TP; ++i) {
-      const int row = trow + NT / (DK / 8) * i;
-      const uint32_t off = offset_of<UT>(row, x.token, tcol, row < n && tcol < p.dk);
-      if constexpr (DIRECT) load_to_lds(rs, &to.x[0][(64 * w + NT * i) * 8], off);
+    for (int i = 0; i < N; ++i) {
+      const int e = lt + NT * i, d = d0 + DeltaTile<COLS, NP>::source(e);
+      const uint32_t off = d < cols ? static_cast<uint32_t>(e / CH) * x.row + d * static_cast<uint32_t>(sizeof(UT)) : kNoLoad;
+      if constexpr (DIRECT) load_to_lds(rs, &to.x[0][(NT * i + (lt & ~63)) * 8], off);
       else r[i].load(rs, off);
     }
   }
-  __device__ __forceinline__ void fetch_v(int ch, const DeltaView& x, Buf& to) {
-    const int t0 = ch * kDeltaChunk, n = min(len - t0, kDeltaChunk);
-    const __amdgpu_buffer_rsrc_t rs = rows_of<UT>(x, b, t0, hv * p.dv, n, p.HV * p.dv);
+  // the next chunk's loads
+  __device__ __forceinline__ void fetch(Buf& to) {
+    fetch_tile<DK, TP>(sk, 0, p.dk, to.k, rk);
+    fetch_tile<DK, TP>(sq, 0, p.dk, to.q, rq);
+    fetch_tile<VC, CP>(sv, wg0, p.dv, to.v, rv);
+    const __amdgpu_buffer_rsrc_t fr = make_rsrc(fp, F::ALL * 16);
 #pragma unroll
-    for (int i = 0; i < CP; ++i) {
-      const int row = vrow + NT / (VC / 8) * i;
-      const uint32_t off = offset_of<UT>(row, x.token, wg0 + vcol, row < n && wg0 + vcol < p.dv);
-      if constexpr (DIRECT) load_to_lds(rs, &to.v.x[0][(64 * w + NT * i) * 8], off);
-      else rv[i].load(rs, off);
-    }
-  }
-  // the triangular operands [FROM, TO) of FP rounds
-  template <int FROM, int TO>
-  __device__ __forceinline__ void fetch_frags(int ch, Buf& to) {
-    const __amdgpu_buffer_rsrc_t fr = make_rsrc(p.frags + (static_cast<long long>(bh) * p.nc + ch) * F::ALL, F::ALL * 16);
-#pragma unroll
-    for (int i = FROM; i < TO; ++i) {
+    for (int i = 0; i < FP; ++i) {
       if constexpr (DIRECT) {
-        if (NT * (i + 1) <= F::ALL || 64 * w + NT * i < F::ALL) load_to_lds(fr, &to.frags[64 * w + NT * i], (tid + NT * i) * 16);
+        if (NT * (i + 1) <= F::ALL || (lt & ~63) + NT * i < F::ALL) load_to_lds(fr, &to.frags[(lt & ~63) + NT * i], (lt + NT * i) * 16);
       } else {
-        rf[i] = __builtin_amdgcn_raw_buffer_load_b128(fr, (tid + NT * i) * 16, 0, 0);
+        rf[i] = __builtin_amdgcn_raw_buffer_load_b128(fr, (lt + NT * i) * 16, 0, 0);
       }
     }
-  }
-  __device__ __forceinline__ void fetch_rows(int ch) {
 #pragma unroll
-    for (int i = 0; i < VP; ++i)
-      rr[i] = p.rows[(static_cast<long long>(bh) * p.nc + ch) * (kRows * 64) + tid + NT * i];
-  }
-  __device__ __forceinline__ void fetch_all(int ch, const DeltaView& v, Buf& to) {
-    fetch_qk(ch, p.k, to.k, rk);
-    fetch_qk(ch, p.q, to.q, rq);
-    fetch_v(ch, v, to);
-    fetch_frags<0, FP>(ch, to);
-    fetch_rows(ch);
+    for (int i = 0; i < VP; ++i) rr[i] = rp[lt + NT * i];
+    sk.at += sk.step;
+    sq.at += sq.step;
+    sv.at += sv.step;
+    fp += dir * F::ALL;
+    rp += dir * (kRows * 64);
+    left -= dir * kDeltaChunk;
   }
   // what came through registers; then the loads that did not are waited for
   __device__ __forceinline__ void land(Buf& to) {
@@ -403,22 +423,25 @@ struct DeltaScan {
       bf16x8 o[NP];
 #pragma unroll
       for (int i = 0; i < TP; ++i) {
-        planes_of(rk[i], p.dk - tcol, o);
-        to.k.put_slot(tid + NT * i, o);
-        planes_of(rq[i], p.dk - tcol, o);
-        to.q.put_slot(tid + NT * i, o);
+        planes_of(rk[i], p.dk - DeltaTile<DK, NP>::source(lt + NT * i), o);
+        to.k.put_slot(lt + NT * i, o);
+      }
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        planes_of(rq[i], p.dk - DeltaTile<DK, NP>::source(lt + NT * i), o);
+        to.q.put_slot(lt + NT * i, o);
       }
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
-        planes_of(rv[i], p.dv - wg0 - vcol, o);
-        to.v.put_slot(tid + NT * i, o);
+        planes_of(rv[i], p.dv - wg0 - DeltaTile<VC, NP>::source(lt + NT * i), o);
+        to.v.put_slot(lt + NT * i, o);
       }
 #pragma unroll
       for (int i = 0; i < FP; ++i)
-        if (NT * (i + 1) <= F::ALL || tid + NT * i < F::ALL) to.frags[tid + NT * i] = __builtin_bit_cast(bf16x8, rf[i]);
+        if (NT * (i + 1) <= F::ALL || lt + NT * i < F::ALL) to.frags[lt + NT * i] = __builtin_bit_cast(bf16x8, rf[i]);
     }
 #pragma unroll
-    for (int i = 0; i < VP; ++i) to.rows[tid + NT * i] = rr[i];
+    for (int i = 0; i < VP; ++i) to.rows[lt + NT * i] = rr[i];
     if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
   }
   // The wave's results Y of a chunk, rows of [..][HV][dv] from `to` on: into the place of its columns of v,
@@ -445,38 +468,30 @@ struct DeltaScan {
         }
     }
   }
-  // A thread takes the slots that it fills (or that its wave's loads fill) with the next chunk of the buffer,
-  // so nobody overwrites what another wave has not taken yet.
-  __device__ __forceinline__ void take(const Buf& u, i32x4 (&v)[CP]) const {
+  // The results of a chunk out of its buffer, by the loading waves: each takes the slots that it fills next, so
+  // nobody overwrites what another wave has not taken yet.
+  __device__ __forceinline__ void send(const Buf& u, const DeltaView& to, int t0, int rows) const {
     if constexpr (INPLACE) {
+      i32x4 v[CP];
 #pragma unroll
-      for (int i = 0; i < CP; ++i) v[i] = *reinterpret_cast<const i32x4*>(&u.v.x[0][(tid + NT * i) * 8]);
-      if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): taken, before a load may write there
-    }
-  }
-  __device__ __forceinline__ void send(const i32x4 (&v)[CP], const DeltaView& to, int t0, int rows) const {
-    if constexpr (INPLACE) {
-      const int at = wg0 + vcol, count = p.dv - at;
-      bf16* o = reinterpret_cast<bf16*>(out_at<UT>(to, b, t0)) + static_cast<long long>(hv) * p.dv + at;
+      for (int i = 0; i < CP; ++i) v[i] = *reinterpret_cast<const i32x4*>(&u.v.x[0][(lt + NT * i) * 8]);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): taken, before a load may write there
+      bf16* o = reinterpret_cast<bf16*>(out_at<UT>(to, b, t0)) + static_cast<long long>(hv) * p.dv + wg0;
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
-        const int row = vrow + NT / (VC / 8) * i;
+        const int e = lt + NT * i, row = e / (VC / 8), d = DeltaTile<VC, NP>::source(e), count = p.dv - wg0 - d;
+        bf16* at = o + row * to.token + d;
         if (row < rows && count > 0) {
           if (p.wide) {  // dv is a multiple of 8
-            *reinterpret_cast<i32x4*>(o + row * to.token) = v[i];
+            *reinterpret_cast<i32x4*>(at) = v[i];
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < count) o[row * to.token + e].bits = static_cast<uint16_t>(static_cast<uint32_t>(v[i][e >> 1]) >> (16 * (e & 1)));
+            for (int k = 0; k < 8; ++k)
+              if (k < count) at[k].bits = static_cast<uint16_t>(static_cast<uint32_t>(v[i][k >> 1]) >> (16 * (k & 1)));
           }
         }
       }
     }
-  }
-  __device__ __forceinline__ void flush(const Buf& u, const DeltaView& to, int t0, int rows) const {
-    i32x4 v[CP] = {};
-    take(u, v);
-    send(v, to, t0, rows);
   }
   __device__ __forceinline__ f32x4 row4(const Buf& u, int kind, int i) const {
     return *reinterpret_cast<const f32x4*>(&u.rows[kind * 64 + 16 * i + 4 * g]);
@@ -562,33 +577,25 @@ __device__ __forceinline__ void state_tiles(f32x4 (&S)[NC][RT], int t0, const bf
       }
 }
 
-// A chunk of the scan. `up` is the chunk's, `top` the next one's, which loads
-// fill meanwhile: restrict is what lets reads of the one pass loads into the other
-// without a wait.
+// A chunk of the scan
 template <class D, class UT, int DK, int NC>
-__device__ __forceinline__ void delta_scan_chunk(D& s, const DeltaArgs& p, const DeltaView& o, int ch, bool more,
-                                                 typename D::Buf* __restrict__ up, typename D::Buf* __restrict__ top,
+__device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p, const DeltaView& o, int ch, typename D::Buf& u,
                                                  f32x4 (&S)[NC][D::RT], bf16x8 (&sb)[NC][D::KB][3]) {
   constexpr int NP = D::NP, NO = DeltaPlanes<UT>::NO, RT = D::RT, KB = D::KB;
   const int m = s.m, g = s.g;
-  typename D::Buf &u = *up, &to = *top;
   const long long id = static_cast<long long>(s.bh) * p.nc + ch;
 
-  // Each part's operands are read while the part before it runs, and the next chunk's loads are dealt out
-  // over the parts: a wave has its matrix core to itself, and nothing else hides what a read takes. The
-  // compiler keeps to the order between sched_barriers.
+  // Each part's operands are read while the part before it runs: a wave has its matrix core to itself, and
+  // nothing else hides what a read takes. The compiler keeps to the order between sched_barriers.
   f32x4 ks[NC][4], qs[NC][4];
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int i = 0; i < 4; ++i) ks[cc][i] = qs[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   bf16x8 ka[2][4][NP], qa[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][NO], vv[NC][2][NP];
-  i32x4 out[D::CP] = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
-  if (ch > 0) s.take(to, out);  // the results of the chunk before, where the next one lands
   if (p.states) s.template store_tiles<RT>(p.states, id, delta_tiles(p.dk), S);
-  if (more) s.fetch_qk(ch + 1, p.k, to.k, s.rk);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
@@ -604,7 +611,7 @@ __device__ __forceinline__ void delta_scan_chunk(D& s, const DeltaArgs& p, const
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) u.v.columns(s.w * NC + cc, kb, m, g, vv[cc][kb]);
-  if (more) s.fetch_qk(ch + 1, p.q, to.q, s.rq);
+  const float whole = u.rows[kRowWhole * 64];
   bf16x8 xb[NC][2][3];
   f32x4 y[NC][4];
 #pragma unroll
@@ -636,24 +643,22 @@ __device__ __forceinline__ void delta_scan_chunk(D& s, const DeltaArgs& p, const
       }
     }
   }
+  __builtin_amdgcn_sched_barrier(0);
+  tri_rows<3, 3, NC>(y, ta, xb);
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) S[cc][t] *= whole;  // beside T's products
 #pragma unroll
   for (int j = 0; j < kTriBlocks; ++j)
 #pragma unroll
     for (int pl = 0; pl < NO; ++pl) pa[j][pl] = u.frags[D::F::T + (j * NO + pl) * 64 + s.lane];
-  if (ch > 0) s.send(out, o, (ch - 1) * kDeltaChunk, kDeltaChunk);
-  if (more) {
-    s.fetch_v(ch + 1, p.v, to);
-    s.fetch_rows(ch + 1);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  tri_rows<3, 3, NC>(y, ta, xb);
-  constexpr int TG = NP == 1 ? (RT < 4 ? RT : 4) : 2;  // tiles of the state at a time
+  constexpr int TG = 2;  // tiles of the state at a time
   bf16x8 yb[NC][2][3], kc[2][TG][2][NP];
 #pragma unroll
   for (int t = 0; t < TG; ++t)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) u.k.columns(t, kb, m, g, kc[0][t][kb]);
-  if (more) s.template fetch_frags<0, D::FP / 2>(ch + 1, to);
   __builtin_amdgcn_sched_barrier(0);
   if (p.ys) s.template store_tiles<4>(p.ys, id, 4, y);
   // the output
@@ -669,17 +674,13 @@ __device__ __forceinline__ void delta_scan_chunk(D& s, const DeltaArgs& p, const
     for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
   tri_rows<NO, NO, NC>(qs, pa, xb);
   // the state
-  const float whole = u.rows[kRowWhole * 64];
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[cc][i] *= s.row4(u, kRowS, i);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], yb[cc][kb]);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) S[cc][t] *= whole;
   }
-  if (more) s.template fetch_frags<D::FP / 2, D::FP>(ch + 1, to);
 #pragma unroll
   for (int t0 = 0; t0 < RT; t0 += TG) {
     if (t0 + TG < RT) {
@@ -699,40 +700,51 @@ __device__ __forceinline__ void delta_scan_chunk(D& s, const DeltaArgs& p, const
 }
 
 template <class UT, int MODE, int DK, int NC, int NW>
-__global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, false>::THREADS)) delta_scan_kernel(const DeltaArgs p) {
   typedef DeltaScan<UT, MODE, DK, NC, NW, false> D;
   typedef typename D::Buf Buf;
   constexpr int RT = D::RT, KB = D::KB;
   __shared__ Buf buf[D::NBUF];
-  D s(p);
+  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
+  D s(p, p.v, 1);
   if (s.idle) return;
-  f32x4 S[NC][RT];
   const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  if (s.nch > 0 && (s.loads || !D::NL)) {
+    s.fetch(buf[0]);
+    s.land(buf[0]);
+  }
+  __syncthreads();
+  if (s.loads) {  // every barrier here has its fellow below
+    for (int ch = 0; ch < s.nch; ++ch) {
+      Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
+      if (ch > 0) s.send(next, o, (ch - 1) * kDeltaChunk, min(p.L - (ch - 1) * kDeltaChunk, kDeltaChunk));
+      if (ch + 1 < s.nch) {
+        s.fetch(next);
+        s.land(next);
+      }
+      __syncthreads();
+    }
+    if (s.nch > 0) s.send(buf[(s.nch - 1) & (D::NBUF - 1)], o, (s.nch - 1) * kDeltaChunk, min(p.L - (s.nch - 1) * kDeltaChunk, kDeltaChunk));
+    return;
+  }
+  f32x4 S[NC][RT];
   s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
   bf16x8 sb[NC][KB][3];
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
-  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
-  if (s.nch > 0) {
-    s.fetch_all(0, p.v, buf[0]);
-    s.land(buf[0]);
-  }
-  __syncthreads();
   for (int ch = 0; ch < s.nch; ++ch) {
-    const int at = ch & (D::NBUF - 1), next = (ch + 1) & (D::NBUF - 1);
-    const bool more = ch + 1 < s.nch;
-    delta_scan_chunk<D, UT, DK, NC>(s, p, o, ch, more, &buf[at], &buf[next], S, sb);
-    if constexpr (D::NBUF == 1) __syncthreads();
-    if (more) s.land(buf[next]);
+    Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
+    if (!D::NL && ch + 1 < s.nch) s.fetch(next);
+    delta_scan_chunk<D, UT, DK, NC>(s, p, o, ch, buf[ch & (D::NBUF - 1)], S, sb);
+    if constexpr (!D::NL) {
+      __syncthreads();
+      if (ch + 1 < s.nch) s.land(next);
+    }
     __syncthreads();
   }
   if (p.sT) s.store_state(p.sT + at_state, S);
-  if (s.nch > 0) {
-    const int t0 = (s.nch - 1) * kDeltaChunk;
-    s.flush(buf[(s.nch - 1) & (D::NBUF - 1)], o, t0, min(p.L - t0, kDeltaChunk));
-  }
   // rows behind the last chunk of the sequence
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
@@ -741,15 +753,12 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaArgs p) 
         store1(out_at<UT>(o, s.b, t) + static_cast<long long>(s.hv) * p.dv + s.col(cc), 0.0f);
 }
 
-// A chunk of the adjoint's scan: as above, from the last to the first. `top` holds
-// the results of chunk ch + 1 (behind: there is one), and then takes chunk ch - 1.
+// A chunk of the adjoint's scan
 template <class D, class UT, int DK, int NC>
-__device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const DeltaView& o, int ch, bool more, bool behind,
-                                                 typename D::Buf* __restrict__ up, typename D::Buf* __restrict__ top,
+__device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p, const DeltaView& o, int ch, typename D::Buf& u,
                                                  f32x4 (&S)[NC][D::RT], bf16x8 (&sb)[NC][D::KB][3]) {
   constexpr int NP = D::NP, RT = D::RT, KB = D::KB;
   const int m = s.m, g = s.g;
-  typename D::Buf &u = *up, &to = *top;
   const long long id = static_cast<long long>(s.bh) * p.nc + ch;
 
   f32x4 y[NC][4], x[NC][4];
@@ -758,12 +767,9 @@ __device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[cc][i] = x[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   bf16x8 ka[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][3], vb[NC][2][NP];
-  i32x4 out[D::CP] = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
-  if (behind) s.take(to, out);
   s.template store_tiles<RT>(p.dstates, id, delta_tiles(p.dk), S);
-  if (more) s.fetch_qk(ch - 1, p.k, to.k, s.rk);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     if (kb + 1 < KB) {
@@ -787,8 +793,6 @@ __device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const
   for (int j = 0; j < kTriBlocks; ++j)
 #pragma unroll
     for (int pl = 0; pl < 3; ++pl) ta[j][pl] = u.frags[(j * 3 + pl) * 64 + s.lane];
-  if (behind) s.send(out, p.gv, (ch + 1) * kDeltaChunk, min(p.L - (ch + 1) * kDeltaChunk, kDeltaChunk));
-  if (more) s.fetch_qk(ch - 1, p.q, to.q, s.rq);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -810,11 +814,6 @@ __device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const
       u.q.columns(t, kb, m, g, qc[0][t][kb]);
       u.k.columns(t, kb, m, g, kc[0][t][kb]);
     }
-  if (more) {
-    s.fetch_v(ch - 1, o, to);
-    s.fetch_rows(ch - 1);
-    s.template fetch_frags<0, D::FP / 2>(ch - 1, to);
-  }
   __builtin_amdgcn_sched_barrier(0);
   tri_rows<3, 3, NC, true>(x, ta, xb);
 #pragma unroll
@@ -833,7 +832,6 @@ __device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const
 #pragma unroll
     for (int t = 0; t < RT; ++t) S[cc][t] *= whole;
   }
-  if (more) s.template fetch_frags<D::FP / 2, D::FP>(ch - 1, to);
   __builtin_amdgcn_sched_barrier(0);
   s.template store_tiles<4>(p.dxs, id, 4, x);
   s.result(u, p.gv, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), x);
@@ -868,38 +866,51 @@ __device__ __forceinline__ void delta_back_chunk(D& s, const DeltaArgs& p, const
 
 // dS from the last chunk to the first; p.s0 is dsT and p.sT is ds0
 template <class UT, int MODE, int DK, int NC, int NW>
-__global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, true>::THREADS)) delta_back_kernel(const DeltaArgs p) {
   typedef DeltaScan<UT, MODE, DK, NC, NW, true> D;
   typedef typename D::Buf Buf;
   constexpr int RT = D::RT, KB = D::KB;
   __shared__ Buf buf[D::NBUF];
-  D s(p);
+  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
+  D s(p, o, -1);
   if (s.idle) return;
-  f32x4 S[NC][RT];
   const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  if (s.nch > 0 && (s.loads || !D::NL)) {
+    s.fetch(buf[(s.nch - 1) & (D::NBUF - 1)]);
+    s.land(buf[(s.nch - 1) & (D::NBUF - 1)]);
+  }
+  __syncthreads();
+  if (s.loads) {  // every barrier here has its fellow below
+    for (int ch = s.nch - 1; ch >= 0; --ch) {
+      Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
+      if (ch + 1 < s.nch) s.send(next, p.gv, (ch + 1) * kDeltaChunk, min(p.L - (ch + 1) * kDeltaChunk, kDeltaChunk));
+      if (ch > 0) {
+        s.fetch(next);
+        s.land(next);
+      }
+      __syncthreads();
+    }
+    if (s.nch > 0) s.send(buf[(0) & (D::NBUF - 1)], p.gv, (0) * kDeltaChunk, min(p.L - (0) * kDeltaChunk, kDeltaChunk));
+    return;
+  }
+  f32x4 S[NC][RT];
   s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
   bf16x8 sb[NC][KB][3];
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
-  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
-  if (s.nch > 0) {
-    Buf& u = buf[(s.nch - 1) & (D::NBUF - 1)];
-    s.fetch_all(s.nch - 1, o, u);
-    s.land(u);
-  }
-  __syncthreads();
   for (int ch = s.nch - 1; ch >= 0; --ch) {
-    const int at = ch & (D::NBUF - 1), next = (ch + 1) & (D::NBUF - 1);
-    const bool more = ch > 0;
-    delta_back_chunk<D, UT, DK, NC>(s, p, o, ch, more, ch + 1 < s.nch, &buf[at], &buf[next], S, sb);
-    if constexpr (D::NBUF == 1) __syncthreads();
-    if (more) s.land(buf[next]);
+    Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
+    if (!D::NL && ch > 0) s.fetch(next);
+    delta_back_chunk<D, UT, DK, NC>(s, p, o, ch, buf[ch & (D::NBUF - 1)], S, sb);
+    if constexpr (!D::NL) {
+      __syncthreads();
+      if (ch > 0) s.land(next);
+    }
     __syncthreads();
   }
   if (p.sT) s.store_state(p.sT + at_state, S);
-  if (s.nch > 0) s.flush(buf[0], p.gv, 0, min(p.L, kDeltaChunk));
   // rows behind the last chunk of the sequence
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
