@@ -83,6 +83,70 @@ int32_t pararnn_delta_step(const pararnn_view* q, const pararnn_view* k, const p
                            const pararnn_view* gates, const float* lam, const int32_t* slots, float* state, void* o,
                            int32_t S, const pararnn_delta_opts* opts, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Norms before and after a block, with the gate and the residual's scale
+ * between them, over rows of D columns:
+ *   n = x / sqrt(mean(x^2) + eps) * w  over groups of `group` columns (x without w),
+ *   p = n * gate * s(gate)  (n without a gate),
+ *   s = residual + alpha * p,  y = s / sqrt(mean(s^2) + eps) * w_next;
+ *   without a residual (and then without alpha, w_next and s): y = p.
+ * x, gate, residual, dy, ds, dx, dgate, dresidual [N][D] in `dtype`; w, dw
+ * [group], alpha, dalpha, w_next, dw_next [D] fp32. w or a residual is given.
+ */
+typedef enum {
+  PARARNN_NORM_BLOCK_SAME = 0, /* y [N][D] in `dtype` */
+  PARARNN_NORM_BLOCK_INT8 = 1  /* y [N][D] int8, scale [N] fp32 */
+} pararnn_norm_block_out;
+
+typedef struct {
+  int64_t N;       /* rows, >= 1 */
+  int32_t D;       /* columns, 1..16384 */
+  int32_t group;   /* columns of a group of x, a divisor of D. Groups of less than D beside a residual or an
+                      8-bit y are 8, 16, 32, ... 512 columns */
+  int32_t dtype;   /* pararnn_dtype */
+  int32_t out;     /* pararnn_norm_block_out; ignored by the adjoint */
+  float eps;       /* >= 0 and finite */
+  int64_t x_row, gate_row, residual_row; /* elements from row to row of those inputs, >= D; the adjoint's s has D */
+} pararnn_norm_block_opts;
+
+/* Forward: y, and s with a residual. y is made from the sum before its
+ * rounding to `dtype`. An 8-bit row has scale = max(max|y|, 2^-100) / 127 and
+ * holds y / scale (the fp32 quotient) rounded to nearest even; a row with an
+ * infinity or a NaN has a scale that is infinite or NaN and stands for no
+ * numbers. */
+int32_t pararnn_norm_block(const void* x, const void* gate, const void* residual, const float* w, const float* alpha,
+                           const float* w_next, void* s, void* y, float* scale, const pararnn_norm_block_opts* o,
+                           void* stream);
+
+/* Workspace of the adjoint's dw, dalpha and dw_next into *bytes. Host-only. */
+int32_t pararnn_norm_block_workspace_bytes(const pararnn_norm_block_opts* o, int32_t residual, size_t* bytes);
+
+/* Adjoint for dy = dL/dy and, with a residual, ds = dL/ds of the other uses of
+ * s (NULL = zero), at the saved s (NULL: the forward call had no residual): dx,
+ * dgate (with a gate), dresidual (with a residual), and, all of them optional,
+ * dw, dalpha and dw_next (all NULL: no workspace needed). An 8-bit y passes its
+ * gradient straight through. */
+int32_t pararnn_norm_block_adjoint(const void* x, const void* gate, const void* s, const float* w, const float* alpha,
+                                   const float* w_next, const void* dy, const void* ds, void* dx, void* dgate,
+                                   void* dresidual, float* dw, float* dalpha, float* dw_next, void* ws,
+                                   size_t ws_bytes, const pararnn_norm_block_opts* o, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Product of 8-bit integer matrices with a scale for each row of both:
+ *   y[m][n] = sum_k a[m][k] w[n][k] * sa[m] * sw[n] + bias[n].
+ * a [M][K], sa [M] fp32 (as norm_block writes them), w [N][K], sw [N] fp32,
+ * bias [N] fp32 or NULL, y [M][N]. The sum is exact (32-bit integers); it is
+ * rounded to fp32 once, and the rest is computed in fp32. K % 16 == 0 with
+ * 16-byte aligned a and w selects the widest accesses.
+ */
+typedef struct {
+  int32_t M, N, K; /* all >= 1; K <= 131071 (whose sum of products of -128 still fits) */
+  int32_t y_dtype; /* pararnn_dtype of y */
+} pararnn_int8_opts;
+
+int32_t pararnn_matmul_int8(const void* a, const float* sa, const void* w, const float* sw, const float* bias, void* y,
+                            const pararnn_int8_opts* o, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

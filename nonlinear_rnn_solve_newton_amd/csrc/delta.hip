@@ -12,6 +12,8 @@
 
 #include "../../include/pararnn_delta.h"
 #include "delta/delta_rule.h"
+#include "delta/matmul_int8.h"
+#include "delta/norm_block.h"
 #include "layer/host_common.h"
 
 namespace pararnn {
@@ -129,6 +131,147 @@ int delta_mode(const pararnn_view* q, const pararnn_view* k, const pararnn_view*
     return rows_aligned(q, es, o->dk, bytes, o->B) && rows_aligned(k, es, o->dk, bytes, o->B) && rows_aligned(v, es, o->dv, bytes, o->B);
   };
   return all(16) ? kDirect : all(4) ? kEven : kOdd;
+}
+
+// ---------------------------------------------------------------------------
+// norms around a block
+
+constexpr int kNormBlockMaxD = 16384;
+
+bool norm_block_ok(const pararnn_norm_block_opts* o) {
+  return o && o->N >= 1 && o->D >= 1 && o->D <= kNormBlockMaxD && o->group >= 1 && o->group <= o->D && o->D % o->group == 0 &&
+         o->eps >= 0.0f && isfinite(o->eps) && o->x_row >= o->D && static_cast<double>(o->N) * o->D < 2.0e18 &&
+         static_cast<double>(o->N) * static_cast<double>(o->x_row) < 2.0e18;
+}
+
+// threads per row and vectors of 8 columns per thread; the adjoint, which holds four times the registers per
+// column, has one vector up to 8192 columns
+struct NormBlockShape {
+  int tpr, nv;
+};
+NormBlockShape norm_block_shape(int D, bool adjoint) {
+  const int v = static_cast<int>(ceil_div(D, 8));
+  for (int t : {16, 32, 64, 128, 256})
+    if (v <= t) return {t, 1};
+  if (adjoint) return v <= 512 ? NormBlockShape{512, 1} : v <= 1024 ? NormBlockShape{1024, 1} : NormBlockShape{1024, 2};
+  return v <= 512 ? NormBlockShape{256, 2} : v <= 1024 ? NormBlockShape{512, 2} : NormBlockShape{1024, 2};
+}
+// workgroups of the adjoint: each leaves a partial row of every parameter, so no more than fill the CUs
+long long norm_block_adjoint_grid(long long N, int D) {
+  const NormBlockShape k = norm_block_shape(D, true);
+  const long long rounds = ceil_div(N, k.tpr < 256 ? 256 / k.tpr : 1), room = kCUs * (k.tpr <= 256 ? 4 : 1024 / k.tpr);
+  return rounds <= room ? rounds : room;
+}
+
+// A call's rows as the kernels take them: groups without a residual and with y in the input's type are rows
+struct NormBlockRows {
+  long long N;
+  int D, H, lanes;
+};
+NormBlockRows norm_block_rows(const pararnn_norm_block_opts* o, bool residual, bool int8) {
+  if (o->group == o->D) return {o->N, o->D, 1, 0};
+  if (!residual && !int8) return {o->N * (o->D / o->group), o->group, o->D / o->group, 0};
+  return {o->N, o->D, 1, o->group / 8};
+}
+// groups within a row: 8 columns times a power of two up to a wave's lanes
+bool norm_block_group_ok(const pararnn_norm_block_opts* o, const NormBlockRows& r) {
+  return r.lanes == 0 ? r.D == o->group || r.H == 1 : o->group % 8 == 0 && r.lanes <= 64 && (r.lanes & (r.lanes - 1)) == 0;
+}
+
+template <bool ADJ, class F>
+int norm_block_dispatch(int D, F go) {
+  const NormBlockShape k = norm_block_shape(D, ADJ);
+#define PARARNN_SHAPE(T, V) \
+  if (k.tpr == T && k.nv == V) return go(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
+  PARARNN_SHAPE(16, 1);
+  PARARNN_SHAPE(32, 1);
+  PARARNN_SHAPE(64, 1);
+  PARARNN_SHAPE(128, 1);
+  PARARNN_SHAPE(256, 1);
+  if constexpr (ADJ) {
+    PARARNN_SHAPE(512, 1);
+    PARARNN_SHAPE(1024, 1);
+  } else {
+    PARARNN_SHAPE(256, 2);
+    PARARNN_SHAPE(512, 2);
+  }
+#undef PARARNN_SHAPE
+  return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+template <class XT, bool PRE, bool INT8, bool ALIGNED>
+int launch_norm_block(const NormBlockArgs& a, bool stream, hipStream_t s) {
+  return norm_block_dispatch<false>(a.D, [&](auto tpr, auto nv) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    long long grid = ceil_div(a.N, TPR < 256 ? 256 / TPR : 1);
+    if (grid > 8192) grid = 8192;
+    const int block = TPR < 256 ? 256 : TPR;
+    if (ALIGNED && stream) return launch(norm_block_kernel<XT, TPR, NV, PRE, INT8, ALIGNED, ALIGNED>, grid, block, s, a);
+    return launch(norm_block_kernel<XT, TPR, NV, PRE, INT8, ALIGNED, false>, grid, block, s, a);
+  });
+}
+template <class XT, bool PRE, bool ALIGNED>
+int launch_norm_block_adjoint(const NormBlockArgs& a, long long grid, bool stream, hipStream_t s) {
+  return norm_block_dispatch<true>(a.D, [&](auto tpr, auto nv) {
+    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    const int block = TPR < 256 ? 256 : TPR;
+    if (ALIGNED && stream) return launch(norm_block_adjoint_kernel<XT, TPR, NV, PRE, ALIGNED, ALIGNED>, grid, block, s, a);
+    return launch(norm_block_adjoint_kernel<XT, TPR, NV, PRE, ALIGNED, false>, grid, block, s, a);
+  });
+}
+// every row of 8-column vectors starts at a multiple of 16 bytes
+bool norm_block_aligned(const NormBlockRows& r, size_t es, std::initializer_list<const void*> ptrs,
+                        std::initializer_list<long long> strides) {
+  bool ok = r.D % 8 == 0;
+  for (const void* q : ptrs) ok = ok && (!q || aligned(q, 16));
+  for (long long t : strides) ok = ok && t * es % 16 == 0;
+  return ok;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit integer product
+
+typedef MatmulShape<2, 2, 4, 4, 1> Int8Mid;
+typedef MatmulShape<2, 2, 2, 2, 1> Int8Small;
+typedef MatmulShape<2, 2, 2, 2, 2> Int8Split2;
+typedef MatmulShape<2, 2, 2, 2, 4> Int8Split4;
+
+// Which large tile: 256 x 256 (4), 256 x 192 (3), or neither (0), by the rounds over the CUs, as in the 8-bit
+// floating-point product
+int int8_large_tile(const Int8Args& p) {
+  const long long tm = ceil_div(p.M, 256);
+  const double kb = p.KB;
+  const double mid = ceil_div(ceil_div(p.M, 128) * ceil_div(p.N, 128), 2 * kCUs) * (2.7 * kb + 14.0);
+  const double l4 = ceil_div(tm * ceil_div(p.N, 256), kCUs) * (4.0 * kb + 20.0);
+  const double l3 = ceil_div(tm * ceil_div(p.N, 192), kCUs) * (3.0 * kb + 20.0);
+  if (mid < l4 && mid < l3) return 0;
+  return l4 <= l3 ? 4 : 3;
+}
+template <class S, bool F32OUT>
+int launch_int8(const Int8Args& p, bool direct, hipStream_t s) {
+  const long long grid = ceil_div(p.M, S::BM) * ceil_div(p.N, S::BN);
+  return direct ? launch(int8_kernel<S, F32OUT, true>, grid, S::NT * S::KS, s, p)
+                : launch(int8_kernel<S, F32OUT, false>, grid, S::NT * S::KS, s, p);
+}
+template <bool F32OUT, int MT, int NT, int UN>
+int launch_int8_few(const Int8Args& p, hipStream_t s) {
+  return launch(int8_few_kernel<F32OUT, MT, NT, UN>, ceil_div(p.N, 16 * NT), 512, s, p);
+}
+template <bool F32OUT>
+int launch_int8_shape(const Int8Args& p, bool direct, hipStream_t s) {
+  const long long n16 = ceil_div(p.N, 16);
+  if (direct && p.M <= 32) {
+    if (n16 >= 3 * kCUs) return p.M <= 16 ? launch_int8_few<F32OUT, 1, 4, 1>(p, s) : launch_int8_few<F32OUT, 2, 4, 1>(p, s);
+    if (n16 >= 2 * kCUs) return p.M <= 16 ? launch_int8_few<F32OUT, 1, 2, 2>(p, s) : launch_int8_few<F32OUT, 2, 2, 2>(p, s);
+    return p.M <= 16 ? launch_int8_few<F32OUT, 1, 1, 4>(p, s) : launch_int8_few<F32OUT, 2, 1, 2>(p, s);
+  }
+  if (direct && p.M <= 64 && n16 <= kCUs / 2) return launch_int8_few<F32OUT, 4, 1, 2>(p, s);
+  const int tn = direct ? int8_large_tile(p) : 0;
+  if (tn == 4) return launch(int8_large_kernel<4, F32OUT>, ceil_div(p.M, 256) * ceil_div(p.N, 256), 512, s, p);
+  if (tn == 3) return launch(int8_large_kernel<3, F32OUT>, ceil_div(p.M, 256) * ceil_div(p.N, 192), 512, s, p);
+  if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= kCUs) return launch_int8<Int8Mid, F32OUT>(p, direct, s);
+  if (ceil_div(p.M, 64) * ceil_div(p.N, 64) <= kCUs && p.KB >= 4)
+    return direct ? launch_int8<Int8Split4, F32OUT>(p, true, s) : launch_int8<Int8Split2, F32OUT>(p, false, s);
+  return launch_int8<Int8Small, F32OUT>(p, direct, s);
 }
 
 }  // namespace
@@ -265,4 +408,154 @@ extern "C" int32_t pararnn_delta_step(const pararnn_view* q, const pararnn_view*
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (opts->dtype == PARARNN_BF16) return launch(delta_step_kernel<bf16>, grid, 256, st, a);
   return launch(delta_step_kernel<float>, grid, 256, st, a);
+}
+
+extern "C" int32_t pararnn_norm_block(const void* x, const void* gate, const void* residual, const float* w,
+                                      const float* alpha, const float* w_next, void* s, void* y, float* scale,
+                                      const pararnn_norm_block_opts* o, void* stream_) {
+  if (!norm_block_ok(o) || !x || !y || (!w && !residual)) return PARARNN_EINVAL;
+  if (residual ? !w_next || !s || o->residual_row < o->D : alpha || w_next || s) return PARARNN_EINVAL;
+  if (gate && o->gate_row < o->D) return PARARNN_EINVAL;
+  if (o->out != PARARNN_NORM_BLOCK_SAME && o->out != PARARNN_NORM_BLOCK_INT8) return PARARNN_EINVAL;
+  const bool int8 = o->out == PARARNN_NORM_BLOCK_INT8;
+  if (int8 && !scale) return PARARNN_EINVAL;
+  if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
+  const size_t es = o->dtype == PARARNN_BF16 ? 2 : 4;
+  for (const void* p : {x, gate, residual, static_cast<const void*>(s)})
+    if (!aligned(p, es)) return PARARNN_EUNSUPPORTED;
+  if ((!int8 && !aligned(y, es)) || !aligned(w, 4) || !aligned(alpha, 4) || !aligned(w_next, 4) || !aligned(scale, 4))
+    return PARARNN_EUNSUPPORTED;
+  const NormBlockRows r = norm_block_rows(o, residual, int8);
+  if (w && !norm_block_group_ok(o, r)) return PARARNN_EUNSUPPORTED;
+  NormBlockArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.gate = gate;
+  a.residual = residual;
+  a.w = w;
+  a.alpha = alpha;
+  a.w_next = w_next;
+  a.s = s;
+  a.y = y;
+  a.scale = scale;
+  a.N = r.N;
+  a.D = r.D;
+  a.H = r.H;
+  a.lanes = w ? r.lanes : 0;
+  a.G = o->group;
+  a.x_row = o->x_row;
+  a.gate_row = o->gate_row;
+  a.residual_row = o->residual_row;
+  a.eps = o->eps;
+  hipStream_t st = static_cast<hipStream_t>(stream_);
+  const bool ok = norm_block_aligned(r, es, {x, gate, residual, s, y, w, alpha, w_next},
+                                     {o->x_row, gate ? o->gate_row : 0, residual ? o->residual_row : 0});
+  // past the caches where the tensors together are larger than the last-level one
+  const bool far = static_cast<double>(o->N) * o->D * es * (2 + (gate != nullptr) + 2 * (residual != nullptr)) >= 256.0 * 1024 * 1024;
+  auto go = [&](auto xt, auto aligned_) {
+    typedef decltype(xt) XT;
+    constexpr bool AL = decltype(aligned_)::value;
+    if (residual) return int8 ? launch_norm_block<XT, true, true, AL>(a, far, st) : launch_norm_block<XT, true, false, AL>(a, far, st);
+    return int8 ? launch_norm_block<XT, false, true, AL>(a, far, st) : launch_norm_block<XT, false, false, AL>(a, far, st);
+  };
+  if (o->dtype == PARARNN_BF16) return ok ? go(bf16{}, std::true_type{}) : go(bf16{}, std::false_type{});
+  return ok ? go(0.0f, std::true_type{}) : go(0.0f, std::false_type{});
+}
+
+extern "C" int32_t pararnn_norm_block_workspace_bytes(const pararnn_norm_block_opts* o, int32_t residual, size_t* bytes) {
+  if (!norm_block_ok(o) || !bytes) return PARARNN_EINVAL;
+  const NormBlockRows r = norm_block_rows(o, residual != 0, false);
+  *bytes = round_up(sizeof(float) * static_cast<size_t>(norm_block_adjoint_grid(r.N, r.D)) * (residual ? 3 : 1) * r.D);
+  return PARARNN_OK;
+}
+
+extern "C" int32_t pararnn_norm_block_adjoint(const void* x, const void* gate, const void* s, const float* w,
+                                              const float* alpha, const float* w_next, const void* dy, const void* ds,
+                                              void* dx, void* dgate, void* dresidual, float* dw, float* dalpha,
+                                              float* dw_next, void* ws, size_t ws_bytes,
+                                              const pararnn_norm_block_opts* o, void* stream_) {
+  if (!norm_block_ok(o) || !x || !dy || !dx || (!w && !s) || (gate != nullptr) != (dgate != nullptr)) return PARARNN_EINVAL;
+  if (s ? !w_next || !dresidual : alpha || w_next || ds || dresidual || dalpha || dw_next) return PARARNN_EINVAL;
+  if ((gate && o->gate_row < o->D) || (dw && !w)) return PARARNN_EINVAL;
+  const bool sums = dw || dalpha || dw_next;
+  if (sums && !ws) return PARARNN_EINVAL;
+  if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
+  const size_t es = o->dtype == PARARNN_BF16 ? 2 : 4;
+  for (const void* p : {x, gate, s, dy, ds, static_cast<const void*>(dx), static_cast<const void*>(dgate),
+                        static_cast<const void*>(dresidual)})
+    if (!aligned(p, es)) return PARARNN_EUNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(w), static_cast<const void*>(alpha), static_cast<const void*>(w_next),
+                        static_cast<const void*>(dw), static_cast<const void*>(dalpha), static_cast<const void*>(dw_next)})
+    if (!aligned(p, 4)) return PARARNN_EUNSUPPORTED;
+  const NormBlockRows r = norm_block_rows(o, s != nullptr, false);
+  if (w && !norm_block_group_ok(o, r)) return PARARNN_EUNSUPPORTED;
+  const long long grid = norm_block_adjoint_grid(r.N, r.D);
+  const int parts = s ? 3 : 1;
+  if (sums && ws_bytes < sizeof(float) * static_cast<size_t>(grid) * parts * r.D) return PARARNN_EWORKSPACE;
+  if (sums && !aligned(ws, kAlign)) return PARARNN_EUNSUPPORTED;
+  NormBlockArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.gate = gate;
+  a.residual = s;
+  a.w = w;
+  a.alpha = alpha;
+  a.w_next = w_next;
+  a.dy = dy;
+  a.ds = ds;
+  a.dx = dx;
+  a.dgate = dgate;
+  a.dresidual = dresidual;
+  a.part = sums ? static_cast<float*>(ws) : nullptr;
+  a.N = r.N;
+  a.D = r.D;
+  a.H = r.H;
+  a.lanes = w ? r.lanes : 0;
+  a.G = o->group;
+  a.x_row = o->x_row;
+  a.gate_row = o->gate_row;
+  a.eps = o->eps;
+  hipStream_t st = static_cast<hipStream_t>(stream_);
+  const bool ok = norm_block_aligned(r, es, {x, gate, s, dy, ds, dx, dgate, dresidual, w, alpha, w_next},
+                                     {o->x_row, gate ? o->gate_row : 0});
+  const bool far = static_cast<double>(o->N) * o->D * es * (3 + 2 * (gate != nullptr) + 2 * (s != nullptr) + (ds != nullptr)) >=
+                   256.0 * 1024 * 1024;
+  auto go = [&](auto xt, auto aligned_) {
+    typedef decltype(xt) XT;
+    constexpr bool AL = decltype(aligned_)::value;
+    return s ? launch_norm_block_adjoint<XT, true, AL>(a, grid, far, st) : launch_norm_block_adjoint<XT, false, AL>(a, grid, far, st);
+  };
+  int rc;
+  if (o->dtype == PARARNN_BF16) rc = ok ? go(bf16{}, std::true_type{}) : go(bf16{}, std::false_type{});
+  else rc = ok ? go(0.0f, std::true_type{}) : go(0.0f, std::false_type{});
+  if (rc || !sums) return rc;
+  hipLaunchKernelGGL(norm_block_sum_kernel, dim3(static_cast<unsigned>(ceil_div(r.D, 32)), parts), dim3(1024), 0, st,
+                     static_cast<const float*>(a.part), dw, dalpha, dw_next, grid, parts, r.D, o->group == o->D ? r.D : o->group);
+  return check_hip(hipGetLastError());
+}
+
+extern "C" int32_t pararnn_matmul_int8(const void* a, const float* sa, const void* w, const float* sw, const float* bias,
+                                       void* y, const pararnn_int8_opts* o, void* stream_) {
+  if (!o || o->M < 1 || o->N < 1 || o->K < 1 || o->K > 131071 || !a || !sa || !w || !sw || !y) return PARARNN_EINVAL;
+  if (o->M > 2147483647 - 256 || o->N > 2147483647 - 256) return PARARNN_EINVAL;
+  if (static_cast<double>(ceil_div(o->M, 64)) * ceil_div(o->N, 64) > 2.0e9) return PARARNN_EINVAL;
+  if (!dtype_ok(o->y_dtype)) return PARARNN_EUNSUPPORTED;
+  const bool f32 = o->y_dtype == PARARNN_F32;
+  if (!aligned(sa, 4) || !aligned(sw, 4) || !aligned(bias, 4) || !aligned(y, f32 ? 4 : 2)) return PARARNN_EUNSUPPORTED;
+  Int8Args p;
+  p.a = static_cast<const uint8_t*>(a);
+  p.sa = sa;
+  p.w = static_cast<const uint8_t*>(w);
+  p.sw = sw;
+  p.bias = bias;
+  p.y = y;
+  p.M = o->M;
+  p.N = o->N;
+  p.K = o->K;
+  p.KB = static_cast<int>(ceil_div(o->K, 128));
+  p.vec = !f32 && o->N % 8 == 0 && o->N <= (1 << 22) && aligned(y, 16) ? 8 : o->N % 4 == 0 && aligned(y, f32 ? 16 : 8) ? 4 : 1;
+  p.stream = 2.0 * p.M * p.N > 256.0 * 1024 * 1024;
+  const bool direct = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
+  hipStream_t s = static_cast<hipStream_t>(stream_);
+  return f32 ? launch_int8_shape<true>(p, direct, s) : launch_int8_shape<false>(p, direct, s);
 }

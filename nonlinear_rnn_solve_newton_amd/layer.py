@@ -9,6 +9,10 @@ of a delta-rule layer (libpararnn_delta.so).
                   gated_step, its form for single tokens
   delta_scan      gated delta rule over the sequence, a matrix of state per head,
                   its adjoint, and delta_step, its form for single tokens
+  norm_block      the norms before and after a block with the gate and the
+                  residual's scale between them, and their adjoint
+  matmul_int8     product of 8-bit integer matrices with a scale for each row of
+                  both
 
 Like `binding`, this module checks tensors, allocates outputs and workspace
 with torch and passes raw device pointers plus torch's current HIP stream to
@@ -76,6 +80,18 @@ class DeltaOpts(ctypes.Structure):
         (n, ctypes.c_float) for n in ("c", "eps", "scale")] + [("lengths", ctypes.c_void_p), ("reset", ctypes.c_void_p)]
 
 
+class NormBlockOpts(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("D", "group", "dtype", "out")] + [
+        ("eps", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("x_row", "gate_row", "residual_row")]
+
+
+class Int8Opts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "y_dtype")]
+
+
+NORM_BLOCK_SAME, NORM_BLOCK_INT8 = 0, 1
+
+
 def header_functions(header=HEADER) -> list[str]:
     """Names of the functions declared in include/pararnn_layer.h (or pararnn_delta.h)."""
     return re.findall(r"^\s*[a-z_0-9]+\s+(pararnn_[a-z_0-9]+)\s*\(", header.read_text(), re.M)
@@ -132,6 +148,11 @@ def delta_lib():
         L.pararnn_delta_scan.argtypes = [V, V, V, V, P, P, P, P, P, P, SZ, D, P]
         L.pararnn_delta_scan_adjoint.argtypes = [V, V, V, V, P, P, P, P, V, V, V, V, P, P, P, SZ, D, P]
         L.pararnn_delta_step.argtypes = [V, V, V, V, P, P, P, P, I32, D, P]
+        N = ctypes.POINTER(NormBlockOpts)
+        L.pararnn_norm_block.argtypes = [P] * 9 + [N, P]
+        L.pararnn_norm_block_workspace_bytes.argtypes = [N, I32, ctypes.POINTER(SZ)]
+        L.pararnn_norm_block_adjoint.argtypes = [P] * 15 + [SZ, N, P]
+        L.pararnn_matmul_int8.argtypes = [P] * 6 + [ctypes.POINTER(Int8Opts), P]
         for n in header_functions(DELTA_HEADER):
             getattr(L, n).restype = I32
         _delta = L
@@ -608,4 +629,169 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.T
         _dev(out, "out", q.dtype, (o.B, o.HV, o.dv), dev)
     _launch_delta("pararnn_delta_step", dev, *map(ctypes.byref, views), _ptr(lam), _ptr(slots), _ptr(state), _ptr(out),
                   S, ctypes.byref(o))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# norms around a block
+
+def _rows_of(t, name: str, dtype, shape: tuple, device) -> int:
+    """Checks [N][D] whose rows may lie apart; the elements from row to row."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PararnnError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise PararnnError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    N, D = shape
+    row = t.stride(0) if N > 1 else D
+    if (D > 1 and t.stride(1) != 1) or row < D:
+        raise PararnnError(f"{name} must have contiguous rows that do not overlap")
+    return row
+
+
+def _norm_block_opts(x, w, gate, group, alpha, w_next, eps, residual: bool):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
+        raise PararnnError("x must be a device tensor [N][D]")
+    dev, (N, D) = x.device, x.shape
+    if x.dtype not in _DTYPE:
+        raise PararnnError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if 0 in x.shape:
+        raise PararnnError("x must not be empty")
+    group = D if group is None else group
+    if not isinstance(group, int) or group < 1 or D % group:
+        raise PararnnError(f"group must be a divisor of {D}, got {group}")
+    if not residual and (alpha is not None or w_next is not None):
+        raise PararnnError("alpha and w_next go with a residual")
+    if residual and w_next is None:
+        raise PararnnError("a residual needs w_next")
+    if not residual and w is None:
+        raise PararnnError("w or a residual must be given")
+    _dev(w, "w", torch.float32, (group,), dev)
+    _dev(alpha, "alpha", torch.float32, (D,), dev)
+    _dev(w_next, "w_next", torch.float32, (D,), dev)
+    o = NormBlockOpts(N, D, group, _DTYPE[x.dtype], NORM_BLOCK_SAME, eps, _rows_of(x, "x", x.dtype, (N, D), dev), D, D)
+    if gate is not None:
+        o.gate_row = _rows_of(gate, "gate", x.dtype, (N, D), dev)
+    return o, dev, N, D
+
+
+def norm_block(x: torch.Tensor, *, w: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               group: Optional[int] = None, residual: Optional[torch.Tensor] = None,
+               alpha: Optional[torch.Tensor] = None, w_next: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               out_dtype: Optional[torch.dtype] = None) -> dict:
+    """p = x / sqrt(mean(x^2) + eps) * w * gate * s(gate); with a residual s =
+    residual + alpha p and y = s / sqrt(mean(s^2) + eps) * w_next, else y = p.
+
+    x, gate, residual [N][D] bf16 or fp32, rows may lie apart (columns of a wider
+    matrix); w [group] fp32 norms groups of that many columns (None: all D; w None:
+    x is not normed), alpha (None: ones) and w_next [D] fp32. out_dtype torch.int8:
+    y in 8-bit integers with a scale per row, as matmul_int8 takes them. Groups of
+    less than D beside a residual or an 8-bit y: 8, 16, 32, ... 512 columns.
+    Returns dict(y, s (None without a residual), scale [N] fp32 or None).
+    """
+    o, dev, N, D = _norm_block_opts(x, w, gate, group, alpha, w_next, eps, residual is not None)
+    s = scale = None
+    if residual is not None:
+        o.residual_row = _rows_of(residual, "residual", x.dtype, (N, D), dev)
+        s = torch.empty(N, D, dtype=x.dtype, device=dev)
+    if out_dtype is None or out_dtype == x.dtype:
+        y = torch.empty(N, D, dtype=x.dtype, device=dev)
+    elif out_dtype == torch.int8:
+        o.out = NORM_BLOCK_INT8
+        y = torch.empty(N, D, dtype=torch.int8, device=dev)
+        scale = torch.empty(N, dtype=torch.float32, device=dev)
+    else:
+        raise PararnnError(f"out_dtype must be {x.dtype} or int8, got {out_dtype}")
+    _launch_delta("pararnn_norm_block", dev, _ptr(x), _ptr(gate), _ptr(residual), _ptr(w), _ptr(alpha), _ptr(w_next),
+                  _ptr(s), _ptr(y), _ptr(scale), ctypes.byref(o))
+    return {"y": y, "s": s, "scale": scale}
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_block_bytes(N: int, D: int, group: int, dtype: int, residual: bool) -> int:
+    n = ctypes.c_size_t()
+    o = NormBlockOpts(N, D, group, dtype, 0, 0.0, D, D, D)
+    st = delta_lib().pararnn_norm_block_workspace_bytes(ctypes.byref(o), int(residual), ctypes.byref(n))
+    if st != 0:
+        raise PararnnError(f"invalid sizes (norm_block takes at most 16384 columns): {st} ({strerror(st)})")
+    return n.value
+
+
+def norm_block_adjoint(x: torch.Tensor, dy: torch.Tensor, *, w: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None, group: Optional[int] = None,
+                       s: Optional[torch.Tensor] = None, ds: Optional[torch.Tensor] = None,
+                       alpha: Optional[torch.Tensor] = None, w_next: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, want_params: bool = True, ws: Optional[torch.Tensor] = None) -> dict:
+    """Adjoint of norm_block for dy = dL/dy [N][D] and, with a residual, ds = dL/ds
+    of the other uses of s (None: zero); s is the forward call's. The other
+    arguments are those of the forward call. Returns dict(dx, dgate, dresidual in
+    x's type, dw [group], dalpha, dw_next [D] fp32, ws); None where there is no such
+    input, and dw, dalpha, dw_next only with want_params."""
+    o, dev, N, D = _norm_block_opts(x, w, gate, group, alpha, w_next, eps, s is not None)
+    _dev(dy, "dy", x.dtype, (N, D), dev)
+    if dy is None:
+        raise PararnnError("dy must be a device tensor")
+    _dev(s, "s", x.dtype, (N, D), dev)
+    _dev(ds, "ds", x.dtype, (N, D), dev)
+    if ds is not None and s is None:
+        raise PararnnError("ds goes with a residual")
+    new = lambda *shape: torch.empty(*shape, dtype=torch.float32, device=dev)  # noqa: E731
+    rows = lambda on: torch.empty(N, D, dtype=x.dtype, device=dev) if on else None  # noqa: E731
+    dx, dgate, dresidual = rows(True), rows(gate is not None), rows(s is not None)
+    dw = new(o.group) if want_params and w is not None else None
+    dalpha = new(D) if want_params and alpha is not None else None
+    dw_next = new(D) if want_params and s is not None else None
+    nws = 0
+    if dw is not None or dw_next is not None:
+        ws, nws = _workspace(ws, _norm_block_bytes(N, D, o.group, o.dtype, s is not None), dev)
+    _launch_delta("pararnn_norm_block_adjoint", dev, _ptr(x), _ptr(gate), _ptr(s), _ptr(w), _ptr(alpha), _ptr(w_next),
+                  _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dgate), _ptr(dresidual), _ptr(dw), _ptr(dalpha), _ptr(dw_next),
+                  _ptr(ws), nws, ctypes.byref(o))
+    return {"dx": dx, "dgate": dgate, "dresidual": dresidual, "dw": dw, "dalpha": dalpha, "dw_next": dw_next, "ws": ws}
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integer product
+
+def quantize_weight_int8(w: torch.Tensor):
+    """Lays out a weight matrix [N][K] for matmul_int8, once: (w in int8, sw [N])
+    with scale = max(max|w|, 2^-100) / 127 over each row. Works on any device."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or not w.is_floating_point():
+        raise PararnnError("w must be a floating-point matrix [N][K]")
+    v = w.float()
+    sw = v.abs().amax(dim=1).clamp_min(2.0 ** -100)
+    sw = sw / sw.new_full((), 127.0)  # by a Python number the card multiplies by a rounded reciprocal
+    return torch.round(v / sw[:, None]).clamp(-127, 127).nan_to_num(0.0).to(torch.int8), sw
+
+
+def matmul_int8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, *,
+                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """(a w^T) * sa * sw + bias for a [M][K] and w [N][K] int8, sa [M] and sw [N] fp32
+    (scales of a's and w's rows), bias [N] fp32. The sum is exact; K at most
+    131071. Returns [M][N] in out_dtype (bfloat16 or float32)."""
+    dev = _first(a, "a", 2)
+    M, K = a.shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise PararnnError("w must be [N][K]")
+    N = w.shape[0]
+    _dev(a, "a", torch.int8, (M, K), dev)
+    _dev(w, "w", torch.int8, (N, K), dev)
+    if sa is None or sw is None:
+        raise PararnnError("sa and sw must be device tensors")
+    _dev(sa, "sa", torch.float32, (M,), dev)
+    _dev(sw, "sw", torch.float32, (N,), dev)
+    _dev(bias, "bias", torch.float32, (N,), dev)
+    if out_dtype not in _DTYPE:
+        raise PararnnError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    else:
+        _dev(out, "out", out_dtype, (M, N), dev)
+    o = Int8Opts(M, N, K, _DTYPE[out_dtype])
+    _launch_delta("pararnn_matmul_int8", dev, _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _ptr(bias), _ptr(out),
+                  ctypes.byref(o))
     return out
