@@ -175,7 +175,7 @@ NormBlockRows norm_block_rows(const pararnn_norm_block_opts* o, bool residual, b
 }
 // groups within a row: 8 columns times a power of two up to a wave's lanes
 bool norm_block_group_ok(const pararnn_norm_block_opts* o, const NormBlockRows& r) {
-  return r.lanes == 0 ? r.D == o->group || r.H == 1 : o->group % 8 == 0 && r.lanes <= 64 && (r.lanes & (r.lanes - 1)) == 0;
+  return r.D == o->group || (o->group % 8 == 0 && r.lanes <= 64 && (r.lanes & (r.lanes - 1)) == 0);
 }
 
 template <bool ADJ, class F>

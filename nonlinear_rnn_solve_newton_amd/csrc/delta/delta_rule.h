@@ -22,8 +22,12 @@
 //   dQ = scale e^G dO S0^T + D0 K,               D0_ij = scale E_ij b_j dO_i.y_j (i >= j)
 //   dK read = D1 K - e^G dX S0^T,                D1_ij = -E_ij b_j dX_i.y_j      (i > j)
 //   dK written = D0^T Q + D1^T K + e^(G_64 - G) b y dS1^T
-//   dG_i = q_i.dQ_i + k_i.(dK read)_i - k_i.(dK written)_i,  + <S1, dS1> at the last
 //   b dL/db = k.(dK written),  which a gate's gradient (1 - b) b dL/db takes as it is.
+// A step's log decay multiplies what passes it: with W_ij = D0_ij q_i.k_j + D1_ij k_i.k_j,
+//   dL/dlog a_t = sum over j < t <= i of W_ij + sum over i >= t of what rows i read from S0
+//               + sum over j < t of what rows j add to S1 + e^G_64 <S0, dS1>.
+// (Row i's decayed terms less column i's, summed from the end, is the same in
+// exact arithmetic, but a difference of large sums where decays are strong.)
 #pragma once
 
 #include "delta_common.h"
@@ -59,9 +63,9 @@ struct DeltaArgs {
   int wide;                      // rows of bf16 o (adjoint: dV) take 16-byte stores
 };
 
-// factors of a chunk's rows
+// factors of a chunk's rows (NotR, NotB: 1 - s(gate) as s(-gate), which keeps its digits)
 enum { kRowX = 0, kRowO = 1, kRowS = 2, kRowWhole = 3, kRowK = 4, kRowQ = 5, kRowB = 6, kRowG = 7, kRowR = 8,
-       kRowSeg = 9, kRows = 10 };
+       kRowSeg = 9, kRowNotR = 10, kRowNotB = 11, kRows = 12 };
 
 // Blocks (16 rows x 32 inner indexes) of a lower triangular 64 x 64 operand,
 // and of its transpose, that are not zero: 6 of 8
@@ -172,7 +176,8 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
     const int i = lane;
     const bool on = i < n;
     const UT* gp = at<UT>(p.gates, b, t0 + min(i, n - 1)) + hv;
-    const float r = on ? sigm(load1(gp)) : 0.0f, beta = on ? sigm(load1(gp + p.HV)) : 0.0f;
+    const float ga = load1(gp), gb = load1(gp + p.HV);
+    const float r = on ? sigm(ga) : 0.0f, beta = on ? sigm(gb) : 0.0f;
     const float coef = -p.c * softplus(p.lam[hv]);
     float G = on ? coef * r : 0.0f;
 #pragma unroll
@@ -190,6 +195,8 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
     rows[kRowG * 64 + i] = G;
     rows[kRowR * 64 + i] = r;
     rows[kRowSeg * 64 + i] = static_cast<float>(seg);
+    rows[kRowNotR * 64 + i] = on ? sigm(-ga) : 0.0f;
+    rows[kRowNotB * 64 + i] = on ? sigm(-gb) : 0.0f;
   }
   __syncthreads();
   constexpr float kLog2e = 1.4426950408889634f;
@@ -932,7 +939,7 @@ struct DeltaGradLds {
   };
   static constexpr bool APART = sizeof(Stage) + 2 * sizeof(Tile) <= 120 * 1024;  // the tiles beside the stage
   static constexpr int ROW = 68;
-  struct Mats { float d0[64 * ROW], d1[64 * ROW]; };
+  struct Mats { float d0[64 * ROW], d1[64 * ROW], w[64 * ROW]; };
   static constexpr size_t a16(size_t x) { return (x + 15) / 16 * 16; }
   // stage | (d0, d1 on the stage where the tiles lie apart, else behind the tiles)
   static constexpr size_t kStage = a16(sizeof(Stage)), kTiles = a16(2 * sizeof(Tile));
@@ -946,10 +953,10 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   typedef DeltaGradLds<UT, DK> M;
   typedef typename M::Tile Tile;
   constexpr int NP = M::NP, RT = M::RT, HT = RT / 2, ROW = M::ROW;
-  static_assert(M::BYTES + 16384 <= 160 * 1024, "fits the workgroup's memory");
+  static_assert(M::BYTES + 10240 <= 160 * 1024, "fits the workgroup's memory");
   static_assert(sizeof(typename M::Mats) <= M::kStage || !M::APART, "the matrices fit where the stage was");
   __shared__ __attribute__((aligned(16))) char lds[M::BYTES];
-  __shared__ float srow[kRows * 64], spart[2][4][64], sdot[8];
+  __shared__ float srow[kRows * 64], spart[2][5][64], sdot[8], scol[8][64], spass[64];
   typename M::Stage& sg = *reinterpret_cast<typename M::Stage*>(lds);
   Tile& tk = reinterpret_cast<Tile*>(lds + M::TILES)[0];
   Tile& tq = reinterpret_cast<Tile*>(lds + M::TILES)[1];
@@ -1087,8 +1094,24 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
     if (lane == 0) sdot[w8] = dot;
-    // D0 and D1
+    if constexpr (!M::APART) __syncthreads();
+    // D0 and D1, and W of the one and the other half of the waves
     float* to = f ? mt.d1 : mt.d0;
+    f32x4 pp[4];  // q.k, or k.k
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pp[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kb = 0; kb < DK / 32; ++kb) {
+      bf16x8 a[NP], c[NP];
+      if (f) tk.rows(w, kb, m, g, a);
+      else tq.rows(w, kb, m, g, a);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+          tk.rows(j, kb, m, g, c);
+          mma<NP, NP>(pp[j], a, c);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = 16 * j + m;
@@ -1098,13 +1121,22 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
         const bool low = (f ? i > c : i >= c) && srow[kRowSeg * 64 + i] == srow[kRowSeg * 64 + c];
         const float x = (f ? -1.0f : p.scale) * srow[kRowB * 64 + c] *
                         __builtin_amdgcn_exp2f((srow[kRowG * 64 + i] - srow[kRowG * 64 + c]) * kLog2e);
-        to[i * ROW + c] = low ? x * dd[j][e] : 0.0f;
+        const float d = low ? x * dd[j][e] : 0.0f;
+        to[i * ROW + c] = d;
+        pp[j][e] *= d * srow[(f ? kRowK : kRowQ) * 64 + i] * srow[kRowK * 64 + c];
+        if (!f) mt.w[i * ROW + c] = pp[j][e];
       }
     }
     __syncthreads();
+    if (f) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mt.w[(16 * w + 4 * g + e) * ROW + 16 * j + m] += pp[j][e];
+    }
     f32x4 kr[HT], kw[HT];
     const float se = srow[kRowSeg * 64 + 63], Ge = srow[kRowG * 64 + 63];
-    float rq[4], rk[4], part[4][4];
+    float rq[4], rk[4], part[5][4];  // q.dQ, k.(dK read), k.(dK written); of S1, from S0
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = 16 * w + 4 * g + r;
@@ -1113,13 +1145,16 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
       const float wr = tail * srow[kRowB * 64 + i];
       rk[r] = srow[kRowK * 64 + i];
       rq[r] = srow[kRowQ * 64 + i];
-      part[0][r] = part[1][r] = part[2][r] = part[3][r] = 0.0f;
+      part[0][r] = part[1][r] = part[2][r] = part[3][r] = part[4][r] = 0.0f;
 #pragma unroll
       for (int t = 0; t < HT; ++t) {
         qo[t][r] *= p.scale * gamma;
         kr[t][r] = -gamma * kx[t][r];
         kw[t][r] = wr * yd[t][r];
-        part[3][r] = fmaf(kw[t][r], rk[r] * tk.at(i, delta_label(f * HT + t, m)), part[3][r]);
+        const int d = delta_label(f * HT + t, m);
+        const float kv = rk[r] * tk.at(i, d);
+        part[3][r] = fmaf(kw[t][r], kv, part[3][r]);
+        part[4][r] = fmaf(kr[t][r], kv, fmaf(qo[t][r], rq[r] * tq.at(i, d), part[4][r]));
       }
     }
 #pragma unroll
@@ -1173,47 +1208,68 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
 #pragma unroll
     for (int off = 8; off >= 1; off >>= 1)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 5; ++k)
 #pragma unroll
         for (int r = 0; r < 4; ++r) part[k][r] += __shfl_xor(part[k][r], off, 64);
     if (m == 0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 5; ++k)
 #pragma unroll
         for (int r = 0; r < 4; ++r) spart[f][k][16 * w + 4 * g + r] = part[k][r];
     }
+    // sums of W over j < t <= i: a wave takes 8 t, a lane a column j
+    {
+      float v = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v += mt.w[(8 * w8 + r) * ROW + lane];
+      scol[w8][lane] = v;
+    }
     __syncthreads();
+    {
+      float v = 0.0f, pass[8];
+      for (int k = 7; k > w8; --k) v += scol[k][lane];
+#pragma unroll
+      for (int r = 7; r >= 0; --r) {
+        v += mt.w[(8 * w8 + r) * ROW + lane];
+        pass[r] = lane < 8 * w8 + r ? v : 0.0f;
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) pass[r] += __shfl_xor(pass[r], off, 64);
+      if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) spass[8 * w8 + r] = pass[r];
+      }
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = 16 * w + 4 * g + r;
       qsum[r] += spart[0][0][i] + spart[1][0][i];
       ksum[r] += spart[0][1][i] + spart[1][1][i] + spart[0][2][i] + spart[1][2][i];
     }
+    __syncthreads();
     if (w8 == 0) {  // the gates: a lane per step
       const int i = lane;
-      const float a = spart[0][0][i] + spart[1][0][i], br = spart[0][1][i] + spart[1][1][i],
-                  bw = spart[0][2][i] + spart[1][2][i];
-      float last = spart[0][3][i] + spart[1][3][i];
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) last += __shfl_xor(last, off, 64);
+      const float bw = spart[0][2][i] + spart[1][2][i], to_s1 = spart[0][3][i] + spart[1][3][i];
+      float from = spart[0][4][i] + spart[1][4][i], into = to_s1;
       float ss = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) ss += sdot[k];
-      last = fmaf(srow[kRowWhole * 64], ss, last);
-      float G = a + br - bw + (i == 63 ? last : 0.0f);
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {  // of log a: the sum over this step and later ones
-        const float u = __shfl_down(G, o, 64);
-        if (i + o < 64) G += u;
+      for (int o = 1; o < 64; o <<= 1) {
+        const float u = __shfl_down(from, o, 64), v = __shfl_up(into, o, 64);
+        if (i + o < 64) from += u;  // over this row and later ones
+        if (i >= o) into += v;
       }
-      // a decay that a document's start hides has no gradient
-      const bool start = i > 0 ? srow[kRowSeg * 64 + i] != srow[kRowSeg * 64 + i - 1] : srow[kRowSeg * 64] != 0.0f;
-      const float dl = start || i >= n ? 0.0f : G;
+      into = __shfl_up(into, 1, 64);  // over the rows in front of this one
+      const float G = spass[i] + from + (i > 0 ? into : 0.0f) + srow[kRowWhole * 64] * ss;
+      const float dl = i < n ? G : 0.0f;
       const float r = srow[kRowR * 64 + i], lam = p.lam[hv];
       if (i < rows_out) {
         UT* go = out_at<UT>(p.dgates, b, t0 + i) + hv;
-        store1(go, -p.c * softplus(lam) * dl * r * (1.0f - r));
-        store1(go + p.HV, i < n ? bw * (1.0f - srow[kRowB * 64 + i]) : 0.0f);
+        store1(go, -p.c * softplus(lam) * dl * r * srow[kRowNotR * 64 + i]);
+        store1(go + p.HV, i < n ? bw * srow[kRowNotB * 64 + i] : 0.0f);
       }
       if (p.dlam_part) {
         float sum = dl * r;
