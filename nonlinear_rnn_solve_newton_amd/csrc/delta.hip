@@ -108,7 +108,10 @@ struct DeltaAdjoint {
     a.sT = ds0;
     if (const int rc = launch(delta_back_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), DeltaScan<UT, MODE, DK, 1, 4, true>::THREADS, s, a))
       return rc;
-    if (const int rc = launch(delta_grad_kernel<UT, EVEN, DK>, static_cast<long long>(a.B) * a.H * a.nc, 512, s, a)) return rc;
+    const long long grid = static_cast<long long>(a.B) * a.H * a.nc;
+    if (const int rc = a.H == a.HV ? launch(delta_grad_kernel<UT, EVEN, DK, false>, grid, 512, s, a)
+                                   : launch(delta_grad_kernel<UT, EVEN, DK, true>, grid, 512, s, a))
+      return rc;
     if (!dlam) return PARARNN_OK;
     return launch(delta_dlam_kernel, a.HV, 256, s, static_cast<const float*>(a.dlam_part), a.lam, dlam, a.B * a.nc, a.c);
   }
@@ -353,6 +356,7 @@ extern "C" int32_t pararnn_delta_scan_adjoint(const pararnn_view* q, const parar
   a.o = const_cast<void*>(d_o);
   const pararnn_view ov = {d_o, static_cast<int64_t>(opts->L) * opts->HV * opts->dv, static_cast<int64_t>(opts->HV) * opts->dv};
   a.wide = rows_aligned(dv, es, opts->dv, 16, opts->B);
+  a.wide_qk = opts->dk % 8 == 0 && rows_aligned(dq, es, opts->dk, 16, opts->B) && rows_aligned(dk, es, opts->dk, 16, opts->B);
   char* w = static_cast<char*>(ws);
   a.frags = reinterpret_cast<bf16x8*>(w);
   w += z.frags;

@@ -110,6 +110,44 @@ struct Piece<bf16, false> {
     return static_cast<uint32_t>(h[2 * i]) | static_cast<uint32_t>(h[2 * i + 1]) << 16;
   }
 };
+// Sums of N values (a power of two) over LANES lanes that differ in the bits
+// below `first`, dealt out: a step of the first log2(N) halves the values that a
+// lane still has. Afterwards v[0] is the sum of value deal_index (of those bits).
+template <int N, int LANES, int M>
+__device__ __forceinline__ void sum_and_deal(float (&v)[M], int lane) {
+  constexpr int OFF = LANES / 2;
+  if constexpr (N > 1) {
+    const bool up = (lane & OFF) != 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float send = up ? v[i] : v[i + N / 2], keep = up ? v[i + N / 2] : v[i];
+      v[i] = keep + __shfl_xor(send, OFF, 64);
+    }
+  } else {
+    v[0] += __shfl_xor(v[0], OFF, 64);
+  }
+  if constexpr (OFF > 1) sum_and_deal<(N > 1 ? N / 2 : 1), OFF>(v, lane);
+}
+// which of the N values a lane ends up with: the lanes' highest bits, in order
+template <int N, int LANES>
+__device__ __forceinline__ int deal_index(int lane) { return (lane & (LANES - 1)) / (LANES / N); }
+
+// 4 x 4 values of 4 neighbouring lanes, transposed: lane q's v[c] becomes lane c's v[q]
+template <int STEP>
+__device__ __forceinline__ void swap_step(float& lo, float& hi, bool up) {
+  const int send = __float_as_int(up ? lo : hi);
+  const float got = __int_as_float(STEP == 1 ? __builtin_amdgcn_mov_dpp(send, 0xb1, 0xf, 0xf, true)    // lane ^ 1
+                                             : __builtin_amdgcn_mov_dpp(send, 0x4e, 0xf, 0xf, true));  // lane ^ 2
+  lo = up ? got : lo;
+  hi = up ? hi : got;
+}
+__device__ __forceinline__ void transpose4(float (&v)[4], int lane) {
+  swap_step<1>(v[0], v[1], lane & 1);
+  swap_step<1>(v[2], v[3], lane & 1);
+  swap_step<2>(v[0], v[2], lane & 2);
+  swap_step<2>(v[1], v[3], lane & 2);
+}
+
 // How tensors come into workgroup memory: through registers (odd elements,
 // 4-byte starts), or by 16-byte loads that write there (bf16 rows of whole chunks)
 enum { kOdd = 0, kEven = 1, kDirect = 2 };
@@ -152,6 +190,26 @@ __device__ __forceinline__ void store1(UT* p, float v) {
   if constexpr (sizeof(UT) == 4) *p = v;
   else p->bits = static_cast<uint16_t>(pack_bf16(v, v));
 }
+// the first `count` of 8 consecutive elements; wide: 16-byte aligned runs of 8
+template <class UT>
+__device__ __forceinline__ void store_run(UT* to, const float (&x)[8], int count, bool wide) {
+  if (wide) {
+    if constexpr (sizeof(UT) == 4) {
+      *reinterpret_cast<f32x4*>(to) = f32x4{x[0], x[1], x[2], x[3]};
+      *reinterpret_cast<f32x4*>(to + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    } else {
+      i32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = static_cast<int>(pack_bf16(x[2 * i], x[2 * i + 1]));
+      *reinterpret_cast<i32x4*>(to) = v;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < count) store1(to + i, x[i]);
+}
+
 // A tile in workgroup memory: NP planes of ROWS rows of COLS bf16. Chunk c (16
 // bytes) of a row lies at c ^ turn(row), so that 16 rows read at one chunk touch
 // all banks, and 4 rows at 4 chunks as well.

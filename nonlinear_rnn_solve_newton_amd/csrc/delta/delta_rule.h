@@ -60,7 +60,7 @@ struct DeltaArgs {
   float* dlam_part;              // adjoint: [HV][B chunks]
   int B, L, H, HV, dk, dv, nc;
   float c, eps, scale;
-  int wide;                      // rows of bf16 o (adjoint: dV) take 16-byte stores
+  int wide, wide_qk;             // rows of bf16 o (adjoint: dV), and of dQ and dK, take 16-byte stores
 };
 
 // factors of a chunk's rows (NotR, NotB: 1 - s(gate) as s(-gate), which keeps its digits)
@@ -948,7 +948,8 @@ struct DeltaGradLds {
   static constexpr size_t BYTES = APART ? kStage + kTiles : (kStage > kTiles + sizeof(Mats) ? kStage : kTiles + sizeof(Mats));
 };
 
-template <class UT, bool EVEN, int DK>
+// SHARED: several value heads to a head of q and k, whose gradients are summed over them
+template <class UT, bool EVEN, int DK, bool SHARED>
 __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   typedef DeltaGradLds<UT, DK> M;
   typedef typename M::Tile Tile;
@@ -962,8 +963,8 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   Tile& tq = reinterpret_cast<Tile*>(lds + M::TILES)[1];
   typename M::Mats& mt = *reinterpret_cast<typename M::Mats*>(lds + M::MATS);
 
-  const int tid = threadIdx.x, lane = tid & 63, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
-  const int w = w8 & 3, f = w8 >> 2, per = p.HV / p.H;
+  const int tid = threadIdx.x, lane = tid & 63, w8 = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = w8 & 3, f = w8 >> 2, per = SHARED ? p.HV / p.H : 1;
   const int ch = blockIdx.x % p.nc, b = blockIdx.x / p.nc / p.H, h = blockIdx.x / p.nc % p.H;
   const int t0 = ch * kDeltaChunk, len = delta_len(p, b), rows_out = min(p.L - t0, kDeltaChunk);
   if (t0 >= len) {  // no step: zeros
@@ -1004,14 +1005,25 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
   };
   if constexpr (M::APART) tiles();
 
-  f32x4 dq[HT], dk[HT];
-  float qsum[4], ksum[4];  // q.dQ and k.dK over the value heads, of the lane's 4 rows
+  f32x4 dq[SHARED ? HT : 1], dk[SHARED ? HT : 1];
+  float qsum[SHARED ? 4 : 1], ksum[SHARED ? 4 : 1];  // q.dQ and k.dK over the value heads, of the lane's 4 rows
+  if constexpr (SHARED) {
 #pragma unroll
-  for (int t = 0; t < HT; ++t) dq[t] = dk[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < HT; ++t) dq[t] = dk[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int r = 0; r < 4; ++r) qsum[r] = ksum[r] = 0.0f;
-
+    for (int r = 0; r < 4; ++r) qsum[r] = ksum[r] = 0.0f;
+  }
   for (int hr = 0; hr < per; ++hr) {
+    // made anew in every round, so that no address is held over the rounds
+    int m = lane & 15, g = lane >> 4;
+    __asm__ volatile("" : "+v"(m), "+v"(g));
+    // the lane's 4 rows of column m of a tile of q or k, from the operand that holds them
+    auto mine = [&](Tile& t, int tile, float (&v)[4]) {
+      bf16x8 o[NP];
+      t.columns(f * HT + tile, w >> 1, m, g, o);
+  #pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = w & 1 ? plane_sum<NP>(o, 4 + r) : plane_sum<NP>(o, r);
+    };
     const int hv = h * per + hr;
     const long long id = (static_cast<long long>(b) * p.HV + hv) * p.nc + ch;
     const int rt = delta_tiles(p.dk), nct = delta_tiles(p.dv);
@@ -1022,25 +1034,30 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
                                  dsr = make_rsrc(p.dstates + id * nct * rt * 64, nct * rt * 1024),
                                  yr = make_rsrc(p.ys + id * nct * 4 * 64, nct * 4096),
                                  xr = make_rsrc(p.dxs + id * nct * 4 * 64, nct * 4096);
-    // the thread's share of a block of 32 columns, one block ahead: waves deal out the tiles
+    // the thread's share of a block of 32 columns, ahead of its use: waves deal out the tiles
     constexpr int NS = RT * 2 / 8;
-    i32x4 fs[NS], fd[NS], fy, fx;
-    Piece<UT, EVEN> fo;
-    auto fetch = [&](int vb) {
+    constexpr int AHEAD = NP == 1 && (DK == 64 || !SHARED) ? 2 : 1;  // blocks on their way, by the registers that are left
+    i32x4 fs[AHEAD][NS], fd[AHEAD][NS], fy[AHEAD], fx[AHEAD];
+    Piece<UT, EVEN> fo[AHEAD];
+    auto fetch = [&](int vb, auto zc) __attribute__((always_inline)) {
+      constexpr int z = decltype(zc)::value;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int e = w8 + 8 * i, c = 2 * vb + e / RT, t = e % RT;
         const uint32_t off = t < rt ? static_cast<uint32_t>((c * rt + t) * 64 + lane) * 16 : kNoLoad;
-        fs[i] = __builtin_amdgcn_raw_buffer_load_b128(sr, off, 0, 0);
-        fd[i] = __builtin_amdgcn_raw_buffer_load_b128(dsr, off, 0, 0);
+        fs[z][i] = __builtin_amdgcn_raw_buffer_load_b128(sr, off, 0, 0);
+        fd[z][i] = __builtin_amdgcn_raw_buffer_load_b128(dsr, off, 0, 0);
       }
       const uint32_t off = static_cast<uint32_t>(((2 * vb + f) * 4 + w) * 64 + lane) * 16;
-      fy = __builtin_amdgcn_raw_buffer_load_b128(yr, off, 0, 0);
-      fx = __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0);
+      fy[z] = __builtin_amdgcn_raw_buffer_load_b128(yr, off, 0, 0);
+      fx[z] = __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0);
       const int row = tid >> 2, d = 32 * vb + sg.o.source(tid);
-      if (f == 0) fo.load(orr, offset_of<UT>(row, ov.token, d, row < n && d < p.dv));
+      if (f == 0) fo[z].load(orr, offset_of<UT>(row, ov.token, d, row < n && d < p.dv));
     };
-    fetch(0);
+    typedef std::integral_constant<int, 0> Z0;
+    typedef std::integral_constant<int, AHEAD - 1> Z1;
+    fetch(0, Z0{});
+    if (AHEAD == 2) fetch(1, Z1{});  // past the last block: zeros
     for (int i = tid; i < kRows * 64; i += 512) srow[i] = p.rows[id * (kRows * 64) + i];
     f32x4 qo[HT], kx[HT], yd[HT], dd[4];
     float dot = 0.0f;
@@ -1049,45 +1066,64 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) dd[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int nb = (p.dv + 31) / 32;
-    for (int vb = 0; vb < nb; ++vb) {
+    auto block = [&](int vb, auto zc) __attribute__((always_inline)) {
+      constexpr int z = decltype(zc)::value;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int e = w8 + 8 * i, c = e / RT, t = e % RT;
-        const f32x4 a = __builtin_bit_cast(f32x4, fs[i]), d = __builtin_bit_cast(f32x4, fd[i]);
+        const f32x4 a = __builtin_bit_cast(f32x4, fs[z][i]), d = __builtin_bit_cast(f32x4, fd[z][i]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) dot = fmaf(a[r], d[r], dot);
         sg.s.put4(16 * c + m, delta_label(t, 4 * g), a);
         sg.ds.put4(16 * c + m, delta_label(t, 4 * g), d);
       }
-      sg.y.put4(16 * f + m, delta_label(w, 4 * g), __builtin_bit_cast(f32x4, fy));
-      sg.x.put4(16 * f + m, delta_label(w, 4 * g), __builtin_bit_cast(f32x4, fx));
+      sg.y.put4(16 * f + m, delta_label(w, 4 * g), __builtin_bit_cast(f32x4, fy[z]));
+      sg.x.put4(16 * f + m, delta_label(w, 4 * g), __builtin_bit_cast(f32x4, fx[z]));
       if (f == 0) {
         bf16x8 o[NP];
-        planes_of(fo, p.dv - 32 * vb - sg.o.source(tid), o);
+        planes_of(fo[z], p.dv - 32 * vb - sg.o.source(tid), o);
         sg.o.put_slot(tid, o);
       }
       __syncthreads();
-      if (vb + 1 < nb) fetch(vb + 1);
-      bf16x8 ao[NP], ax[3], ay[3], bb[3];
+      if (vb + AHEAD < nb) fetch(vb + AHEAD, zc);
+      bf16x8 ao[NP], ax[3], ay[3], bs[2][3], bd[2][3];
       sg.o.rows(w, 0, m, g, ao);
       sg.x.columns(w, 0, m, g, ax);
       sg.y.columns(w, 0, m, g, ay);
+      sg.s.columns(f * HT, 0, m, g, bs[0]);
+      sg.ds.columns(f * HT, 0, m, g, bd[0]);
 #pragma unroll
-      for (int t = 0; t < HT; ++t) {
-        sg.s.columns(f * HT + t, 0, m, g, bb);
-        mma<NP, 3>(qo[t], ao, bb);
-        mma<3, 3>(kx[t], ax, bb);
-        sg.ds.columns(f * HT + t, 0, m, g, bb);
-        mma<3, 3>(yd[t], ay, bb);
+      for (int t = 0; t < HT; ++t) {  // the next tile's operands under this one's products
+        if (t + 1 < HT) {
+          sg.s.columns(f * HT + t + 1, 0, m, g, bs[(t + 1) & 1]);
+          sg.ds.columns(f * HT + t + 1, 0, m, g, bd[(t + 1) & 1]);
+        } else {
+          sg.y.columns(0, 0, m, g, bs[(t + 1) & 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const bf16x8(&u)[3] = bs[t & 1], (&v)[3] = bd[t & 1];
+#pragma unroll
+        for (int q = 2; q >= 0; --q)
+#pragma unroll
+          for (int i = 0; i <= q; ++i) {
+            kx[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i], u[q - i], kx[t], 0, 0, 0);
+            yd[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ay[i], v[q - i], yd[t], 0, 0, 0);
+            if (i < NP) qo[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ao[i], u[q - i], qo[t], 0, 0, 0);
+          }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w) {
-          sg.y.columns(j, 0, m, g, bb);
-          if (f == 0) mma<NP, 3>(dd[j], ao, bb);
-          else mma<3, 3>(dd[j], ax, bb);
+          if (j < w) sg.y.columns(j + 1, 0, m, g, bs[(HT + j + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (f == 0) mma<NP, 3>(dd[j], ao, bs[(HT + j) & 1]);
+          else mma<3, 3>(dd[j], ax, bs[(HT + j) & 1]);
         }
+    };
+    for (int vb = 0; vb < nb; vb += AHEAD) {
+      block(vb, Z0{});
+      if (AHEAD == 2 && vb + 1 < nb) block(vb + 1, Z1{});
     }
     __syncthreads();  // the stage has been read
     if constexpr (!M::APART) tiles();
@@ -1112,110 +1148,148 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
           mma<NP, NP>(pp[j], a, c);
         }
     }
+    {
+      const f32x4 Gi = *reinterpret_cast<const f32x4*>(&srow[kRowG * 64 + 16 * w + 4 * g]);
+      const f32x4 si = *reinterpret_cast<const f32x4*>(&srow[kRowSeg * 64 + 16 * w + 4 * g]);
+      const f32x4 li = *reinterpret_cast<const f32x4*>(&srow[(f ? kRowK : kRowQ) * 64 + 16 * w + 4 * g]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = 16 * j + m;
+      for (int j = 0; j < 4; ++j) {
+        const int c = 16 * j + m;
+        float* const at = to + (16 * w + 4 * g) * ROW + c;
+        if (j > w) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * w + 4 * g + e;
-        const bool low = (f ? i > c : i >= c) && srow[kRowSeg * 64 + i] == srow[kRowSeg * 64 + c];
-        const float x = (f ? -1.0f : p.scale) * srow[kRowB * 64 + c] *
-                        __builtin_amdgcn_exp2f((srow[kRowG * 64 + i] - srow[kRowG * 64 + c]) * kLog2e);
-        const float d = low ? x * dd[j][e] : 0.0f;
-        to[i * ROW + c] = d;
-        pp[j][e] *= d * srow[(f ? kRowK : kRowQ) * 64 + i] * srow[kRowK * 64 + c];
-        if (!f) mt.w[i * ROW + c] = pp[j][e];
+          for (int e = 0; e < 4; ++e) {
+            at[e * ROW] = 0.0f;
+            if (!f) mt.w[(16 * w + 4 * g + e) * ROW + c] = 0.0f;
+          }
+          continue;
+        }
+        const float Gc = srow[kRowG * 64 + c], sc = srow[kRowSeg * 64 + c], kc = srow[kRowK * 64 + c];
+        const float bc = (f ? -1.0f : p.scale) * srow[kRowB * 64 + c];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * w + 4 * g + e;
+          const bool low = (f ? i > c : i >= c) && si[e] == sc;
+          const float d = low ? bc * __builtin_amdgcn_exp2f((Gi[e] - Gc) * kLog2e) * dd[j][e] : 0.0f;
+          at[e * ROW] = d;
+          pp[j][e] *= d * li[e] * kc;
+          if (!f) mt.w[i * ROW + c] = pp[j][e];
+        }
       }
     }
     __syncthreads();
     if (f) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
+        if (j <= w) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mt.w[(16 * w + 4 * g + e) * ROW + 16 * j + m] += pp[j][e];
+          for (int e = 0; e < 4; ++e) mt.w[(16 * w + 4 * g + e) * ROW + 16 * j + m] += pp[j][e];
+        }
     }
-    f32x4 kr[HT], kw[HT];
     const float se = srow[kRowSeg * 64 + 63], Ge = srow[kRowG * 64 + 63];
-    float rq[4], rk[4], part[5][4];  // q.dQ, k.(dK read), k.(dK written); of S1, from S0
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * w + 4 * g + r;
-      const float gamma = srow[kRowSeg * 64 + i] == 0.0f ? __builtin_amdgcn_exp2f(srow[kRowG * 64 + i] * kLog2e) : 0.0f;
-      const float tail = srow[kRowSeg * 64 + i] == se ? __builtin_amdgcn_exp2f((Ge - srow[kRowG * 64 + i]) * kLog2e) : 0.0f;
-      const float wr = tail * srow[kRowB * 64 + i];
-      rk[r] = srow[kRowK * 64 + i];
-      rq[r] = srow[kRowQ * 64 + i];
-      part[0][r] = part[1][r] = part[2][r] = part[3][r] = part[4][r] = 0.0f;
-#pragma unroll
-      for (int t = 0; t < HT; ++t) {
-        qo[t][r] *= p.scale * gamma;
-        kr[t][r] = -gamma * kx[t][r];
-        kw[t][r] = wr * yd[t][r];
-        const int d = delta_label(f * HT + t, m);
-        const float kv = rk[r] * tk.at(i, d);
-        part[3][r] = fmaf(kw[t][r], kv, part[3][r]);
-        part[4][r] = fmaf(kr[t][r], kv, fmaf(qo[t][r], rq[r] * tq.at(i, d), part[4][r]));
-      }
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      bf16x8 c0[3], c1[3], c2[3], c3[3];
-      float x[8], y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {  // rows of D0 and D1 with the keys' lengths
-        const int c = 32 * kb + (e < 4 ? 0 : 16) + 4 * g + (e & 3), r = 16 * w + m;
-        const float s = srow[kRowK * 64 + c];
-        x[e] = mt.d0[r * ROW + c] * s;
-        y[e] = mt.d1[r * ROW + c] * s;
-      }
-      split8<3>(x, c0);
-      split8<3>(y, c1);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {  // their columns, with the lengths of q and k
-        const int c = 32 * kb + (e < 4 ? 0 : 16) + 4 * g + (e & 3), r = 16 * w + m;
-        x[e] = mt.d0[c * ROW + r] * srow[kRowQ * 64 + c];
-        y[e] = mt.d1[c * ROW + r] * srow[kRowK * 64 + c];
-      }
-      split8<3>(x, c2);
-      split8<3>(y, c3);
-#pragma unroll
-      for (int t = 0; t < HT; ++t) {
-        bf16x8 bk[NP], bq[NP];
-        tk.columns(f * HT + t, kb, m, g, bk);
-        tq.columns(f * HT + t, kb, m, g, bq);
-        if (kb <= w / 2) {
-          mma<3, NP>(qo[t], c0, bk);
-          mma<3, NP>(kr[t], c1, bk);
-        }
-        if (kb >= w / 2) {
-          mma<3, NP>(kw[t], c2, bq);
-          mma<3, NP>(kw[t], c3, bk);
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < HT; ++t)
+    const f32x4 rq = *reinterpret_cast<const f32x4*>(&srow[kRowQ * 64 + 16 * w + 4 * g]);
+    const f32x4 rk = *reinterpret_cast<const f32x4*>(&srow[kRowK * 64 + 16 * w + 4 * g]);
+    float part[5][4];  // q.dQ, k.(dK read), k.(dK written); of S1, from S0
+    {
+      float cq[4], ck[4], cw[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * w + 4 * g + r, d = delta_label(f * HT + t, m);
-        const float qv = rq[r] * tq.at(i, d), kv = rk[r] * tk.at(i, d);
-        part[0][r] = fmaf(qv, qo[t][r], part[0][r]);
-        part[1][r] = fmaf(kv, kr[t][r], part[1][r]);
-        part[2][r] = fmaf(kv, kw[t][r], part[2][r]);
-        dq[t][r] += qo[t][r];
-        dk[t][r] += kr[t][r] + kw[t][r];
+        const int i = 16 * w + 4 * g + r;
+        const float G = srow[kRowG * 64 + i], seg = srow[kRowSeg * 64 + i];
+        ck[r] = seg == 0.0f ? -__builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
+        cq[r] = -p.scale * ck[r];
+        cw[r] = seg == se ? __builtin_amdgcn_exp2f((Ge - G) * kLog2e) * srow[kRowB * 64 + i] : 0.0f;
+        part[0][r] = part[1][r] = part[2][r] = part[3][r] = part[4][r] = 0.0f;
       }
 #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1)
+      for (int t = 0; t < HT; ++t) {  // what the states bring: kx and yd become the two parts of dK
+        float qv[4], kv[4];
+        mine(tq, t, qv);
+        mine(tk, t, kv);
 #pragma unroll
-      for (int k = 0; k < 5; ++k)
+        for (int r = 0; r < 4; ++r) {
+          qo[t][r] *= cq[r];
+          kx[t][r] *= ck[r];
+          yd[t][r] *= cw[r];
+          part[3][r] = fmaf(yd[t][r], rk[r] * kv[r], part[3][r]);
+          part[4][r] = fmaf(kx[t][r], rk[r] * kv[r], fmaf(qo[t][r], rq[r] * qv[r], part[4][r]));
+        }
+      }
+    }
+    // rows (COLS false) or columns of a matrix, block kb of 32 inner indexes, times a factor of those
+    auto operand = [&](const float* mat, bool cols, int kind, int kb, bf16x8 (&o)[3]) {
+      float x[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) part[k][r] += __shfl_xor(part[k][r], off, 64);
-    if (m == 0) {
+      for (int h2 = 0; h2 < 2; ++h2) {
+        const int c = 32 * kb + 16 * h2 + 4 * g, r = 16 * w + m;
+        const f32x4 fc = *reinterpret_cast<const f32x4*>(&srow[kind * 64 + c]);
+        f32x4 v;
+        if (cols) {
 #pragma unroll
-      for (int k = 0; k < 5; ++k)
+          for (int e = 0; e < 4; ++e) v[e] = mat[(c + e) * ROW + r];
+        } else {
+          v = *reinterpret_cast<const f32x4*>(&mat[r * ROW + c]);
+        }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) spart[f][k][16 * w + 4 * g + r] = part[k][r];
+        for (int e = 0; e < 4; ++e) x[4 * h2 + e] = v[e] * fc[e];
+      }
+      split8<3>(x, o);
+    };
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      bf16x8 ca[3], cb[3];
+      if (kb <= w / 2) {  // rows of D0 and D1 on k
+        operand(mt.d0, false, kRowK, kb, ca);
+        operand(mt.d1, false, kRowK, kb, cb);
+#pragma unroll
+        for (int t = 0; t < HT; ++t) {
+          bf16x8 o[NP];
+          tk.columns(f * HT + t, kb, m, g, o);
+          mma<3, NP>(qo[t], ca, o);
+          mma<3, NP>(kx[t], cb, o);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (kb >= w / 2) {  // their columns on q and k
+        operand(mt.d0, true, kRowQ, kb, ca);
+        operand(mt.d1, true, kRowK, kb, cb);
+#pragma unroll
+        for (int t = 0; t < HT; ++t) {
+          bf16x8 o[NP], o2[NP];
+          tq.columns(f * HT + t, kb, m, g, o);
+          tk.columns(f * HT + t, kb, m, g, o2);
+          mma<3, NP>(yd[t], ca, o);
+          mma<3, NP>(yd[t], cb, o2);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = 0; t < HT; ++t) {
+      float qv[4], kv[4];
+      mine(tq, t, qv);
+      mine(tk, t, kv);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        part[0][r] = fmaf(rq[r] * qv[r], qo[t][r], part[0][r]);
+        part[1][r] = fmaf(rk[r] * kv[r], kx[t][r], part[1][r]);
+        part[2][r] = fmaf(rk[r] * kv[r], yd[t][r], part[2][r]);
+      }
+      if constexpr (SHARED) {
+        dq[t] += qo[t];
+        dk[t] += kx[t] + yd[t];
+      }
+    }
+    {  // over the 16 lanes of a row: lane m ends up with kind m / 4 of row 4 g + m % 4, and with the fifth kind's
+      float v[16], u[4];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = part[i >> 2][i & 3];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) u[r] = part[4][r];
+      sum_and_deal<16, 16>(v, lane);
+      sum_and_deal<4, 16>(u, lane);
+      spart[f][m >> 2][16 * w + 4 * g + (m & 3)] = v[0];
+      if ((m & 3) == 0) spart[f][4][16 * w + 4 * g + (m >> 2)] = u[0];
     }
     // sums of W over j < t <= i: a wave takes 8 t, a lane a column j
     {
@@ -1233,21 +1307,73 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
         v += mt.w[(8 * w8 + r) * ROW + lane];
         pass[r] = lane < 8 * w8 + r ? v : 0.0f;
       }
+      sum_and_deal<8, 64>(pass, lane);
+      if ((lane & 7) == 0) spass[8 * w8 + deal_index<8, 64>(lane)] = pass[0];
+    }
+    if constexpr (SHARED) {
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1)
-#pragma unroll
-        for (int r = 0; r < 8; ++r) pass[r] += __shfl_xor(pass[r], off, 64);
-      if (lane == 0) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) spass[8 * w8 + r] = pass[r];
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * w + 4 * g + r;
+        qsum[r] += spart[0][0][i] + spart[1][0][i];
+        ksum[r] += spart[0][1][i] + spart[1][1][i] + spart[0][2][i] + spart[1][2][i];
       }
     }
+    // Gradients through the lengths of q and k: r (d - unit (unit.d))
+    auto finish = [&]() {
+      float qs[4], ks[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * w + 4 * g + r;
-      qsum[r] += spart[0][0][i] + spart[1][0][i];
-      ksum[r] += spart[0][1][i] + spart[1][1][i] + spart[0][2][i] + spart[1][2][i];
-    }
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * w + 4 * g + r;
+        if constexpr (SHARED) {
+          qs[r] = qsum[r];
+          ks[r] = ksum[r];
+        } else {
+          qs[r] = spart[0][0][i] + spart[1][0][i];
+          ks[r] = spart[0][1][i] + spart[1][1][i] + spart[0][2][i] + spart[1][2][i];
+        }
+      }
+      // two tiles are 8 neighbouring columns of 4 lanes' rows: transposed within those lanes, a lane has 8
+      // columns of its row m % 4
+      const int row = 16 * w + 4 * g + (m & 3);
+      UT* const qo_ = out_at<UT>(p.gq, b, t0 + row) + h * p.dk;
+      UT* const ko_ = out_at<UT>(p.gk, b, t0 + row) + h * p.dk;
+#pragma unroll
+      for (int t = 0; t < HT; t += 2) {
+        float oq[8], ok[8];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          float qv[4], kv[4], vq[4], vk[4];
+          mine(tq, t + z, qv);
+          mine(tk, t + z, kv);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float a, c;
+            if constexpr (SHARED) {
+              a = dq[t + z][r];
+              c = dk[t + z][r];
+            } else {
+              a = qo[t + z][r];
+              c = kx[t + z][r] + yd[t + z][r];
+            }
+            vq[r] = rq[r] * fmaf(-rq[r] * qv[r], qs[r], a);
+            vk[r] = rk[r] * fmaf(-rk[r] * kv[r], ks[r], c);
+          }
+          transpose4(vq, lane);
+          transpose4(vk, lane);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            oq[4 * z + c] = vq[c];
+            ok[4 * z + c] = vk[c];
+          }
+        }
+        const int d = 16 * f * HT + 16 * t + 8 * (m >> 2), count = p.dk - d;
+        if (row < rows_out && count > 0) {
+          store_run(qo_ + d, oq, count, p.wide_qk);
+          store_run(ko_ + d, ok, count, p.wide_qk);
+        }
+      }
+    };
+    if (!SHARED || hr + 1 == per) finish();
     __syncthreads();
     if (w8 == 0) {  // the gates: a lane per step
       const int i = lane;
@@ -1278,25 +1404,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
         if (i == 0) p.dlam_part[static_cast<long long>(hv) * p.B * p.nc + b * p.nc + ch] = sum;
       }
     }
-    __syncthreads();
-  }
-  // through the lengths of q and k
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = 16 * w + 4 * g + r;
-    const float rk = srow[kRowK * 64 + i], rq = srow[kRowQ * 64 + i];
-    if (i < rows_out) {
-      UT* qo = out_at<UT>(p.gq, b, t0 + i) + h * p.dk;
-      UT* ko = out_at<UT>(p.gk, b, t0 + i) + h * p.dk;
-#pragma unroll
-      for (int t = 0; t < HT; ++t) {
-        const int d = delta_label(f * HT + t, m);
-        if (d < p.dk) {
-          store1(qo + d, rq * fmaf(-rq * tq.at(i, d), qsum[r], dq[t][r]));
-          store1(ko + d, rk * fmaf(-rk * tk.at(i, d), ksum[r], dk[t][r]));
-        }
-      }
-    }
+    if (SHARED && hr + 1 < per) __syncthreads();
   }
 }
 
