@@ -112,13 +112,60 @@ __device__ __forceinline__ f32x4 mul16(const float* a, const f32x4& b, f32x4 c) 
   return c;
 }
 
+// Inverse of 1 + a for a strictly lower triangular block of 16 x 16 in workgroup
+// memory: lane (m, g) solves column m of block g by substitution. The rows come
+// in three parts, each read while the one before is worked on.
+template <int ROW>
+__device__ __forceinline__ void invert16(const float* a, int m, float (&x)[16]) {
+  f32x4 r0[8], r1[13], r2[11];
+  auto row = [&](int i, int j4) { return *reinterpret_cast<const f32x4*>(a + i * ROW + 4 * j4); };
+#pragma unroll
+  for (int i = 1; i <= 6; ++i) {
+    if (i <= 4) r0[i - 1] = row(i, 0);
+    else {
+      r0[4 + 2 * (i - 5)] = row(i, 0);
+      r0[5 + 2 * (i - 5)] = row(i, 1);
+    }
+  }
+#pragma unroll
+  for (int i = 7; i <= 11; ++i)
+#pragma unroll
+    for (int j = 0; j < (i + 3) / 4; ++j) r1[i <= 8 ? 2 * (i - 7) + j : 4 + 3 * (i - 9) + j] = row(i, j);
+  x[0] = m == 0 ? 1.0f : 0.0f;
+  auto solve = [&](int i, const f32x4* r) {
+    float v = i == m ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < i) v = fmaf(-r[j >> 2][j & 3], x[j], v);
+    x[i] = v;
+  };
+#pragma unroll
+  for (int i = 1; i <= 6; ++i) solve(i, &r0[i <= 4 ? i - 1 : 4 + 2 * (i - 5)]);
+#pragma unroll
+  for (int i = 12; i <= 15; ++i)
+#pragma unroll
+    for (int j = 0; j < (i == 12 ? 3 : 4); ++j)
+      if (i < 15) r2[i == 12 ? j : 3 + 4 * (i - 13) + j] = row(i, j);
+#pragma unroll
+  for (int i = 7; i <= 11; ++i) solve(i, &r1[i <= 8 ? 2 * (i - 7) : 4 + 3 * (i - 9)]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r0[j] = row(15, j);
+#pragma unroll
+  for (int i = 12; i <= 14; ++i) solve(i, &r2[i == 12 ? 0 : 3 + 4 * (i - 13)]);
+  solve(15, r0);
+}
+
 // A workgroup per chunk and value head: row factors, T and P (ADJ: their
-// transposes) as operands of the scan, in memory order of its reads.
+// transposes) as operands of the scan, in memory order of its reads. A wave takes
+// the 16 steps of tile w: of its queries, the products with the keys up to them,
+// or (ADJ) of its keys, with the queries from them on. A lane then has 4 inner
+// indexes of its row of P, as the operand wants them, and P never leaves
+// registers; the keys' own products go to workgroup memory to be inverted.
 template <class UT, bool EVEN, int DK, bool ADJ>
-__global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kernel(const DeltaArgs p) {
   typedef DeltaFrags<UT, ADJ> F;
   constexpr int NP = DeltaPlanes<UT>::NP, KB = DK / 32, ROW = 68;
-  __shared__ float sm[64 * ROW], sp[64 * ROW], st[64 * ROW];
+  __shared__ float sm[64 * ROW], st[64 * ROW];
   __shared__ float sg[64], sb[64], sseg[64], srk[64], srq[64];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
   const int ch = blockIdx.x % p.nc, bh = blockIdx.x / p.nc, b = bh / p.HV, hv = bh % p.HV, h = hv / (p.HV / p.H);
@@ -127,7 +174,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
   const int n = min(len - t0, kDeltaChunk);
   float* rows = p.rows + (static_cast<long long>(bh) * p.nc + ch) * (kRows * 64);
 
-  // products of the wave's 16 rows of k and q with the keys up to them
+  // own: the wave's 16 rows, column of the results; tile j of the others: their rows
   f32x4 kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -136,31 +183,46 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
     const int H = p.H * p.dk;
     const __amdgpu_buffer_rsrc_t kr = rows_of<UT>(p.k, b, t0, h * p.dk, n, H), qr = rows_of<UT>(p.q, b, t0, h * p.dk, n, H);
     const int i = 16 * w + m;
+    // which tiles the wave multiplies with: the keys up to its own, or the queries (and keys) from it on
+    auto other = [&](int j) { return ADJ ? j >= w : j <= w; };
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       const int d = 32 * kb + 8 * g, count = p.dk - d;
-      Piece<UT, EVEN> rk[4], rq;
-      rq.load(qr, offset_of<UT>(i, p.q.token, d, i < n && count > 0));
+      Piece<UT, EVEN> rk[4], rq[ADJ ? 4 : 1];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j <= w) rk[j].load(kr, offset_of<UT>(16 * j + m, p.k.token, d, 16 * j + m < n && count > 0));
-      bf16x8 aq[NP], ak[NP], bk[NP];
-      planes_of(rq, count, aq);
+        if (other(j)) rk[j].load(kr, offset_of<UT>(16 * j + m, p.k.token, d, 16 * j + m < n && count > 0));
+      if constexpr (ADJ) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (other(j)) rq[j].load(qr, offset_of<UT>(16 * j + m, p.q.token, d, 16 * j + m < n && count > 0));
+      } else {
+        rq[0].load(qr, offset_of<UT>(i, p.q.token, d, i < n && count > 0));
+      }
+      bf16x8 ok[NP], oq[NP], c[NP];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j == w) planes_of(rk[j], count, ak);
+        if (j == w) {
+          planes_of(rk[j], count, ok);
+          planes_of(rq[ADJ ? j : 0], count, oq);
+        }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = plane_sum<NP>(ak, e), y = plane_sum<NP>(aq, e);
+        const float x = plane_sum<NP>(ok, e), y = plane_sum<NP>(oq, e);
         nk = fmaf(x, x, nk);
         nq = fmaf(y, y, nq);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          planes_of(rk[j], count, bk);
-          mma<NP, NP>(kk[j], ak, bk);
-          mma<NP, NP>(qk[j], aq, bk);
+        if (other(j)) {
+          planes_of(rk[j], count, c);
+          mma<NP, NP>(kk[j], c, ok);
+          if constexpr (ADJ) {
+            planes_of(rq[j], count, c);
+            mma<NP, NP>(qk[j], c, ok);
+          } else {
+            mma<NP, NP>(qk[j], c, oq);
+          }
         }
     }
   }
@@ -172,7 +234,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
     srk[16 * w + m] = 1.0f / sqrtf(nk + p.eps);
     srq[16 * w + m] = 1.0f / sqrtf(nq + p.eps);
   }
-  if (w == 0) {  // the gates: a lane per step
+  if (w == (ADJ ? 3 : 0)) {  // the gates: a lane per step, in the wave with the fewest products
     const int i = lane;
     const bool on = i < n;
     const UT* gp = at<UT>(p.gates, b, t0 + min(i, n - 1)) + hv;
@@ -200,7 +262,61 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
   }
   __syncthreads();
   constexpr float kLog2e = 1.4426950408889634f;
-  if (w == 1) {
+  bf16x8* const out = p.frags + (static_cast<long long>(bh) * p.nc + ch) * F::ALL;
+  {
+    // element (row i, column j) of both: E_ij with the lengths, b_j and the scale. The lane's own index is the
+    // row i (ADJ: the column j), and it has 4 of the other.
+    const int own = 16 * w + m;
+    const float Go = sg[own], so = sseg[own], ko = srk[own], qo = srq[own] * p.scale, bo = sb[own];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4 mv = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (ADJ ? j >= w : j <= w) {
+        const int c = 16 * j + 4 * g;
+        const f32x4 Gc = *reinterpret_cast<const f32x4*>(&sg[c]), sc = *reinterpret_cast<const f32x4*>(&sseg[c]);
+        const f32x4 kc = *reinterpret_cast<const f32x4*>(&srk[c]);
+        const f32x4 fc = *reinterpret_cast<const f32x4*>(ADJ ? &srq[c] : &sb[c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = ADJ ? c + e : own, col = ADJ ? own : c + e;
+          const bool low = row >= col && sc[e] == so;
+          const float x = low ? __builtin_amdgcn_exp2f((ADJ ? Gc[e] - Go : Go - Gc[e]) * kLog2e) : 0.0f;
+          // k_i k_j b_j and scale q_i k_j b_j
+          const float y = x * kc[e] * ko * (ADJ ? bo : fc[e]);
+          mv[e] = row > col ? y * kk[j][e] : 0.0f;
+          qk[j][e] *= ADJ ? x * p.scale * fc[e] * ko * bo : x * kc[e] * fc[e] * qo;
+        }
+      } else {
+        qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      if constexpr (ADJ) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sm[(16 * j + 4 * g + e) * ROW + own] = mv[e];
+      } else {
+        *reinterpret_cast<f32x4*>(&sm[own * ROW + 16 * j + 4 * g]) = mv;
+      }
+      if (ADJ ? j < w : j > w) {  // above the diagonal
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[(ADJ ? 16 * j + 4 * g + e : own) * ROW + (ADJ ? own : 16 * j + 4 * g + e)] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+      if (ADJ ? kb >= w / 2 : kb <= w / 2) {
+        bf16x8 o[3];
+        split_tiles<F::NP>(qk[2 * kb], qk[2 * kb + 1], o);
+        const int id = ADJ ? up_block(w, kb) : low_block(w, kb);
+#pragma unroll
+        for (int pl = 0; pl < F::NP; ++pl) out[F::T + (id * F::NP + pl) * 64 + lane] = o[pl];
+      }
+  }
+  __syncthreads();
+  if (w == 0) {  // the four diagonal blocks
+    float x[16];
+    invert16<ROW>(sm + 16 * g * ROW + 16 * g, m, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st[(16 * g + i) * ROW + 16 * g + m] = x[i];
+  } else if (w == 1) {
     const int i = lane;
     const float G = sg[i], Ge = sg[63], se = sseg[63];
     const float gamma = sseg[i] == 0.0f ? __builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
@@ -212,49 +328,18 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
     rows[kRowK * 64 + i] = srk[i];
     rows[kRowQ * 64 + i] = srq[i];
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = 16 * j + m;
-    const float Gc = sg[c], sc = sseg[c], kc = srk[c] * sb[c];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 16 * w + 4 * g + e;
-      const bool low = i >= c && sseg[i] == sc;
-      const float d = low ? __builtin_amdgcn_exp2f((sg[i] - Gc) * kLog2e) * kc : 0.0f;
-      sm[i * ROW + c] = low && i > c ? d * srk[i] * kk[j][e] : 0.0f;
-      sp[i * ROW + c] = low ? p.scale * d * srq[i] * qk[j][e] : 0.0f;
-      if (j > w) st[i * ROW + c] = 0.0f;
-    }
-  }
-  __syncthreads();
-  if (w == 0) {  // the four diagonal blocks: lane (m, g) solves column m of block g
-    float x[16];
-    const float* a = sm + 16 * g * ROW + 16 * g;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == m ? 1.0f : 0.0f;
-#pragma unroll
-      for (int j4 = 0; j4 < i; j4 += 4) {
-        const f32x4 r = *reinterpret_cast<const f32x4*>(a + i * ROW + j4);
-#pragma unroll
-        for (int j = j4; j < i && j < j4 + 4; ++j) v = fmaf(-r[j - j4], x[j], v);
-      }
-      x[i] = v;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) st[(16 * g + i) * ROW + 16 * g + m] = x[i];
-  }
   __syncthreads();
 #pragma unroll
   for (int d = 1; d < 4; ++d) {  // the blocks below: T_ij = -T_ii (sum of M_ik T_kj over j <= k < i)
     if (w >= d) {
       const int j = w - d;
       f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = j; k < w; ++k) {
+#pragma unroll
+      for (int k = 0; k < d; ++k) {
         f32x4 t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = st[(16 * k + 4 * g + e) * ROW + 16 * j + m];
-        s = mul16(sm + (16 * w + m) * ROW + 16 * k + 4 * g, t, s);
+        for (int e = 0; e < 4; ++e) t[e] = st[(16 * (j + k) + 4 * g + e) * ROW + 16 * j + m];
+        s = mul16(sm + (16 * w + m) * ROW + 16 * (j + k) + 4 * g, t, s);
       }
       const f32x4 r = mul16(st + (16 * w + m) * ROW + 16 * w + 4 * g, s, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
@@ -262,34 +347,26 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
     }
     __syncthreads();
   }
-  bf16x8* out = p.frags + (static_cast<long long>(bh) * p.nc + ch) * F::ALL;
-  for (int item = w; item < 2 * kTriBlocks; item += 4) {
-    const int id = item % kTriBlocks;
-    const float* src = item < kTriBlocks ? st : sp;
-    int i, kb;
-    if constexpr (ADJ) {
-      i = id < 4 ? id / 2 : id - 2;
-      kb = id < 4 ? id % 2 : 1;
-    } else {
-      i = id < 2 ? id : 2 + (id - 2) / 2;
-      kb = id < 2 ? 0 : (id - 2) % 2;
-    }
+  for (int id = w; id < kTriBlocks; id += 4) {
+    const int i = ADJ ? (id < 4 ? id / 2 : id - 2) : id < 2 ? id : 2 + (id - 2) / 2;
+    const int kb = ADJ ? (id < 4 ? id % 2 : 1) : id < 2 ? 0 : (id - 2) % 2;
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = 32 * kb + (e < 4 ? 0 : 16) + 4 * g + (e & 3), r = 16 * i + m;
-      x[e] = ADJ ? src[c * ROW + r] : src[r * ROW + c];
+    for (int h2 = 0; h2 < 2; ++h2) {
+      const int c = 32 * kb + 16 * h2 + 4 * g, r = 16 * i + m;
+      if constexpr (ADJ) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * h2 + e] = st[(c + e) * ROW + r];
+      } else {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(&st[r * ROW + c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * h2 + e] = v[e];
+      }
     }
     bf16x8 o[3];
-    if (item < kTriBlocks) {
-      split8<3>(x, o);
+    split8<3>(x, o);
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) out[(id * 3 + pl) * 64 + lane] = o[pl];
-    } else {
-      split8<F::NP>(x, o);
-#pragma unroll
-      for (int pl = 0; pl < F::NP; ++pl) out[F::T + (id * F::NP + pl) * 64 + lane] = o[pl];
-    }
+    for (int pl = 0; pl < 3; ++pl) out[(id * 3 + pl) * 64 + lane] = o[pl];
   }
 }
 
@@ -528,8 +605,8 @@ struct DeltaScan {
           }
       }
   }
-  // N tiles of each of the wave's columns as they lie, n of them per column tile in memory
-  template <int N>
+  // tiles [FROM, TO) of each of the wave's columns as they lie, n of them per column tile in memory
+  template <int FROM, int TO, int N>
   __device__ __forceinline__ void store_tiles(f32x4* to, long long id, int n, const f32x4 (&Y)[NC][N]) const {
     const int nct = delta_tiles(p.dv), c0 = col0;
 #pragma unroll
@@ -537,7 +614,7 @@ struct DeltaScan {
       if (c0 + cc < nct) {
         f32x4* at = to + ((id * nct + c0 + cc) * n) * 64 + lane;
 #pragma unroll
-        for (int t = 0; t < N; ++t)
+        for (int t = FROM; t < TO; ++t)
           if (t < n) at[t * 64] = Y[cc][t];
       }
   }
@@ -602,7 +679,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
   bf16x8 ka[2][4][NP], qa[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][NO], vv[NC][2][NP];
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
-  if (p.states) s.template store_tiles<RT>(p.states, id, delta_tiles(p.dk), S);
+  if (p.states) s.template store_tiles<0, RT>(p.states, id, delta_tiles(p.dk), S);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
@@ -667,7 +744,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) u.k.columns(t, kb, m, g, kc[0][t][kb]);
   __builtin_amdgcn_sched_barrier(0);
-  if (p.ys) s.template store_tiles<4>(p.ys, id, 4, y);
+  if (p.ys) s.template store_tiles<0, 4>(p.ys, id, 4, y);
   // the output
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -776,7 +853,7 @@ __device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p,
   bf16x8 ka[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][3], vb[NC][2][NP];
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
-  s.template store_tiles<RT>(p.dstates, id, delta_tiles(p.dk), S);
+  s.template store_tiles<0, RT>(p.dstates, id, delta_tiles(p.dk), S);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     if (kb + 1 < KB) {
@@ -840,7 +917,7 @@ __device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p,
     for (int t = 0; t < RT; ++t) S[cc][t] *= whole;
   }
   __builtin_amdgcn_sched_barrier(0);
-  s.template store_tiles<4>(p.dxs, id, 4, x);
+  s.template store_tiles<0, 4>(p.dxs, id, 4, x);
   s.result(u, p.gv, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), x);
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc) {
