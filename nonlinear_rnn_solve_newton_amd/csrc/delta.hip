@@ -34,16 +34,52 @@ bool delta_ok(const pararnn_delta_opts* o) {
 
 // sizes of a call's pieces, in bytes (chunks of all value heads)
 struct DeltaSizes {
-  size_t frags, rows, states, ys, part;
+  size_t frags, rows, states, ys, part, seg_add, seg_map;
 };
+// Segments that the scans cut a sequence into, and chunks of each: as many as give every CU a workgroup, and no
+// more than sqrt(1.6 chunks), where a segment's scan (1.6 times its chunks) takes as long as the product over the
+// others' maps (a chunk's time each). The segments' scan before the scans pays from three of them on (bf16, B = 5
+// L = 4096 H = 8, three: 210 -> 188 us; two, B = 8: 234 -> 272), in the adjoint, which both scans are less of, from
+// four on (three: 570 -> 584 us; B = 1 L = 4096 H = 32, four: 507 -> 500), and in bf16, whose chunks are passed in a
+// third of fp32's time, from 16 chunks on (H = 8, 9 chunks: 37 -> 44 us, 16: 55 -> 56, 32 and B = 4: 106 -> 99;
+// fp32, 6 chunks: 49 -> 38, 16: 106 -> 58). B = 1 L = 65536 H = 16: 2815 -> 1082 us.
+struct DeltaSegments {
+  int n, per;
+};
+DeltaSegments delta_segments(const pararnn_delta_opts* o, bool adj) {
+  const long long nc = ceil_div(o->L, kDeltaChunk), groups = static_cast<long long>(o->B) * o->HV * ceil_div(o->dv, 64);
+  const long long most = static_cast<long long>(sqrt(1.6 * static_cast<double>(nc))), room = kCUs / groups;
+  const long long n = room < most ? room : most;
+  if (n < (adj ? 4 : 3) || (o->dtype == PARARNN_BF16 && nc < 16)) return {1, static_cast<int>(nc)};
+  const int per = static_cast<int>(ceil_div(nc, n));
+  return {static_cast<int>(ceil_div(nc, per)), per};
+}
 DeltaSizes delta_sizes(const pararnn_delta_opts* o, bool adj) {
   const size_t chunks = static_cast<size_t>(o->B) * o->HV * ceil_div(o->L, kDeltaChunk);
   const size_t frag = o->dtype == PARARNN_BF16
                           ? (adj ? DeltaFrags<bf16, true>::ALL : DeltaFrags<bf16, false>::ALL)
                           : (adj ? DeltaFrags<float, true>::ALL : DeltaFrags<float, false>::ALL);
+  const int DK = o->dk <= 64 ? 64 : 128, n = delta_segments(o, adj).n;
+  const size_t segs = n > 1 ? static_cast<size_t>(o->B) * o->HV * n : 0;
   return {round_up(chunks * frag * sizeof(bf16x8)), round_up(chunks * kRows * 64 * sizeof(float)),
           chunks * delta_tiles(o->dv) * delta_tiles(o->dk) * 1024, chunks * delta_tiles(o->dv) * 4096,
-          round_up(chunks * sizeof(float))};
+          round_up(chunks * sizeof(float)), segs * delta_tiles(o->dv) * (DK / 16) * 1024, segs * DK * DK * 4};
+}
+
+size_t delta_bytes(const DeltaSizes& z, bool adj) {
+  return z.frags + z.rows + z.seg_add + z.seg_map + (adj ? z.states + z.ys + z.part : 0);
+}
+// the workspace's pieces that both directions have; returns what follows them
+char* delta_carve(DeltaArgs& a, void* ws, const DeltaSizes& z) {
+  char* w = static_cast<char*>(ws);
+  a.frags = reinterpret_cast<bf16x8*>(w);
+  w += z.frags;
+  a.rows = reinterpret_cast<float*>(w);
+  w += z.rows;
+  a.seg_add = reinterpret_cast<f32x4*>(w);
+  w += z.seg_add;
+  a.seg_map = reinterpret_cast<float*>(w);
+  return w + z.seg_map;
 }
 
 // every row and head starts at a multiple of `bytes`
@@ -64,7 +100,7 @@ bool views_ok(const pararnn_view* q, const pararnn_view* k, const pararnn_view* 
 DeltaView view(const pararnn_view* v) { return {v->p, v->batch, v->token}; }
 
 void delta_fill(DeltaArgs& a, const pararnn_view* q, const pararnn_view* k, const pararnn_view* v,
-                const pararnn_view* gates, const float* lam, const pararnn_delta_opts* o, size_t es) {
+                const pararnn_view* gates, const float* lam, const pararnn_delta_opts* o, bool adj) {
   memset(&a, 0, sizeof(a));
   a.q = view(q);
   a.k = view(k);
@@ -83,6 +119,9 @@ void delta_fill(DeltaArgs& a, const pararnn_view* q, const pararnn_view* k, cons
   a.c = o->c;
   a.eps = o->eps;
   a.scale = o->scale;
+  const DeltaSegments g = delta_segments(o, adj);
+  a.nseg = g.n;
+  a.per = g.per;
 }
 
 template <class UT, bool EVEN, int DK, bool ADJ>
@@ -90,17 +129,33 @@ int run_prep(const DeltaArgs& a, hipStream_t s) {
   return launch(delta_prep_kernel<UT, EVEN, DK, ADJ>, static_cast<long long>(a.B) * a.HV * a.nc, 256, s, a);
 }
 // the scans' grid: every head's slices on one XCD
-long long scan_grid(const DeltaArgs& a, int cols) { return ceil_div(static_cast<long long>(a.B) * a.HV, 8) * 8 * ceil_div(a.dv, cols); }
+long long scan_grid(const DeltaArgs& a, long long slices) {
+  return ceil_div(static_cast<long long>(a.B) * a.HV * a.nseg, 8) * 8 * slices;
+}
+template <class UT, int MODE, int DK, bool ADJ>
+int run_segments(const DeltaArgs& a, hipStream_t s) {
+  if (a.nseg == 1) return PARARNN_OK;
+  // Forward, bf16 and more than 64 columns: 8 waves, for which 168 registers are enough, read a chunk once for 128
+  // (B = 5 L = 1237 HV = 6: 34 -> 25 us; with 4 waves the matrix cores wait for each wave's chain)
+  if constexpr (!ADJ && sizeof(UT) == 2 && DK == 128) {
+    if (a.dv > 64)
+      return launch(delta_segment_kernel<UT, MODE, DK, 1, 8, false>, scan_grid(a, ceil_div(a.dv, 128) + 1),
+                    DeltaScan<UT, MODE, DK, 1, 8, false, true>::THREADS, s, a);
+  }
+  return launch(delta_segment_kernel<UT, MODE, DK, 1, 4, ADJ>, scan_grid(a, ceil_div(a.dv, 64) + ceil_div(a.dk, 64)),
+                DeltaScan<UT, MODE, DK, 1, 4, ADJ, true>::THREADS, s, a);
+}
 
 // Few heads: half as many columns to a workgroup, on twice as many CUs (128 workgroups of 64: 301 us as 272, 30: 71 as 68)
-bool narrow(const DeltaArgs& a) { return static_cast<long long>(a.B) * a.HV * ceil_div(a.dv, 64) <= kCUs / 2; }
+bool narrow(const DeltaArgs& a) { return static_cast<long long>(a.B) * a.HV * a.nseg * ceil_div(a.dv, 64) <= kCUs / 2; }
 
 struct DeltaForward {
   template <class UT, int MODE, int DK>
   static int run(const DeltaArgs& a, const float*, float*, float*, hipStream_t s) {
     if (const int rc = run_prep<UT, MODE != kOdd, DK, false>(a, s)) return rc;
-    return narrow(a) ? launch(delta_scan_kernel<UT, MODE, DK, 1, 2>, scan_grid(a, 32), DeltaScan<UT, MODE, DK, 1, 2, false>::THREADS, s, a)
-                     : launch(delta_scan_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), DeltaScan<UT, MODE, DK, 1, 4, false>::THREADS, s, a);
+    if (const int rc = run_segments<UT, MODE, DK, false>(a, s)) return rc;
+    return narrow(a) ? launch(delta_scan_kernel<UT, MODE, DK, 1, 2>, scan_grid(a, ceil_div(a.dv, 32)), DeltaScan<UT, MODE, DK, 1, 2, false>::THREADS, s, a)
+                     : launch(delta_scan_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, ceil_div(a.dv, 64)), DeltaScan<UT, MODE, DK, 1, 4, false>::THREADS, s, a);
   }
 };
 struct DeltaAdjoint {
@@ -110,8 +165,9 @@ struct DeltaAdjoint {
     if (const int rc = run_prep<UT, EVEN, DK, true>(a, s)) return rc;
     a.s0 = dsT;
     a.sT = ds0;
-    if (const int rc = narrow(a) ? launch(delta_back_kernel<UT, MODE, DK, 1, 2>, scan_grid(a, 32), DeltaScan<UT, MODE, DK, 1, 2, true>::THREADS, s, a)
-                                 : launch(delta_back_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, 64), DeltaScan<UT, MODE, DK, 1, 4, true>::THREADS, s, a))
+    if (const int rc = run_segments<UT, MODE, DK, true>(a, s)) return rc;
+    if (const int rc = narrow(a) ? launch(delta_back_kernel<UT, MODE, DK, 1, 2>, scan_grid(a, ceil_div(a.dv, 32)), DeltaScan<UT, MODE, DK, 1, 2, true>::THREADS, s, a)
+                                 : launch(delta_back_kernel<UT, MODE, DK, 1, 4>, scan_grid(a, ceil_div(a.dv, 64)), DeltaScan<UT, MODE, DK, 1, 4, true>::THREADS, s, a))
       return rc;
     const long long grid = static_cast<long long>(a.B) * a.H * a.nc;
     if (const int rc = a.H == a.HV ? launch(delta_grad_kernel<UT, EVEN, DK, false>, grid, 512, s, a)
@@ -291,7 +347,7 @@ extern "C" int32_t pararnn_delta_workspace_bytes(int32_t adjoint, const pararnn_
   if (!bytes || !delta_ok(o) || (adjoint != 0 && adjoint != 1)) return PARARNN_EINVAL;
   if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
   const DeltaSizes z = delta_sizes(o, adjoint);
-  *bytes = z.frags + z.rows + (adjoint ? z.states + z.ys + z.part : 0);
+  *bytes = delta_bytes(z, adjoint);
   return PARARNN_OK;
 }
 
@@ -316,15 +372,13 @@ extern "C" int32_t pararnn_delta_scan(const pararnn_view* q, const pararnn_view*
       !aligned(saved, kAlign))
     return PARARNN_EUNSUPPORTED;
   const DeltaSizes z = delta_sizes(opts, false);
-  if (ws_bytes < z.frags + z.rows) return PARARNN_EWORKSPACE;
+  if (ws_bytes < delta_bytes(z, false)) return PARARNN_EWORKSPACE;
   DeltaArgs a;
-  delta_fill(a, q, k, v, gates, lam, opts, es);
+  delta_fill(a, q, k, v, gates, lam, opts, false);
   a.s0 = s0;
   a.sT = sT;
   a.o = o;
-  char* w = static_cast<char*>(ws);
-  a.frags = reinterpret_cast<bf16x8*>(w);
-  a.rows = reinterpret_cast<float*>(w + z.frags);
+  delta_carve(a, ws, z);
   if (saved) {
     a.states = static_cast<f32x4*>(saved);
     a.ys = reinterpret_cast<f32x4*>(static_cast<char*>(saved) + z.states);
@@ -351,9 +405,9 @@ extern "C" int32_t pararnn_delta_scan_adjoint(const pararnn_view* q, const parar
       !aligned(ws, kAlign) || !aligned(saved, kAlign))
     return PARARNN_EUNSUPPORTED;
   const DeltaSizes z = delta_sizes(opts, true);
-  if (ws_bytes < z.frags + z.rows + z.states + z.ys + z.part) return PARARNN_EWORKSPACE;
+  if (ws_bytes < delta_bytes(z, true)) return PARARNN_EWORKSPACE;
   DeltaArgs a;
-  delta_fill(a, q, k, v, gates, lam, opts, es);
+  delta_fill(a, q, k, v, gates, lam, opts, true);
   a.gq = view(dq);
   a.gk = view(dk);
   a.gv = view(dv);
@@ -362,11 +416,7 @@ extern "C" int32_t pararnn_delta_scan_adjoint(const pararnn_view* q, const parar
   const pararnn_view ov = {d_o, static_cast<int64_t>(opts->L) * opts->HV * opts->dv, static_cast<int64_t>(opts->HV) * opts->dv};
   a.wide = rows_aligned(dv, es, opts->dv, 16, opts->B);
   a.wide_qk = opts->dk % 8 == 0 && rows_aligned(dq, es, opts->dk, 16, opts->B) && rows_aligned(dk, es, opts->dk, 16, opts->B);
-  char* w = static_cast<char*>(ws);
-  a.frags = reinterpret_cast<bf16x8*>(w);
-  w += z.frags;
-  a.rows = reinterpret_cast<float*>(w);
-  w += z.rows;
+  char* w = delta_carve(a, ws, z);
   a.dstates = reinterpret_cast<f32x4*>(w);
   w += z.states;
   a.dxs = reinterpret_cast<f32x4*>(w);

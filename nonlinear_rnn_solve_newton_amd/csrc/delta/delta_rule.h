@@ -58,7 +58,12 @@ struct DeltaArgs {
   f32x4* dstates;                // adjoint: dS behind each chunk
   f32x4* dxs;                    // adjoint: dX
   float* dlam_part;              // adjoint: [HV][B chunks]
+  // Of each segment, as the scans cross it: the state (adjoint: dS) that it puts out for none coming in, as result
+  // tiles, and the matrix [DK][DK] that takes what comes in to what it adds to that
+  f32x4* seg_add;
+  float* seg_map;
   int B, L, H, HV, dk, dv, nc;
+  int nseg, per;                 // segments, chunks of each
   float c, eps, scale;
   int wide, wide_qk;             // rows of bf16 o (adjoint: dV), and of dQ and dK, take 16-byte stores
 };
@@ -373,14 +378,16 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
 // What a chunk brings into workgroup memory for the scans; VC: columns of v
 // (dO) that the workgroup takes. Where the tensors are bf16, a wave leaves its
 // results in the place of its own columns of v, and they go out by whole rows
-// while the next chunk is worked on.
-template <class UT, int DK, int VC, bool ADJ>
+// while the next chunk is worked on. KONLY: neither q nor P.
+template <class UT, int DK, int VC, bool ADJ, bool KONLY>
 struct DeltaBuf {
   static constexpr int NP = DeltaPlanes<UT>::NP;
   typedef DeltaFrags<UT, ADJ> F;
-  DeltaTile<DK, NP> k, q;
+  static constexpr int FA = KONLY ? F::T : F::ALL;  // of the chunk's triangular operands
+  DeltaTile<DK, NP> k;
+  DeltaTile<KONLY ? 32 : DK, NP, KONLY ? 1 : 64> q;
   DeltaTile<VC, NP> v;
-  bf16x8 frags[F::ALL];
+  bf16x8 frags[FA];
   float rows[4 * 64];
 };
 
@@ -392,17 +399,24 @@ struct DeltaBuf {
 // write to workgroup memory (kDirect), four where they pass through registers;
 // fp32 needs the registers of two waves for one, and its waves load for
 // themselves.
-template <class UT, int MODE, int DK, int NC, int NW, bool ADJ>
+//
+// Few heads leave CUs idle, so a sequence is cut into segments. What a segment
+// makes of the state in front of it is affine: delta_segment_kernel (SEG) scans
+// all segments at once for the state that each adds, and with the columns of the
+// identity and no v for the matrix; the scans then start every segment from the
+// product over those before it.
+template <class UT, int MODE, int DK, int NC, int NW, bool ADJ, bool SEG = false>
 struct DeltaScan {
   static constexpr int NP = DeltaPlanes<UT>::NP, RT = DK / 16, KB = DK / 32, VC = 16 * NC * NW;
   static constexpr bool DIRECT = MODE == kDirect, INPLACE = sizeof(UT) == 2;
   static constexpr int NL = DIRECT ? 1 : INPLACE ? 4 : 0, THREADS = 64 * (NW + NL), NT = 64 * (NL ? NL : NW);
+  static constexpr bool SEGMENT = SEG, KONLY = SEG && !ADJ;
   typedef DeltaFrags<UT, ADJ> F;
-  typedef DeltaBuf<UT, DK, VC, ADJ> Buf;
+  typedef DeltaBuf<UT, DK, VC, ADJ, KONLY> Buf;
   static constexpr int NBUF = 2 * sizeof(Buf) <= 160 * 1024 ? 2 : 1;
   static_assert(NL == 0 || NBUF == 2, "a buffer to work on and one to fill");
   // rounds of the loading threads: chunks of q or k, of v, of the triangular operands, row factors
-  static constexpr int TP = 64 * DK / 8 / NT, CP = 64 * VC / 8 / NT, FP = (F::ALL + NT - 1) / NT, VP = 256 / NT;
+  static constexpr int TP = 64 * DK / 8 / NT, CP = 64 * VC / 8 / NT, FP = (Buf::FA + NT - 1) / NT, VP = 256 / NT;
   static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0 && 64 * VC / 8 % NT == 0 && F::ALL % 64 == 0, "whole rounds");
 
   // A tensor's rows of the chunk that is fetched next. Rows behind a row's last step lie past the resource's
@@ -422,8 +436,8 @@ struct DeltaScan {
   };
 
   const DeltaArgs& p;
-  int lane, w, m, g, b, hv, h, bh, wg0, col0, len, nch;
-  bool idle, loads;
+  int lane, w, m, g, b, hv, h, bh, wg0, col0, cols, len, seg, c0, nch;  // chunks c0 to c0 + nch - 1
+  bool idle, loads, last, ident;  // last: no chunks behind the segment's; ident: columns of the identity
   // of the loading threads
   int lt, dir, left;  // number, direction, steps of the chunk that is fetched next
   Source sk, sq, sv;
@@ -440,22 +454,32 @@ struct DeltaScan {
     w = __builtin_amdgcn_readfirstlane(tid >> 6);
     m = lane & 15;
     g = lane >> 4;
-    // the slices of a head follow each other on one XCD, whose L2 holds its chunk
-    const int nsl = (p.dv + VC - 1) / VC;
-    const int x = blockIdx.x % 8, l = blockIdx.x / 8;
-    bh = (l / nsl) * 8 + x;
-    idle = bh >= p.B * p.HV;
-    bh = idle ? 0 : bh;
+    // the slices of a segment follow each other on one XCD, whose L2 holds its chunk
+    const int nslv = (p.dv + VC - 1) / VC, nsl = SEG ? nslv + (p.dk + VC - 1) / VC : nslv;
+    const int x = blockIdx.x % 8, l = blockIdx.x / 8, unit = (l / nsl) * 8 + x;
+    idle = unit >= p.B * p.HV * p.nseg;
+    bh = unit % (p.B * p.HV);
+    seg = idle ? 0 : unit / (p.B * p.HV);
     b = bh / p.HV;
     hv = bh % p.HV;
     h = hv / (p.HV / p.H);
-    wg0 = (l % nsl) * VC;
+    ident = SEG && l % nsl >= nslv;
+    wg0 = (l % nsl - (ident ? nslv : 0)) * VC;
     col0 = wg0 / 16 + w * NC;
+    cols = ident ? p.dk : p.dv;
     len = delta_len(p, b);
-    nch = (len + kDeltaChunk - 1) / kDeltaChunk;
+    const int all = (len + kDeltaChunk - 1) / kDeltaChunk;
+    c0 = seg * p.per;
+    nch = max(min(all - c0, p.per), 0);
+    last = c0 + nch >= all;
+    idle = idle || (seg > 0 && nch == 0);  // the first segment takes rows without steps
+    if (SEG) {  // what nothing comes after or before in the scan's order
+      const bool end = ADJ ? seg == 0 : last, start = ADJ ? last : seg == 0;
+      idle = idle || end || (ident && start);
+    }
     loads = NL && w >= NW;
     lt = NL ? tid - 64 * NW : tid;
-    const int first = dir > 0 || nch == 0 ? 0 : nch - 1;
+    const int first = dir > 0 || nch == 0 ? c0 : c0 + nch - 1;
     left = len - first * kDeltaChunk;
     sk.set(p.k, b, static_cast<long long>(first) * kDeltaChunk, h * p.dk, p.H * p.dk, dir);
     sq.set(p.q, b, static_cast<long long>(first) * kDeltaChunk, h * p.dk, p.H * p.dk, dir);
@@ -481,13 +505,13 @@ struct DeltaScan {
   // the next chunk's loads
   __device__ __forceinline__ void fetch(Buf& to) {
     fetch_tile<DK, TP>(sk, 0, p.dk, to.k, rk);
-    fetch_tile<DK, TP>(sq, 0, p.dk, to.q, rq);
-    fetch_tile<VC, CP>(sv, wg0, p.dv, to.v, rv);
-    const __amdgpu_buffer_rsrc_t fr = make_rsrc(fp, F::ALL * 16);
+    if constexpr (!KONLY) fetch_tile<DK, TP>(sq, 0, p.dk, to.q, rq);
+    fetch_tile<VC, CP>(sv, wg0, ident ? 0 : p.dv, to.v, rv);
+    const __amdgpu_buffer_rsrc_t fr = make_rsrc(fp, Buf::FA * 16);
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
       if constexpr (DIRECT) {
-        if (NT * (i + 1) <= F::ALL || (lt & ~63) + NT * i < F::ALL) load_to_lds(fr, &to.frags[(lt & ~63) + NT * i], (lt + NT * i) * 16);
+        if (NT * (i + 1) <= Buf::FA || (lt & ~63) + NT * i < Buf::FA) load_to_lds(fr, &to.frags[(lt & ~63) + NT * i], (lt + NT * i) * 16);
       } else {
         rf[i] = __builtin_amdgcn_raw_buffer_load_b128(fr, (lt + NT * i) * 16, 0, 0);
       }
@@ -511,18 +535,18 @@ struct DeltaScan {
         to.k.put_slot(lt + NT * i, o);
       }
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
+      for (int i = 0; i < (KONLY ? 0 : TP); ++i) {
         planes_of(rq[i], p.dk - DeltaTile<DK, NP>::source(lt + NT * i), o);
         to.q.put_slot(lt + NT * i, o);
       }
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
-        planes_of(rv[i], p.dv - wg0 - DeltaTile<VC, NP>::source(lt + NT * i), o);
+        planes_of(rv[i], (ident ? 0 : p.dv) - wg0 - DeltaTile<VC, NP>::source(lt + NT * i), o);
         to.v.put_slot(lt + NT * i, o);
       }
 #pragma unroll
       for (int i = 0; i < FP; ++i)
-        if (NT * (i + 1) <= F::ALL || lt + NT * i < F::ALL) to.frags[lt + NT * i] = __builtin_bit_cast(bf16x8, rf[i]);
+        if (NT * (i + 1) <= Buf::FA || lt + NT * i < Buf::FA) to.frags[lt + NT * i] = __builtin_bit_cast(bf16x8, rf[i]);
     }
 #pragma unroll
     for (int i = 0; i < VP; ++i) to.rows[lt + NT * i] = rr[i];
@@ -605,6 +629,76 @@ struct DeltaScan {
           }
       }
   }
+  // What the segments in front of this one in the scan's order (ADJ: behind it) make of `start`
+  __device__ __forceinline__ void join(const float* start, f32x4 (&S)[NC][RT]) const {
+    const int nct = delta_tiles(p.dv), all = (len + kDeltaChunk - 1) / kDeltaChunk;
+    const int from = ADJ ? (all + p.per - 1) / p.per - 1 : 0;  // the one that starts from `start` itself
+    if (all == 0 || seg == from) {
+      load_state(start, S);
+      return;
+    }
+    for (int e = from; e != seg; e += ADJ ? -1 : 1) {
+      const long long unit = static_cast<long long>(bh) * p.nseg + e;
+      const float* map = p.seg_map + unit * (DK * DK);
+      f32x4 N[NC][RT];
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          N[cc][t] = col0 + cc < nct ? p.seg_add[((unit * nct + col0 + cc) * RT + t) * 64 + lane] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (e != from) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          bf16x8 sb[NC][3];
+#pragma unroll
+          for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc]);
+#pragma unroll
+          for (int t0 = 0; t0 < RT; t0 += 4) {
+            bf16x8 a[4][3];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const f32x4* r = reinterpret_cast<const f32x4*>(map + delta_label(t0 + t, m) * DK + 32 * kb + 8 * g);
+              split_tiles<3>(r[0], r[1], a[t]);
+            }
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+              f32x4(&c)[4] = *reinterpret_cast<f32x4(*)[4]>(&N[cc][t0]);
+              mma_rows<3, 3>(c, a, sb[cc]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) S[cc][t] = N[cc][t];
+    }
+  }
+  // SEG: the identity's columns, and what became of them or of the state's
+  __device__ __forceinline__ void identity(f32x4 (&S)[NC][RT]) const {
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = delta_label(t, 4 * g + r);
+          S[cc][t][r] = row == col(cc) && row < p.dk ? 1.0f : 0.0f;
+        }
+  }
+  __device__ __forceinline__ void store_segment(const f32x4 (&S)[NC][RT]) const {
+    const long long unit = static_cast<long long>(bh) * p.nseg + seg;
+    if (!ident) {
+      store_tiles<0, RT>(p.seg_add, unit, RT, S);
+      return;
+    }
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p.seg_map[unit * (DK * DK) + delta_label(t, 4 * g + r) * DK + col(cc)] = S[cc][t][r];
+  }
   // tiles [FROM, TO) of each of the wave's columns as they lie, n of them per column tile in memory
   template <int FROM, int TO, int N>
   __device__ __forceinline__ void store_tiles(f32x4* to, long long id, int n, const f32x4 (&Y)[NC][N]) const {
@@ -679,13 +773,13 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
   bf16x8 ka[2][4][NP], qa[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][NO], vv[NC][2][NP];
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
-  if (p.states) s.template store_tiles<0, RT>(p.states, id, delta_tiles(p.dk), S);
+  if (!D::KONLY && p.states) s.template store_tiles<0, RT>(p.states, id, delta_tiles(p.dk), S);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (kb + 1 < KB) u.k.rows(i, kb + 1, m, g, ka[(kb + 1) & 1][i]);
-      else u.q.rows(i, 0, m, g, qa[0][i]);
+      else if constexpr (!D::KONLY) u.q.rows(i, 0, m, g, qa[0][i]);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -700,10 +794,12 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
   f32x4 y[NC][4];
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
-    if (kb + 1 < KB) {
+    if (!D::KONLY && kb + 1 < KB) {
+      if constexpr (!D::KONLY) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u.q.rows(i, kb + 1, m, g, qa[(kb + 1) & 1][i]);
-    } else {
+        for (int i = 0; i < 4; ++i) u.q.rows(i, kb + 1, m, g, qa[(kb + 1) & 1][i]);
+      }
+    } else if (!D::KONLY || kb == 0) {
 #pragma unroll
       for (int j = 0; j < kTriBlocks; ++j)
 #pragma unroll
@@ -711,7 +807,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int cc = 0; cc < NC; ++cc) mma_rows<NP, NO>(qs[cc], qa[kb & 1], sb[cc][kb]);
+    for (int cc = 0; cc < (D::KONLY ? 0 : NC); ++cc) mma_rows<NP, NO>(qs[cc], qa[kb & 1], sb[cc][kb]);
     if (kb < 2) {  // beside q's products
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) {
@@ -733,10 +829,12 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int t = 0; t < RT; ++t) S[cc][t] *= whole;  // beside T's products
+  if constexpr (!D::KONLY) {
 #pragma unroll
-  for (int j = 0; j < kTriBlocks; ++j)
+    for (int j = 0; j < kTriBlocks; ++j)
 #pragma unroll
-    for (int pl = 0; pl < NO; ++pl) pa[j][pl] = u.frags[D::F::T + (j * NO + pl) * 64 + s.lane];
+      for (int pl = 0; pl < NO; ++pl) pa[j][pl] = u.frags[D::F::T + (j * NO + pl) * 64 + s.lane];
+  }
   constexpr int TG = 2;  // tiles of the state at a time
   bf16x8 yb[NC][2][3], kc[2][TG][2][NP];
 #pragma unroll
@@ -744,19 +842,20 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) u.k.columns(t, kb, m, g, kc[0][t][kb]);
   __builtin_amdgcn_sched_barrier(0);
-  if (p.ys) s.template store_tiles<0, 4>(p.ys, id, 4, y);
-  // the output
+  if constexpr (!D::KONLY) {  // the output
+    if (p.ys) s.template store_tiles<0, 4>(p.ys, id, 4, y);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f32x4 og = s.row4(u, kRowO, i);
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 og = s.row4(u, kRowO, i);
 #pragma unroll
-    for (int cc = 0; cc < NC; ++cc) qs[cc][i] *= og;
+      for (int cc = 0; cc < NC; ++cc) qs[cc][i] *= og;
+    }
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+    tri_rows<NO, NO, NC>(qs, pa, xb);
   }
-#pragma unroll
-  for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
-  tri_rows<NO, NO, NC>(qs, pa, xb);
   // the state
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc) {
@@ -780,7 +879,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][t], S[cc][t + 1], sb[cc][t / 2]);
   }
-  s.result(u, o, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), qs);
+  if constexpr (!D::KONLY) s.result(u, o, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), qs);
 }
 
 template <class UT, int MODE, int DK, int NC, int NW>
@@ -793,47 +892,49 @@ __global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, false>::THREA
   D s(p, p.v, 1);
   if (s.idle) return;
   const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  const int end = s.c0 + s.nch;
   if (s.nch > 0 && (s.loads || !D::NL)) {
-    s.fetch(buf[0]);
-    s.land(buf[0]);
+    s.fetch(buf[s.c0 & (D::NBUF - 1)]);
+    s.land(buf[s.c0 & (D::NBUF - 1)]);
   }
   __syncthreads();
   if (s.loads) {  // every barrier here has its fellow below
-    for (int ch = 0; ch < s.nch; ++ch) {
+    for (int ch = s.c0; ch < end; ++ch) {
       Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
-      if (ch > 0) s.send(next, o, (ch - 1) * kDeltaChunk, min(p.L - (ch - 1) * kDeltaChunk, kDeltaChunk));
-      if (ch + 1 < s.nch) {
+      if (ch > s.c0) s.send(next, o, (ch - 1) * kDeltaChunk, min(p.L - (ch - 1) * kDeltaChunk, kDeltaChunk));
+      if (ch + 1 < end) {
         s.fetch(next);
         s.land(next);
       }
       __syncthreads();
     }
-    if (s.nch > 0) s.send(buf[(s.nch - 1) & (D::NBUF - 1)], o, (s.nch - 1) * kDeltaChunk, min(p.L - (s.nch - 1) * kDeltaChunk, kDeltaChunk));
+    if (s.nch > 0) s.send(buf[(end - 1) & (D::NBUF - 1)], o, (end - 1) * kDeltaChunk, min(p.L - (end - 1) * kDeltaChunk, kDeltaChunk));
     return;
   }
   f32x4 S[NC][RT];
-  s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
+  s.join(p.s0 ? p.s0 + at_state : nullptr, S);
   bf16x8 sb[NC][KB][3];
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
-  for (int ch = 0; ch < s.nch; ++ch) {
+  for (int ch = s.c0; ch < end; ++ch) {
     Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
-    if (!D::NL && ch + 1 < s.nch) s.fetch(next);
+    if (!D::NL && ch + 1 < end) s.fetch(next);
     delta_scan_chunk<D, UT, DK, NC>(s, p, o, ch, buf[ch & (D::NBUF - 1)], S, sb);
     if constexpr (!D::NL) {
       __syncthreads();
-      if (ch + 1 < s.nch) s.land(next);
+      if (ch + 1 < end) s.land(next);
     }
     __syncthreads();
   }
+  if (!s.last) return;
   if (p.sT) s.store_state(p.sT + at_state, S);
   // rows behind the last chunk of the sequence
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
     if (s.col(cc) < p.dv)
-      for (long long t = static_cast<long long>(s.nch) * kDeltaChunk + s.g; t < p.L; t += 4)
+      for (long long t = static_cast<long long>(end) * kDeltaChunk + s.g; t < p.L; t += 4)
         store1(out_at<UT>(o, s.b, t) + static_cast<long long>(s.hv) * p.dv + s.col(cc), 0.0f);
 }
 
@@ -853,7 +954,7 @@ __device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p,
   bf16x8 ka[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][3], vb[NC][2][NP];
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
-  s.template store_tiles<0, RT>(p.dstates, id, delta_tiles(p.dk), S);
+  if constexpr (!D::SEGMENT) s.template store_tiles<0, RT>(p.dstates, id, delta_tiles(p.dk), S);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     if (kb + 1 < KB) {
@@ -917,8 +1018,10 @@ __device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p,
     for (int t = 0; t < RT; ++t) S[cc][t] *= whole;
   }
   __builtin_amdgcn_sched_barrier(0);
-  s.template store_tiles<0, 4>(p.dxs, id, 4, x);
-  s.result(u, p.gv, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), x);
+  if constexpr (!D::SEGMENT) {
+    s.template store_tiles<0, 4>(p.dxs, id, 4, x);
+    s.result(u, p.gv, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), x);
+  }
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc) {
 #pragma unroll
@@ -959,48 +1062,99 @@ __global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, true>::THREAD
   D s(p, o, -1);
   if (s.idle) return;
   const long long at_state = static_cast<long long>(s.bh) * p.dk * p.dv;
+  const int end = s.c0 + s.nch;
   if (s.nch > 0 && (s.loads || !D::NL)) {
-    s.fetch(buf[(s.nch - 1) & (D::NBUF - 1)]);
-    s.land(buf[(s.nch - 1) & (D::NBUF - 1)]);
+    s.fetch(buf[(end - 1) & (D::NBUF - 1)]);
+    s.land(buf[(end - 1) & (D::NBUF - 1)]);
   }
   __syncthreads();
   if (s.loads) {  // every barrier here has its fellow below
-    for (int ch = s.nch - 1; ch >= 0; --ch) {
+    for (int ch = end - 1; ch >= s.c0; --ch) {
       Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
-      if (ch + 1 < s.nch) s.send(next, p.gv, (ch + 1) * kDeltaChunk, min(p.L - (ch + 1) * kDeltaChunk, kDeltaChunk));
-      if (ch > 0) {
+      if (ch + 1 < end) s.send(next, p.gv, (ch + 1) * kDeltaChunk, min(p.L - (ch + 1) * kDeltaChunk, kDeltaChunk));
+      if (ch > s.c0) {
         s.fetch(next);
         s.land(next);
       }
       __syncthreads();
     }
-    if (s.nch > 0) s.send(buf[(0) & (D::NBUF - 1)], p.gv, (0) * kDeltaChunk, min(p.L - (0) * kDeltaChunk, kDeltaChunk));
+    if (s.nch > 0) s.send(buf[s.c0 & (D::NBUF - 1)], p.gv, s.c0 * kDeltaChunk, min(p.L - s.c0 * kDeltaChunk, kDeltaChunk));
     return;
   }
   f32x4 S[NC][RT];
-  s.load_state(p.s0 ? p.s0 + at_state : nullptr, S);
+  s.join(p.s0 ? p.s0 + at_state : nullptr, S);
   bf16x8 sb[NC][KB][3];
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
-  for (int ch = s.nch - 1; ch >= 0; --ch) {
+  for (int ch = end - 1; ch >= s.c0; --ch) {
     Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
-    if (!D::NL && ch > 0) s.fetch(next);
+    if (!D::NL && ch > s.c0) s.fetch(next);
     delta_back_chunk<D, UT, DK, NC>(s, p, o, ch, buf[ch & (D::NBUF - 1)], S, sb);
     if constexpr (!D::NL) {
       __syncthreads();
-      if (ch > 0) s.land(next);
+      if (ch > s.c0) s.land(next);
     }
     __syncthreads();
   }
-  if (p.sT) s.store_state(p.sT + at_state, S);
+  if (p.sT && s.seg == 0) s.store_state(p.sT + at_state, S);
+  if (!s.last) return;
   // rows behind the last chunk of the sequence
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc)
     if (s.col(cc) < p.dv)
-      for (long long t = static_cast<long long>(s.nch) * kDeltaChunk + s.g; t < p.L; t += 4)
+      for (long long t = static_cast<long long>(end) * kDeltaChunk + s.g; t < p.L; t += 4)
         store1(out_at<UT>(p.gv, s.b, t) + static_cast<long long>(s.hv) * p.dv + s.col(cc), 0.0f);
+}
+
+// What each segment makes of the state in front of it (ADJ: of dS behind it)
+template <class UT, int MODE, int DK, int NC, int NW, bool ADJ>
+__global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, ADJ, true>::THREADS)) delta_segment_kernel(const DeltaArgs p) {
+  typedef DeltaScan<UT, MODE, DK, NC, NW, ADJ, true> D;
+  typedef typename D::Buf Buf;
+  constexpr int RT = D::RT, KB = D::KB, DIR = ADJ ? -1 : 1;
+  __shared__ Buf buf[D::NBUF];
+  const DeltaView o = {p.o, static_cast<long long>(p.L) * p.HV * p.dv, static_cast<long long>(p.HV) * p.dv};
+  D s(p, ADJ ? o : p.v, DIR);
+  if (s.idle) return;  // else there are chunks
+  const int first = ADJ ? s.c0 + s.nch - 1 : s.c0, end = ADJ ? s.c0 - 1 : s.c0 + s.nch;
+  if (s.loads || !D::NL) {
+    s.fetch(buf[first & (D::NBUF - 1)]);
+    s.land(buf[first & (D::NBUF - 1)]);
+  }
+  __syncthreads();
+  if (s.loads) {  // every barrier here has its fellow below
+    for (int ch = first; ch != end; ch += DIR) {
+      Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
+      if (ch + DIR != end) {
+        s.fetch(next);
+        s.land(next);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  f32x4 S[NC][RT];
+  if (s.ident) s.identity(S);
+  else s.load_state(p.s0 && (ADJ ? s.last : s.seg == 0) ? p.s0 + static_cast<long long>(s.bh) * p.dk * p.dv : nullptr, S);
+  bf16x8 sb[NC][KB][3];
+#pragma unroll
+  for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) split_tiles<3>(S[cc][2 * kb], S[cc][2 * kb + 1], sb[cc][kb]);
+  for (int ch = first; ch != end; ch += DIR) {
+    Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
+    if (!D::NL && ch + DIR != end) s.fetch(next);
+    if constexpr (ADJ) delta_back_chunk<D, UT, DK, NC>(s, p, o, ch, buf[ch & (D::NBUF - 1)], S, sb);
+    else delta_scan_chunk<D, UT, DK, NC>(s, p, o, ch, buf[ch & (D::NBUF - 1)], S, sb);
+    if constexpr (!D::NL) {
+      __syncthreads();
+      if (ch + DIR != end) s.land(next);
+    }
+    __syncthreads();
+  }
+  s.store_segment(S);
 }
 
 // A workgroup per chunk and head of q and k: the gradients of q, k, v and the

@@ -233,6 +233,27 @@ def test_a_long_row_against_its_parts():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1100, 1, 2, 72, 100), (5, 1030, 1, 1, 128, 128), (3, 1024, 1, 2, 33, 21),
+                                   (1, 2500, 2, 2, 64, 64)], ids=str)
+def test_segments(shape, dtype):
+    """Few heads over many chunks: the sequence is scanned in segments, of rows that end
+    inside, at the edge and in front of them."""
+    say(f"delta segments {shape} {dtype}")
+    B, L, H, HV, dk, dv = shape
+    x = make(*shape, DT[dtype], seed=L, packed=B > 1, lam=-6.0)  # weak decay: what a segment adds is seen in the next
+    if B > 1:
+        x["lengths"] = torch.tensor([0, 256, 257, 1000, L][-B:], dtype=torch.int32)
+        x["reset"][-2:] = 0
+        x["reset"][-1, 700] = 1
+    want = reference(x)
+    d = cuda(x)
+    got = run(d)
+    check(got, want, DT[dtype], dk, dv, L)
+    for name, y in run(d).items():
+        assert torch.equal(y, got[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 8, 8), (3, 2, 4, 64, 64), (5, 1, 3, 72, 100), (2, 2, 2, 128, 128),
                                    (4, 1, 1, 127, 33), (2, 1, 1, 1, 1), (130, 1, 1, 16, 40)], ids=str)
 def test_step(shape, dtype):
