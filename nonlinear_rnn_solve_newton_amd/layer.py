@@ -182,6 +182,20 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple,
         raise PararnnError(f"{name} must be contiguous")
 
 
+def _like(t, name: str, dtype: torch.dtype, shape: tuple, device: torch.device):
+    """Checks an argument but for how it lies in memory."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device:
+        return
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PararnnError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise PararnnError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
 def _first(t, name: str, dims: int) -> torch.device:
     """The device of a call, from its first tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -485,17 +499,12 @@ def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Ten
 def _view(t, name: str, dtype, shape: tuple, device) -> View:
     """A tensor [B][L][...] (or [B][...] of a step) that is packed from its third
     (second) dimension on; its rows and tokens may lie further apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise PararnnError(f"{name} must be a device tensor")
-    if t.device != device:
-        raise PararnnError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _like(t, name, dtype, shape, device)
     lead = len(shape) - 2  # [B] or [B][L]
-    size, stride = t.shape, t.stride()
-    n = size[-1] * size[-2]
+    size, n = shape, shape[-1] * shape[-2]
+    if t.is_contiguous():
+        return View(t.data_ptr(), n * shape[1] if lead == 2 else n, n)
+    stride = t.stride()
     packed = (size[-1] == 1 or stride[-1] == 1) and (size[-2] == 1 or stride[-2] == size[-1])
     token = stride[1] if lead == 2 and size[1] > 1 else n
     batch = stride[0] if size[0] > 1 else token * (size[1] if lead == 2 else 1)
@@ -506,7 +515,7 @@ def _view(t, name: str, dtype, shape: tuple, device) -> View:
 
 def _delta_opts(q, k, v, gates, lam, c, eps, scale, lead, lengths=None, reset=None):
     """Options, views and device of a call; lead: dimensions in front of the heads."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (gates, "gates")):
+    for t, name in ((q, "q"), (v, "v")):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise PararnnError(f"{name} must be a device tensor")
         if t.dim() != lead + 2:
@@ -518,8 +527,9 @@ def _delta_opts(q, k, v, gates, lam, c, eps, scale, lead, lengths=None, reset=No
     HV, dv = v.shape[lead:]
     if 0 in q.shape or 0 in v.shape or HV % H:
         raise PararnnError("q, k and v must not be empty, and v's heads a multiple of q's")
-    views = tuple(_view(t, n, q.dtype, (*at, *s), dev) for t, n, s in (
-        (q, "q", (H, dk)), (k, "k", (H, dk)), (v, "v", (HV, dv)), (gates, "gates", (2, HV))))
+    dt, qk = q.dtype, (*at, H, dk)
+    views = (_view(q, "q", dt, qk, dev), _view(k, "k", dt, qk, dev), _view(v, "v", dt, (*at, HV, dv), dev),
+             _view(gates, "gates", dt, (*at, 2, HV), dev))
     _dev(lam, "lam", torch.float32, (HV,), dev)
     if lam is None:
         raise PararnnError("lam must be a device tensor")
@@ -637,14 +647,7 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.T
 
 def _rows_of(t, name: str, dtype, shape: tuple, device) -> int:
     """Checks [N][D] whose rows may lie apart; the elements from row to row."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise PararnnError(f"{name} must be a device tensor")
-    if t.device != device:
-        raise PararnnError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise PararnnError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _like(t, name, dtype, shape, device)
     N, D = shape
     row = t.stride(0) if N > 1 else D
     if (D > 1 and t.stride(1) != 1) or row < D:
