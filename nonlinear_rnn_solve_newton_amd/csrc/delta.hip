@@ -208,21 +208,26 @@ bool norm_block_ok(const pararnn_norm_block_opts* o) {
          static_cast<double>(o->N) * static_cast<double>(o->x_row) < 2.0e18;
 }
 
-// threads per row and vectors of 8 columns per thread; the adjoint, which holds four times the registers per
-// column, has one vector up to 8192 columns
+// Threads per row and vectors of 8 columns per thread: as few threads as have one vector each up to 2048 columns
+// (twice as many: 4999 x 1000 9.3 -> 12.4 us, 262144 x 128 45 -> 49 us), two above, since a workgroup's sum waits for
+// its last wave (4096 x 4096, 256 or 512 threads: 24 and 30 us; 4096 x 8192, 512 or 1024: 49 and 72). The adjoint,
+// which holds four times the registers per column, has one up to 4096 columns (256 threads with two there: 66 ->
+// 92 us), and above, with a residual (pre), whose three partial sums do not fit in 1024 threads' registers, two up
+// to 8192 (126 us, 1024 threads 150; without a residual 62 and 56).
 struct NormBlockShape {
   int tpr, nv;
 };
-NormBlockShape norm_block_shape(int D, bool adjoint) {
+NormBlockShape norm_block_shape(int D, bool adjoint, bool pre) {
   const int v = static_cast<int>(ceil_div(D, 8));
   for (int t : {16, 32, 64, 128, 256})
     if (v <= t) return {t, 1};
-  if (adjoint) return v <= 512 ? NormBlockShape{512, 1} : v <= 1024 ? NormBlockShape{1024, 1} : NormBlockShape{1024, 2};
+  if (adjoint && v <= 512) return {512, 1};
+  if (adjoint && !pre && v <= 1024) return {1024, 1};
   return v <= 512 ? NormBlockShape{256, 2} : v <= 1024 ? NormBlockShape{512, 2} : NormBlockShape{1024, 2};
 }
 // workgroups of the adjoint: each leaves a partial row of every parameter, so no more than fill the CUs
-long long norm_block_adjoint_grid(long long N, int D) {
-  const NormBlockShape k = norm_block_shape(D, true);
+long long norm_block_adjoint_grid(long long N, int D, bool pre) {
+  const NormBlockShape k = norm_block_shape(D, true, pre);
   const long long rounds = ceil_div(N, k.tpr < 256 ? 256 / k.tpr : 1), room = kCUs * (k.tpr <= 256 ? 4 : 1024 / k.tpr);
   return rounds <= room ? rounds : room;
 }
@@ -242,9 +247,9 @@ bool norm_block_group_ok(const pararnn_norm_block_opts* o, const NormBlockRows& 
   return r.D == o->group || (o->group % 8 == 0 && r.lanes <= 64 && (r.lanes & (r.lanes - 1)) == 0);
 }
 
-template <bool ADJ, class F>
+template <bool ADJ, bool PRE, class F>
 int norm_block_dispatch(int D, F go) {
-  const NormBlockShape k = norm_block_shape(D, ADJ);
+  const NormBlockShape k = norm_block_shape(D, ADJ, PRE);
 #define PARARNN_SHAPE(T, V) \
   if (k.tpr == T && k.nv == V) return go(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
   PARARNN_SHAPE(16, 1);
@@ -254,9 +259,12 @@ int norm_block_dispatch(int D, F go) {
   PARARNN_SHAPE(256, 1);
   if constexpr (ADJ) {
     PARARNN_SHAPE(512, 1);
-    PARARNN_SHAPE(1024, 1);
   } else {
     PARARNN_SHAPE(256, 2);
+  }
+  if constexpr (ADJ && !PRE) {
+    PARARNN_SHAPE(1024, 1);
+  } else {
     PARARNN_SHAPE(512, 2);
   }
 #undef PARARNN_SHAPE
@@ -264,7 +272,7 @@ int norm_block_dispatch(int D, F go) {
 }
 template <class XT, bool PRE, bool INT8, bool ALIGNED>
 int launch_norm_block(const NormBlockArgs& a, bool stream, hipStream_t s) {
-  return norm_block_dispatch<false>(a.D, [&](auto tpr, auto nv) {
+  return norm_block_dispatch<false, PRE>(a.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     long long grid = ceil_div(a.N, TPR < 256 ? 256 / TPR : 1);
     if (grid > 8192) grid = 8192;
@@ -275,7 +283,7 @@ int launch_norm_block(const NormBlockArgs& a, bool stream, hipStream_t s) {
 }
 template <class XT, bool PRE, bool ALIGNED>
 int launch_norm_block_adjoint(const NormBlockArgs& a, long long grid, bool stream, hipStream_t s) {
-  return norm_block_dispatch<true>(a.D, [&](auto tpr, auto nv) {
+  return norm_block_dispatch<true, PRE>(a.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     const int block = TPR < 256 ? 256 : TPR;
     if (ALIGNED && stream) return launch(norm_block_adjoint_kernel<XT, TPR, NV, PRE, ALIGNED, ALIGNED>, grid, block, s, a);
@@ -299,8 +307,9 @@ typedef MatmulShape<2, 2, 2, 2, 1> Int8Small;
 typedef MatmulShape<2, 2, 2, 2, 2> Int8Split2;
 typedef MatmulShape<2, 2, 2, 2, 4> Int8Split4;
 
-// Which large tile: 256 x 256 (4), 256 x 192 (3), or neither (0), by the rounds over the CUs, as in the 8-bit
-// floating-point product
+// Which large tile: 256 x 256 (4), 256 x 192 (3), or neither (0), by the rounds over the CUs and the steps of a
+// round (measured, 256 x 256, 256 x 192 and 128 x 128: 32768 x 16384 x 4096 1789, 1924, 2005 us; 6000 x 6000 x 3968
+// 158, 132, 140; 2048 x 4096 x 4096 51, 43, 33; 8192 x 5120 x 2048, where it misses the best by 6%, 94, 99, 89)
 int int8_large_tile(const Int8Args& p) {
   const long long tm = ceil_div(p.M, 256);
   const double kb = p.KB;
@@ -323,18 +332,24 @@ int launch_int8_few(const Int8Args& p, hipStream_t s) {
 template <bool F32OUT>
 int launch_int8_shape(const Int8Args& p, bool direct, hipStream_t s) {
   const long long n16 = ceil_div(p.N, 16);
+  // Up to 32 rows w goes from memory straight into registers, as wide a piece for each workgroup as leaves every CU
+  // one (16 x 16384 x 4096, 64, 32 or 16 columns: 12.7, 15.7, 17.8 us, in tiles 15.2; 16 x 4096: 10.9, 7.8, 6.0, 8.3;
+  // 64 rows, 2048 x 4096: 11.1, in tiles 8.4)
   if (direct && p.M <= 32) {
     if (n16 >= 3 * kCUs) return p.M <= 16 ? launch_int8_few<F32OUT, 1, 4, 1>(p, s) : launch_int8_few<F32OUT, 2, 4, 1>(p, s);
     if (n16 >= 2 * kCUs) return p.M <= 16 ? launch_int8_few<F32OUT, 1, 2, 2>(p, s) : launch_int8_few<F32OUT, 2, 2, 2>(p, s);
     return p.M <= 16 ? launch_int8_few<F32OUT, 1, 1, 4>(p, s) : launch_int8_few<F32OUT, 2, 1, 2>(p, s);
   }
-  if (direct && p.M <= 64 && n16 <= kCUs / 2) return launch_int8_few<F32OUT, 4, 1, 2>(p, s);
   const int tn = direct ? int8_large_tile(p) : 0;
   if (tn == 4) return launch(int8_large_kernel<4, F32OUT>, ceil_div(p.M, 256) * ceil_div(p.N, 256), 512, s, p);
   if (tn == 3) return launch(int8_large_kernel<3, F32OUT>, ceil_div(p.M, 256) * ceil_div(p.N, 192), 512, s, p);
+  // 128 x 128 tiles from one per CU on (2048 x 4096 x 4096: 33 us, 64 x 64 48; 1024 rows: 27 and 25)
   if (ceil_div(p.M, 128) * ceil_div(p.N, 128) >= kCUs) return launch_int8<Int8Mid, F32OUT>(p, direct, s);
-  if (ceil_div(p.M, 64) * ceil_div(p.N, 64) <= kCUs && p.KB >= 4)
-    return direct ? launch_int8<Int8Split4, F32OUT>(p, true, s) : launch_int8<Int8Split2, F32OUT>(p, false, s);
+  // few tiles: K dealt out to groups of waves (256 x 4096 x 4096, one, two or four: 12.4, 10.3, 10.0 us; 512 rows:
+  // 16.8, 15.3, 20.3; 1024: 25, 28, 39; 300 x 1000 x 512: 4.0, 4.1, 4.5)
+  const long long tiles = ceil_div(p.M, 64) * ceil_div(p.N, 64);
+  if (direct && tiles <= kCUs && p.KB >= 8) return launch_int8<Int8Split4, F32OUT>(p, true, s);
+  if (tiles <= 2 * kCUs && p.KB >= 8) return launch_int8<Int8Split2, F32OUT>(p, direct, s);
   return launch_int8<Int8Small, F32OUT>(p, direct, s);
 }
 
@@ -524,7 +539,7 @@ extern "C" int32_t pararnn_norm_block(const void* x, const void* gate, const voi
 extern "C" int32_t pararnn_norm_block_workspace_bytes(const pararnn_norm_block_opts* o, int32_t residual, size_t* bytes) {
   if (!norm_block_ok(o) || !bytes) return PARARNN_EINVAL;
   const NormBlockRows r = norm_block_rows(o, residual != 0, false);
-  *bytes = round_up(sizeof(float) * static_cast<size_t>(norm_block_adjoint_grid(r.N, r.D)) * (residual ? 3 : 1) * r.D);
+  *bytes = round_up(sizeof(float) * static_cast<size_t>(norm_block_adjoint_grid(r.N, r.D, residual)) * (residual ? 3 : 1) * r.D);
   return PARARNN_OK;
 }
 
@@ -548,7 +563,7 @@ extern "C" int32_t pararnn_norm_block_adjoint(const void* x, const void* gate, c
     if (!aligned(p, 4)) return PARARNN_EUNSUPPORTED;
   const NormBlockRows r = norm_block_rows(o, s != nullptr, false);
   if (w && !norm_block_group_ok(o, r)) return PARARNN_EUNSUPPORTED;
-  const long long grid = norm_block_adjoint_grid(r.N, r.D);
+  const long long grid = norm_block_adjoint_grid(r.N, r.D, s != nullptr);
   const int parts = s ? 3 : 1;
   if (sums && ws_bytes < sizeof(float) * static_cast<size_t>(grid) * parts * r.D) return PARARNN_EWORKSPACE;
   if (sums && !aligned(ws, kAlign)) return PARARNN_EUNSUPPORTED;

@@ -303,14 +303,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_block_adjoint_kern
   __shared__ float fold[RW > 1 ? RW : 1][RW > 1 ? TPR * NV * 8 : 1];
   const int tid = threadIdx.x, t = tid % TPR, rw = tid / TPR;
   const float inv_g = 1.0f / static_cast<float>(p.lanes ? p.G : p.D), inv_d = 1.0f / static_cast<float>(p.D);
-  float wv[NV][8], al[PRE ? NV : 1][8], wn[PRE ? NV : 1][8], part[NP][NV][8];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
+  // The parameters are held over the rows, or, where a thread has 16 columns or 128 registers, read anew for every
+  // row (4096 x 8192 with a residual, 512 threads: 126 us, held 241; 4096 x 4096, one vector: 71, held 66)
+  constexpr bool HOLD = TPR * NV <= 512;
+  constexpr int NH = HOLD ? NV : 1;
+  const float *pw = p.w, *pa = p.alpha, *pn = p.w_next;
+  float wv[NH][8], al[PRE ? NH : 1][8], wn[PRE ? NH : 1][8], part[NP][NV][8];
+  auto load_w = [&](int k, float (&v)[8]) {
     const int d = 8 * (t + TPR * k);
-    load_param<ALIGNED>(p.w, p.lanes ? d % p.G : d, p.lanes ? p.G : p.D, wv[k]);
-    if constexpr (PRE) {
-      load_param<ALIGNED>(p.alpha, d, p.D, al[k]);
-      load_param<ALIGNED>(p.w_next, d, p.D, wn[k]);
+    load_param<ALIGNED>(pw, p.lanes ? d % p.G : d, p.lanes ? p.G : p.D, v);
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      load_w(k, wv[k]);
+      if constexpr (PRE) {
+        load_param<ALIGNED>(pa, 8 * (t + TPR * k), p.D, al[k]);
+        load_param<ALIGNED>(pn, 8 * (t + TPR * k), p.D, wn[k]);
+      }
     }
   }
 #pragma unroll
@@ -322,6 +332,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_block_adjoint_kern
   for (long long row0 = static_cast<long long>(blockIdx.x) * RW; row0 < p.N; row0 += static_cast<long long>(gridDim.x) * RW) {
     const bool on = row0 + rw < p.N;
     const long long row = on ? row0 + rw : 0, out = row * p.D;
+    if constexpr (!HOLD) __asm__ volatile("" : "+s"(pw), "+s"(pa), "+s"(pn));  // not before the loop
     V x[NV], z[NV], s[NV], dy[NV], ds[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -347,10 +358,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_block_adjoint_kern
       }
       sum[0] += q[0];
       if constexpr (PRE) {
+        if constexpr (!HOLD) load_param<ALIGNED>(pn, 8 * (t + TPR * k), p.D, wn[0]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float r = s[k].at(i);
-          u[k][i] = dy[k].at(i) * wn[k][i];
+          u[k][i] = dy[k].at(i) * wn[HOLD ? k : 0][i];
           sum[1] = fmaf(r, r, sum[1]);
           sum[2] = fmaf(u[k][i], r, sum[2]);
         }
@@ -384,9 +396,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_block_adjoint_kern
         }
       }
       float q = 0.0f;
+      if constexpr (!HOLD) {
+        load_w(k, wv[0]);
+        if constexpr (PRE) load_param<ALIGNED>(pa, d, p.D, al[0]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float xh = x[k].at(i) * rstd[k], n = xh * wv[k][i];
+        const float xh = x[k].at(i) * rstd[k], n = xh * wv[HOLD ? k : 0][i];
         float c = 1.0f, dc = 0.0f;
         if (p.gate) {
           const float zi = z[k].at(i), sz = sigm(zi);
@@ -395,12 +411,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_block_adjoint_kern
         }
         if constexpr (PRE) {
           if (on) part[1][k][i] = fmaf(u[k][i], n * c, part[1][k][i]);
-          u[k][i] *= al[k][i];
+          u[k][i] *= al[HOLD ? k : 0][i];
         }
         g[i] = u[k][i] * n * dc;
         const float v = u[k][i] * c;
         if (on) part[0][k][i] = fmaf(v, xh, part[0][k][i]);
-        u[k][i] = v * wv[k][i];
+        u[k][i] = v * wv[HOLD ? k : 0][i];
         q = fmaf(u[k][i], xh, q);
       }
       if (p.gate && on) {
