@@ -35,7 +35,8 @@ extern "C" {
  * product are taken as they lie. Rows and tokens do not overlap. */
 typedef struct {
   const void* p;
-  int64_t batch, token; /* elements; token >= the packed size, batch >= L token (or B = 1) */
+  int64_t batch, token; /* elements; token from the packed size to 2^22, batch from (L - 1) token + the packed size
+                           to 2^50 (or B = 1) */
 } pararnn_view;
 
 typedef struct {

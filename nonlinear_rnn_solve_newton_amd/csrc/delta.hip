@@ -29,7 +29,9 @@ bool delta_ok(const pararnn_delta_opts* o) {
          o->dk <= kMaxDk && o->dv >= 1 && o->dv <= kMaxDv && o->c > 0.0f && isfinite(o->c) && o->eps > 0.0f &&
          isfinite(o->eps) && isfinite(o->scale) && o->L <= 2147483647 - kDeltaChunk &&
          static_cast<long long>(o->B) * o->HV <= 2147483647LL &&
-         static_cast<long long>(o->B) * o->HV * ceil_div(o->L, kDeltaChunk) <= kMaxThreads / 512;
+         // the largest launches: a chunk of all heads at once, and a scan's slices of all heads
+         static_cast<long long>(o->B) * o->HV * ceil_div(o->L, kDeltaChunk) <= kMaxThreads / 512 &&
+         (static_cast<long long>(o->B) * o->HV + 7) * ceil_div(o->dv, 64) <= kMaxThreads / 512;
 }
 
 // sizes of a call's pieces, in bytes (chunks of all value heads)
