@@ -48,7 +48,8 @@ typedef struct {
   const int32_t* lengths;   /* [B] (device) steps of each row, clamped to 0..L; NULL = L. Later steps leave the
                                state alone and put out zeros, whatever the inputs hold there */
   const uint8_t* reset;     /* [B][L] (device) nonzero: a document starts at this step, S_{t-1} counts as zero;
-                               NULL = none */
+                               NULL = none. (An infinity or a NaN among a row's steps reaches the steps after it,
+                               over a start too.) */
 } pararnn_delta_opts;
 
 /* Workspace of pararnn_delta_scan (adjoint = 0) or _adjoint (adjoint = 1), and

@@ -35,7 +35,9 @@ __device__ __forceinline__ void scaled(const i32x4& c, float sa, const float (&s
 
 // Between the few rows and the large tiles, and unaligned operands: BN x BM of
 // y per workgroup, two buffers, as in Matmul; KS groups of waves take every
-// KS-th block of K and their sums are joined (integers: in any order).
+// KS-th block of K and their sums are joined (integers: in any order). The latency
+// of the blocks bounds them: 777 x 1000 x 1333, whose rows no wide load can take, 13 us,
+// 777 x 1000 x 1344 6.0.
 template <class S, bool F32OUT, bool DIRECT>
 __global__ void __launch_bounds__(S::NT * S::KS) int8_kernel(const Int8Args p) {
   constexpr int BN = S::BN, BM = S::BM, NT = S::NT, TN = S::TN, TM = S::TM, KS = S::KS;
@@ -187,7 +189,9 @@ __global__ void __launch_bounds__(S::NT * S::KS) int8_kernel(const Int8Args p) {
 // Large products: 256 rows by 64 TN columns of y by 8 waves (4 along n, 2 along
 // m), in the half steps of MatmulLarge: after the first half of a block nobody
 // needs its w and first a rows any more, and the block after the next takes
-// their place, so that every load has a step and a half to arrive.
+// their place, so that every load has a step and a half to arrive. The matrix
+// instructions bound it: 32768 x 16384 x 4096 in 1.79 ms, 2460 TOP/s (2030 on a warm
+// card; the same product of 8-bit floating-point numbers 2290 to 2390 TFLOP/s).
 template <int TN, bool F32OUT>
 struct Int8Large {
   static constexpr int BN = 64 * TN, BM = 256, NT = 512, TM = 8, WC = 16 * TN;
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(512) int8_large_kernel(const Int8Args p) {
 // workgroup of 8 waves takes 16 NT columns of y; its waves take the 128-blocks
 // of K in turn, straight from HBM into registers (nothing of w is used twice),
 // UN blocks in flight per wave, and their sums are joined through workgroup
-// memory.
+// memory. 16 x 16384 x 4096: 12.7 us, 5.3 TB/s of w.
 template <bool F32OUT, int MT, int NT, int UN>
 __global__ void __launch_bounds__(512) int8_few_kernel(const Int8Args p) {
   constexpr int W = 8;
