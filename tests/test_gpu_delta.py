@@ -234,7 +234,7 @@ def test_a_long_row_against_its_parts():
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 1100, 1, 2, 72, 100), (5, 1030, 1, 1, 128, 128), (3, 1024, 1, 2, 33, 21),
-                                   (1, 2500, 2, 2, 64, 64)], ids=str)
+                                   (1, 2500, 2, 2, 64, 64), (1, 1090, 1, 1, 65, 512), (2, 1024, 1, 1, 128, 130)], ids=str)
 def test_segments(shape, dtype):
     """Few heads over many chunks: the sequence is scanned in segments, of rows that end
     inside, at the edge and in front of them."""
@@ -329,6 +329,27 @@ def test_another_stream_and_a_replayed_graph():
         after = pool.clone()
         pool.copy_(y["s0"])
         assert torch.equal(step(), o) and torch.equal(pool, after)
+
+
+def test_replayed_segments():
+    """The scans of few heads over many chunks, captured: a call's launches wait for
+    each other in the graph as on the stream."""
+    say("delta graph of segments")
+    x = cuda(make(1, 1100, 1, 2, 64, 64, torch.bfloat16, lam=-6.0))
+    run(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = run(x)
+    for seed in (3, 4, 5):
+        y = cuda(make(1, 1100, 1, 2, 64, 64, torch.bfloat16, seed=seed, lam=-6.0))
+        for n in x:
+            if x[n] is not None:
+                x[n].copy_(y[n])
+        g.replay()
+        torch.cuda.synchronize()
+        eager = run(x)
+        for n in eager:
+            assert torch.equal(r[n], eager[n]), (seed, n)
 
 
 def test_refusals():
