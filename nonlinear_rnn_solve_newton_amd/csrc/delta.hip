@@ -526,8 +526,9 @@ extern "C" int32_t pararnn_norm_block(const void* x, const void* gate, const voi
   hipStream_t st = static_cast<hipStream_t>(stream_);
   const bool ok = norm_block_aligned(r, es, {x, gate, residual, s, y, w, alpha, w_next},
                                      {o->x_row, gate ? o->gate_row : 0, residual ? o->residual_row : 0});
-  // past the caches where the tensors together are larger than the last-level one
-  const bool far = static_cast<double>(o->N) * o->D * es * (2 + (gate != nullptr) + 2 * (residual != nullptr)) >= 256.0 * 1024 * 1024;
+  // past the caches where the tensors together are larger than the last-level one (2048 columns, 256 MB: 46 us,
+  // through them 41; 512 MB: 91 and 99)
+  const bool far = static_cast<double>(o->N) * o->D * es * (2 + (gate != nullptr) + 2 * (residual != nullptr)) > 256.0 * 1024 * 1024;
   auto go = [&](auto xt, auto aligned_) {
     typedef decltype(xt) XT;
     constexpr bool AL = decltype(aligned_)::value;
@@ -630,6 +631,8 @@ extern "C" int32_t pararnn_matmul_int8(const void* a, const float* sa, const voi
   p.K = o->K;
   p.KB = static_cast<int>(ceil_div(o->K, 128));
   p.vec = !f32 && o->N % 8 == 0 && o->N <= (1 << 22) && aligned(y, 16) ? 8 : o->N % 4 == 0 && aligned(y, f32 ? 16 : 8) ? 4 : 1;
+  // y past the caches where it is larger than the last one (16384 x 8192, K = 1024, 256 MB: 177 us, through them
+  // 165; 16384 x 16384: 308 and 387)
   p.stream = 2.0 * p.M * p.N > 256.0 * 1024 * 1024;
   const bool direct = o->K % 16 == 0 && aligned(a, 16) && aligned(w, 16);
   hipStream_t s = static_cast<hipStream_t>(stream_);
