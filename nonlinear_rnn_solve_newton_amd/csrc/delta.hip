@@ -39,18 +39,21 @@ struct DeltaSizes {
   size_t frags, rows, states, ys, part, seg_add, seg_map;
 };
 // Segments that the scans cut a sequence into, and chunks of each: as many as give every CU a workgroup, and no
-// more than sqrt(1.6 chunks), where a segment's scan (1.6 times its chunks) takes as long as the product over the
-// others' maps (a chunk's time each). The segments' scan before the scans pays from three of them on (bf16, B = 5
-// L = 4096 H = 8, three: 210 -> 188 us; two, B = 8: 234 -> 272), in the adjoint, which both scans are less of, from
-// four on (three: 570 -> 584 us; B = 1 L = 4096 H = 32, four: 507 -> 500), and in bf16, whose chunks are passed in a
-// third of fp32's time, from 16 chunks on (H = 8, 9 chunks: 37 -> 44 us, 16: 55 -> 56, 32 and B = 4: 106 -> 99;
-// fp32, 6 chunks: 49 -> 38, 16: 106 -> 58). B = 1 L = 65536 H = 16: 2815 -> 1082 us.
+// more than make the product over the others' maps as long as the scan of the own chunks. A map takes as long as
+// two chunks in bf16 and half a chunk in fp32: sqrt(0.8 chunks) and sqrt(4.5 chunks) (forward with factors 0.8, 1.6
+// and 4.5: B = 1 L = 65536 H = 2 128 wide bf16 424, 514, 673 us, L = 1024 H = 1 64 wide fp32 71, 58, 47). The
+// segments' scan before the scans pays from three of them on (bf16, B = 5 L = 4096 H = 8, three: 210 -> 188 us; two,
+// B = 8: 234 -> 272), in the adjoint, which both scans are less of, from four on (three: 570 -> 584 us; B = 1 L =
+// 4096 H = 32, four: 507 -> 500), and in bf16, whose chunks are passed in a third of fp32's time, from 16 chunks on
+// (H = 8, 9 chunks: 37 -> 44 us, 16: 55 -> 56, 32 and B = 4: 106 -> 99; fp32, 6 chunks: 49 -> 38). B = 1 L = 65536
+// H = 16: 2815 -> 1082 us.
 struct DeltaSegments {
   int n, per;
 };
 DeltaSegments delta_segments(const pararnn_delta_opts* o, bool adj) {
   const long long nc = ceil_div(o->L, kDeltaChunk), groups = static_cast<long long>(o->B) * o->HV * ceil_div(o->dv, 64);
-  const long long most = static_cast<long long>(sqrt(1.6 * static_cast<double>(nc))), room = kCUs / groups;
+  const double share = o->dtype == PARARNN_BF16 ? 0.8 : 4.5;
+  const long long most = static_cast<long long>(sqrt(share * static_cast<double>(nc))), room = kCUs / groups;
   const long long n = room < most ? room : most;
   if (n < (adj ? 4 : 3) || (o->dtype == PARARNN_BF16 && nc < 16)) return {1, static_cast<int>(nc)};
   const int per = static_cast<int>(ceil_div(nc, n));
