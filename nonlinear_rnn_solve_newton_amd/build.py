@@ -7,6 +7,7 @@ flag goes to the device pass only, where it exists.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -58,10 +59,15 @@ def build_one(src: Path, out: Path, verbose: bool = False, extra_flags=(), host_
 
 
 def build(verbose: bool = False, extra_flags=()) -> Path:
-    build_one(CSRC / "ceilings.hip", CEIL_LIB, verbose, extra_flags)
-    build_one(CSRC / "layer.hip", LAYER_LIB, verbose, extra_flags)
-    build_one(CSRC / "delta.hip", DELTA_LIB, verbose, extra_flags, device_flags=DELTA_FLAGS)
-    return build_one(CSRC / "pararnn.hip", LIB, verbose, extra_flags)
+    """Compiles every library, side by side."""
+    jobs = [(CSRC / "delta.hip", DELTA_LIB, DELTA_FLAGS), (CSRC / "pararnn.hip", LIB, ()),
+            (CSRC / "layer.hip", LAYER_LIB, ()), (CSRC / "ceilings.hip", CEIL_LIB, ())]
+    with concurrent.futures.ThreadPoolExecutor(len(jobs)) as pool:
+        done = [pool.submit(build_one, src, out, verbose, extra_flags, device_flags=flags) for src, out, flags in jobs]
+        for d in done:
+            d.result()
+    return LIB
+
 
 
 if __name__ == "__main__":
