@@ -64,7 +64,8 @@ DeltaSizes delta_sizes(const pararnn_delta_opts* o, bool adj) {
   const size_t frag = o->dtype == PARARNN_BF16
                           ? (adj ? DeltaFrags<bf16, true>::ALL : DeltaFrags<bf16, false>::ALL)
                           : (adj ? DeltaFrags<float, true>::ALL : DeltaFrags<float, false>::ALL);
-  const int DK = o->dk <= 64 ? 64 : 128, n = delta_segments(o, adj).n;
+  // the forward pass's segments, which are the adjoint's or more: a workspace of the adjoint serves both
+  const int DK = o->dk <= 64 ? 64 : 128, n = delta_segments(o, false).n;
   const size_t segs = n > 1 ? static_cast<size_t>(o->B) * o->HV * n : 0;
   return {round_up(chunks * frag * sizeof(bf16x8)), round_up(chunks * kRows * 64 * sizeof(float)),
           chunks * delta_tiles(o->dv) * delta_tiles(o->dk) * 1024, chunks * delta_tiles(o->dv) * 4096,
