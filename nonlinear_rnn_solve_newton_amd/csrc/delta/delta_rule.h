@@ -1538,6 +1538,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
       spart[f][m >> 2][16 * w + 4 * g + (m & 3)] = v[0];
       if ((m & 3) == 0) spart[f][4][16 * w + 4 * g + (m >> 2)] = u[0];
     }
+    __syncthreads();  // W has both halves' part: its rows are summed by other waves than those that added to it
     // sums of W over j < t <= i: a wave takes 8 t, a lane a column j
     {
       float v = 0.0f;
