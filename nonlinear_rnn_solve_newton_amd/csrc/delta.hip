@@ -59,15 +59,12 @@ DeltaSegments delta_segments(const pararnn_delta_opts* o, bool adj) {
   const int per = static_cast<int>(ceil_div(nc, n));
   return {static_cast<int>(ceil_div(nc, per)), per};
 }
-DeltaSizes delta_sizes(const pararnn_delta_opts* o, bool adj) {
+DeltaSizes delta_sizes(const pararnn_delta_opts* o) {
   const size_t chunks = static_cast<size_t>(o->B) * o->HV * ceil_div(o->L, kDeltaChunk);
-  const size_t frag = o->dtype == PARARNN_BF16
-                          ? (adj ? DeltaFrags<bf16, true>::ALL : DeltaFrags<bf16, false>::ALL)
-                          : (adj ? DeltaFrags<float, true>::ALL : DeltaFrags<float, false>::ALL);
   // the forward pass's segments, which are the adjoint's or more: a workspace of the adjoint serves both
   const int DK = o->dk <= 64 ? 64 : 128, n = delta_segments(o, false).n;
   const size_t segs = n > 1 ? static_cast<size_t>(o->B) * o->HV * n : 0;
-  return {round_up(chunks * frag * sizeof(bf16x8)), round_up(chunks * kRows * 64 * sizeof(float)),
+  return {round_up(chunks * DeltaFrags::ALL * sizeof(bf16x8)), round_up(chunks * kRows * 64 * sizeof(float)),
           chunks * delta_tiles(o->dv) * delta_tiles(o->dk) * 1024, chunks * delta_tiles(o->dv) * 4096,
           round_up(chunks * sizeof(float)), segs * delta_tiles(o->dv) * (DK / 16) * 1024, segs * DK * DK * 4};
 }
@@ -367,7 +364,7 @@ using namespace pararnn;
 extern "C" int32_t pararnn_delta_workspace_bytes(int32_t adjoint, const pararnn_delta_opts* o, size_t* bytes) {
   if (!bytes || !delta_ok(o) || (adjoint != 0 && adjoint != 1)) return PARARNN_EINVAL;
   if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
-  const DeltaSizes z = delta_sizes(o, adjoint);
+  const DeltaSizes z = delta_sizes(o);
   *bytes = delta_bytes(z, adjoint);
   return PARARNN_OK;
 }
@@ -375,7 +372,7 @@ extern "C" int32_t pararnn_delta_workspace_bytes(int32_t adjoint, const pararnn_
 extern "C" int32_t pararnn_delta_saved_bytes(const pararnn_delta_opts* o, size_t* bytes) {
   if (!bytes || !delta_ok(o)) return PARARNN_EINVAL;
   if (!dtype_ok(o->dtype)) return PARARNN_EUNSUPPORTED;
-  const DeltaSizes z = delta_sizes(o, false);
+  const DeltaSizes z = delta_sizes(o);
   *bytes = z.states + z.ys;
   return PARARNN_OK;
 }
@@ -392,7 +389,7 @@ extern "C" int32_t pararnn_delta_scan(const pararnn_view* q, const pararnn_view*
   if (!aligned(lam, 4) || !aligned(s0, 4) || !aligned(sT, 4) || !aligned(opts->lengths, 4) || !aligned(ws, kAlign) ||
       !aligned(saved, kAlign))
     return PARARNN_EUNSUPPORTED;
-  const DeltaSizes z = delta_sizes(opts, false);
+  const DeltaSizes z = delta_sizes(opts);
   if (ws_bytes < delta_bytes(z, false)) return PARARNN_EWORKSPACE;
   DeltaArgs a;
   delta_fill(a, q, k, v, gates, lam, opts, false);
@@ -425,7 +422,7 @@ extern "C" int32_t pararnn_delta_scan_adjoint(const pararnn_view* q, const parar
   if (!aligned(lam, 4) || !aligned(dsT, 4) || !aligned(ds0, 4) || !aligned(dlam, 4) || !aligned(opts->lengths, 4) ||
       !aligned(ws, kAlign) || !aligned(saved, kAlign))
     return PARARNN_EUNSUPPORTED;
-  const DeltaSizes z = delta_sizes(opts, true);
+  const DeltaSizes z = delta_sizes(opts);
   if (ws_bytes < delta_bytes(z, true)) return PARARNN_EWORKSPACE;
   DeltaArgs a;
   delta_fill(a, q, k, v, gates, lam, opts, true);

@@ -77,11 +77,9 @@ enum { kRowX = 0, kRowO = 1, kRowS = 2, kRowWhole = 3, kRowK = 4, kRowQ = 5, kRo
 constexpr int kTriBlocks = 6;
 __host__ __device__ constexpr int low_block(int i, int kb) { return i < 2 ? i : 2 + 2 * (i - 2) + kb; }
 __host__ __device__ constexpr int up_block(int j, int kb) { return j < 2 ? 2 * j + kb : 4 + (j - 2); }
-// planes per chunk: T, then P
-template <class UT, bool ADJ>
+// operands per chunk, three planes of each: T's blocks, then P's
 struct DeltaFrags {
-  static constexpr int NT = 3, NP = ADJ ? 3 : DeltaPlanes<UT>::NO;
-  static constexpr int T = kTriBlocks * NT * 64, P = kTriBlocks * NP * 64, ALL = T + P;
+  static constexpr int T = kTriBlocks * 3 * 64, ALL = 2 * T;
 };
 
 // tiles of 16 that n rows or columns take, in pairs
@@ -171,7 +169,6 @@ __device__ __forceinline__ void invert16(const float* a, int m, float (&x)[16]) 
 // memory 111 us); the adjoint's 92 us, 318 MB.
 template <class UT, bool EVEN, int DK, bool ADJ>
 __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kernel(const DeltaArgs p) {
-  typedef DeltaFrags<UT, ADJ> F;
   constexpr int NP = DeltaPlanes<UT>::NP, KB = DK / 32, ROW = 68;
   __shared__ float sm[64 * ROW], st[64 * ROW];
   __shared__ float sg[64], sb[64], sseg[64], srk[64], srq[64];
@@ -270,7 +267,7 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
   }
   __syncthreads();
   constexpr float kLog2e = 1.4426950408889634f;
-  bf16x8* const out = p.frags + (static_cast<long long>(bh) * p.nc + ch) * F::ALL;
+  bf16x8* const out = p.frags + (static_cast<long long>(bh) * p.nc + ch) * DeltaFrags::ALL;
   {
     // element (row i, column j) of both: E_ij with the lengths, b_j and the scale. The lane's own index is the
     // row i (ADJ: the column j), and it has 4 of the other.
@@ -312,10 +309,10 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     for (int kb = 0; kb < 2; ++kb)
       if (ADJ ? kb >= w / 2 : kb <= w / 2) {
         bf16x8 o[3];
-        split_tiles<F::NP>(qk[2 * kb], qk[2 * kb + 1], o);
+        split_tiles<3>(qk[2 * kb], qk[2 * kb + 1], o);
         const int id = ADJ ? up_block(w, kb) : low_block(w, kb);
 #pragma unroll
-        for (int pl = 0; pl < F::NP; ++pl) out[F::T + (id * F::NP + pl) * 64 + lane] = o[pl];
+        for (int pl = 0; pl < 3; ++pl) out[DeltaFrags::T + (id * 3 + pl) * 64 + lane] = o[pl];
       }
   }
   __syncthreads();
@@ -385,8 +382,7 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
 template <class UT, int DK, int VC, bool ADJ, bool KONLY>
 struct DeltaBuf {
   static constexpr int NP = DeltaPlanes<UT>::NP;
-  typedef DeltaFrags<UT, ADJ> F;
-  static constexpr int FA = KONLY ? F::T : F::ALL;  // of the chunk's triangular operands
+  static constexpr int FA = KONLY ? DeltaFrags::T : DeltaFrags::ALL;  // of the chunk's triangular operands
   DeltaTile<DK, NP> k;
   DeltaTile<KONLY ? 32 : DK, NP, KONLY ? 1 : 64> q;
   DeltaTile<VC, NP> v;
@@ -396,7 +392,7 @@ struct DeltaBuf {
 
 // The scans' common part. NW waves have 16 NC columns of dv each and work on a
 // chunk; NL more waves bring the next one meanwhile and send the results of the
-// one before. A CU takes 25 bytes a cycle from memory, so that a chunk (70 KB)
+// one before. A CU takes 25 bytes a cycle from memory, so that a chunk (77 KB)
 // keeps whoever asks for it waiting for 3000 cycles of the 5500 that its products
 // take (with each wave loading its share, 8500). One such wave does where loads
 // write to workgroup memory (kDirect), four where they pass through registers;
@@ -421,13 +417,12 @@ struct DeltaScan {
   static constexpr bool DIRECT = MODE == kDirect, INPLACE = sizeof(UT) == 2;
   static constexpr int NL = DIRECT ? 1 : INPLACE ? 4 : 0, THREADS = 64 * (NW + NL), NT = 64 * (NL ? NL : NW);
   static constexpr bool SEGMENT = SEG, KONLY = SEG && !ADJ;
-  typedef DeltaFrags<UT, ADJ> F;
   typedef DeltaBuf<UT, DK, VC, ADJ, KONLY> Buf;
   static constexpr int NBUF = 2 * sizeof(Buf) <= 160 * 1024 ? 2 : 1;
   static_assert(NL == 0 || NBUF == 2, "a buffer to work on and one to fill");
   // rounds of the loading threads: chunks of q or k, of v, of the triangular operands, row factors
   static constexpr int TP = 64 * DK / 8 / NT, CP = 64 * VC / 8 / NT, FP = (Buf::FA + NT - 1) / NT, VP = 256 / NT;
-  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0 && 64 * VC / 8 % NT == 0 && F::ALL % 64 == 0, "whole rounds");
+  static_assert(64 * DK / 8 % NT == 0 && 256 % NT == 0 && 64 * VC / 8 % NT == 0 && DeltaFrags::ALL % 64 == 0, "whole rounds");
 
   // A tensor's rows of the chunk that is fetched next. Rows behind a row's last step lie past the resource's
   // extent (a token is at least as long as its packed elements) and so come as zeros: nothing but the
@@ -494,7 +489,7 @@ struct DeltaScan {
     sk.set(p.k, b, static_cast<long long>(first) * kDeltaChunk, h * p.dk, p.H * p.dk, dir);
     sq.set(p.q, b, static_cast<long long>(first) * kDeltaChunk, h * p.dk, p.H * p.dk, dir);
     sv.set(v, b, static_cast<long long>(first) * kDeltaChunk, hv * p.dv, p.HV * p.dv, dir);
-    fp = p.frags + (static_cast<long long>(bh) * p.nc + first) * F::ALL;
+    fp = p.frags + (static_cast<long long>(bh) * p.nc + first) * DeltaFrags::ALL;
     rp = p.rows + (static_cast<long long>(bh) * p.nc + first) * (kRows * 64);
   }
   // the lane's column of v: column m of tile col0 + cc
@@ -531,7 +526,7 @@ struct DeltaScan {
     sk.at += sk.step;
     sq.at += sq.step;
     sv.at += sv.step;
-    fp += dir * F::ALL;
+    fp += dir * DeltaFrags::ALL;
     rp += dir * (kRows * 64);
     left -= dir * kDeltaChunk;
   }
@@ -769,7 +764,7 @@ __device__ __forceinline__ void state_tiles(f32x4 (&S)[NC][RT], int t0, const bf
 template <class D, class UT, int DK, int NC>
 __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p, const DeltaView& o, int ch, typename D::Buf& u,
                                                  f32x4 (&S)[NC][D::RT], bf16x8 (&sb)[NC][D::KB][3]) {
-  constexpr int NP = D::NP, NO = DeltaPlanes<UT>::NO, RT = D::RT, KB = D::KB;
+  constexpr int NP = D::NP, RT = D::RT, KB = D::KB;
   const int m = s.m, g = s.g;
   const long long id = static_cast<long long>(s.bh) * p.nc + ch;
 
@@ -780,7 +775,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
   for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
     for (int i = 0; i < 4; ++i) ks[cc][i] = qs[cc][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  bf16x8 ka[2][4][NP], qa[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][NO], vv[NC][2][NP];
+  bf16x8 ka[2][4][NP], qa[2][4][NP], ta[kTriBlocks][3], pa[kTriBlocks][3], vv[NC][2][NP];
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.k.rows(i, 0, m, g, ka[0][i]);
   if (!D::KONLY && p.states) s.template store_tiles<0, RT>(p.states, id, delta_tiles(p.dk), S);
@@ -817,7 +812,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int cc = 0; cc < (D::KONLY ? 0 : NC); ++cc) mma_rows<NP, NO>(qs[cc], qa[kb & 1], sb[cc][kb]);
+    for (int cc = 0; cc < (D::KONLY ? 0 : NC); ++cc) mma_rows<NP, 3>(qs[cc], qa[kb & 1], sb[cc][kb]);
     if (kb < 2) {  // beside q's products
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) {
@@ -843,7 +838,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
     for (int j = 0; j < kTriBlocks; ++j)
 #pragma unroll
-      for (int pl = 0; pl < NO; ++pl) pa[j][pl] = u.frags[D::F::T + (j * NO + pl) * 64 + s.lane];
+      for (int pl = 0; pl < 3; ++pl) pa[j][pl] = u.frags[DeltaFrags::T + (j * 3 + pl) * 64 + s.lane];
   }
   constexpr int TG = 2;  // tiles of the state at a time
   bf16x8 yb[NC][2][3], kc[2][TG][2][NP];
@@ -863,8 +858,8 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
     for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) split_tiles<NO>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
-    tri_rows<NO, NO, NC>(qs, pa, xb);
+      for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
+    tri_rows<3, 3, NC>(qs, pa, xb);
   }
   // the state
 #pragma unroll
@@ -978,7 +973,7 @@ __device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
       for (int j = 0; j < kTriBlocks; ++j)
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) pa[j][pl] = u.frags[D::F::T + (j * 3 + pl) * 64 + s.lane];
+        for (int pl = 0; pl < 3; ++pl) pa[j][pl] = u.frags[DeltaFrags::T + (j * 3 + pl) * 64 + s.lane];
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
