@@ -70,7 +70,7 @@ struct DeltaArgs {
 
 // factors of a chunk's rows (NotR, NotB: 1 - s(gate) as s(-gate), which keeps its digits)
 enum { kRowX = 0, kRowO = 1, kRowS = 2, kRowWhole = 3, kRowK = 4, kRowQ = 5, kRowB = 6, kRowG = 7, kRowR = 8,
-       kRowSeg = 9, kRowNotR = 10, kRowNotB = 11, kRows = 12 };
+       kRowSeg = 9, kRowNotR = 10, kRowNotB = 11, kRowGLow = 12, kRows = 13 };
 
 // Blocks (16 rows x 32 inner indexes) of a lower triangular 64 x 64 operand,
 // and of its transpose, that are not zero: 6 of 8
@@ -84,6 +84,10 @@ struct DeltaFrags {
 
 // tiles of 16 that n rows or columns take, in pairs
 __host__ __device__ constexpr int delta_tiles(int n) { return (n + 31) / 32 * 2; }
+// G_i - G_j of the sums of log a, in two floats each. Strong decays in front of weak ones leave sums of hundreds
+// whose differences are of 0.1: from one float they, and the decays, are off by 2^-24 of the sums.
+template <class V>
+__device__ __forceinline__ V log_gap(V hi, V low, float hj, float lj) { return (hi - hj) + (low - lj); }
 __device__ __forceinline__ int delta_len(const DeltaArgs& p, int b) {
   return p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
 }
@@ -171,7 +175,7 @@ template <class UT, bool EVEN, int DK, bool ADJ>
 __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kernel(const DeltaArgs p) {
   constexpr int NP = DeltaPlanes<UT>::NP, KB = DK / 32, ROW = 68;
   __shared__ float sm[64 * ROW], st[64 * ROW];
-  __shared__ float sg[64], sb[64], sseg[64], srk[64], srq[64];
+  __shared__ float sg[64], sgl[64], sb[64], sseg[64], srk[64], srq[64];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, g = lane >> 4;
   const int ch = blockIdx.x % p.nc, bh = blockIdx.x / p.nc, b = bh / p.HV, hv = bh % p.HV, h = hv / (p.HV / p.H);
   const int t0 = ch * kDeltaChunk, len = delta_len(p, b);
@@ -246,20 +250,25 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     const float ga = load1(gp), gb = load1(gp + p.HV);
     const float r = on ? sigm(ga) : 0.0f, beta = on ? sigm(gb) : 0.0f;
     const float coef = -p.c * softplus(p.lam[hv]);
-    float G = on ? coef * r : 0.0f;
+    // e^-1024 is 0 beside any float: held there, no sum is infinite
+    const float la = coef * r;
+    double sum = on ? (la < -1024.0f ? -1024.0f : la) : 0.0f;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const float u = __shfl_up(G, o, 64);
-      if (i >= o) G += u;
+      const double u = __shfl_up(sum, o, 64);
+      if (i >= o) sum += u;
     }
+    const float G = static_cast<float>(sum), low = static_cast<float>(sum - static_cast<double>(G));
     const bool start = on && p.reset && p.reset[static_cast<long long>(b) * p.L + t0 + i] != 0;
     const unsigned long long starts = __ballot(start);
     const int seg = __popcll(starts & (~0ull >> (63 - i)));
     sg[i] = G;
+    sgl[i] = low;
     sb[i] = beta;
     sseg[i] = static_cast<float>(seg);
     rows[kRowB * 64 + i] = beta;
     rows[kRowG * 64 + i] = G;
+    rows[kRowGLow * 64 + i] = low;
     rows[kRowR * 64 + i] = r;
     rows[kRowSeg * 64 + i] = static_cast<float>(seg);
     rows[kRowNotR * 64 + i] = on ? sigm(-ga) : 0.0f;
@@ -272,20 +281,21 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     // element (row i, column j) of both: E_ij with the lengths, b_j and the scale. The lane's own index is the
     // row i (ADJ: the column j), and it has 4 of the other.
     const int own = 16 * w + m;
-    const float Go = sg[own], so = sseg[own], ko = srk[own], qo = srq[own] * p.scale, bo = sb[own];
+    const float Go = sg[own], lo = sgl[own], so = sseg[own], ko = srk[own], qo = srq[own] * p.scale, bo = sb[own];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f32x4 mv = {0.0f, 0.0f, 0.0f, 0.0f};
       if (ADJ ? j >= w : j <= w) {
         const int c = 16 * j + 4 * g;
         const f32x4 Gc = *reinterpret_cast<const f32x4*>(&sg[c]), sc = *reinterpret_cast<const f32x4*>(&sseg[c]);
+        const f32x4 gap = log_gap(Gc, *reinterpret_cast<const f32x4*>(&sgl[c]), Go, lo);  // columns' less the own
         const f32x4 kc = *reinterpret_cast<const f32x4*>(&srk[c]);
         const f32x4 fc = *reinterpret_cast<const f32x4*>(ADJ ? &srq[c] : &sb[c]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = ADJ ? c + e : own, col = ADJ ? own : c + e;
           const bool low = row >= col && sc[e] == so;
-          const float x = low ? __builtin_amdgcn_exp2f((ADJ ? Gc[e] - Go : Go - Gc[e]) * kLog2e) : 0.0f;
+          const float x = low ? __builtin_amdgcn_exp2f((ADJ ? gap[e] : -gap[e]) * kLog2e) : 0.0f;
           // k_i k_j b_j and scale q_i k_j b_j
           const float y = x * kc[e] * ko * (ADJ ? bo : fc[e]);
           mv[e] = row > col ? y * kk[j][e] : 0.0f;
@@ -323,9 +333,9 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     for (int i = 0; i < 16; ++i) st[(16 * g + i) * ROW + 16 * g + m] = x[i];
   } else if (w == 1) {
     const int i = lane;
-    const float G = sg[i], Ge = sg[63], se = sseg[63];
+    const float G = sg[i], Ge = sg[63], se = sseg[63], rest = log_gap(Ge, sgl[63], G, sgl[i]);
     const float gamma = sseg[i] == 0.0f ? __builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
-    const float tail = sseg[i] == se ? __builtin_amdgcn_exp2f((Ge - G) * kLog2e) : 0.0f;
+    const float tail = sseg[i] == se ? __builtin_amdgcn_exp2f(rest * kLog2e) : 0.0f;
     rows[kRowX * 64 + i] = gamma * srk[i];
     rows[kRowO * 64 + i] = p.scale * gamma * srq[i];
     rows[kRowS * 64 + i] = tail * srk[i] * sb[i];
@@ -1392,6 +1402,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
     }
     {
       const f32x4 Gi = *reinterpret_cast<const f32x4*>(&srow[kRowG * 64 + 16 * w + 4 * g]);
+      const f32x4 Li = *reinterpret_cast<const f32x4*>(&srow[kRowGLow * 64 + 16 * w + 4 * g]);
       const f32x4 si = *reinterpret_cast<const f32x4*>(&srow[kRowSeg * 64 + 16 * w + 4 * g]);
       const f32x4 li = *reinterpret_cast<const f32x4*>(&srow[(f ? kRowK : kRowQ) * 64 + 16 * w + 4 * g]);
 #pragma unroll
@@ -1407,12 +1418,13 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
           continue;
         }
         const float Gc = srow[kRowG * 64 + c], sc = srow[kRowSeg * 64 + c], kc = srow[kRowK * 64 + c];
+        const f32x4 gap = log_gap(Gi, Li, Gc, srow[kRowGLow * 64 + c]);
         const float bc = (f ? -1.0f : p.scale) * srow[kRowB * 64 + c];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 16 * w + 4 * g + e;
           const bool low = (f ? i > c : i >= c) && si[e] == sc;
-          const float d = low ? bc * __builtin_amdgcn_exp2f((Gi[e] - Gc) * kLog2e) * dd[j][e] : 0.0f;
+          const float d = low ? bc * __builtin_amdgcn_exp2f(gap[e] * kLog2e) * dd[j][e] : 0.0f;
           at[e * ROW] = d;
           pp[j][e] *= d * li[e] * kc;
           if (!f) mt.w[i * ROW + c] = pp[j][e];
@@ -1428,7 +1440,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
           for (int e = 0; e < 4; ++e) mt.w[(16 * w + 4 * g + e) * ROW + 16 * j + m] += pp[j][e];
         }
     }
-    const float se = srow[kRowSeg * 64 + 63], Ge = srow[kRowG * 64 + 63];
+    const float se = srow[kRowSeg * 64 + 63], Ge = srow[kRowG * 64 + 63], Le = srow[kRowGLow * 64 + 63];
     const f32x4 rq = *reinterpret_cast<const f32x4*>(&srow[kRowQ * 64 + 16 * w + 4 * g]);
     const f32x4 rk = *reinterpret_cast<const f32x4*>(&srow[kRowK * 64 + 16 * w + 4 * g]);
     float part[5][4];  // q.dQ, k.(dK read), k.(dK written); of S1, from S0
@@ -1440,7 +1452,8 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
         const float G = srow[kRowG * 64 + i], seg = srow[kRowSeg * 64 + i];
         ck[r] = seg == 0.0f ? -__builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
         cq[r] = -p.scale * ck[r];
-        cw[r] = seg == se ? __builtin_amdgcn_exp2f((Ge - G) * kLog2e) * srow[kRowB * 64 + i] : 0.0f;
+        const float rest = log_gap(Ge, Le, G, srow[kRowGLow * 64 + i]);
+        cw[r] = seg == se ? __builtin_amdgcn_exp2f(rest * kLog2e) * srow[kRowB * 64 + i] : 0.0f;
         part[0][r] = part[1][r] = part[2][r] = part[3][r] = part[4][r] = 0.0f;
       }
 #pragma unroll
