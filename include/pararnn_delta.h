@@ -46,10 +46,11 @@ typedef struct {
   int32_t dtype;            /* pararnn_dtype of q, k, v, gates, o and their gradients */
   float c, eps, scale;      /* c > 0, eps > 0, scale finite */
   const int32_t* lengths;   /* [B] (device) steps of each row, clamped to 0..L; NULL = L. Later steps leave the
-                               state alone and put out zeros, whatever the inputs hold there */
+                               state alone and put out zeros, whatever the inputs hold there or before */
   const uint8_t* reset;     /* [B][L] (device) nonzero: a document starts at this step, S_{t-1} counts as zero;
-                               NULL = none. (An infinity or a NaN among a row's steps reaches the steps after it,
-                               over a start too.) */
+                               NULL = none. (An infinity or a NaN among a row's steps reaches, in its heads, the
+                               steps after it, over a start too, and none in front of it; in the adjoint all of the
+                               row's. |q|^2 and |k|^2 that pass the largest fp32 number count as infinities.) */
 } pararnn_delta_opts;
 
 /* Workspace of pararnn_delta_scan (adjoint = 0) or _adjoint (adjoint = 1), and

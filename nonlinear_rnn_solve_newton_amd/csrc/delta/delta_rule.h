@@ -282,6 +282,15 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     // row i (ADJ: the column j), and it has 4 of the other.
     const int own = 16 * w + m;
     const float Go = sg[own], lo = sgl[own], so = sseg[own], ko = srk[own], qo = srq[own] * p.scale, bo = sb[own];
+    // The first step whose key or gates are no numbers (a key's length is a positive one else). Rows from there on
+    // stay out of T and P, whose zeros above the diagonal would carry them to the rows in front; the scan has them
+    // from kRowX. (The adjoint's gradients run the other way as well, and are not kept apart.)
+    int good = 64;
+    if constexpr (!ADJ) {
+      const unsigned long long bad = __ballot(!(srk[lane] > 0.0f) || sg[lane] != sg[lane] || sb[lane] != sb[lane]);
+      good = bad ? __builtin_ctzll(bad) : 64;
+    }
+    const bool live = ADJ || own < good;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f32x4 mv = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -294,12 +303,12 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = ADJ ? c + e : own, col = ADJ ? own : c + e;
-          const bool low = row >= col && sc[e] == so;
+          const bool low = row >= col && sc[e] == so && live;
           const float x = low ? __builtin_amdgcn_exp2f((ADJ ? gap[e] : -gap[e]) * kLog2e) : 0.0f;
           // k_i k_j b_j and scale q_i k_j b_j
           const float y = x * kc[e] * ko * (ADJ ? bo : fc[e]);
-          mv[e] = row > col ? y * kk[j][e] : 0.0f;
-          qk[j][e] *= ADJ ? x * p.scale * fc[e] * ko * bo : x * kc[e] * fc[e] * qo;
+          mv[e] = row > col && live ? y * kk[j][e] : 0.0f;
+          qk[j][e] = ADJ || low ? qk[j][e] * (ADJ ? x * p.scale * fc[e] * ko * bo : x * kc[e] * fc[e] * qo) : 0.0f;
         }
       } else {
         qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     const float G = sg[i], Ge = sg[63], se = sseg[63], rest = log_gap(Ge, sgl[63], G, sgl[i]);
     const float gamma = sseg[i] == 0.0f ? __builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
     const float tail = sseg[i] == se ? __builtin_amdgcn_exp2f(rest * kLog2e) : 0.0f;
-    rows[kRowX * 64 + i] = gamma * srk[i];
+    rows[kRowX * 64 + i] = srk[i] > 0.0f ? gamma * srk[i] : __uint_as_float(0x7fc00000u);
     rows[kRowO * 64 + i] = p.scale * gamma * srq[i];
     rows[kRowS * 64 + i] = tail * srk[i] * sb[i];
     rows[kRowWhole * 64 + i] = se == 0.0f ? __builtin_amdgcn_exp2f(Ge * kLog2e) : 0.0f;
@@ -567,9 +576,12 @@ struct DeltaScan {
     for (int i = 0; i < VP; ++i) to.rows[lt + NT * i] = rr[i];
     if constexpr (DIRECT) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
   }
-  // The wave's results Y of a chunk, rows of [..][HV][dv] from `to` on: into the place of its columns of v,
-  // to be sent later, or straight to memory
-  __device__ __forceinline__ void result(Buf& u, const DeltaView& to, int t0, int rows, const f32x4 (&Y)[NC][4]) const {
+  // rows of a chunk in memory, and of those the ones with steps: zeros behind them, whatever the others are
+  __device__ __forceinline__ int rows_of_chunk(int ch) const { return min(p.L - ch * kDeltaChunk, kDeltaChunk); }
+  __device__ __forceinline__ int live_of_chunk(int ch) const { return len - ch * kDeltaChunk; }
+  // The wave's results Y of a chunk, rows of [..][HV][dv]: into the place of its columns of v, to be sent later, or
+  // straight to memory
+  __device__ __forceinline__ void result(Buf& u, const DeltaView& to, int ch, const f32x4 (&Y)[NC][4]) const {
     if constexpr (INPLACE) {
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc)
@@ -579,7 +591,8 @@ struct DeltaScan {
           for (int r = 0; r < 4; ++r)
             u.v.x[0][u.v.pos(16 * i + 4 * g + r, delta_label(w * NC + cc, m))] = static_cast<__bf16>(Y[cc][i][r]);
     } else {
-      UT* o = out_at<UT>(to, b, t0) + static_cast<long long>(hv) * p.dv;
+      const int rows = rows_of_chunk(ch), live = live_of_chunk(ch);
+      UT* o = out_at<UT>(to, b, static_cast<long long>(ch) * kDeltaChunk) + static_cast<long long>(hv) * p.dv;
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc)
         if (col(cc) < p.dv) {
@@ -587,23 +600,27 @@ struct DeltaScan {
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (16 * i + 4 * g + r < rows) store1(o + (16 * i + 4 * g + r) * to.token + col(cc), Y[cc][i][r]);
+              if (16 * i + 4 * g + r < rows)
+                store1(o + (16 * i + 4 * g + r) * to.token + col(cc), 16 * i + 4 * g + r < live ? Y[cc][i][r] : 0.0f);
         }
     }
   }
   // The results of a chunk out of its buffer, by the loading waves: each takes the slots that it fills next, so
   // nobody overwrites what another wave has not taken yet.
-  __device__ __forceinline__ void send(const Buf& u, const DeltaView& to, int t0, int rows) const {
+  __device__ __forceinline__ void send(const Buf& u, const DeltaView& to, int ch) const {
     if constexpr (INPLACE) {
+      const int rows = rows_of_chunk(ch), live = live_of_chunk(ch);
       i32x4 v[CP];
 #pragma unroll
       for (int i = 0; i < CP; ++i) v[i] = *reinterpret_cast<const i32x4*>(&u.v.x[0][(lt + NT * i) * 8]);
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): taken, before a load may write there
-      bf16* o = reinterpret_cast<bf16*>(out_at<UT>(to, b, t0)) + static_cast<long long>(hv) * p.dv + wg0;
+      bf16* o = reinterpret_cast<bf16*>(out_at<UT>(to, b, static_cast<long long>(ch) * kDeltaChunk)) +
+                static_cast<long long>(hv) * p.dv + wg0;
 #pragma unroll
       for (int i = 0; i < CP; ++i) {
         const int e = lt + NT * i, row = e / (VC / 8), d = DeltaTile<VC, NP>::source(e), count = p.dv - wg0 - d;
         bf16* at = o + row * to.token + d;
+        if (row >= live) v[i] = i32x4{0, 0, 0, 0};
         if (row < rows && count > 0) {
           if (p.wide) {  // dv is a multiple of 8
             *reinterpret_cast<i32x4*>(at) = v[i];
@@ -770,6 +787,48 @@ __device__ __forceinline__ void state_tiles(f32x4 (&S)[NC][RT], int t0, const bf
       }
 }
 
+// Rows of a wave's chunk from the first one on whose value is no number. They are kept from T's and P's products,
+// whose zeros above the diagonal would carry them to the rows in front (0 times a NaN is one), and then are NaN.
+struct DeltaBadRows {
+  int first;  // of the lane's column
+  static __device__ __forceinline__ int row(int i, int g, int r) { return 16 * i + 4 * g + r; }
+  // from the operand of the values read, whose rows from `first` on become zeros; the lanes of a column agree
+  __device__ __forceinline__ void take(bf16x8 (&x)[2][3], int g) {
+    first = 64;
+    i32x4 w[2][3];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) w[kb][pl] = __builtin_bit_cast(i32x4, x[kb][pl]);
+#pragma unroll
+    for (int e = 15; e >= 0; --e) {  // row 4 e + r of the column, r = e & 3
+      const int u = w[e >> 3][0][(e & 7) >> 1], bits = e & 1 ? u >> 16 : u;
+      if ((bits & 0x7f80) == 0x7f80) first = row(e >> 2, g, e & 3);
+    }
+    first = min(first, __shfl_xor(first, 16, 64));
+    first = min(first, __shfl_xor(first, 32, 64));
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 8 * kb + 2 * i, r = row(e >> 2, g, e & 3);
+        const int keep = r + 1 < first ? -1 : r < first ? 0xffff : 0;
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) w[kb][pl][i] &= keep;
+      }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) x[kb][pl] = __builtin_bit_cast(bf16x8, w[kb][pl]);
+  }
+  __device__ __forceinline__ void mark(f32x4 (&y)[4], int g) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[i][r] = row(i, g, r) >= first ? __uint_as_float(0x7fc00000u) : y[i][r];
+  }
+};
+
 // A chunk of the scan
 template <class D, class UT, int DK, int NC>
 __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p, const DeltaView& o, int ch, typename D::Buf& u,
@@ -807,6 +866,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
   const float whole = u.rows[kRowWhole * 64];
   bf16x8 xb[NC][2][3];
   f32x4 y[NC][4];
+  float odd = 0.0f;  // not zero where a value read is no number
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     if (!D::KONLY && kb + 1 < KB) {
@@ -832,11 +892,21 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             ks[cc][2 * kb + i][r] = fmaf(-xg[r], ks[cc][2 * kb + i][r], plane_sum<NP>(vv[cc][kb], 4 * i + r));
+          if (!D::KONLY) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) odd = fmaf(ks[cc][2 * kb + i][r], 0.0f, odd);
+          }
           y[cc][2 * kb + i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         split_tiles<3>(ks[cc][2 * kb], ks[cc][2 * kb + 1], xb[cc][kb]);
       }
     }
+  }
+  DeltaBadRows bad[NC];
+  const bool apart = !D::KONLY && __builtin_expect(__any(odd != 0.0f), 0);
+  if (apart) {
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) bad[cc].take(xb[cc], g);
   }
   __builtin_amdgcn_sched_barrier(0);
   tri_rows<3, 3, NC>(y, ta, xb);
@@ -858,7 +928,6 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
     for (int kb = 0; kb < 2; ++kb) u.k.columns(t, kb, m, g, kc[0][t][kb]);
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (!D::KONLY) {  // the output
-    if (p.ys) s.template store_tiles<0, 4>(p.ys, id, 4, y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 og = s.row4(u, kRowO, i);
@@ -870,6 +939,14 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) split_tiles<3>(y[cc][2 * kb], y[cc][2 * kb + 1], xb[cc][kb]);
     tri_rows<3, 3, NC>(qs, pa, xb);
+    if (apart) {
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc) {
+        bad[cc].mark(qs[cc], g);
+        bad[cc].mark(y[cc], g);
+      }
+    }
+    if (p.ys) s.template store_tiles<0, 4>(p.ys, id, 4, y);
   }
   // the state
 #pragma unroll
@@ -894,7 +971,7 @@ __device__ __forceinline__ void delta_scan_chunk(const D& s, const DeltaArgs& p,
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc) split_tiles<3>(S[cc][t], S[cc][t + 1], sb[cc][t / 2]);
   }
-  if constexpr (!D::KONLY) s.result(u, o, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), qs);
+  if constexpr (!D::KONLY) s.result(u, o, ch, qs);
 }
 
 template <class UT, int MODE, int DK, int NC, int NW>
@@ -916,14 +993,14 @@ __global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, false>::THREA
   if (s.loads) {  // every barrier here has its fellow below
     for (int ch = s.c0; ch < end; ++ch) {
       Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
-      if (ch > s.c0) s.send(next, o, (ch - 1) * kDeltaChunk, min(p.L - (ch - 1) * kDeltaChunk, kDeltaChunk));
+      if (ch > s.c0) s.send(next, o, ch - 1);
       if (ch + 1 < end) {
         s.fetch(next);
         s.land(next);
       }
       __syncthreads();
     }
-    if (s.nch > 0) s.send(buf[(end - 1) & (D::NBUF - 1)], o, (end - 1) * kDeltaChunk, min(p.L - (end - 1) * kDeltaChunk, kDeltaChunk));
+    if (s.nch > 0) s.send(buf[(end - 1) & (D::NBUF - 1)], o, end - 1);
     return;
   }
   f32x4 S[NC][RT];
@@ -1035,7 +1112,7 @@ __device__ __forceinline__ void delta_back_chunk(const D& s, const DeltaArgs& p,
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (!D::SEGMENT) {
     s.template store_tiles<0, 4>(p.dxs, id, 4, x);
-    s.result(u, p.gv, ch * kDeltaChunk, min(p.L - ch * kDeltaChunk, kDeltaChunk), x);
+    s.result(u, p.gv, ch, x);
   }
 #pragma unroll
   for (int cc = 0; cc < NC; ++cc) {
@@ -1086,14 +1163,14 @@ __global__ void __launch_bounds__((DeltaScan<UT, MODE, DK, NC, NW, true>::THREAD
   if (s.loads) {  // every barrier here has its fellow below
     for (int ch = end - 1; ch >= s.c0; --ch) {
       Buf& next = buf[(ch + 1) & (D::NBUF - 1)];
-      if (ch + 1 < end) s.send(next, p.gv, (ch + 1) * kDeltaChunk, min(p.L - (ch + 1) * kDeltaChunk, kDeltaChunk));
+      if (ch + 1 < end) s.send(next, p.gv, ch + 1);
       if (ch > s.c0) {
         s.fetch(next);
         s.land(next);
       }
       __syncthreads();
     }
-    if (s.nch > 0) s.send(buf[s.c0 & (D::NBUF - 1)], p.gv, s.c0 * kDeltaChunk, min(p.L - s.c0 * kDeltaChunk, kDeltaChunk));
+    if (s.nch > 0) s.send(buf[s.c0 & (D::NBUF - 1)], p.gv, s.c0);
     return;
   }
   f32x4 S[NC][RT];
@@ -1611,8 +1688,9 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
               a = qo[t + z][r];
               c = kx[t + z][r] + yd[t + z][r];
             }
-            vq[r] = rq[r] * fmaf(-rq[r] * qv[r], qs[r], a);
-            vk[r] = rk[r] * fmaf(-rk[r] * kv[r], ks[r], c);
+            const bool live = 16 * w + 4 * g + r < n;  // else zero, whatever the other rows are
+            vq[r] = live ? rq[r] * fmaf(-rq[r] * qv[r], qs[r], a) : 0.0f;
+            vk[r] = live ? rk[r] * fmaf(-rk[r] * kv[r], ks[r], c) : 0.0f;
           }
           transpose4(vq, lane);
           transpose4(vk, lane);
@@ -1650,7 +1728,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
       const float r = srow[kRowR * 64 + i], lam = p.lam[hv];
       if (i < rows_out) {
         UT* go = out_at<UT>(p.dgates, b, t0 + i) + hv;
-        store1(go, -p.c * softplus(lam) * dl * r * srow[kRowNotR * 64 + i]);
+        store1(go, i < n ? -p.c * softplus(lam) * dl * r * srow[kRowNotR * 64 + i] : 0.0f);
         store1(go + p.HV, i < n ? bw * srow[kRowNotB * 64 + i] : 0.0f);
       }
       if (p.dlam_part) {

@@ -568,7 +568,8 @@ def delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.T
     packed (columns of one product, say); value head v takes head v // (HV // H) of
     q and k. lam [HV] fp32, s0 [B][HV][dk][dv] fp32 or None (zero), lengths and
     reset as in gated_scan (but an infinity or a NaN among a row's steps reaches those
-    after it, over a start too); scale None: dk^-1/2. dk at most 128, dv at most 512.
+    after it, over a start too, and in the adjoint those in front of it); scale None:
+    dk^-1/2. dk at most 128, dv at most 512.
     Returns dict(o [B][L][HV][dv], sT [B][HV][dk][dv] fp32 state after the last
     step, saved (with save=True, for the adjoint), ws).
     """
