@@ -1306,7 +1306,8 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaArgs p) {
       store1(to, 0.0f);
       store1(to + p.HV, 0.0f);
     }
-    if (tid < per && p.dlam_part) p.dlam_part[(static_cast<long long>(h) * per + tid) * p.B * p.nc + b * p.nc + ch] = 0.0f;
+    for (int i = tid; i < (p.dlam_part ? per : 0); i += 512)
+      p.dlam_part[(static_cast<long long>(h) * per + i) * p.B * p.nc + b * p.nc + ch] = 0.0f;
     return;
   }
   const int n = min(len - t0, kDeltaChunk);
