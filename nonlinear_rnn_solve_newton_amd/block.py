@@ -157,8 +157,9 @@ class DeltaBlock:
     """norm_w [E] fp32, w [2 H dk + 2 HV dv + 2 HV][E] (rows of q, k, v, the output's
     gate z, the decays and the write strengths; any float type, quantized here),
     lam [HV] fp32, head_w [dv] fp32, w_out [E][HV dv]; alpha [E] fp32, the scale of
-    x where it is added to the residual, or None. dk at most 128, dv one of 8, 16,
-    32, ... 512."""
+    x where it is added to the residual, or None. dk at most 128; dv one of 8, 16,
+    32, ... 512, or with one value head any up to 512: the heads' norm writes 8-bit
+    rows, whose groups have these sizes. E and HV dv at most 16384."""
 
     def __init__(self, norm_w: torch.Tensor, w: torch.Tensor, lam: torch.Tensor, head_w: torch.Tensor,
                  w_out: torch.Tensor, *, heads: int, dk: int, alpha: Optional[torch.Tensor] = None, c: float = 8.0,
@@ -167,8 +168,15 @@ class DeltaBlock:
                 t.dim() != 1 for t in (norm_w, lam, head_w)) or w.dim() != 2 or w_out.dim() != 2:
             raise PararnnError("norm_w, lam, head_w (vectors), w and w_out (matrices) must be tensors")
         self.H, self.HV, self.dk, self.dv, self.E = heads, lam.shape[0], dk, head_w.shape[0], norm_w.shape[0]
-        if heads < 1 or dk < 1 or self.HV % heads:
+        if heads < 1 or dk < 1 or self.HV < 1 or self.HV % heads:
             raise PararnnError(f"lam's heads ({self.HV}) must be a multiple of heads ({heads}), dk at least 1")
+        if dk > 128 or not 1 <= self.dv <= 512 or (self.HV > 1 and self.dv not in (8, 16, 32, 64, 128, 256, 512)):
+            raise PararnnError(f"dk must be at most 128 and dv 8, 16, 32, ... 512 (with one value head any up to 512), "
+                               f"got {dk} and {self.dv}")
+        if not 1 <= self.E <= 16384 or self.HV * self.dv > 16384:
+            raise PararnnError(f"E and HV dv must be at most 16384, got {self.E} and {self.HV * self.dv}")
+        if alpha is not None and (not isinstance(alpha, torch.Tensor) or alpha.shape != (self.E,)):
+            raise PararnnError(f"alpha must be a tensor of shape {(self.E,)}")
         self.cols = (heads * dk, heads * dk, self.HV * self.dv, self.HV * self.dv, 2 * self.HV)
         if w.shape != (sum(self.cols), self.E) or w_out.shape != (self.E, self.HV * self.dv):
             raise PararnnError(f"w must be [{sum(self.cols)}][{self.E}] and w_out [{self.E}][{self.HV * self.dv}], got "
