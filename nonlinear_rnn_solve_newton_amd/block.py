@@ -248,13 +248,14 @@ class DeltaBlock:
         = dL/ds and dstate = dL/dstate, straight through the roundings to 8 bits:
         dict(dx, dresidual (None without one), dnorm_w, dalpha, dw, dlam, dhead_w,
         dw_out, dstate0). Steps past a row's length, whatever x, the residual, dx and
-        ds hold there, add nothing to the gradients of the weights."""
+        ds hold there, add nothing to the gradients of the weights, and their own dx
+        and dresidual are zero (what ds holds there stops here)."""
         if ctx is None:
             raise PararnnError("backward needs the ctx of forward(train=True)")
         x, s, with_residual, p, o, saved, lengths, reset = ctx
         for t, n in ((dx, "dx"), (ds, "ds")):
-            if (t is not None or n == "dx") and (not isinstance(t, torch.Tensor) or t.shape != x.shape):
-                raise PararnnError(f"{n} must be a tensor of shape {tuple(x.shape)}")
+            if t is not None or n == "dx":
+                layer._like(t, n, x.dtype, x.shape, x.device)
         lead = x.shape[:2]
         if lengths is not None:
             # padding may hold anything, and the sums over the rows would take 0 x NaN from it
