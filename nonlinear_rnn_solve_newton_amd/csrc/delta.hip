@@ -527,8 +527,8 @@ extern "C" int32_t pararnn_norm_block(const void* x, const void* gate, const voi
   hipStream_t st = static_cast<hipStream_t>(stream_);
   const bool ok = norm_block_aligned(r, es, {x, gate, residual, s, y, w, alpha, w_next},
                                      {o->x_row, gate ? o->gate_row : 0, residual ? o->residual_row : 0});
-  // past the caches where the tensors together are larger than the last-level one (2048 columns, 256 MB: 46 us,
-  // through them 41; 512 MB: 91 and 99)
+  // past the caches where the tensors together are larger than the last-level one (2048 columns, past them and
+  // through them: 230 MB 38.9 and 36.0 us, 307 MB 52.1 and 56.4)
   const bool far = static_cast<double>(o->N) * o->D * es * (2 + (gate != nullptr) + 2 * (residual != nullptr)) > 256.0 * 1024 * 1024;
   auto go = [&](auto xt, auto aligned_) {
     typedef decltype(xt) XT;
@@ -596,8 +596,9 @@ extern "C" int32_t pararnn_norm_block_adjoint(const void* x, const void* gate, c
   hipStream_t st = static_cast<hipStream_t>(stream_);
   const bool ok = norm_block_aligned(r, es, {x, gate, s, dy, ds, dx, dgate, dresidual, w, alpha, w_next},
                                      {o->x_row, gate ? o->gate_row : 0});
-  const bool far = static_cast<double>(o->N) * o->D * es * (3 + 2 * (gate != nullptr) + 2 * (s != nullptr) + (ds != nullptr)) >=
-                   256.0 * 1024 * 1024;
+  // as forward (2048 columns without a residual, past the caches and through them: 256 MB 58.9 and 53.0 us, 320 MB
+  // 67.9 and 72.3; with one within 3% on both sides)
+  const bool far = static_cast<double>(o->N) * o->D * es * (3 + 2 * (gate != nullptr) + 2 * (s != nullptr) + (ds != nullptr)) > 256.0 * 1024 * 1024;
   auto go = [&](auto xt, auto aligned_) {
     typedef decltype(xt) XT;
     constexpr bool AL = decltype(aligned_)::value;
