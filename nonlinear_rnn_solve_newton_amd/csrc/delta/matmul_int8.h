@@ -4,11 +4,11 @@
 // The sum over k is exact, in the 32-bit integers of the matrix instructions
 // (16 x 16 x 64, two for a block of 128), so the scales wait for the end: they
 // and the bias are the epilogue. Operands, tiles and the order of tiles are
-// those of the 8-bit floating-point product: a wave holds 16 x 16 tiles of y^T,
-// a lane 4 consecutive columns of one row of y.
+// those of the 8-bit floating-point product (matmul_tiles.h): a wave holds 16 x
+// 16 tiles of y^T, a lane 4 consecutive columns of one row of y.
 #pragma once
 
-#include "../layer/matmul_fp8.h"
+#include "../layer/matmul_tiles.h"
 
 namespace pararnn {
 
@@ -34,74 +34,23 @@ __device__ __forceinline__ void scaled(const i32x4& c, float sa, const float (&s
 }
 
 // Between the few rows and the large tiles, and unaligned operands: BN x BM of
-// y per workgroup, two buffers, as in Matmul; KS groups of waves take every
-// KS-th block of K and their sums are joined (integers: in any order). The latency
+// y per workgroup; KS groups of waves take every KS-th block of K and their sums
+// are joined (integers: in any order). The latency
 // of the blocks bounds them: 777 x 1000 x 1333, whose rows no wide load can take, 13 us,
 // 777 x 1000 x 1344 6.0.
 template <class S, bool F32OUT, bool DIRECT>
-__global__ void __launch_bounds__(S::NT * S::KS) int8_kernel(const Int8Args p) {
-  constexpr int BN = S::BN, BM = S::BM, NT = S::NT, TN = S::TN, TM = S::TM, KS = S::KS;
-  constexpr int LN = BN * 8 / NT, LM = BM * 8 / NT, HALF = (BN + BM) * 8;  // 16-byte chunks
-  typedef __attribute__((address_space(3))) void lds_void;
-  __shared__ i32x4 lds[KS * 2 * HALF];
-  const int kg = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / NT);  // the wave's group
-  i32x4* const mine = lds + kg * 2 * HALF;
-  const int tid = static_cast<int>(threadIdx.x) - kg * NT, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int tm, tn;
-  tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &tm, &tn);
-  const int m0 = tm * BM, n0 = tn * BN, mrows = min(p.M - m0, BM), nrows = min(p.N - n0, BN);
-  const int wn = (wave % S::WN) * TN * 16, wm = (wave / S::WN) * TM * 16;
-  // thread's chunk i: row (tid + NT i) / 8, position tid % 8, column chunk c0
-  const int q0 = tid >> 3, c0 = (tid & 7) ^ (q0 & 7);
-  const uint32_t v0 = static_cast<uint32_t>(q0) * p.K + c0 * 16;
-  const uint8_t* const ab = p.a + static_cast<long long>(m0) * p.K;
-  const uint8_t* const wb = p.w + static_cast<long long>(n0) * p.K;
-  const __amdgpu_buffer_rsrc_t rsa = make_rsrc(ab, static_cast<uint32_t>(mrows) * p.K);
-  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(wb, static_cast<uint32_t>(nrows) * p.K);
-  i32x4 ra[DIRECT ? 1 : LM], rw[DIRECT ? 1 : LN];  // in flight
-  auto fetch = [&](int kb, i32x4* sw, i32x4* sa) {
-    if constexpr (DIRECT) {
-      // the row is in the lane's offset, which the extent is checked against; the block of columns is not
-      const bool in = kb * 128 + c0 * 16 < p.K;
-      const int so = kb < p.KB ? kb * 128 : 0;
-#pragma unroll
-      for (int i = 0; i < LN; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(sw + wave * 64 + NT * i), 16,
-                                                 in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u, so, 0, 0);
-#pragma unroll
-      for (int i = 0; i < LM; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sa + wave * 64 + NT * i), 16,
-                                                 in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u, so, 0, 0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < LN; ++i)
-        rw[i] = load16(wb + static_cast<long long>(min(q0 + i * (NT / 8), nrows - 1)) * p.K, kb * 128 + c0 * 16, p.K);
-#pragma unroll
-      for (int i = 0; i < LM; ++i)
-        ra[i] = load16(ab + static_cast<long long>(min(q0 + i * (NT / 8), mrows - 1)) * p.K, kb * 128 + c0 * 16, p.K);
-    }
-  };
-  auto land = [&](i32x4* sw, i32x4* sa) {
-    if constexpr (!DIRECT) {
-#pragma unroll
-      for (int i = 0; i < LN; ++i) sw[tid + NT * i] = rw[i];
-#pragma unroll
-      for (int i = 0; i < LM; ++i) sa[tid + NT * i] = ra[i];
-    }
-  };
+struct Int8Tiles : SmallTiles<Int8Args, S, DIRECT> {
+  typedef SmallTiles<Int8Args, S, DIRECT> T;
+  using T::p, T::kg, T::r, T::g, T::m0, T::wn, T::wm;
+  static constexpr int BN = S::BN, TN = S::TN, TM = S::TM, KS = S::KS;
   i32x4 acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  // lane's two chunks of a row of its tile 0; tile i: 128 i further
-  const int bw0 = (wn + r) * 8 + (g ^ (r & 7)), bw1 = (wn + r) * 8 + ((g + 4) ^ (r & 7));
-  const int ba0 = (wm + r) * 8 + (g ^ (r & 7)), ba1 = (wm + r) * 8 + ((g + 4) ^ (r & 7));
+
   // The pointers' restrict lets reads of this block pass the next one's loads into workgroup memory.
-  auto step = [&](int kb, const i32x4* __restrict__ c, i32x4* __restrict__ nx) {
-    const bool more = kb + KS < p.KB + KS - 1;  // another group may have a block where this one has none
-    if (more) fetch(kb + KS, nx, nx + BN * 8);
+  __device__ __forceinline__ void step(int kb, const i32x4* __restrict__ c, i32x4* __restrict__ nx) {
+    // lane's two chunks of a row of its tile 0; tile i: 128 i further
+    const int bw0 = (wn + r) * 8 + (g ^ (r & 7)), bw1 = (wn + r) * 8 + ((g + 4) ^ (r & 7));
+    const int ba0 = (wm + r) * 8 + (g ^ (r & 7)), ba1 = (wm + r) * 8 + ((g + 4) ^ (r & 7));
+    if (T::more(kb)) T::fetch(kb + KS, nx, nx + BN * 8);
     if (kb < p.KB) {
       const i32x4* ca = c + BN * 8;
       i32x4 wl[TN], wh[TN];
@@ -123,111 +72,58 @@ __global__ void __launch_bounds__(S::NT * S::KS) int8_kernel(const Int8Args p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (more) land(nx, nx + BN * 8);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the loads into workgroup memory are done
-    __syncthreads();
-  };
-  fetch(kg, mine, mine + BN * 8);
-  land(mine, mine + BN * 8);
-  __builtin_amdgcn_s_waitcnt(0x0f70);
-  __syncthreads();
-  int odd = 0;  // every group takes as many steps as the first
-  for (int kb = 0; kb < p.KB; kb += KS, odd ^= 1) step(kb + kg, mine + odd * HALF, mine + (1 - odd) * HALF);
-  if constexpr (KS > 1) {
-    constexpr int PER = TN * TM * NT;
-    static_assert((KS - 1) * PER <= KS * 2 * HALF, "the sums fit where the blocks were");
-    if (kg > 0) {
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) lds[(kg - 1) * PER + (i * TM + j) * NT + tid] = acc[i][j];
-    }
-    __syncthreads();
-    if (kg == 0) {
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-          for (int k = 0; k < KS - 1; ++k) acc[i][j] += lds[k * PER + (i * TM + j) * NT + tid];
-    }
-    __syncthreads();
+    if (T::more(kb)) T::land(nx, nx + BN * 8);
+    T::arrived();
   }
-  const bool whole = !F32OUT && p.vec == 8;  // the last step ended with a barrier
-  TileStore<BM, BN, NT> st{lds};
-  if (kg > 0) {
-    if (whole) __syncthreads();
-    return;
+  __device__ __forceinline__ void run(i32x4* lds) {
+    T::begin();
+    i32x4* const mine = lds + kg * 2 * T::HALF;
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    T::fetch(kg, mine, mine + BN * 8);
+    T::land(mine, mine + BN * 8);
+    T::arrived();
+    int odd = 0;  // every group takes as many steps as the first
+    for (int kb = 0; kb < p.KB; kb += KS, odd ^= 1) step(kb + kg, mine + odd * T::HALF, mine + (1 - odd) * T::HALF);
+    T::join(acc, lds);
+    float sa[TM], sw[4], bv[4];
+    T::template out<F32OUT>(
+        lds,
+        [&](int i, int n) {
+          if (i == 0) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j) sa[j] = p.sa[min(m0 + wm + 16 * j + r, p.M - 1)];
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            sw[v] = p.sw[min(n + v, p.N - 1)];
+            bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
+          }
+        },
+        [&](int i, int j, float(&o)[4]) { scaled(acc[i][j], sa[j], sw, bv, o); });
   }
-  float sa[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) sa[j] = p.sa[min(m0 + wm + 16 * j + r, p.M - 1)];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int n = n0 + wn + 16 * i + 4 * g;
-    float sw[4], bv[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      sw[v] = p.sw[min(n + v, p.N - 1)];
-      bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const long long m = m0 + wm + 16 * j + r;
-      float o[4];
-      scaled(acc[i][j], sa[j], sw, bv, o);
-      if (whole) st.put(wm + 16 * j + r, n - n0, o);
-      else if (m < p.M && n < p.N) store_row4<F32OUT>(p.y, m * p.N + n, p.N - n, p.vec, o);
-    }
-  }
-  if (whole) {
-    __syncthreads();
-    st.flush(p.y, m0, n0, mrows, p.N - n0, p.N, p.stream, tid);
-  }
+};
+template <class S, bool F32OUT, bool DIRECT>
+__global__ void __launch_bounds__(S::NT * S::KS) int8_kernel(const Int8Args p) {
+  typedef Int8Tiles<S, F32OUT, DIRECT> M;
+  __shared__ i32x4 lds[S::KS * 2 * M::HALF];
+  M m;
+  m.p = p;
+  m.run(lds);
 }
 
-// Large products: 256 rows by 64 TN columns of y by 8 waves (4 along n, 2 along
-// m), in the half steps of MatmulLarge: after the first half of a block nobody
-// needs its w and first a rows any more, and the block after the next takes
-// their place, so that every load has a step and a half to arrive. The matrix
-// instructions bound it: 32768 x 16384 x 4096 in 1.79 ms, 2460 TOP/s (2030 on a warm
+// Large products: tiles of 256 rows by 64 TN columns. The matrix instructions bound it: 32768 x
+// 16384 x 4096 in 1.79 ms, 2460 TOP/s (2030 on a warm
 // card; the same product of 8-bit floating-point numbers 2290 to 2390 TFLOP/s).
 template <int TN, bool F32OUT>
-struct Int8Large {
-  static constexpr int BN = 64 * TN, BM = 256, NT = 512, TM = 8, WC = 16 * TN;
-  // 16-byte chunks of one buffer: w, then the first and the second a rows of both waves along m
-  static constexpr int OX0 = BN * 8, OX1 = OX0 + BM * 4, BUF = OX1 + BM * 4;
-  static constexpr int NWL = TN, NXL = 2;  // loads per thread: w, half of a
-  // loads that may be on their way when a half step begins
-  static constexpr int WAIT = 0x0f70 | (NWL + 2 * NXL);
-  static constexpr int TILE_BUF = TileStore<BM, BN, NT>::CHUNKS, LDS = 2 * BUF > TILE_BUF ? 2 * BUF : TILE_BUF;
-  typedef __attribute__((address_space(3))) void lds_void;
-
-  Int8Args p;
-  int tid, wave, r, g, m0, n0, wni, wmi;
-  __amdgpu_buffer_rsrc_t rsa, rsw;
-  uint32_t v0;
-  int c16;  // the thread's column within a block, bytes
+struct Int8Large : LargeTiles<Int8Args, TN> {
+  typedef LargeTiles<Int8Args, TN> T;
+  using T::p, T::tid, T::r, T::g, T::m0, T::n0, T::wni, T::wmi;
+  static constexpr int BN = T::BN, TM = T::TM, WC = T::WC, OX0 = T::OX0, OX1 = T::OX1, BUF = T::BUF;
   i32x4 acc[TN][TM], wl[TN], wh[TN];
 
-  __device__ __forceinline__ void load_w(int kb, i32x4* buf) {
-    const bool in = kb * 128 + c16 < p.K;
-    const int so = kb < p.KB ? kb * 128 : 0;
-#pragma unroll
-    for (int i = 0; i < NWL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(buf + wave * 64 + NT * i), 16,
-                                               in ? v0 + static_cast<uint32_t>(i * 64) * p.K : 0x80000000u, so, 0, 0);
-  }
-  // rows 64 half + (0..63) of both 128-row parts
-  __device__ __forceinline__ void load_a(int kb, int half, i32x4* buf) {
-    const bool in = kb * 128 + c16 < p.K;
-    const int so = kb < p.KB ? kb * 128 : 0;
-#pragma unroll
-    for (int i = 0; i < NXL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(buf + (half ? OX1 : OX0) + wave * 64 + NT * i), 16,
-                                               in ? v0 + static_cast<uint32_t>(i * 128 + half * 64) * p.K : 0x80000000u,
-                                               so, 0, 0);
-  }
   // 4 row tiles of the wave by its TN column tiles
   template <int HALF>
   __device__ __forceinline__ void products(const i32x4* __restrict__ x) {
@@ -252,15 +148,6 @@ struct Int8Large {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // Orders workgroup memory between the waves, and only that: unlike a fence it leaves the loads into it that
-  // are counted separately on their way.
-  static __device__ __forceinline__ void hand_over() {
-    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    __asm__ volatile("" ::: "memory");
-  }
   // One block. rd and wr are the same memory: restrict says that what the loads write does not change what is
   // still read before the next barrier. The buffer's offset is opaque, so that nothing read in one step is
   // taken for known in a later one.
@@ -269,9 +156,9 @@ struct Int8Large {
     __asm__ volatile("" : "+s"(cur));
     const int nxt = BUF - cur;
     // first half: w and the first a rows of this block have arrived; newer loads may not have
-    __builtin_amdgcn_s_waitcnt(WAIT);
-    hand_over();
-    load_a(kb + 1, 1, wr + nxt);
+    T::wait();
+    T::hand_over();
+    T::load_a(kb + 1, 1, wr + nxt);
     const int b0 = (wni * WC + r) * 8 + (g ^ (r & 7)), b1 = (wni * WC + r) * 8 + ((g + 4) ^ (r & 7));
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
@@ -280,30 +167,15 @@ struct Int8Large {
     }
     products<0>(rd + cur + OX0);
     // second half: the other a rows have arrived
-    __builtin_amdgcn_s_waitcnt(WAIT);
-    hand_over();
-    load_w(kb + 2, wr + cur);
-    load_a(kb + 2, 0, wr + cur);
+    T::wait();
+    T::hand_over();
+    T::load_w(kb + 2, wr + cur);
+    T::load_a(kb + 2, 0, wr + cur);
     products<1>(rd + cur + OX1);
   }
 
   __device__ __forceinline__ void run(i32x4* lds, float* rows) {
-    tid = threadIdx.x;
-    const int lane = tid & 63;
-    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    r = lane & 15;
-    g = lane >> 4;
-    wni = wave & 3;
-    wmi = wave >> 2;
-    int tm, tn;
-    tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &tm, &tn);
-    m0 = tm * BM;
-    n0 = tn * BN;
-    const int q0 = tid >> 3;
-    c16 = ((tid & 7) ^ (q0 & 7)) * 16;
-    v0 = static_cast<uint32_t>(q0) * p.K + c16;
-    rsa = make_rsrc(p.a + static_cast<long long>(m0) * p.K, static_cast<uint32_t>(min(p.M - m0, BM)) * p.K);
-    rsw = make_rsrc(p.w + static_cast<long long>(n0) * p.K, static_cast<uint32_t>(min(p.N - n0, BN)) * p.K);
+    T::begin();
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -313,41 +185,26 @@ struct Int8Large {
     const float f1 = p.bias && tid < BN && n0 + tid < p.N ? p.bias[n0 + tid] : 0.0f;
     rows[tid] = f0;
     if (tid < 256) rows[512 + tid] = f1;
-    load_w(0, lds);
-    load_a(0, 0, lds);
-    load_a(0, 1, lds);
-    load_w(1, lds + BUF);
-    load_a(1, 0, lds + BUF);
+    T::load_w(0, lds);
+    T::load_a(0, 0, lds);
+    T::load_a(0, 1, lds);
+    T::load_w(1, lds + BUF);
+    T::load_a(1, 0, lds + BUF);
     for (int kb = 0; kb < p.KB; ++kb) step(kb, lds, lds);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into workgroup memory outlives the products
-    const bool whole = !F32OUT && p.vec == 8;
-    TileStore<BM, BN, NT> st{lds};
-    if (whole) __syncthreads();
-    float sa[TM];
+    T::wait_all();
+    float sa[TM], sw[4], bv[4];
 #pragma unroll
     for (int j = 0; j < TM; ++j) sa[j] = rows[wmi * 128 + 16 * j + r];
+    T::template out<F32OUT>(
+        lds,
+        [&](int, int nl) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int nl = wni * WC + 16 * i + 4 * g, n = n0 + nl;
-      float sw[4], bv[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        sw[v] = rows[256 + nl + v];
-        bv[v] = rows[512 + nl + v];
-      }
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const long long m = m0 + wmi * 128 + 16 * j + r;
-        float o[4];
-        scaled(acc[i][j], sa[j], sw, bv, o);
-        if (whole) st.put(wmi * 128 + 16 * j + r, nl, o);
-        else if (m < p.M && n < p.N) store_row4<F32OUT>(p.y, m * p.N + n, p.N - n, p.vec, o);
-      }
-    }
-    if (whole) {
-      __syncthreads();
-      st.flush(p.y, m0, n0, p.M - m0, p.N - n0, p.N, p.stream, tid);
-    }
+          for (int v = 0; v < 4; ++v) {
+            sw[v] = rows[256 + nl + v];
+            bv[v] = rows[512 + nl + v];
+          }
+        },
+        [&](int i, int j, float(&o)[4]) { scaled(acc[i][j], sa[j], sw, bv, o); });
   }
 };
 
@@ -379,30 +236,18 @@ __global__ void __launch_bounds__(512) int8_few_kernel(const Int8Args p) {
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  // rows past the end read the last row, and are not stored
-  const uint8_t* wp[NT];
-  const uint8_t* ap[MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) wp[i] = p.w + static_cast<long long>(min(n0 + 16 * i + r, p.N - 1)) * p.K;
-#pragma unroll
-  for (int j = 0; j < MT; ++j) ap[j] = p.a + static_cast<long long>(min(16 * j + r, p.M - 1)) * p.K;
-  // the two 16-byte chunks g and g + 4 of a row's block; past column K zeros (K is a multiple of 16)
-  auto ld = [&](const uint8_t* row, int kb, i32x4& lo, i32x4& hi) {
-    const int k0 = kb * 128 + 16 * g, k1 = k0 + 64;
-    const i32x4 z = {0, 0, 0, 0};
-    lo = k0 < p.K ? *reinterpret_cast<const i32x4*>(row + k0) : z;
-    hi = k1 < p.K ? *reinterpret_cast<const i32x4*>(row + k1) : z;
-  };
+  FewRows<MT, NT> x;
+  x.begin(p, n0, r, g);
   for (int kb0 = wave * UN; kb0 < p.KB; kb0 += W * UN) {
     i32x4 wl[UN][NT], wh[UN][NT], al[UN][MT], ah[UN][MT];
 #pragma unroll
     for (int u = 0; u < UN; ++u)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) ld(wp[i], kb0 + u, wl[u][i], wh[u][i]);
+      for (int i = 0; i < NT; ++i) x.load(x.wp[i], kb0 + u, wl[u][i], wh[u][i]);
 #pragma unroll
     for (int u = 0; u < UN; ++u)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) ld(ap[j], kb0 + u, al[u][j], ah[u][j]);
+      for (int j = 0; j < MT; ++j) x.load(x.ap[j], kb0 + u, al[u][j], ah[u][j]);
 #pragma unroll
     for (int u = 0; u < UN; ++u)
 #pragma unroll

@@ -29,7 +29,7 @@
 
 #include <type_traits>
 
-#include "layer_common.h"
+#include "matmul_tiles.h"
 
 namespace pararnn {
 
@@ -45,31 +45,6 @@ struct MatmulArgs {
   int stream;         // y is larger than the last-level cache
 };
 
-// 4 columns of y at element i, `left` of them inside the row
-template <bool F32OUT>
-__device__ __forceinline__ void store_row4(void* y, long long i, int left, int vec, const float (&o)[4]) {
-  if constexpr (F32OUT) {
-    float* q = static_cast<float*>(y) + i;
-    if (vec >= 4) {
-      *reinterpret_cast<f32x4*>(q) = f32x4{o[0], o[1], o[2], o[3]};
-    } else {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (v < left) q[v] = o[v];
-    }
-  } else {
-    bf16* q = static_cast<bf16*>(y) + i;
-    const uint32_t lo = pack_bf16(o[0], o[1]), hi = pack_bf16(o[2], o[3]);
-    if (vec >= 4) {
-      *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
-    } else {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (v < left) q[v].bits = static_cast<uint16_t>((v < 2 ? lo : hi) >> (16 * (v & 1)));
-    }
-  }
-}
-
 // fp32 value of a scale: fp32 itself, or e8m0 (2^(b - 127), 255: NaN)
 template <bool E8>
 __device__ __forceinline__ float scale_at(const void* p, long long i) {
@@ -80,45 +55,6 @@ __device__ __forceinline__ float scale_at(const void* p, long long i) {
     return static_cast<const float*>(p)[i];
   }
 }
-
-// Stores a BM x BN tile of bf16 results through workgroup memory: written as
-// the matrix instructions leave them (4 columns of 16 rows per instruction) a
-// wave would touch 32 bytes of a row at a time, which HBM takes at a quarter
-// of its rate. NT threads; put(row, column, 4 values) fills the tile, then
-// whole rows go out 16 bytes per lane. So that 16 rows written at one column
-// touch different banks, chunk c of row m lies at c ^ (m & 15) where a row is
-// a power of two of chunks, and rows are one chunk longer where it is not.
-template <int BM, int BN, int NT>
-struct TileStore {
-  static constexpr int CH = BN / 8;  // 16-byte chunks per row
-  static constexpr bool POW2 = (CH & (CH - 1)) == 0;
-  static constexpr int MASK = POW2 ? (CH < 16 ? CH : 16) - 1 : 0, ROW = POW2 ? CH : CH + 1;
-  static constexpr int CHUNKS = BM * ROW;
-  i32x4* lds;
-  __device__ __forceinline__ void put(int m, int n, const float (&o)[4]) {
-    const int c = n >> 3;
-    reinterpret_cast<u32x2*>(lds + m * ROW + (c ^ (m & MASK)))[(n >> 2) & 1] =
-        u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
-  }
-  // stream: y is larger than the last-level cache and so is not kept in L2,
-  // where it would displace the operands (2 % of the time of a 1 GB result)
-  __device__ __forceinline__ void flush(void* y, long long m0, int n0, int mrows, int ncols, int N, int stream, int tid) {
-    // rows past the tile's last are past the extent, columns past N are not sent
-    const __amdgpu_buffer_rsrc_t to =
-        make_rsrc(static_cast<uint16_t*>(y) + m0 * N + n0, static_cast<uint32_t>((min(mrows, BM) - 1) * N + min(ncols, BN)) * 2);
-    static_assert(BM * CH % NT == 0, "whole rounds");
-#pragma unroll
-    for (int i = 0; i < BM * CH / NT; ++i) {
-      const int e = tid + NT * i, m = e / CH, c = e % CH;
-      if (c * 8 < ncols) {
-        const i32x4 v = lds[m * ROW + (c ^ (m & MASK))];
-        const uint32_t at = static_cast<uint32_t>(m * N + c * 8) * 2;
-        if (stream) __builtin_amdgcn_raw_buffer_store_b128(v, to, at, 0, kBufNT);
-        else __builtin_amdgcn_raw_buffer_store_b128(v, to, at, 0, 0);
-      }
-    }
-  }
-};
 
 // 32 e4m3 values widened to bf16, which holds each of them
 __device__ __forceinline__ void widen(const i32x8& v, bf16x8 (&o)[4]) {
@@ -168,111 +104,25 @@ __device__ __forceinline__ f32x4 tile_product(const Frag<MODE>& w, const Frag<MO
   return d;
 }
 
-// 16 bytes of a row from column k on, zeros past column K, at any alignment
-__device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else if (k < K) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) v[i / 4] |= static_cast<int>(static_cast<uint32_t>(row[k + i]) << (8 * (i % 4)));
-  }
-  return v;
-}
-
-// Tiles in the order of their numbers run near each other in time. Workgroup
-// i runs on XCD i % 8, each with an L2 of its own: consecutive numbers go to
-// one XCD, and 8 row tiles by as many column tiles as it takes follow each
-// other, so that an XCD's workgroups share the panels in its L2.
-__device__ __forceinline__ void tile_of(unsigned int id, unsigned int ntm, unsigned int ntn, int* tm, int* tn) {
-  const unsigned int total = ntm * ntn, per = total / 8, rest = total % 8, x = id % 8, l = id / 8;
-  const unsigned int t = x * per + min(x, rest) + l;
-  const unsigned int grp = t / (8 * ntn), m0 = grp * 8, gm = min(ntm - m0, 8u), u = t - grp * 8 * ntn;
-  *tm = static_cast<int>(m0 + u % gm);
-  *tn = static_cast<int>(u / gm);
-}
-
-// The shape of a tile: waves along n and m, 16 x 16 tiles per wave along n and
-// m; KS groups of such waves, each with every KS-th block of K
-template <int WN_, int WM_, int TN_, int TM_, int KS_>
-struct MatmulShape {
-  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, KS = KS_;
-  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, NT = 64 * WN * WM;  // NT: threads of a group
-};
-
 // Products between the few rows and the large tiles, unaligned operands and
 // fp32 results: BM x BN of y per workgroup, bound by the latency of a step's
-// loads (256 x 4096 x 4096: 12.4 us; 777 x 1000 x 1333 to fp32: 14.6 us). Each
-// step brings 128 columns of both operands into workgroup memory while the
-// matrix cores work on the step before (two buffers); DIRECT: by 16-byte loads
-// that write there without passing through registers, where every row is
-// aligned for them, else through registers. 16-byte chunk c of row q lies at
-// position c ^ (q & 7) of its 128 bytes, so that 8 rows read at one c touch
-// different banks.
+// loads (256 x 4096 x 4096: 12.4 us; 777 x 1000 x 1333 to fp32: 14.6 us).
 // ROWS: rows of w that share a scale, 128 (uniform per wave: TN * 16 <= 64
 // columns that start at a multiple of that) or 1.
 template <class S, int MODE, bool E8, int ROWS, bool F32OUT, bool DIRECT>
-struct Matmul {
-  static constexpr int BN = S::BN, BM = S::BM, NT = S::NT, TN = S::TN, TM = S::TM, KS = S::KS;
-  static constexpr int LN = BN * 8 / NT, LM = BM * 8 / NT;  // 16-byte chunks per thread
+struct Matmul : SmallTiles<MatmulArgs, S, DIRECT> {
+  typedef SmallTiles<MatmulArgs, S, DIRECT> T;
+  using T::p, T::kg, T::r, T::g, T::m0, T::n0, T::wn, T::wm;
+  static constexpr int BN = S::BN, TN = S::TN, TM = S::TM, KS = S::KS;
   static_assert(TN * 16 <= 64, "one scale block of w per wave");
-  static_assert(NT % 64 == 0, "a thread's rows share their low 3 bits");
   typedef std::conditional_t<MODE == kMulE8m0, int, float> SV;
   // e8m0 rows of w scale the first operand's rows, lane % 16; fp32 ones the
   // result's rows, 4 per lane
   static constexpr int NSW = ROWS == 128 ? 1 : MODE == kMulE8m0 ? TN : TN * 4;
-  typedef __attribute__((address_space(3))) void lds_void;
 
-  MatmulArgs p;
-  int tid, wave, r, g, m0, n0, wn, wm, mrows, nrows;
-  __amdgpu_buffer_rsrc_t rsa, rsw;
-  uint32_t v0;  // the thread's first chunk
-  int q0, c0;
-  i32x4 ra[DIRECT ? 1 : LM], rw[DIRECT ? 1 : LN];  // in flight
-  SV fsa[TM], fsw[NSW];                            // scales in flight
+  SV fsa[TM], fsw[NSW];  // scales in flight
   f32x4 acc[TN][TM];
 
-  // thread's chunk i: row (tid + NT i) / 8, position tid % 8, column chunk c0
-  __device__ __forceinline__ void fetch(int kb, i32x4* sw, i32x4* sa) {
-    if constexpr (DIRECT) {
-      // the row is in the lane's offset, which the extent is checked against;
-      // the column's block, the uniform offset, is not. Extents stay below 2^31.
-      const bool in = kb * 128 + c0 * 16 < p.K;
-      const int so = kb < p.KB ? kb * 128 : 0;
-#pragma unroll
-      for (int i = 0; i < LN; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(sw + wave * 64 + NT * i), 16,
-                                                 in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u,
-                                                 so, 0, 0);
-#pragma unroll
-      for (int i = 0; i < LM; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sa + wave * 64 + NT * i), 16,
-                                                 in ? v0 + static_cast<uint32_t>(i * (NT / 8)) * p.K : 0x80000000u,
-                                                 so, 0, 0);
-    } else {
-      const uint8_t* abase = p.a + static_cast<long long>(m0) * p.K;
-      const uint8_t* wbase = p.w + static_cast<long long>(n0) * p.K;
-#pragma unroll
-      for (int i = 0; i < LN; ++i) {
-        const int q = q0 + i * (NT / 8);
-        rw[i] = load16(wbase + static_cast<long long>(min(q, nrows - 1)) * p.K, kb * 128 + c0 * 16, p.K);
-      }
-#pragma unroll
-      for (int i = 0; i < LM; ++i) {
-        const int q = q0 + i * (NT / 8);
-        ra[i] = load16(abase + static_cast<long long>(min(q, mrows - 1)) * p.K, kb * 128 + c0 * 16, p.K);
-      }
-    }
-  }
-  __device__ __forceinline__ void land(i32x4* sw, i32x4* sa) {
-    if constexpr (!DIRECT) {
-#pragma unroll
-      for (int i = 0; i < LN; ++i) sw[tid + NT * i] = rw[i];
-#pragma unroll
-      for (int i = 0; i < LM; ++i) sa[tid + NT * i] = ra[i];
-    }
-  }
   __device__ __forceinline__ SV scale_of(const void* q, long long i) const {
     if constexpr (MODE == kMulE8m0) return static_cast<const uint8_t*>(q)[i];
     else return scale_at<E8>(q, i);
@@ -302,8 +152,8 @@ struct Matmul {
     for (int j = 0; j < TM; ++j) csa[j] = fsa[j];
 #pragma unroll
     for (int i = 0; i < NSW; ++i) csw[i] = fsw[i];
-    if (kb + KS < p.KB + KS - 1) {  // another group may have a block where this one has none
-      fetch(kb + KS, nw, na);
+    if (T::more(kb)) {
+      T::fetch(kb + KS, nw, na);
       scales(kb + KS);
     }
     // lane's two chunks of a row of its tile 0; tile i: 128 i further
@@ -337,96 +187,40 @@ struct Matmul {
       __builtin_amdgcn_sched_barrier(0);
     }
     }
-    if (kb + KS < p.KB + KS - 1) land(nw, na);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the loads into workgroup memory are done
-    __syncthreads();
+    if (T::more(kb)) T::land(nw, na);
+    T::arrived();
   }
 
   __device__ __forceinline__ void run(i32x4* lds) {
-    constexpr int HALF = (BN + BM) * 8;
-    const int kg = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / NT);  // the wave's group
+    T::begin();
     i32x4* const all = lds;
-    lds += kg * 2 * HALF;
-    tid = static_cast<int>(threadIdx.x) - kg * NT;
-    const int lane = tid & 63;
-    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    r = lane & 15;
-    g = lane >> 4;
-    int tm, tn;
-    tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &tm, &tn);
-    m0 = tm * BM;
-    n0 = tn * BN;
-    wn = (wave % S::WN) * TN * 16;
-    wm = (wave / S::WN) * TM * 16;
-    mrows = min(p.M - m0, BM);
-    nrows = min(p.N - n0, BN);
-    q0 = tid >> 3;
-    c0 = (tid & 7) ^ (q0 & 7);
-    v0 = static_cast<uint32_t>(q0) * p.K + c0 * 16;
-    rsa = make_rsrc(p.a + static_cast<long long>(m0) * p.K, static_cast<uint32_t>(mrows) * p.K);
-    rsw = make_rsrc(p.w + static_cast<long long>(n0) * p.K, static_cast<uint32_t>(nrows) * p.K);
+    lds += kg * 2 * T::HALF;
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    fetch(kg, lds, lds + BN * 8);
+    T::fetch(kg, lds, lds + BN * 8);
     scales(kg);
-    land(lds, lds + BN * 8);
-    __builtin_amdgcn_s_waitcnt(0x0f70);
-    __syncthreads();
+    T::land(lds, lds + BN * 8);
+    T::arrived();
     int odd = 0;  // every group takes as many steps as the first
     for (int kb = 0; kb < p.KB; kb += KS, odd ^= 1) {
-      i32x4* c = lds + odd * HALF;
-      i32x4* n = lds + (1 - odd) * HALF;
+      i32x4* c = lds + odd * T::HALF;
+      i32x4* n = lds + (1 - odd) * T::HALF;
       step(kb + kg, c, c + BN * 8, n, n + BN * 8);
     }
-    if constexpr (KS > 1) {  // the groups' sums, joined in order
-      f32x4* sum = reinterpret_cast<f32x4*>(all);
-      constexpr int PER = TN * TM * NT;
-      static_assert((KS - 1) * PER <= KS * 2 * HALF, "the sums fit where the blocks were");
-      if (kg > 0) {
+    T::join(acc, all);
+    float bv[4];
+    T::template out<F32OUT>(
+        all,
+        [&](int, int n) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
+          for (int v = 0; v < 4; ++v) bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
+        },
+        [&](int i, int j, float(&o)[4]) {
 #pragma unroll
-          for (int j = 0; j < TM; ++j) sum[(kg - 1) * PER + (i * TM + j) * NT + tid] = acc[i][j];
-      }
-      __syncthreads();
-      if (kg == 0) {
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-          for (int j = 0; j < TM; ++j)
-#pragma unroll
-            for (int k = 0; k < KS - 1; ++k) acc[i][j] += sum[k * PER + (i * TM + j) * NT + tid];
-      }
-      __syncthreads();
-    }
-    const bool whole = !F32OUT && p.vec == 8;  // the last step ended with a barrier
-    TileStore<BM, BN, NT> st{all};
-    if (kg > 0) {
-      if (whole) __syncthreads();
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int n = n0 + wn + 16 * i + 4 * g;
-      float bv[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) bv[v] = p.bias && n + v < p.N ? p.bias[n + v] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const long long m = m0 + wm + 16 * j + r;
-        float o[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
-        if (whole) st.put(wm + 16 * j + r, n - n0, o);
-        else if (m < p.M && n < p.N) store_row4<F32OUT>(p.y, m * p.N + n, p.N - n, p.vec, o);
-      }
-    }
-    if (whole) {
-      __syncthreads();
-      st.flush(p.y, m0, n0, mrows, p.N - n0, p.N, p.stream, tid);
-    }
+          for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
+        });
   }
 };
 
@@ -439,64 +233,26 @@ __global__ void __launch_bounds__(S::NT * S::KS) matmul_kernel(const MatmulArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Large products: 256 rows by 64 TN columns of y by 8 waves (4 along n, 2
-// along m; 16 TN x 128 each), two waves per SIMD. What bounds it is the time
-// from the issue of a block's loads to their arrival, about a step and a half
-// of products, and workgroup memory holds two blocks only. So a step has two halves: the first
-// multiplies the wave's w rows by the first half of its a rows, the second by
-// the other half. After the first half nobody needs this block's w and first
-// a rows any more (w's stay in registers), and their place takes the block
-// after the next; the place of the second a rows is taken one half later.
-// Every load so has a step and a half to arrive, and the waits count the loads
-// that may still be on their way. 32768 x 16384 x 4096 with e8m0 scales takes
+// Large products: tiles of 256 rows by 64 TN columns. 32768 x 16384 x 4096 with e8m0 scales takes
 // 1.84 to 1.92 ms (2290 to 2390 TFLOP/s, by the box), 4096 x 6144 x 2048 with
 // fp32 scales 61 to 66 us (1570 to 1690);
 // with 32 or 16 blocks of K, what a tile costs before its first product and
 // behind its last (5 us) is a sixth to a third of its time.
 template <int TN, int MODE, bool E8, int ROWS>
-struct MatmulLarge {
-  static constexpr int BN = 64 * TN, BM = 256, NT = 512, TM = 8, WC = 16 * TN;
-  // 16-byte chunks of one buffer: w, then the first and the second a rows of both waves along m
-  static constexpr int OX0 = BN * 8, OX1 = OX0 + BM * 4, BUF = OX1 + BM * 4;
+struct MatmulLarge : LargeTiles<MatmulArgs, TN> {
+  typedef LargeTiles<MatmulArgs, TN> T;
+  using T::p, T::tid, T::r, T::g, T::m0, T::n0, T::wni, T::wmi;
+  static constexpr int BN = T::BN, TM = T::TM, WC = T::WC, OX0 = T::OX0, OX1 = T::OX1, BUF = T::BUF;
   static constexpr int SB = MODE == kMulE8m0 ? 1 : 4;      // bytes of a scale in workgroup memory
   static constexpr int SCH = 256 * SB;  // bytes of 256 scales: two buffers for a, two for w
-  static constexpr int NWL = TN, NXL = 2;  // loads per thread: w, half of a
-  // loads that may be on their way when a half step begins: this or the next
-  // block's second a rows, and w and the first a rows of the next block
-  static constexpr int WAIT = 0x0f70 | (NWL + 2 * NXL);
   // a lane's scales of w: with one per block, 64 columns are in one block, 48 may be in two
   static constexpr int NB = TN == 4 ? 1 : TN, NSC = ROWS == 128 ? NB : SB == 1 ? 1 : 4 * TN;
-  static constexpr int TILE_BUF = TileStore<BM, BN, NT>::CHUNKS, LDS = 2 * BUF > TILE_BUF ? 2 * BUF : TILE_BUF;
-  typedef __attribute__((address_space(3))) void lds_void;
 
-  MatmulArgs p;
-  int tid, wave, r, g, m0, n0, wni, wmi;
-  __amdgpu_buffer_rsrc_t rsa, rsw;
-  uint32_t v0;
-  int c16;                 // the thread's column within a block, bytes
   f32x4 acc[TN][TM];
   i32x8 fw[TN];
   uint32_t vs;  // scale on its way: of row tid (first half of the threads), of a column or block of w (second)
   f32x4 d[MODE == kMulE8m0 ? 1 : TN];  // products not yet scaled: of row tile dj, by ds
 
-  __device__ __forceinline__ void load_w(int kb, i32x4* buf) {
-    const bool in = kb * 128 + c16 < p.K;
-    const int so = kb < p.KB ? kb * 128 : 0;
-#pragma unroll
-    for (int i = 0; i < NWL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_void*)(buf + wave * 64 + NT * i), 16,
-                                               in ? v0 + static_cast<uint32_t>(i * 64) * p.K : 0x80000000u, so, 0, 0);
-  }
-  // rows 64 half + (0..63) of both 128-row parts
-  __device__ __forceinline__ void load_a(int kb, int half, i32x4* buf) {
-    const bool in = kb * 128 + c16 < p.K;
-    const int so = kb < p.KB ? kb * 128 : 0;
-#pragma unroll
-    for (int i = 0; i < NXL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(buf + (half ? OX1 : OX0) + wave * 64 + NT * i), 16,
-                                               in ? v0 + static_cast<uint32_t>(i * 128 + half * 64) * p.K : 0x80000000u,
-                                               so, 0, 0);
-  }
   static __device__ __forceinline__ uint32_t raw_scale(const void* q, long long i) {
     if constexpr (MODE == kMulE8m0) return static_cast<const uint8_t*>(q)[i];
     else return __float_as_uint(scale_at<E8>(q, i));
@@ -590,16 +346,6 @@ struct MatmulLarge {
 #undef PARARNN_MFMA
   }
 
-  // Orders workgroup memory between the waves, and only that: unlike a fence
-  // it leaves the loads into it that are counted separately on their way.
-  static __device__ __forceinline__ void hand_over() {
-    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    __asm__ volatile("" ::: "memory");
-  }
-
   // One block. rd and wr are the same memory, and so are rs and ws: restrict
   // says that what is written (by the loads into workgroup memory, which the
   // compiler would otherwise wait for) does not change what is still read
@@ -611,13 +357,13 @@ struct MatmulLarge {
     __asm__ volatile("" : "+s"(cur));
     const int nxt = BUF - cur;
     // first half: w and the first a rows of this block have arrived, and the
-    // next block's scales; 8 newer loads may not have
-    __builtin_amdgcn_s_waitcnt(WAIT);
+    // next block's scales; newer loads may not have
+    T::wait();
     land_scales(kb + 1, ws);
-    hand_over();
+    T::hand_over();
     load_scales(kb + 2);
     __builtin_amdgcn_sched_barrier(0);
-    load_a(kb + 1, 1, wr + nxt);
+    T::load_a(kb + 1, 1, wr + nxt);
     i32x4 sc[SB == 1 ? 1 : 2];
     uint32_t csw[NSC];
     {
@@ -652,31 +398,16 @@ struct MatmulLarge {
     for (int i = 0; i < TN; ++i)
       fw[i] = __builtin_shufflevector(rd[cur + b0 + 128 * i], rd[cur + b1 + 128 * i], 0, 1, 2, 3, 4, 5, 6, 7);
     products<0>(rd + cur + OX0, sc, csw);
-    // second half: the other a rows have arrived; again WAIT's newer loads may not have
-    __builtin_amdgcn_s_waitcnt(WAIT);
-    hand_over();
-    load_w(kb + 2, wr + cur);
-    load_a(kb + 2, 0, wr + cur);
+    // second half: the other a rows have arrived; again newer loads may not have
+    T::wait();
+    T::hand_over();
+    T::load_w(kb + 2, wr + cur);
+    T::load_a(kb + 2, 0, wr + cur);
     products<1>(rd + cur + OX1, sc, csw);
   }
 
   __device__ __forceinline__ void run(i32x4* lds, char* scales) {
-    tid = threadIdx.x;
-    const int lane = tid & 63;
-    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    r = lane & 15;
-    g = lane >> 4;
-    wni = wave & 3;
-    wmi = wave >> 2;
-    int tm, tn;
-    tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &tm, &tn);
-    m0 = tm * BM;
-    n0 = tn * BN;
-    const int q0 = tid >> 3;
-    c16 = ((tid & 7) ^ (q0 & 7)) * 16;
-    v0 = static_cast<uint32_t>(q0) * p.K + c16;
-    rsa = make_rsrc(p.a + static_cast<long long>(m0) * p.K, static_cast<uint32_t>(min(p.M - m0, BM)) * p.K);
-    rsw = make_rsrc(p.w + static_cast<long long>(n0) * p.K, static_cast<uint32_t>(min(p.N - n0, BN)) * p.K);
+    T::begin();
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -686,41 +417,27 @@ struct MatmulLarge {
     const float bias = p.bias && tid < BN && n0 + tid < p.N ? p.bias[n0 + tid] : 0.0f;
     load_scales(0);
     const uint32_t vs0 = vs;
-    load_w(0, lds);
-    load_a(0, 0, lds);
+    T::load_w(0, lds);
+    T::load_a(0, 0, lds);
     load_scales(1);
     __builtin_amdgcn_sched_barrier(0);
-    load_a(0, 1, lds);
-    load_w(1, lds + BUF);
-    load_a(1, 0, lds + BUF);
+    T::load_a(0, 1, lds);
+    T::load_w(1, lds + BUF);
+    T::load_a(1, 0, lds + BUF);
     const uint32_t vs1 = vs;
     vs = vs0;
     land_scales(0, scales);
     vs = vs1;
     if (tid < BN) s_bias[tid] = bias;
     for (int kb = 0; kb < p.KB; ++kb) step(kb, lds, lds, scales, scales);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // no load into workgroup memory outlives the products
-    const bool whole = p.vec == 8;
-    TileStore<BM, BN, NT> st{lds};
-    if (whole) __syncthreads();
+    T::wait_all();
+    f32x4 bv;
+    T::template out<false>(
+        lds, [&](int, int nl) { bv = *reinterpret_cast<const f32x4*>(s_bias + nl); },
+        [&](int i, int j, float(&o)[4]) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int n = n0 + wni * WC + 16 * i + 4 * g;
-      const f32x4 bv = *reinterpret_cast<const f32x4*>(s_bias + (n - n0));
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const long long m = m0 + wmi * 128 + 16 * j + r;
-        float o[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
-        if (whole) st.put(wmi * 128 + 16 * j + r, n - n0, o);
-        else if (m < p.M && n < p.N) store_row4<false>(p.y, m * p.N + n, p.N - n, p.vec, o);
-      }
-    }
-    if (whole) {
-      __syncthreads();
-      st.flush(p.y, m0, n0, p.M - m0, p.N - n0, p.N, p.stream, tid);
-    }
+          for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] + bv[v];
+        });
   }
 };
 
@@ -753,21 +470,8 @@ __global__ void __launch_bounds__(512) matmul_few_kernel(const MatmulArgs p) {
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // rows past the end read the last row, and are not stored
-  const uint8_t* wp[NT];
-  const uint8_t* ap[MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) wp[i] = p.w + static_cast<long long>(min(n0 + 16 * i + r, p.N - 1)) * p.K;
-#pragma unroll
-  for (int j = 0; j < MT; ++j) ap[j] = p.a + static_cast<long long>(min(16 * j + r, p.M - 1)) * p.K;
-
-  // the two 16-byte chunks g and g + 4 of a row's block; past column K zeros (K is a multiple of 16)
-  auto ld = [&](const uint8_t* row, int kb, i32x4& lo, i32x4& hi) {
-    const int k0 = kb * 128 + 16 * g, k1 = k0 + 64;
-    const i32x4 z = {0, 0, 0, 0};
-    lo = k0 < p.K ? *reinterpret_cast<const i32x4*>(row + k0) : z;
-    hi = k1 < p.K ? *reinterpret_cast<const i32x4*>(row + k1) : z;
-  };
+  FewRows<MT, NT> x;
+  x.begin(p, n0, r, g);
   for (int kb0 = wave * UN; kb0 < p.KB; kb0 += W * UN) {
     i32x4 wl[UN][NT], wh[UN][NT], al[UN][MT], ah[UN][MT];
     float sa[UN][MT], sw[UN][ROWS == 128 ? 1 : NT * 4];
@@ -775,14 +479,14 @@ __global__ void __launch_bounds__(512) matmul_few_kernel(const MatmulArgs p) {
     for (int u = 0; u < UN; ++u) {
       const int kb = kb0 + u;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) ld(wp[i], kb, wl[u][i], wh[u][i]);
+      for (int i = 0; i < NT; ++i) x.load(x.wp[i], kb, wl[u][i], wh[u][i]);
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int kb = kb0 + u, k = min(kb, p.KB - 1);
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        ld(ap[j], kb, al[u][j], ah[u][j]);
+        x.load(x.ap[j], kb, al[u][j], ah[u][j]);
         sa[u][j] = scale_at<E8>(p.sa, static_cast<long long>(k) * p.M + min(16 * j + r, p.M - 1));
       }
       if constexpr (ROWS == 128) {
