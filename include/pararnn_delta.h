@@ -8,7 +8,9 @@
  * asynchronous on `stream`, status codes PARARNN_*, nothing launched on an
  * error other than PARARNN_EHIP, inputs and outputs that do not alias (except
  * where a call says "in place"). Sums, states and statistics are held in 32
- * bits; results are rounded once, to nearest even. Repeated calls give the
+ * bits, those that go to bf16 outputs too; results are rounded once, to
+ * nearest even. Squares are summed in fp32: |q|^2, |k|^2 and the squares of a
+ * normed row must not pass its largest number. Repeated calls give the
  * same bits. Sizes whose launch would have 2^32 threads or more are
  * PARARNN_EINVAL.
  */
@@ -50,11 +52,14 @@ typedef struct {
   const uint8_t* reset;     /* [B][L] (device) nonzero: a document starts at this step, S_{t-1} counts as zero;
                                NULL = none. (An infinity or a NaN among a row's steps reaches, in its heads, the
                                steps after it, over a start too, and none in front of it; in the adjoint all of the
-                               row's. |q|^2 and |k|^2 that pass the largest fp32 number count as infinities.) */
+                               row's.) */
 } pararnn_delta_opts;
 
 /* Workspace of pararnn_delta_scan (adjoint = 0) or _adjoint (adjoint = 1), and
- * bytes of `saved`, into *bytes. Host-only. */
+ * bytes of `saved`, into *bytes. Host-only. Of each value head and 64 steps,
+ * with dk and dv up to the next multiples of 32, `saved` takes 4 dv (dk + 64)
+ * bytes (96 KB at 128 x 128), the workspace 39 KB, and in the adjoint as much as
+ * `saved` besides; few heads add their segments' matrices, up to 32 MB. */
 int32_t pararnn_delta_workspace_bytes(int32_t adjoint, const pararnn_delta_opts* o, size_t* bytes);
 int32_t pararnn_delta_saved_bytes(const pararnn_delta_opts* o, size_t* bytes);
 

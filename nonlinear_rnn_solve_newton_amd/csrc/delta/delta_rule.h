@@ -9,7 +9,7 @@
 //   y = T X,  T = (1 + strictly lower(E_ij k_i.k_j b_j))^-1   (v less what k reads)
 //   O = scale e^G Q S0 + P y,   P = lower(scale E_ij q_i.k_j b_j)
 //   S1 = e^G_64 S0 + K^T (e^(G_64 - G) b y).
-// |T_ij| <= b_j <= 1: it is a product of contractions between two unit keys. T
+// T_ii = 1 and |T_ij| <= b_j <= 1 for i > j: a product of contractions between two unit keys. T
 // is inverted by substitution in blocks of 16 and joined, never by its series,
 // whose terms reach C(63, 31) for equal keys.
 //

@@ -583,7 +583,10 @@ def delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.T
     after it, over a start too, and in the adjoint those in front of it); scale None:
     dk^-1/2. dk at most 128, dv at most 512.
     Returns dict(o [B][L][HV][dv], sT [B][HV][dk][dv] fp32 state after the last
-    step, saved (with save=True, for the adjoint), ws).
+    step, saved (with save=True, for the adjoint), ws). saved is the fp32 state in
+    front of every 64 steps and the values between: 4 dv (dk + 64) bytes of each value
+    head (dk, dv up to multiples of 32), 0.4 GB for B = 8 L = 4096 and 8 heads of 128 x
+    128; ws 0.16 GB there, the adjoint's 0.56.
     """
     o, views, dev = _delta_opts(q, k, v, gates, lam, c, eps, scale, 2, lengths, reset)
     B, L, H, HV, dk, dv = o.B, o.L, o.H, o.HV, o.dk, o.dv
