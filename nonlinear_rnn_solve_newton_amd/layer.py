@@ -196,10 +196,20 @@ def _like(t, name: str, dtype: torch.dtype, shape: tuple, device: torch.device):
         raise PararnnError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _int32(*sizes: int):
+_INT32 = 0x7fffffff
+
+
+def _sizes32(*sizes: int):
+    for n in sizes:
+        if n > _INT32:
+            raise PararnnError(f"every size must be at most {_INT32}, got {n}")
+
+
+def _int32(*tensors: torch.Tensor):
     """Sizes go to the library as 32-bit numbers, which would be the low bits of larger ones."""
-    if max(sizes) > 0x7fffffff:
-        raise PararnnError(f"every size must be at most 2147483647, got {max(sizes)}")
+    for t in tensors:
+        if t.numel() > _INT32:  # none is larger than all of them together
+            _sizes32(*t.shape)
 
 
 def _first(t, name: str, dims: int) -> torch.device:
@@ -272,7 +282,7 @@ def _gated_opts(u, lam, c, lengths, reset):
     B, L, G, D = u.shape
     if G != 3:
         raise PararnnError("u must be [B][L][3][D]")
-    _int32(B, L, D)
+    _int32(u)
     if u.dtype not in _DTYPE:
         raise PararnnError(f"u must be float32 or bfloat16, got {u.dtype}")
     _dev(lam, "lam", torch.float32, (D,), dev)
@@ -350,7 +360,7 @@ def gated_step(u: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *, c: fl
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise PararnnError("state must be [S][D]")
     S = state.shape[0]
-    _int32(B, D, S)
+    _int32(u, state)
     _dev(state, "state", torch.float32, (S, D), dev)
     _dev(slots, "slots", torch.int32, (B,), dev)
     if out is None:
@@ -382,7 +392,7 @@ def norm_residual(x: torch.Tensor, w: torch.Tensor, *, residual: Optional[torch.
     """
     dev = _first(x, "x", 2)
     N, D = x.shape
-    _int32(D)
+    _sizes32(D)
     if x.dtype not in _DTYPE:
         raise PararnnError(f"x must be float32 or bfloat16, got {x.dtype}")
     _dev(residual, "residual", x.dtype, (N, D), dev)
@@ -411,7 +421,7 @@ def norm_residual_adjoint(s: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, *,
     gradient of x and of the residual, in s's type, dw [D] fp32, ws)."""
     dev = _first(s, "s", 2)
     N, D = s.shape
-    _int32(D)
+    _sizes32(D)
     if s.dtype not in _DTYPE:
         raise PararnnError(f"s must be float32 or bfloat16, got {s.dtype}")
     _dev(w, "w", torch.float32, (D,), dev)
@@ -481,7 +491,7 @@ def matmul_fp8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Ten
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise PararnnError("w must be [N][K]")
     N = w.shape[0]
-    _int32(M, N, K)
+    _int32(a, w)
     _dev(a, "a", torch.float8_e4m3fn, (M, K), dev)
     _dev(w, "w", torch.float8_e4m3fn, (N, K), dev)
     KB = -(-K // BLOCK)
@@ -538,7 +548,7 @@ def _delta_opts(q, k, v, gates, lam, c, eps, scale, lead, lengths=None, reset=No
     HV, dv = v.shape[lead:]
     if 0 in q.shape or 0 in v.shape or HV % H:
         raise PararnnError("q, k and v must not be empty, and v's heads a multiple of q's")
-    _int32(*q.shape, HV, dv)
+    _int32(q, v)
     dt, qk = q.dtype, (*at, H, dk)
     views = (_view(q, "q", dt, qk, dev), _view(k, "k", dt, qk, dev), _view(v, "v", dt, (*at, HV, dv), dev),
              _view(gates, "gates", dt, (*at, 2, HV), dev))
@@ -648,7 +658,7 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gates: torch.T
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise PararnnError("state must be [S][HV][dk][dv]")
     S = state.shape[0]
-    _int32(S)
+    _int32(state)
     _dev(state, "state", torch.float32, (S, o.HV, o.dk, o.dv), dev)
     _dev(slots, "slots", torch.int32, (o.B,), dev)
     if out is None:
@@ -681,7 +691,7 @@ def _norm_block_opts(x, w, gate, group, alpha, w_next, eps, residual: bool):
         raise PararnnError(f"x must be float32 or bfloat16, got {x.dtype}")
     if 0 in x.shape:
         raise PararnnError("x must not be empty")
-    _int32(D)
+    _sizes32(D)
     group = D if group is None else group
     if not isinstance(group, int) or group < 1 or D % group:
         raise PararnnError(f"group must be a divisor of {D}, got {group}")
@@ -800,7 +810,7 @@ def matmul_int8(a: torch.Tensor, sa: torch.Tensor, w: torch.Tensor, sw: torch.Te
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise PararnnError("w must be [N][K]")
     N = w.shape[0]
-    _int32(M, N, K)
+    _int32(a, w)
     _dev(a, "a", torch.int8, (M, K), dev)
     _dev(w, "w", torch.int8, (N, K), dev)
     if sa is None or sw is None:
