@@ -46,7 +46,7 @@ struct DeltaSizes {
 // B = 8: 234 -> 272), in the adjoint, which both scans are less of, from four on (three: 570 -> 584 us; B = 1 L =
 // 4096 H = 32, four: 507 -> 500), and in bf16, whose chunks are passed in a third of fp32's time, from 16 chunks on
 // (H = 8, 9 chunks: 37 -> 44 us, 16: 55 -> 56, 32 and B = 4: 106 -> 99; fp32, 6 chunks: 49 -> 38). B = 1 L = 65536
-// H = 16: 2815 -> 1082 us.
+// H = 16: 2815 -> 1082 us (all measured with two planes in what goes to bf16 outputs; with three 1220).
 struct DeltaSegments {
   int n, per;
 };

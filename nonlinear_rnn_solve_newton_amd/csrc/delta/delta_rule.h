@@ -169,8 +169,8 @@ __device__ __forceinline__ void invert16(const float* a, int m, float (&x)[16]) 
 // indexes of its row of P, as the operand wants them, and P never leaves
 // registers; the keys' own products go to workgroup memory to be inverted, and at
 // 36 KB four workgroups to a CU hide each other's substitution, the longest part.
-// B = 8 L = 4096 H = 8, 128 wide, bf16: 70 us, 291 MB (4.1 TB/s; with P in workgroup
-// memory 111 us); the adjoint's 92 us, 318 MB.
+// B = 8 L = 4096 H = 8, 128 wide, bf16: 74 us, 318 MB (4.3 TB/s; with P in workgroup
+// memory it took 1.6 times as long); the adjoint's 91 us, 319 MB.
 template <class UT, bool EVEN, int DK, bool ADJ>
 __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kernel(const DeltaArgs p) {
   constexpr int NP = DeltaPlanes<UT>::NP, KB = DK / 32, ROW = 68;
@@ -419,17 +419,17 @@ struct DeltaBuf {
 // themselves. Eight waves that each load a share of a chunk of 128 columns, two on
 // a SIMD, take 10 us for it, two workgroups of four 7.5.
 //
-// B = 8 L = 4096 H = 8, 128 wide, bf16, with what the adjoint needs: 266 us forward,
-// 300 back (886 MB each, half of them the fp32 states and y, or dS and dX, going out;
-// 3.0 to 3.3 TB/s); a chunk of a workgroup takes 4.2 us, 2.6 where no states go out,
+// B = 8 L = 4096 H = 8, 128 wide, bf16, with what the adjoint needs: 281 us forward,
+// 297 back (910 and 886 MB, half of them the fp32 states and y, or dS and dX, going out;
+// 3.0 to 3.2 TB/s); a chunk of a workgroup takes 4.4 us, 3.4 where no states go out,
 // of which the matrix instructions are 1.2. The chain of a chunk's products bounds it.
 //
 // Few heads leave CUs idle, so a sequence is cut into segments. What a segment
 // makes of the state in front of it is affine: delta_segment_kernel (SEG) scans
 // all segments at once for the state that each adds, and with the columns of the
 // identity and no v for the matrix; the scans then start every segment from the
-// product over those before it. B = 1 L = 65536 H = 16: 500 us for the segments, 480
-// for the scan, which took 2650 in one piece; all CUs at once then ask for 4.8 TB/s.
+// product over those before it. B = 1 L = 65536 H = 16: 480 to 560 us for the segments, 530 to
+// 630 for the scan (1.9 GB, 3.0 to 3.6 TB/s), which took 2650 in one piece.
 template <class UT, int MODE, int DK, int NC, int NW, bool ADJ, bool SEG = false>
 struct DeltaScan {
   static constexpr int NP = DeltaPlanes<UT>::NP, RT = DK / 16, KB = DK / 32, VC = 16 * NC * NW;
@@ -1774,8 +1774,8 @@ struct DeltaStepArgs {
 // One token: a workgroup per request, value head and 32 columns of the state,
 // 4 columns and every 32nd row per thread. o = a S^T q + (q.k) u needs the old
 // state only, so both sums over the rows come from one pass, and the state is read
-// and written once. 64 requests of 32 heads of 128 x 128: 57 us, 4.7 TB/s, what a copy
-// reaches; one request of 8 heads: 5.9 us, the latency of two dependent loads and a launch.
+// and written once. 64 requests of 32 heads of 128 x 128: 53 to 57 us, 4.7 to 5.1 TB/s, what a copy
+// reaches; one request of 8 heads: 5.5 us, the latency of two dependent loads and a launch.
 template <class UT>
 __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaStepArgs p) {
   constexpr int NR = 4;  // rows per thread: dk <= 128
