@@ -277,20 +277,20 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
   __syncthreads();
   constexpr float kLog2e = 1.4426950408889634f;
   bf16x8* const out = p.frags + (static_cast<long long>(bh) * p.nc + ch) * DeltaFrags::ALL;
+  // The first step whose key or gates are no numbers (a key's length is a positive one else). Rows from there on
+  // stay out of T and P, whose zeros above the diagonal would carry them to the rows in front; the scan has them
+  // from kRowX. (The adjoint's gradients run the other way as well, and are not kept apart.)
+  int good = 64;
+  if constexpr (!ADJ) {
+    const unsigned long long bad = __ballot(!(srk[lane] > 0.0f) || sg[lane] != sg[lane] || sb[lane] != sb[lane]);
+    good = bad ? __builtin_ctzll(bad) : 64;
+  }
   {
     // element (row i, column j) of both: E_ij with the lengths, b_j and the scale. The lane's own index is the
     // row i (ADJ: the column j), and it has 4 of the other.
     const int own = 16 * w + m;
     const float Go = sg[own], lo = sgl[own], so = sseg[own], ko = srk[own], qo = srq[own] * p.scale, bo = sb[own];
-    // The first step whose key or gates are no numbers (a key's length is a positive one else). Rows from there on
-    // stay out of T and P, whose zeros above the diagonal would carry them to the rows in front; the scan has them
-    // from kRowX. (The adjoint's gradients run the other way as well, and are not kept apart.)
-    int good = 64;
-    if constexpr (!ADJ) {
-      const unsigned long long bad = __ballot(!(srk[lane] > 0.0f) || sg[lane] != sg[lane] || sb[lane] != sb[lane]);
-      good = bad ? __builtin_ctzll(bad) : 64;
-    }
-    const bool live = ADJ || own < good;
+    const bool live = own < good;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f32x4 mv = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(256, sizeof(UT) == 2 ? 4 : 1) delta_prep_kerne
     const float G = sg[i], Ge = sg[63], se = sseg[63], rest = log_gap(Ge, sgl[63], G, sgl[i]);
     const float gamma = sseg[i] == 0.0f ? __builtin_amdgcn_exp2f(G * kLog2e) : 0.0f;
     const float tail = sseg[i] == se ? __builtin_amdgcn_exp2f(rest * kLog2e) : 0.0f;
-    rows[kRowX * 64 + i] = srk[i] > 0.0f ? gamma * srk[i] : __uint_as_float(0x7fc00000u);
+    rows[kRowX * 64 + i] = i < good ? gamma * srk[i] : __uint_as_float(0x7fc00000u);
     rows[kRowO * 64 + i] = p.scale * gamma * srq[i];
     rows[kRowS * 64 + i] = tail * srk[i] * sb[i];
     rows[kRowWhole * 64 + i] = se == 0.0f ? __builtin_amdgcn_exp2f(Ge * kLog2e) : 0.0f;

@@ -20,7 +20,7 @@ def inputs(dtype, H, HV):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=str)
-@pytest.mark.parametrize("where", ["q", "k", "v", "gates"])
+@pytest.mark.parametrize("where", ["q", "k", "v", "gates", "strength"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_reach(dtype, where, bad):
     """Results of the steps in front, of the other row and of the other heads are what they are without it, bit for
@@ -31,13 +31,13 @@ def test_reach(dtype, where, bad):
     x = inputs(DT[dtype], H, HV)
     clean = run(cuda(x))
     h = 1
-    if where == "gates":
-        x["gates"][0, AT, 0, h] = bad
+    if where in ("gates", "strength"):  # the decay's, or that of what is written
+        x["gates"][0, AT, int(where == "strength"), h] = bad
     else:
         x[where][0, AT, h, 3] = bad
     got = run(cuda(x))
     # value heads that take head h of q or k
-    hit = [h] if where in ("v", "gates") else [hv for hv in range(HV) if hv // (HV // H) == h]
+    hit = [h] if where in ("v", "gates", "strength") else [hv for hv in range(HV) if hv // (HV // H) == h]
     free = [hv for hv in range(HV) if hv not in hit]
     for n in ("o", "dv"):
         assert torch.equal(got[n][1], clean[n][1]) and torch.equal(got[n][0][:, free], clean[n][0][:, free]), n
