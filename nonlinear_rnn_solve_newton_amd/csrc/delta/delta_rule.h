@@ -801,7 +801,7 @@ struct DeltaBadRows {
 #pragma unroll
       for (int pl = 0; pl < 3; ++pl) w[kb][pl] = __builtin_bit_cast(i32x4, x[kb][pl]);
 #pragma unroll
-    for (int e = 15; e >= 0; --e) {  // row 4 e + r of the column, r = e & 3
+    for (int e = 15; e >= 0; --e) {  // element e: row e % 4 of the lane's in tile e / 4
       const int u = w[e >> 3][0][(e & 7) >> 1], bits = e & 1 ? u >> 16 : u;
       if ((bits & 0x7f80) == 0x7f80) first = row(e >> 2, g, e & 3);
     }
